@@ -11,6 +11,9 @@ Tensors must be contiguous CUDA (HIP) tensors of these dtypes:
   scales_f32, y           torch.float32
   x_bf16, w_bf16, out     torch.bfloat16, torch.int16 or torch.uint16 (bf16 bit patterns)
   ws                      any dtype, or None when the op needs no workspace
+The norms, router, expert layer and 4-bit linear at the end of this file take
+tensors of any one device, and run on that device's current stream unless
+`stream` names another one of it.
 """
 from __future__ import annotations
 
@@ -21,7 +24,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp8blk.so")
 
 OK, ERR_ARG, ERR_SCALE_FF, ERR_NAN_CODE, ERR_INEXACT, ERR_WORKSPACE, ERR_HIP, ERR_BAD_SCALE, ERR_TIMEOUT = range(9)
-OP_LOAD_CHECK, OP_DEQUANT_BF16, OP_GEMV, OP_BF16_TWIN, OP_GEMM_STAGED, OP_BF16_GEMM = range(6)
+OP_LOAD_CHECK, OP_DEQUANT_BF16, OP_GEMV, OP_BF16_TWIN, OP_GEMM_STAGED, OP_BF16_GEMM, OP_MOE_ROUTE = range(7)
 MIN_COLS, MAX_COLS, MAX_M, MAX_PANEL = 16, 65536, 16, 65536
 
 # Every symbol include/fp8blk.h declares.
@@ -35,13 +38,16 @@ EXPORTS = ("fp8blk_abi_version", "fp8blk_strerror", "fp8blk_workspace_bytes", "f
            "bf16_gemv_twin_mfma_sequence", "fp8blk_gemm_staged", "bf16_gemm_twin", "fp8blk_act_quant",
            "fp4_load_check", "fp4_dequant_bf16", "fp4_expert_gemv", "fp4_expert_sequence_init",
            "fp4_expert_sequence", "fp8blk_chain_bytes", "fp8blk_chain_init", "fp8blk_gemv_chain",
-           "fp8blk_chain_status")
+           "fp8blk_chain_status", "fp8blk_block_norm", "fp8blk_moe_route", "fp4_moe_bytes", "fp4_moe", "int4_gemv")
 MAX_GROUP = 8
 MAX_SEQ = 65536
 MAX_CHAIN = 65536
 CHAIN_COLS = (1024, 2048, 3072, 4096)
 ARM_FP8, ARM_BF16, ARM_FP8_MFMA, ARM_BF16_MFMA, ARM_MXFP4, ARM_NVFP4 = 0, 1, 2, 3, 4, 5
 FMT_MXFP4, FMT_NVFP4 = 0, 1
+MAX_EXPERTS, MAX_TOP_K = 1024, 16
+SCORE_SOFTMAX, SCORE_SIGMOID, SCORE_SQRT_SOFTPLUS = 0, 1, 2
+TYPE_F32, TYPE_BF16 = 0, 1
 
 
 class Linear(ctypes.Structure):
@@ -81,6 +87,14 @@ class ChainHandle(ctypes.Structure):
     """fp8blk_chain: the host-side record of a planned chained launch."""
     _fields_ = [("plan", ctypes.c_void_p), ("units", ctypes.c_int64), ("n_linears", ctypes.c_int32),
                 ("n_groups", ctypes.c_int32), ("grid", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class Fp4MoeLayer(ctypes.Structure):
+    """fp4_moe_layer: the stacked slabs of a mixture-of-experts layer."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("gate", "gate_scales", "up", "up_scales", "down", "down_scales",
+                                               "gate_global", "up_global", "down_global")] + [
+        ("experts", ctypes.c_int64), ("hidden", ctypes.c_int64), ("inter", ctypes.c_int64), ("fmt", ctypes.c_int32),
+        ("limit", ctypes.c_float)]
 
 
 _lib = None
@@ -165,6 +179,14 @@ def load():
     L.fp8blk_chain_init.restype = i32
     L.fp8blk_gemv_chain.argtypes, L.fp8blk_gemv_chain.restype = [ctypes.POINTER(ChainHandle), vp, vp], i32
     L.fp8blk_chain_status.argtypes, L.fp8blk_chain_status.restype = [ctypes.POINTER(ChainHandle), vp], i32
+    L.fp8blk_block_norm.argtypes = [vp, i32, vp, i64, i64, vp, vp, i64, f32, vp, vp, f32, vp, vp]
+    L.fp8blk_block_norm.restype = i32
+    L.fp8blk_moe_route.argtypes = [vp, vp, i64, i64, vp, i64, i32, i32, i32, f32, vp, vp, vp, sz, vp]
+    L.fp8blk_moe_route.restype = i32
+    L.fp4_moe_bytes.argtypes, L.fp4_moe_bytes.restype = [i64, i64, i32], sz
+    L.fp4_moe.argtypes = [ctypes.POINTER(Fp4MoeLayer), vp, i64, vp, vp, i32, vp, vp, vp, sz, vp]
+    L.fp4_moe.restype = i32
+    L.int4_gemv.argtypes, L.int4_gemv.restype = [vp, vp, vp, i32, i64, i64, vp, i64, vp, vp], i32
     _lib = L
     return L
 
@@ -831,6 +853,212 @@ def fp4_expert_sequence(seq, stream=None, check=True):
     return st
 
 
+# --- around the linears: norms, router, expert layer, 4-bit linear ------------------
+
+class _On:
+    """The device and stream of one call: every tensor has to be on `device`,
+    and `stream` (or that device's current stream) belongs to it."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.device = device
+        s = torch.cuda.current_stream(device) if stream is None else stream
+        if s.device_index != device:
+            raise ValueError(f"the stream belongs to device {s.device_index}, the tensors are on device {device}")
+        self.stream = s.cuda_stream
+
+    def __call__(self, fn, args, name, check):
+        import torch
+        if torch.cuda.current_device() == self.device:
+            st = fn(*args, self.stream)
+        else:
+            with torch.cuda.device(self.device):
+                st = fn(*args, self.stream)
+        if check and st != OK:
+            raise Fp8BlkError(st, name)
+        return st
+
+
+def _buf(t, device, dtypes, shape, name):
+    """Pointer of a contiguous tensor on `device` that has this shape; None stays None."""
+    if t is None:
+        return None
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on device {device}, it is on {t.device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {shape}, got shape {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _matrix(t, name):
+    """Device and the two sizes of a matrix that is on a GPU."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got shape {tuple(t.shape)}")
+    return (t.get_device(), *t.shape)
+
+
+def _need(name, **tensors):
+    for k, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name}: {k} is needed")
+
+
+def _workspace(ws, device):
+    if ws is None:
+        return None, 0
+    if ws.get_device() != device:
+        raise ValueError(f"ws must be on device {device}, it is on {ws.device}")
+    return _dev(ws, None, "ws"), ws.numel() * ws.element_size()
+
+
+def _block_norm_args(resid, y, post_w, gate, scale, resid_out, pre_w, eps, x_next):
+    import torch
+    dev, N, cols = _matrix(resid, "resid")
+    f32, bf16 = (torch.float32,), _bf16_dtypes()
+    if resid.dtype is torch.float32:
+        kind, types = TYPE_F32, f32
+    else:
+        kind, types = TYPE_BF16, bf16
+    panel, row = (N, cols), (cols,)
+    gate_rows = 0
+    if gate is not None:
+        gate_rows = gate.shape[0] if gate.dim() == 2 else 1
+        if gate_rows not in (1, N):
+            raise ValueError(f"gate must be [cols], [1, cols] or [N, cols], got shape {tuple(gate.shape)}")
+    gate_shape = row if gate is not None and gate.dim() == 1 else (gate_rows, cols)
+    return dev, (_buf(resid, dev, types, panel, "resid"), kind, _buf(y, dev, f32, panel, "y"), N, cols,
+                 _buf(post_w, dev, bf16, row, "post_w"), _buf(gate, dev, bf16, gate_shape, "gate"), gate_rows, scale,
+                 _buf(resid_out, dev, types, panel, "resid_out"), _buf(pre_w, dev, bf16, row, "pre_w"), eps,
+                 _buf(x_next, dev, bf16, panel, "x_next"))
+
+
+def fp8blk_block_norm(resid, y, post_w, gate, scale, resid_out, pre_w, eps, x_next, stream=None, check=True):
+    """resid_out = resid + scale * (gate . norm(y, post_w)) and x_next =
+    bf16(norm(resid_out before its rounding, pre_w)), norm the RMS norm over a
+    row. resid and resid_out [N, cols] f32 or bf16 (may be one tensor), y f32
+    [N, cols], post_w and pre_w bf16 [cols], gate bf16 [cols] or [N, cols].
+    None for what is left out: post_w (no norm of y), gate, y with post_w, gate
+    and resid_out (only the norm of resid), pre_w with x_next (only the sum)."""
+    dev, args = _block_norm_args(resid, y, post_w, gate, scale, resid_out, pre_w, eps, x_next)
+    return _On(dev, stream)(load().fp8blk_block_norm, args, "fp8blk_block_norm", check)
+
+
+def _moe_route_args(w_bf16, bias, x_bf16, score, normalize, scale, ids, weights, ws):
+    import torch
+    dev, E, cols = _matrix(w_bf16, "w_bf16")
+    _, M, K = _matrix(ids, "ids")
+    bf16, f32 = _bf16_dtypes(), (torch.float32,)
+    _need("fp8blk_moe_route", x_bf16=x_bf16, weights=weights)
+    wsp, wsb = _workspace(ws, dev)
+    return dev, (_buf(w_bf16, dev, bf16, (E, cols), "w_bf16"), _buf(bias, dev, f32, (E,), "bias"), E, cols,
+                 _buf(x_bf16, dev, bf16, (M, cols), "x_bf16"), M, score, K, bool(normalize), scale,
+                 _buf(ids, dev, (torch.int32,), (M, K), "ids"), _buf(weights, dev, f32, (M, K), "weights"), wsp, wsb)
+
+
+def fp8blk_moe_route(w_bf16, bias, x_bf16, score, normalize, scale, ids, weights, ws, stream=None, check=True):
+    """ids int32 [M, K] and weights f32 [M, K] of each token's K best experts:
+    scores (SCORE_*) of x_bf16 [M, cols] . w_bf16 [experts, cols], chosen by
+    score + bias (f32 [experts] or None), weighted by score. ws:
+    fp8blk_workspace_bytes(OP_MOE_ROUTE, experts, cols, M) bytes."""
+    dev, args = _moe_route_args(w_bf16, bias, x_bf16, score, normalize, scale, ids, weights, ws)
+    return _On(dev, stream)(load().fp8blk_moe_route, args, "fp8blk_moe_route", check)
+
+
+class MoeLayer:
+    """A mixture-of-experts layer's weights (fp4_moe_weights): `handle` is the
+    record that fp4_moe takes, `keep` the tensors it points at."""
+
+    def __init__(self, handle, device, keep):
+        self.handle = handle
+        self.device = device
+        self.keep = keep
+        self.hidden, self.inter = handle.hidden, handle.inter
+
+
+def fp4_moe_weights(fmt, gate, gate_scales, gate_global, up, up_scales, up_global, down, down_scales, down_global,
+                    limit=0.0):
+    """The weights of fp4_moe: stacked FP4 slabs as stored, gate and up codes
+    [experts, inter, hidden/2], down [experts, hidden, inter/2], scales with
+    /B in place of /2 (B = 32 for FMT_MXFP4, 16 for FMT_NVFP4), global scales
+    f32 [experts] or None; limit > 0 clamps gate and up. Checked here, once;
+    the tensors must stay as they are while the layer is used."""
+    import torch
+    B = {FMT_MXFP4: 32, FMT_NVFP4: 16}.get(fmt)
+    if B is None:
+        raise ValueError(f"fmt {fmt} is not FMT_MXFP4 or FMT_NVFP4")
+    for name, t in (("gate", gate), ("down", down)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dim() != 3:
+            raise ValueError(f"{name} must be [experts, rows, cols/2], got shape {tuple(t.shape)}")
+    E, inter, hidden, dev = gate.shape[0], gate.shape[1], 2 * gate.shape[2], gate.get_device()
+    u8, f32 = (torch.uint8,), (torch.float32,)
+    _need("fp4_moe_weights", gate_scales=gate_scales, up=up, up_scales=up_scales, down_scales=down_scales)
+    h = Fp4MoeLayer(experts=E, hidden=hidden, inter=inter, fmt=fmt, limit=limit)
+    for name, codes, scales, top, rows, cols in (("gate", gate, gate_scales, gate_global, inter, hidden),
+                                                 ("up", up, up_scales, up_global, inter, hidden),
+                                                 ("down", down, down_scales, down_global, hidden, inter)):
+        setattr(h, name, _buf(codes, dev, u8, (E, rows, cols // 2), name))
+        setattr(h, name + "_scales", _buf(scales, dev, u8, (E, rows, cols // B), name + "_scales"))
+        setattr(h, name + "_global", _buf(top, dev, f32, (E,), name + "_global"))
+    return MoeLayer(h, dev, (gate, gate_scales, gate_global, up, up_scales, up_global, down, down_scales, down_global))
+
+
+def fp4_moe_bytes(inter: int, M: int, top_k: int) -> int:
+    return load().fp4_moe_bytes(inter, M, top_k)
+
+
+def _moe_args(layer, x_bf16, ids, weights, base, y, ws):
+    import torch
+    dev, M, K = _matrix(ids, "ids")
+    if dev != layer.device:
+        raise ValueError(f"ids must be on the layer's device {layer.device}, they are on {dev}")
+    f32, panel = (torch.float32,), (M, layer.hidden)
+    _need("fp4_moe", x_bf16=x_bf16, weights=weights, y=y)
+    wsp, wsb = _workspace(ws, dev)
+    return dev, (ctypes.byref(layer.handle), _buf(x_bf16, dev, _bf16_dtypes(), panel, "x_bf16"), M,
+                 _buf(ids, dev, (torch.int32,), (M, K), "ids"), _buf(weights, dev, f32, (M, K), "weights"), K,
+                 _buf(base, dev, f32, panel, "base"), _buf(y, dev, f32, panel, "y"), wsp, wsb)
+
+
+def fp4_moe(layer, x_bf16, ids, weights, base, y, ws, stream=None, check=True):
+    """y[M, hidden] = base (f32, or None for 0) + the weighted sum of the
+    chosen experts (fp4_moe_weights) on x_bf16 [M, hidden]: ids int32 and
+    weights f32 [M, K] as fp8blk_moe_route writes them. ws:
+    fp4_moe_bytes(inter, M, K) bytes."""
+    dev, args = _moe_args(layer, x_bf16, ids, weights, base, y, ws)
+    return _On(dev, stream)(load().fp4_moe, args, "fp4_moe", check)
+
+
+def _int4_args(codes, scales_bf16, zeros, group, x_bf16, y):
+    import torch
+    dev, rows, half = _matrix(codes, "codes")
+    _, M, cols = _matrix(x_bf16, "x_bf16")
+    u8, bf16 = (torch.uint8,), _bf16_dtypes()
+    if cols != 2 * half:
+        raise ValueError(f"x_bf16 must be [M, cols={2 * half}], got shape {tuple(x_bf16.shape)}")
+    _need("int4_gemv", scales_bf16=scales_bf16, y=y)
+    grid = (rows, cols // group if group in (32, 64, 128) else 0)
+    return dev, (_buf(codes, dev, u8, (rows, half), "codes"), _buf(scales_bf16, dev, bf16, grid, "scales_bf16"),
+                 _buf(zeros, dev, u8, grid, "zeros"), group, rows, cols, _buf(x_bf16, dev, bf16, (M, cols), "x_bf16"), M,
+                 _buf(y, dev, (torch.float32,), (M, rows), "y"))
+
+
+def int4_gemv(codes, scales_bf16, zeros, group, x_bf16, y, stream=None, check=True):
+    """y[M, rows] = x_bf16 [M, cols] . ((q - zeros) * scales)^T with 4-bit codes
+    q [rows, cols/2], bf16 scales and uint8 zero points (None: 8) [rows,
+    cols/group], group 32, 64 or 128."""
+    dev, args = _int4_args(codes, scales_bf16, zeros, group, x_bf16, y)
+    return _On(dev, stream)(load().int4_gemv, args, "int4_gemv", check)
+
+
 def raw_call(name: str, *args):
     """Call an exported symbol with raw ctypes arguments (pointers as ints).
     Used by tests that exercise the C ABI's argument checks directly."""
@@ -846,9 +1074,16 @@ def prepared(name: str, *tensors_and_sizes, stream=None):
     x_bf16, y), the grouped launches (members, x_bf16), the scaled-input
     launches (codes, scales_f32, src_f32, c, y) and (members, src_f32, c), the
     next-input launches (codes, scales_f32, x_bf16, y, c, x_next) and
-    (members, x_bf16, k, c, x_next), the staged GEMMs (..., ws) and the sequence launches (a planned Sequence)."""
+    (members, x_bf16, k, c, x_next), the staged GEMMs (..., ws), the sequence launches (a planned Sequence), and
+    "fp8blk_block_norm", "fp8blk_moe_route", "fp4_moe" and "int4_gemv" with their own arguments."""
     import torch
     fn = getattr(load(), name)
+    around = {"fp8blk_block_norm": _block_norm_args, "fp8blk_moe_route": _moe_route_args, "fp4_moe": _moe_args,
+              "int4_gemv": _int4_args}.get(name)
+    if around is not None:
+        dev, args = around(*tensors_and_sizes)
+        on = _On(dev, stream)
+        return lambda: on(fn, args, name, False)
     s = _stream(stream)
     if name == "fp8blk_gemv":
         codes, grid, x, y = tensors_and_sizes

@@ -219,7 +219,6 @@ extern "C" const char* fp8blk_strerror(int status) {
 }
 
 extern "C" size_t fp8blk_workspace_bytes(int op, int64_t rows, int64_t cols, int64_t M) {
-    (void)M;
     switch (op) {
         case FP8BLK_OP_LOAD_CHECK: return 256;  // three 64-bit verdict slots, padded
         case FP8BLK_OP_DEQUANT_BF16: return 0;
@@ -227,6 +226,7 @@ extern "C" size_t fp8blk_workspace_bytes(int op, int64_t rows, int64_t cols, int
         case FP8BLK_OP_BF16_TWIN: return 0;
         case FP8BLK_OP_GEMM_STAGED:
         case FP8BLK_OP_BF16_GEMM: return gemm_workspace_bytes(op, rows, cols);
+        case FP8BLK_OP_MOE_ROUTE: return route_workspace_bytes(rows, cols, M);
         default: return 0;
     }
 }

@@ -20,6 +20,13 @@ inline bool shape_ok(int64_t rows, int64_t cols) {
     return rows <= (INT64_C(1) << 46) / cols;
 }
 
+// Whether the byte ranges [a, a + na) and [b, b + nb) share a byte; a null
+// range shares none.
+inline bool ranges_meet(const void* a, int64_t na, const void* b, int64_t nb) {
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+    return a && b && pa < pb + (uint64_t)nb && pb < pa + (uint64_t)na;
+}
+
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Launch-error status after enqueueing kernels.
@@ -67,5 +74,8 @@ int64_t mf_sequence_plan(unsigned char* host, bool fp8, const fp8blk_seq_linear*
 // Workspace of the staged prefill GEMM (fp8blk_gemm.hip): the bf16 slab (for
 // FP8BLK_OP_GEMM_STAGED) plus the library GEMM's workspace; 0 for a bad shape.
 size_t gemm_workspace_bytes(int op, int64_t rows, int64_t cols);
+
+// Workspace of the router (fp8blk_route.hip); 0 for a bad shape.
+size_t route_workspace_bytes(int64_t experts, int64_t cols, int64_t M);
 
 }  // namespace fp8blk

@@ -100,7 +100,8 @@ typedef enum fp8blk_op {
     FP8BLK_OP_GEMV = 2,
     FP8BLK_OP_BF16_TWIN = 3,
     FP8BLK_OP_GEMM_STAGED = 4,
-    FP8BLK_OP_BF16_GEMM = 5
+    FP8BLK_OP_BF16_GEMM = 5,
+    FP8BLK_OP_MOE_ROUTE = 6 /* rows = experts */
 } fp8blk_op;
 
 /* Shape limits. cols must be a multiple of 16 (one 16-byte code load). */
@@ -665,6 +666,141 @@ typedef struct fp4_expert_linear {
 int fp4_expert_sequence_init(fp8blk_sequence *seq, int fmt, const fp4_expert_linear *linears, int n,
                              void *ws, size_t ws_bytes, fp8blk_stream_t stream);
 int fp4_expert_sequence(const fp8blk_sequence *seq, fp8blk_stream_t stream);
+
+/*
+ * The rest of a decode, verify or prefill step around the linears: the norms
+ * between two blocks, the router, a whole mixture-of-experts layer over FP4
+ * experts, and a 4-bit linear. None of them allocates, waits or keeps state;
+ * all may be captured in a HIP graph; two calls that overlap in time need
+ * workspaces of their own (calls in stream order may share one).
+ */
+
+/*
+ * Norms around a block. With n(v, w)[c] = v[c] / sqrt(mean_c v[c]^2 + eps) * w[c]:
+ *   r'     = resid + scale * (gate . n(y, post_w))   (product by column)
+ *   x_next = bf16(n(r', pre_w))
+ * y is a block's f32 output (a linear's y), resid the residual stream before
+ * it, r' the stream after it and x_next the next block's input. Statistics and
+ * products are f32; r' is rounded once, to resid's type, and x_next is formed
+ * from the unrounded f32 r'. Squares are summed in f32: a row with a value
+ * beyond about 1e18 overflows them.
+ *   resid, resid_out: [N, cols], f32 or bf16 (resid_type FP8BLK_F32 or
+ *     FP8BLK_BF16, the same for both); resid_out may be resid itself.
+ *   y: f32 [N, cols]. NULL: the first norm of a model (r' = resid); then
+ *     post_w, gate and resid_out are NULL and x_next is not.
+ *   post_w: bf16 [cols]; NULL: no norm after the block, n(y) = y.
+ *   gate: bf16 [gate_rows, cols], gate_rows 1 (one gate per column) or N; NULL
+ *     (gate_rows 0): 1.
+ *   pre_w: bf16 [cols], x_next: bf16 [N, cols]; both NULL: no norm after the
+ *     sum (the last block); then y is not NULL.
+ *   1 <= N <= FP8BLK_MAX_PANEL; cols as for fp8blk_gemv; eps >= 0 and finite.
+ *   All pointers: device, 16-byte aligned. An output may overlap no input or
+ *   other output, resid_out == resid apart (else FP8BLK_ERR_ARG).
+ * Row i of an N-row call equals the 1-row call on it bit for bit. Enqueued on
+ * `stream`; does not wait.
+ */
+#define FP8BLK_F32 0
+#define FP8BLK_BF16 1
+int fp8blk_block_norm(const void *resid, int resid_type, const float *y, int64_t N, int64_t cols,
+                      const uint16_t *post_w, const uint16_t *gate, int64_t gate_rows, float scale, void *resid_out,
+                      const uint16_t *pre_w, float eps, uint16_t *x_next, fp8blk_stream_t stream);
+
+/*
+ * Router. For each of M tokens the top_k of `experts` experts, and their
+ * weights:
+ *   l[e]    = sum_c w_bf16[e, c] * x_bf16[m, c]
+ *   s[e]    = softmax of l over all experts (FP8BLK_SCORE_SOFTMAX), sigmoid(l)
+ *             (_SIGMOID) or sqrt(log(1 + exp(l))) (_SQRT_SOFTPLUS)
+ *   ids[m]  = the top_k experts of largest s[e] + bias[e], largest first, ties
+ *             to the lower index
+ *   weights = scale * s[id], first divided by the sum of s over the chosen
+ *             experts if `normalize` (a sum of 0 leaves weights of 0)
+ * A choice is a decision, so all of it is computed in 64 bits and only the
+ * weights are rounded, once, to f32.
+ *   bias: f32 [experts] or NULL. An expert whose s + bias is -inf (a masked
+ *     one) or NaN is never chosen; when fewer than top_k are left, the last
+ *     ids are -1 and their weights 0. Every other id is in [0, experts), and
+ *     a token's ids are distinct, whatever the inputs hold.
+ *   w_bf16 [experts, cols], x_bf16 [M, cols]: device, 16-byte aligned;
+ *   ids int32 [M, top_k], weights f32 [M, top_k], bias: device, 4-byte aligned.
+ *   1 <= experts <= FP8BLK_MAX_EXPERTS; 1 <= top_k <= min(experts,
+ *   FP8BLK_MAX_TOP_K); 1 <= M <= FP8BLK_MAX_PANEL; cols as for fp8blk_gemv.
+ *   ws: device, 256-byte aligned, >= fp8blk_workspace_bytes(FP8BLK_OP_MOE_ROUTE,
+ *     experts, cols, M) bytes; its contents on entry do not matter.
+ * Enqueued on `stream`; does not wait.
+ */
+#define FP8BLK_MAX_EXPERTS 1024
+#define FP8BLK_MAX_TOP_K 16
+#define FP8BLK_SCORE_SOFTMAX 0
+#define FP8BLK_SCORE_SIGMOID 1
+#define FP8BLK_SCORE_SQRT_SOFTPLUS 2
+int fp8blk_moe_route(const uint16_t *w_bf16, const float *bias, int64_t experts, int64_t cols,
+                     const uint16_t *x_bf16, int64_t M, int score, int top_k, int normalize, float scale,
+                     int32_t *ids, float *weights, void *ws, size_t ws_bytes, fp8blk_stream_t stream);
+
+/*
+ * A whole mixture-of-experts layer over FP4 experts for a few tokens, the
+ * choice of experts read on the device. For token m and its k-th expert
+ * e = ids[m, k]:
+ *   g = Wgate_e x_m, u = Wup_e x_m; with limit > 0: g = min(g, limit),
+ *   u = min(max(u, -limit), limit)
+ *   h = g / (1 + exp(-g)) * u
+ *   y_m = base_m + sum_k weights[m, k] * (Wdown_e h)
+ * W is e2m1(code) * block scale * global scale, as for fp4_expert_gemv, on
+ * bf16 activations as they are. Sums are f32 and h is held to f32 accuracy.
+ * The sum over k is taken in order of k; row m of an M-row call equals the
+ * 1-row call on token m bit for bit.
+ *   layer (HOST struct): gate, up: codes [experts, inter, hidden/2], scales
+ *     [experts, inter, hidden/B]; down: codes [experts, hidden, inter/2],
+ *     scales [experts, hidden, inter/B] (B = 32 for FP8BLK_FMT_MXFP4, 16 for
+ *     FP8BLK_FMT_NVFP4), each expert's slab as fp4_load_check accepts it;
+ *     *_global: f32 [experts] or NULL (1): device, 4-byte aligned.
+ *     hidden and inter: multiples of 32, 32 .. FP8BLK_MAX_COLS;
+ *     1 <= experts <= FP8BLK_MAX_EXPERTS; limit >= 0 and finite (0: none).
+ *   x_bf16 [M, hidden]; ids int32, weights f32 [M, top_k]; 1 <= M <=
+ *     FP8BLK_MAX_M; 1 <= top_k <= FP8BLK_MAX_TOP_K. An id outside
+ *     [0, experts) adds nothing (no choice, or another rank's expert); an id
+ *     may occur more than once in a row.
+ *   base: f32 [M, hidden], or NULL (0); may be y itself.
+ *   y: f32 [M, hidden]; overlaps nothing else (else FP8BLK_ERR_ARG for x,
+ *     weights, ids and base).
+ *   codes, x_bf16, base, y: device, 16-byte aligned; scales: device, 4-byte
+ *   (MXFP4) or 8-byte (NVFP4) aligned.
+ *   ws: device, 256-byte aligned, >= fp4_moe_bytes(inter, M, top_k) bytes (0:
+ *     bad sizes); its contents on entry do not matter.
+ * Enqueued on `stream`; does not wait.
+ */
+typedef struct fp4_moe_layer {
+    const uint8_t *gate, *gate_scales;
+    const uint8_t *up, *up_scales;
+    const uint8_t *down, *down_scales;
+    const float *gate_global, *up_global, *down_global;
+    int64_t experts, hidden, inter;
+    int32_t fmt; /* FP8BLK_FMT_* */
+    float limit;
+} fp4_moe_layer;
+
+size_t fp4_moe_bytes(int64_t inter, int64_t M, int top_k);
+int fp4_moe(const fp4_moe_layer *layer, const uint16_t *x_bf16, int64_t M, const int32_t *ids, const float *weights,
+            int top_k, const float *base, float *y, void *ws, size_t ws_bytes, fp8blk_stream_t stream);
+
+/*
+ * Matrix-vector products with unsigned 4-bit weights and a scale (and zero
+ * point) per group of columns of a row:
+ *   y[m, r] = sum over c of (q[r, c] - z[r, c/group]) * s[r, c/group] * x[m, c]
+ *   codes: [rows, cols/2], q = 0 .. 15, two per byte, the even column in the
+ *     low nibble; scales_bf16: bf16 [rows, cols/group], any finite value;
+ *     zeros: uint8 [rows, cols/group], any byte is that number; NULL: 8.
+ *   group: 32, 64 or 128; cols: a multiple of group, 32 .. FP8BLK_MAX_COLS;
+ *   rows >= 1; 1 <= M <= FP8BLK_MAX_M.
+ *   codes, x_bf16: device, 16-byte aligned; scales_bf16: 2-byte aligned; y:
+ *   4-byte aligned.
+ * Every code, zero point and x is exact in the products; sums are f32. Row m
+ * of an M-row call equals the 1-row call on x[m] bit for bit. y must not
+ * overlap the inputs. No workspace. Enqueued on `stream`; does not wait.
+ */
+int int4_gemv(const uint8_t *codes, const uint16_t *scales_bf16, const uint8_t *zeros, int group, int64_t rows,
+              int64_t cols, const uint16_t *x_bf16, int64_t M, float *y, fp8blk_stream_t stream);
 
 #ifdef __cplusplus
 }

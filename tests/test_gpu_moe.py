@@ -1,0 +1,157 @@
+"""GPU: fp4_moe against its plain form in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+from block_scaled_fp8_fp8blk_amd import inputs as I
+from layer_plain import Slab, assert_within, moe, normal
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+MX, NV = I.MXFP4, I.NVFP4
+
+
+class Layer:
+    def __init__(self, gpu, fmt, E, hidden, inter, seed, limit=0.0, **kw):
+        rng = np.random.default_rng(seed)
+        self.gate, self.up = (Slab(rng, fmt, E, inter, hidden, **kw) for _ in range(2))
+        self.down = Slab(rng, fmt, E, hidden, inter, **kw)
+        self.hidden, self.inter, self.limit, self.rng, self.E = hidden, inter, limit, rng, E
+        self.handle = gpu.fp4_moe_weights(fmt, *self.gate.on(DEV), *self.up.on(DEV), *self.down.on(DEV), limit=limit)
+
+    def tokens(self, M, K, base=True):
+        x = normal(self.rng, M, self.hidden).bfloat16()
+        ids = torch.from_numpy(np.stack([self.rng.permutation(self.E)[:K] if K <= self.E else self.rng.integers(0, self.E, K)
+                                         for _ in range(M)]).astype(np.int32))
+        p = torch.from_numpy(self.rng.uniform(0.05, 1.0, (M, K)).astype(np.float32))
+        return x, ids, p, normal(self.rng, M, self.hidden) * 4 if base else None
+
+    def run(self, gpu, x, ids, p, base, in_place=False):
+        M, K = ids.shape
+        y = torch.full((M, self.hidden), float("nan"), device=DEV)
+        b = None if base is None else base.to(DEV)
+        if in_place:
+            y.copy_(b)
+            b = y
+        ws = torch.full((gpu.fp4_moe_bytes(self.inter, M, K),), 0xFF, dtype=torch.uint8, device=DEV)
+        gpu.fp4_moe(self.handle, x.to(DEV), ids.to(DEV), p.to(DEV), b, y, ws)
+        torch.cuda.synchronize()
+        return y
+
+    def check(self, gpu, x, ids, p, base, what):
+        y = self.run(gpu, x, ids, p, base)
+        assert_within(y, *moe(self.gate, self.up, self.down, x, ids, p, base, self.limit), what)
+        return y
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("M,K,E,hidden,inter", [(1, 1, 1, 32, 32), (1, 2, 8, 64, 96), (1, 8, 16, 1024, 512), (2, 4, 5, 160, 1056),
+                                                (3, 4, 32, 1440, 736), (5, 8, 12, 544, 256), (8, 2, 4, 256, 2080),
+                                                (13, 6, 9, 416, 320), (16, 8, 24, 512, 384), (16, 16, 16, 96, 64),
+                                                (16, 1, 2, 2080, 128)])
+def test_matches_plain(gpu, fmt, M, K, E, hidden, inter):
+    print("moe", fmt, M, K, E, hidden, inter, flush=True)
+    L = Layer(gpu, fmt, E, hidden, inter, M * hidden + inter + fmt, limit=(0.0, 3.0)[M % 2])
+    L.check(gpu, *L.tokens(M, K, base=K % 2 == 0), f"{fmt} {M}x{K} of {E}, {hidden}x{inter}")
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_workload_shape(gpu, fmt):
+    """A decode token and a verify panel over experts of 4096 x 2048."""
+    L = Layer(gpu, fmt, 10, 4096, 2048, 77)
+    for M in (1, 4):
+        L.check(gpu, *L.tokens(M, 8), f"{fmt} M={M}")
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_ids_without_an_expert_add_nothing(gpu, fmt):
+    L = Layer(gpu, fmt, 6, 288, 160, 5)
+    x, ids, p, base = L.tokens(5, 4)
+    ids[0] = -1
+    ids[1] = torch.tensor([6, 2, -1, 100])
+    ids[2] = torch.tensor([2 ** 31 - 1, -2 ** 31, 7, 8])
+    p[0, 2] = float("nan")  # of a choice that is none
+    y = L.check(gpu, x, ids, p, base, "ids outside")
+    assert torch.equal(y[0].cpu(), base[0]) and torch.equal(y[2].cpu(), base[2])
+    y = L.run(gpu, x, ids, p, None)
+    assert (y[0] == 0).all() and (y[2] == 0).all()
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("M,K", [(1, 16), (16, 16), (7, 5)])
+def test_the_same_expert_many_times(gpu, fmt, M, K):
+    """Every choice the same expert (up to 256 of one), and two experts in turn."""
+    L = Layer(gpu, fmt, 3, 160, 96, 8)
+    x, ids, p, base = L.tokens(M, K)
+    ids[:] = 1
+    L.check(gpu, x, ids, p, base, "one expert")
+    ids[:, 1::2] = 2
+    L.check(gpu, x, ids, p, base, "two experts")
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_tokens_do_not_depend_on_the_panel(gpu, fmt):
+    L = Layer(gpu, fmt, 7, 1056, 544, 15)
+    x, ids, p, base = L.tokens(16, 5)
+    y = L.run(gpu, x, ids, p, base)
+    for n in (1, 3, 6, 9):
+        for at in (0, 16 - n):
+            s = slice(at, at + n)
+            assert torch.equal(L.run(gpu, x[s], ids[s], p[s], base[s]), y[s]), (n, at)
+    assert torch.equal(L.run(gpu, x, ids, p, base, in_place=True), y)
+
+
+@pytest.mark.parametrize("fmt,lo,hi", [(MX, 0, 6), (MX, 90, 150), (NV, 0, 9), (NV, 0x70, 0x7E)])
+def test_extreme_block_scales(gpu, fmt, lo, hi):
+    """Subnormal products and scales of very different sizes in one row."""
+    L = Layer(gpu, fmt, 4, 192, 128, 31, scale_range=(lo, hi), with_global=False)
+    x, ids, p, base = L.tokens(3, 3)
+    if (fmt, lo) == (MX, 0):  # weights near 2^-124: h underflows, y is the base
+        y = L.run(gpu, x, ids, p, base)
+        assert torch.equal(y.cpu(), base)
+        return
+    if (fmt, lo) == (MX, 90):
+        x *= 2.0 ** -23
+    if hi == 0x7E:
+        x *= 2.0 ** -10
+    L.check(gpu, x, ids, p, base, f"{fmt} scales {lo}..{hi}")
+
+
+def test_values_that_are_not_finite_stay_in_their_token(gpu):
+    L = Layer(gpu, MX, 4, 160, 96, 41)
+    x, ids, p, base = L.tokens(6, 3)
+    clean = L.run(gpu, x, ids, p, base)
+    x[2, 9], p[4, 1] = float("nan"), float("inf")
+    y = L.run(gpu, x, ids, p, base)
+    ok = [0, 1, 3, 5]
+    assert torch.equal(y[ok], clean[ok]) and y[2].isnan().all() and not torch.isfinite(y[4]).any()
+
+
+def test_large_gates(gpu):
+    """silu far from 0: exp(-g) overflows to infinity and h is 0, or h is g u."""
+    L = Layer(gpu, MX, 2, 96, 64, 51, scale_range=(127, 131))
+    x, ids, p, base = L.tokens(4, 2)
+    L.check(gpu, x, ids, p, base, "large gates")
+
+
+def test_experts_past_32_bit_offsets(gpu):
+    """Slabs of more than 2^32 bytes: the last of 1024 experts of 4096 x 2304."""
+    E, hidden, inter = 1024, 4096, 2304
+    dev = [torch.zeros((E, r, c // 2), dtype=torch.uint8, device=DEV) for r, c in ((inter, hidden), (inter, hidden), (hidden, inter))]
+    sc = [torch.full((E, r, c // 32), 120, dtype=torch.uint8, device=DEV) for r, c in ((inter, hidden), (inter, hidden), (hidden, inter))]
+    assert dev[0].numel() > 1 << 32
+    rng = np.random.default_rng(61)
+    small = [Slab(rng, MX, 2, *s) for s in ((inter, hidden), (inter, hidden), (hidden, inter))]
+    at = torch.tensor([3, E - 1], device=DEV)
+    for d, s, slab in zip(dev, sc, small):
+        d[at], s[at] = torch.from_numpy(slab.codes).to(DEV), torch.from_numpy(slab.scales).to(DEV)
+    layer = gpu.fp4_moe_weights(MX, dev[0], sc[0], None, dev[1], sc[1], None, dev[2], sc[2], None)
+    x = normal(rng, 2, hidden).bfloat16()
+    p = torch.tensor([[0.25, 0.75], [0.5, 0.125]])
+    ids = torch.tensor([[3, E - 1], [E - 1, 500]], dtype=torch.int32)
+    y = torch.empty((2, hidden), device=DEV)
+    ws = torch.empty(gpu.fp4_moe_bytes(inter, 2, 2), dtype=torch.uint8, device=DEV)
+    gpu.fp4_moe(layer, x.to(DEV), ids.to(DEV), p.to(DEV), None, y, ws)
+    torch.cuda.synchronize()
+    near = torch.tensor([[0, 1], [1, -1]])
+    assert_within(y, *moe(*small, x, near, p, None, 0.0), "experts past 2^32")
