@@ -1,5 +1,32 @@
 // Matrix-vector products with unsigned 4-bit weights and a scale and zero
 // point per group of columns.
+//
+// For token m and weight row r the sum over a group is taken apart as
+//   sum_c (q - z) s x = s * (D - z X),  D = sum_c q x,  X = sum_c x,
+// so that the matrix instruction (v_mfma_f32_16x16x32_bf16) runs on the codes
+// themselves: q = 0 .. 15 is a bf16 value, z and s (whose product with q is
+// not one) are applied to a group's f32 sum. X comes from the same
+// instruction with a column of ones and is shared by a wave's row tiles.
+// Where every code equals a zero point of 8, or another power of two, D and
+// z X are the same sums scaled and cancel exactly.
+//
+// Codes to bf16: byte values 0 .. 15 are e4m3's subnormals and first binade,
+// which are linear (code * 2^-9), so two masks spread a dword's nibbles over
+// bytes and one scaled conversion turns two of them into bf16: 7 instructions
+// for 8 weights.
+//
+// The token panel lies in LDS in the order the instruction's operand takes it,
+// so that a step's four reads are 16 bytes per lane without bank conflicts;
+// panels larger than kPanelBytes are staged in pieces. Workgroups are
+// persistent, one or more per compute unit; a wave takes a tile of 16 weight
+// rows x 512 columns at a time: lane (n, k) = (l % 16, l / 16) loads 16 bytes,
+// 32 codes, of row n in each 128-column step, and the loads of its next
+// 512 columns are in flight while it computes. Where a group is shorter than
+// a step, an exchange of the lane group with the dword index hands lane group
+// k the k-th eighth of each 32-column block, so that one instruction stays
+// inside a group. `split` waves share a row tile's columns, in turn, and add
+// their sums in wave order through LDS; split depends on rows and cols alone,
+// so a token's bits do not depend on M.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -10,6 +37,20 @@
 namespace fp8blk {
 namespace {
 
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef uint32_t v4u32 __attribute__((ext_vector_type(4)));
+
+constexpr int kTile = 16;               // weight rows of a matrix instruction
+constexpr int kStep = 128;              // columns of one 16-byte load per lane
+constexpr int kSuper = 512;             // columns a wave takes at a time
+constexpr int kSteps = kSuper / kStep;
+constexpr int kPanelBytes = 128 * 1024; // LDS for the token panel
+
+constexpr int kWaves = 16;              // of a workgroup, at most
+constexpr int kPlanCUs = 256;           // compute units that a plan is made for
+
 struct Int4Args {
     const uint8_t* codes;
     const uint16_t* scales;
@@ -17,24 +58,333 @@ struct Int4Args {
     const uint16_t* x;
     float* y;
     int64_t rows;
-    int32_t cols, group;
+    int32_t cols, M, split, piece;  // piece: columns of the panel in LDS at a time (a multiple of kSuper)
 };
 
-// One wave per (weight row, token).
-__global__ __launch_bounds__(64) void k_int4(Int4Args a) {
-    const int64_t r = blockIdx.x, m = blockIdx.y, groups = a.cols / a.group;
-    float s = 0.0f;
-    for (int c = 2 * threadIdx.x; c < a.cols; c += 128) {
-        const uint32_t b = a.codes[r * (a.cols / 2) + c / 2];
-        const int64_t g = r * groups + c / a.group;
-        const float z = a.zeros ? (float)a.zeros[g] : 8.0f, sc = as_f32((uint32_t)a.scales[g] << 16);
-        float w[2];
-        widen2_bf16(*reinterpret_cast<const uint32_t*>(a.x + m * a.cols + c), w);
-        s = __builtin_fmaf(((float)(b & 15u) - z) * sc, w[0], s);
-        s = __builtin_fmaf(((float)(b >> 4) - z) * sc, w[1], s);
+// The 8 codes of a dword (columns 0 .. 7, low nibble first) as bf16 values in
+// the order 0 2 4 6 1 3 5 7.
+__device__ __forceinline__ v8bf codes_bf16(uint32_t d) {
+    const uint32_t lo = d & 0x0F0F0F0Fu, hi = (d >> 4) & 0x0F0F0F0Fu;
+    const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false);
+    const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true);
+    const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false);
+    const v2bf e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true);
+    return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], e[0], e[1]};
+}
+
+// 8 consecutive bf16 values in that order.
+__device__ __forceinline__ v8bf even_odd(const uint4& v) {
+    const v4u32 o = {__builtin_amdgcn_perm(v.y, v.x, 0x05040100u), __builtin_amdgcn_perm(v.w, v.z, 0x05040100u),
+                     __builtin_amdgcn_perm(v.y, v.x, 0x07060302u), __builtin_amdgcn_perm(v.w, v.z, 0x07060302u)};
+    return __builtin_bit_cast(v8bf, o);
+}
+
+// Exchange the dword index with the lane group: afterwards dword j of lane
+// group k is what dword k of lane group j was.
+__device__ __forceinline__ void transpose_groups(uint4& v) {
+    const auto a = __builtin_amdgcn_permlane32_swap(v.x, v.z, false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(v.y, v.w, false, false);
+    const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    v = make_uint4(c[0], c[1], d[0], d[1]);
+}
+
+// The scales and zero points of N groups of a row; zeros past the row's end.
+template <int N>
+struct Groups {
+    uint32_t s[N / 2];
+    uint32_t z[(N + 3) / 4];
+};
+
+template <int N, bool ZERO>
+__device__ __forceinline__ void load_groups(Groups<N>& g, const uint16_t* s, const uint8_t* z, int left) {
+    if (left >= N) {
+        __builtin_memcpy(g.s, s, 2 * N);
+        if constexpr (ZERO) __builtin_memcpy(g.z, z, N);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) g.s[i] = 0;
+#pragma unroll
+        for (int i = 0; i < (N + 3) / 4; ++i) g.z[i] = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < left) {
+                g.s[i / 2] |= (uint32_t)s[i] << (16 * (i % 2));
+                if constexpr (ZERO) g.z[i / 4] |= (uint32_t)z[i] << (8 * (i % 4));
+            }
     }
-    s = tree64(s);
-    if (threadIdx.x == 0) a.y[m * a.rows + r] = s;
+}
+
+// One wave's loads of a tile's 512 columns.
+template <int G>
+struct Load {
+    uint4 q[kSteps];
+    Groups<kSuper / G> g;
+};
+
+template <int G, bool ZERO>
+__device__ __forceinline__ void issue(Load<G>& b, const Int4Args& a, const uint8_t* lo, const uint8_t* hi, int64_t row,
+                                      int lane, int c0) {
+#pragma unroll
+    for (int s = 0; s < kSteps; s += 2) {  // columns past the end meet zeros of the panel: any code will do
+        const int c = min(c0 + s * kStep + 16 * (lane & 8) + 32 * (lane >> 4), a.cols - 32) / 2;
+        b.q[s] = load_stream16(lo + c);
+        b.q[s + 1] = load_stream16(hi + c);
+    }
+    const int64_t g = row * (a.cols / G) + c0 / G;
+    load_groups<kSuper / G, ZERO>(b.g, a.scales + g, ZERO ? a.zeros + g : nullptr, (a.cols - c0) / G);
+}
+
+// acc += the 512 columns of b times the panel's columns from x on (LDS).
+template <int G, bool ZERO, int NI>
+__device__ __forceinline__ void compute(Load<G>& b, const uint4* x, const float* xsum, float (&acc)[NI]) {
+    constexpr int per_step = kStep / G;  // groups of a step
+    constexpr int per_group = 4 / per_step;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        if (s % 2 == 0) {
+            swap_lane_bit3(b.q[s].x, b.q[s + 1].x);
+            swap_lane_bit3(b.q[s].y, b.q[s + 1].y);
+            swap_lane_bit3(b.q[s].z, b.q[s + 1].z);
+            swap_lane_bit3(b.q[s].w, b.q[s + 1].w);
+        }
+        if constexpr (G != kStep) transpose_groups(b.q[s]);
+        const uint32_t d[4] = {b.q[s].x, b.q[s].y, b.q[s].z, b.q[s].w};
+#pragma unroll
+        for (int g = 0; g < per_step; ++g) {
+            v4f D = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int j = g * per_group; j < (g + 1) * per_group; ++j) {
+                const v8bf xb = __builtin_bit_cast(v8bf, x[(s * 4 + j) * 16 * NI]);
+                D = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, codes_bf16(d[j]), D, 0, 0, 0);
+            }
+            const int i = s * per_step + g;
+            const uint32_t sc = b.g.s[i / 2];
+            const float scale = as_f32(i % 2 ? sc & 0xFFFF0000u : sc << 16);
+            const float zero = ZERO ? (float)((b.g.z[i / 4] >> (8 * (i % 4))) & 0xFFu) : 8.0f;
+#pragma unroll
+            for (int k = 0; k < NI; ++k)
+                acc[k] = __builtin_fmaf(scale, __builtin_fmaf(-zero, xsum[i * 4 * NI + k], D[k]), acc[k]);
+        }
+    }
+}
+
+// NI: registers of a result tile that hold tokens. The instruction's operand
+// row n carries token 4 (n % NI) + n / 4 (rows repeat where NI < 4), so that
+// token t ends in register t / 4 of lane group t % 4.
+template <int G, bool ZERO, int NI>
+__global__ __launch_bounds__(1024) void k_int4(Int4Args a) {
+    extern __shared__ uint4 lds[];  // the panel's piece: [step][j][lane group][token]
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int n = lane & 15, kg = lane >> 4;
+    const int side = wave / a.split, part = wave % a.split, across = waves / a.split;  // across: tiles a workgroup takes at once
+    const int64_t tiles = (a.rows + kTile - 1) / kTile;
+    const uint4* x = lds + kg * 4 * NI + 4 * (n & (NI - 1)) + (n >> 2);
+    float* const xsums = reinterpret_cast<float*>(lds + a.piece / 8 * 4 * NI);  // [group][lane group][NI]
+    float* const sums = xsums + a.piece / G * 4 * NI;
+    const float* xsum = xsums + kg * NI;
+    const int pieces = (a.cols + a.piece - 1) / a.piece;
+
+    auto stage = [&](int p0, int cols) {
+        for (int o = threadIdx.x; o < cols / 8 * 4 * NI; o += blockDim.x) {
+            const int t = o % (4 * NI), k = o / (4 * NI) % 4, j = o / (16 * NI) % 4, s = o / (64 * NI);
+            const int c = p0 + s * kStep + (G == kStep ? 32 * k + 8 * j : 32 * j + 8 * k);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (t < a.M && c < a.cols) v = load_global16(a.x + (int64_t)t * a.cols + c);
+            lds[o] = __builtin_bit_cast(uint4, even_odd(v));
+        }
+        __syncthreads();
+        const v8bf ones = {(__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f,
+                           (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f};
+        for (int g = wave; g < cols / G; g += waves) {
+            v4f X = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < G / 32; ++j)
+                X = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, x[(g * (G / 32) + j) * 16 * NI]), ones, X,
+                                                            0, 0, 0);
+            if (n < NI) xsums[(g * 4 + kg) * NI + n] = n == 0 ? X[0] : n == 1 ? X[1] : n == 2 ? X[2] : X[3];
+        }
+    };
+
+    for (int64_t first = (int64_t)blockIdx.x * across; first < tiles; first += (int64_t)gridDim.x * across) {
+        const int64_t tile = first + side;
+        const int64_t row0 = min(tile, tiles - 1) * kTile, row = min(row0 + n, a.rows - 1);
+        const uint8_t* lo = a.codes + min(row0 + (lane & 7), a.rows - 1) * (a.cols / 2);
+        const uint8_t* hi = a.codes + min(row0 + 8 + (lane & 7), a.rows - 1) * (a.cols / 2);
+        float acc[NI];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) acc[i] = 0.0f;
+        for (int p = 0; p < pieces; ++p) {
+            const int p0 = p * a.piece, p1 = min(p0 + a.piece, a.cols);
+            int c0 = p0 + part * kSuper;
+            Load<G> A, B;
+            if (c0 < p1) issue<G, ZERO>(A, a, lo, hi, row, lane, c0);
+            if (pieces > 1 || first == (int64_t)blockIdx.x * across) {
+                if (pieces > 1) __syncthreads();
+                stage(p0, (p1 - p0 + kSuper - 1) / kSuper * kSuper);
+                __syncthreads();
+            }
+            const int stride = a.split * kSuper;
+            while (c0 < p1) {
+                const int c1 = c0 + stride;
+                if (c1 < p1) issue<G, ZERO>(B, a, lo, hi, row, lane, c1);
+                compute<G, ZERO, NI>(A, x + (c0 - p0) / 8 * 4 * NI, xsum + (c0 - p0) / G * 4 * NI, acc);
+                if (c1 >= p1) break;
+                c0 = c1 + stride;
+                if (c0 < p1) issue<G, ZERO>(A, a, lo, hi, row, lane, c0);
+                compute<G, ZERO, NI>(B, x + (c1 - p0) / 8 * 4 * NI, xsum + (c1 - p0) / G * 4 * NI, acc);
+            }
+        }
+        if (a.split > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < NI; ++i) sums[(wave * NI + i) * 64 + lane] = acc[i];
+            __syncthreads();
+            if (part != 0) continue;
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                for (int v = 1; v < a.split; ++v) acc[i] += sums[((wave + v) * NI + i) * 64 + lane];
+        }
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int m = kg + 4 * i;
+            const int64_t r = tile * kTile + n;
+            if (m < a.M && r < a.rows) store_global_f32(a.y + (int64_t)m * a.rows + r, acc[i]);
+        }
+    }
+}
+
+// Few tiles: one workgroup per tile, each wave taking NS steps of its columns
+// (more only where there are more than 16 waves' worth), the panel read where
+// it is needed instead of staged, every load issued before any is used.
+template <int G, bool ZERO, int NI, int NS>
+__global__ __launch_bounds__(1024) void k_int4_shot(Int4Args a) {
+    __shared__ float sums[16 * NI * 64];
+    constexpr int per_step = kStep / G, per_group = 4 / per_step, N = NS * per_step;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int n = lane & 15, kg = lane >> 4, last = a.cols - 32;
+    const int64_t row0 = (int64_t)blockIdx.x * kTile, row = min(row0 + n, a.rows - 1);
+    const uint8_t* lo = a.codes + min(row0 + (lane & 7), a.rows - 1) * (a.cols / 2);
+    const uint8_t* hi = a.codes + min(row0 + 8 + (lane & 7), a.rows - 1) * (a.cols / 2);
+    const uint16_t* x = a.x + (int64_t)min(4 * (n & (NI - 1)) + (n >> 2), a.M - 1) * a.cols;
+    const v8bf ones = {(__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f,
+                       (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f};
+    float acc[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) acc[i] = 0.0f;
+    for (int c0 = wave * NS * kStep; c0 < a.cols; c0 += waves * NS * kStep) {
+        uint4 q[NS], v[NS][4];
+        Groups<N> g;
+#pragma unroll
+        for (int s = 0; s < NS; s += 2) {
+            const int c = min(c0 + s * kStep + 16 * (lane & 8) + 32 * kg, last) / 2;
+            q[s] = load_stream16(lo + c);
+            q[s + 1] = load_stream16(hi + c);
+        }
+        const int64_t g0 = row * (a.cols / G) + c0 / G;
+        load_groups<N, ZERO>(g, a.scales + g0, ZERO ? a.zeros + g0 : nullptr, (a.cols - c0) / G);
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[s][j] = load_global16(x + (G == kStep ? min(c0 + s * kStep + 32 * kg, last) + 8 * j
+                                                        : min(c0 + s * kStep + 32 * j, last) + 8 * kg));
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            if (s % 2 == 0) {
+                swap_lane_bit3(q[s].x, q[s + 1].x);
+                swap_lane_bit3(q[s].y, q[s + 1].y);
+                swap_lane_bit3(q[s].z, q[s + 1].z);
+                swap_lane_bit3(q[s].w, q[s + 1].w);
+            }
+            if constexpr (G != kStep) transpose_groups(q[s]);
+            const uint32_t d[4] = {q[s].x, q[s].y, q[s].z, q[s].w};
+#pragma unroll
+            for (int h = 0; h < per_step; ++h) {
+                v4f D = {0.0f, 0.0f, 0.0f, 0.0f}, X = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int j = h * per_group; j < (h + 1) * per_group; ++j) {
+                    const v8bf xb = even_odd(v[s][j]);
+                    D = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, codes_bf16(d[j]), D, 0, 0, 0);
+                    X = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, ones, X, 0, 0, 0);
+                }
+                const int i = s * per_step + h;
+                const float scale = as_f32(i % 2 ? g.s[i / 2] & 0xFFFF0000u : g.s[i / 2] << 16);
+                const float zero = ZERO ? (float)((g.z[i / 4] >> (8 * (i % 4))) & 0xFFu) : 8.0f;
+#pragma unroll
+                for (int k = 0; k < NI; ++k) acc[k] = __builtin_fmaf(scale, __builtin_fmaf(-zero, X[k], D[k]), acc[k]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) sums[(wave * NI + i) * 64 + lane] = acc[i];
+    __syncthreads();
+    for (int o = threadIdx.x; o < NI * 64; o += blockDim.x) {
+        float s = sums[o];
+        for (int v = 1; v < waves; ++v) s += sums[v * NI * 64 + o];
+        const int m = (o >> 4 & 3) + 4 * (o >> 6);
+        const int64_t r = row0 + (o & 15);
+        if (m < a.M && r < a.rows) store_global_f32(a.y + (int64_t)m * a.rows + r, s);
+    }
+}
+
+// How a workgroup's waves share the tiles: `split` waves per tile, `across`
+// tiles at once. Chosen for the least work of the busiest of kPlanCUs compute
+// units, counted in tiles x 512 columns.
+struct Plan {
+    int split, across;
+};
+Plan plan(int64_t tiles, int supers) {
+    Plan best = {1, 1};
+    double least = 1e300;
+    for (int split = 1; split <= 8 && split <= supers; split *= 2)
+        for (int across = 1; across * split <= kWaves; ++across) {
+            const int w = split * across;
+            const int64_t rounds = ceil_div(ceil_div(tiles, across), kPlanCUs);
+            const double busy = (double)(rounds * across * ceil_div(supers, split) * split);
+            const double cost = busy * (0.7 + 0.3 * kWaves / w) + (double)rounds * (split > 1 ? 2.0 : 0.0);
+            if (cost < least) {
+                least = cost;
+                best = {split, across};
+            }
+        }
+    return best;
+}
+
+template <int G, bool ZERO, int NI>
+void launch(Int4Args a, int cus, hipStream_t s) {
+    const int64_t tiles = ceil_div(a.rows, kTile);
+    const int supers = (int)ceil_div(a.cols, kSuper);
+    if (tiles <= 2 * kPlanCUs) {
+        const int64_t w2 = ceil_div(a.cols, 2 * kStep), w4 = ceil_div(a.cols, 4 * kStep);
+        if (tiles * w2 <= 8 * kPlanCUs)
+            k_int4_shot<G, ZERO, NI, 2><<<(int)tiles, 64 * (int)(w2 < kWaves ? w2 : kWaves), 0, s>>>(a);
+        else
+            k_int4_shot<G, ZERO, NI, 4><<<(int)tiles, 64 * (int)(w4 < kWaves ? w4 : kWaves), 0, s>>>(a);
+        return;
+    }
+    const Plan p = plan(tiles, supers);
+    a.split = p.split;
+    const int64_t padded = (int64_t)supers * kSuper, most = kPanelBytes / (8 * NI);
+    a.piece = (int)(padded < most ? padded : most);
+    const size_t lds = (size_t)a.piece * 8 * NI + (size_t)(a.piece / G) * 16 * NI +
+                       (p.split > 1 ? (size_t)p.split * p.across * NI * 256 : 0);
+    const int64_t groups = ceil_div(tiles, p.across);
+    const int grid = (int)(groups < cus ? groups : cus);
+    k_int4<G, ZERO, NI><<<grid, 64 * p.split * p.across, lds, s>>>(a);
+}
+
+template <int G, bool ZERO>
+void run(const Int4Args& a, int cus, hipStream_t s) {
+    if (a.M <= 4) launch<G, ZERO, 1>(a, cus, s);
+    else if (a.M <= 8) launch<G, ZERO, 2>(a, cus, s);
+    else launch<G, ZERO, 4>(a, cus, s);
+}
+
+template <int G>
+void run_zeros(const Int4Args& a, int cus, hipStream_t s) {
+    if (a.zeros) run<G, true>(a, cus, s);
+    else run<G, false>(a, cus, s);
 }
 
 }  // namespace
@@ -51,10 +401,13 @@ extern "C" int int4_gemv(const uint8_t* codes, const uint16_t* scales_bf16, cons
     if (!codes || !scales_bf16 || !x_bf16 || !y || !aligned(codes, 16) || !aligned(scales_bf16, 2) ||
         !aligned(x_bf16, 16) || !aligned(y, 4))
         return FP8BLK_ERR_ARG;
-    if (rows > INT32_MAX) return FP8BLK_ERR_ARG;
-    const Int4Args a = {codes, scales_bf16, zeros, x_bf16, y, rows, (int32_t)cols, group};
+    const Int4Args a = {codes, scales_bf16, zeros, x_bf16, y, rows, (int32_t)cols, (int32_t)M, 1, kSuper};
+    const int cus = device_cus();
+    if (cus < 1) return FP8BLK_ERR_HIP;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     (void)hipGetLastError();
-    k_int4<<<dim3((unsigned)rows, (unsigned)M), 64, 0, s>>>(a);
+    if (group == 32) run_zeros<32>(a, cus, s);
+    else if (group == 64) run_zeros<64>(a, cus, s);
+    else run_zeros<128>(a, cus, s);
     return launch_status();
 }
