@@ -755,7 +755,8 @@ int fp8blk_moe_route(const uint16_t *w_bf16, const float *bias, int64_t experts,
  *     scales [experts, hidden, inter/B] (B = 32 for FP8BLK_FMT_MXFP4, 16 for
  *     FP8BLK_FMT_NVFP4), each expert's slab as fp4_load_check accepts it;
  *     *_global: f32 [experts] or NULL (1): device, 4-byte aligned.
- *     hidden and inter: multiples of 32, 32 .. FP8BLK_MAX_COLS;
+ *     hidden: a multiple of 32, 32 .. FP8BLK_MAX_COLS; inter: a multiple of 32,
+ *     32 .. FP8BLK_MAX_INTER;
  *     1 <= experts <= FP8BLK_MAX_EXPERTS; limit >= 0 and finite (0: none).
  *   x_bf16 [M, hidden]; ids int32, weights f32 [M, top_k]; 1 <= M <=
  *     FP8BLK_MAX_M; 1 <= top_k <= FP8BLK_MAX_TOP_K. An id outside
@@ -770,6 +771,7 @@ int fp8blk_moe_route(const uint16_t *w_bf16, const float *bias, int64_t experts,
  *     bad sizes); its contents on entry do not matter.
  * Enqueued on `stream`; does not wait.
  */
+#define FP8BLK_MAX_INTER 24576
 typedef struct fp4_moe_layer {
     const uint8_t *gate, *gate_scales;
     const uint8_t *up, *up_scales;
