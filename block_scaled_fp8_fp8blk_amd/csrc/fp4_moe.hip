@@ -22,6 +22,8 @@ constexpr int64_t kMoeAlign = 256;
 constexpr int kTile = 16;   // weight rows of a matrix instruction
 constexpr int kStep = 128;  // columns of one 16-byte load per lane
 constexpr int kWaves = 8;   // of a workgroup, at most
+constexpr int kTurns = 4;   // tiles that a workgroup takes one after another, at most,
+constexpr int kGroups = 2048;  // and only where there are this many workgroups even so
 constexpr int kPieces = 3;  // bf16 values that hold an f32 h
 constexpr int kSlots = FP8BLK_MAX_M * FP8BLK_MAX_TOP_K;
 
@@ -38,60 +40,85 @@ struct MoeArgs {
     int32_t rows, cols;
     int32_t slots, K;
     int32_t most;          // slots of one expert that a workgroup takes
+    int32_t turns;         // tiles (of R * 16 rows) that it takes, one after another
     float limit;
 };
 
-// A wave's weights: one tile of gate and one of up, or four tiles of down,
-// NS steps of each, all loaded before any is used.
+// What a wave takes at a time: one tile of gate and one of up, or four tiles
+// of down, NS steps of each.
 template <int FMT, bool DOWN, int NS>
-struct Load {
+struct Unit {
     static constexpr int MATS = DOWN ? 1 : 2, R = DOWN ? 4 : 1, T = MATS * R;
-    static constexpr int SB = NS * kStep / (FMT == kMX ? 32 : 16);  // block scales of a row
-    static constexpr int PER = FMT == kNV && DOWN ? 2 : 4;          // slots of a matrix operand
-    static constexpr int LANES = DOWN ? kPieces : 1;                // operand rows of a slot in LDS
-    uint4 q[T][NS];
-    uint32_t sc[T][SB / 4];
+    static constexpr int PER = FMT == kNV && DOWN ? 2 : 4;  // slots of a matrix operand
+    static constexpr int LANES = DOWN ? kPieces : 1;        // operand rows of a slot in LDS
+    static constexpr int SLICE = NS * kStep;                // columns
+    static constexpr int B = FMT == kMX ? 32 : 16;          // columns of a block scale
+    static constexpr int ROW = SLICE / B;                   // block scales of a row, and of a pair of steps
+    static constexpr int PAIR = 2 * kStep / B;
+    static constexpr int CHUNK = ROW < 16 ? ROW : 16, LOADS = (T * kTile * ROW / CHUNK + 63) / 64;  // a lane's scale loads
 };
 
-template <int FMT, bool DOWN, int NS>
-__device__ __forceinline__ void issue(Load<FMT, DOWN, NS>& b, const MoeArgs& a, int64_t expert, int tile, int lane, int c0) {
-    using L = Load<FMT, DOWN, NS>;
-    constexpr int B = FMT == kMX ? 32 : 16;
-    const uint32_t wide = a.cols / 2, blocks = a.cols / B;  // bytes of a row: an expert's slab is less than 2^31 bytes
-    const int64_t slab = expert * a.rows;
+// The weights of two steps.
+template <int T>
+struct Pair {
+    uint4 q[T][2];
+};
+
+template <typename U>
+__device__ __forceinline__ void issue(Pair<U::T>& b, const MoeArgs& a, int64_t expert, int tile, int lane, int c0) {
+    const uint32_t wide = a.cols / 2;  // bytes of a row: an expert's slab is less than 2^31 bytes
+    const int64_t slab = expert * a.rows * wide;
+    // columns past the end meet zeros of the operand: any code will do
+    const uint32_t c = min(c0 + 16 * (lane & 8) + 32 * (lane >> 4), a.cols - 32) / 2;
 #pragma unroll
-    for (int t = 0; t < L::T; ++t) {
-        const int m = t / L::R, r0 = (tile * L::R + t % L::R) * kTile;
-        const uint8_t* w = a.w[m] + slab * wide;
-        const uint32_t lo = min(r0 + (lane & 7), a.rows - 1) * wide, hi = min(r0 + 8 + (lane & 7), a.rows - 1) * wide;
-#pragma unroll
-        for (int s = 0; s < NS; s += 2) {  // columns past the end meet zeros of the operand: any code will do
-            const uint32_t c = min(c0 + s * kStep + 16 * (lane & 8) + 32 * (lane >> 4), a.cols - 32) / 2;
-            b.q[t][s] = load_stream16(w + (lo + c));
-            b.q[t][s + 1] = load_stream16(w + (hi + c));
-        }
+    for (int t = 0; t < U::T; ++t) {
+        const int r0 = (tile * U::R + t % U::R) * kTile;
+        const uint8_t* w = a.w[t / U::R] + slab;
+        b.q[t][0] = load_stream16(w + (min(r0 + (lane & 7), a.rows - 1) * wide + c));
+        b.q[t][1] = load_stream16(w + (min(r0 + 8 + (lane & 7), a.rows - 1) * wide + c));
     }
+}
+
+// The block scales of a unit. A lane's matrix column is one weight row, and
+// reading that row's few scales in place would ask for 16 lines per load and
+// every line many times over (measured: a third of the whole time). So a load
+// takes them as they lie, and they change places in LDS, [tile][row][block].
+template <typename U>
+struct Scales {
+    uint32_t d[U::LOADS][U::CHUNK / 4];
+};
+
+template <typename U>
+__device__ __forceinline__ void issue_scales(Scales<U>& b, const MoeArgs& a, int64_t expert, int tile, int lane, int c0) {
+    constexpr int PER_ROW = U::ROW / U::CHUNK;
+    const uint32_t blocks = a.cols / U::B;
+    const int64_t end = (a.experts - expert) * a.rows * blocks;  // of the array, from this expert's scales
 #pragma unroll
-    for (int t = 0; t < L::T; ++t) {
-        const int m = t / L::R, r0 = (tile * L::R + t % L::R) * kTile;
-        const uint8_t* sc = a.sc[m] + slab * blocks;
-        const uint32_t at = min(r0 + (lane & 15), a.rows - 1) * blocks + c0 / B;
-        if (c0 + NS * kStep <= a.cols) {
-            __builtin_memcpy(b.sc[t], sc + at, L::SB);
-        } else {
-            // Past the row's end other rows' scales are as good (the operand
-            // is zero there), past the last row's there are none: the last
-            // dword, shifted.
-            const uint32_t last = (uint32_t)min((a.experts - expert) * a.rows * blocks, (int64_t)INT32_MAX) - 4;
+    for (int i = 0; i < U::LOADS; ++i) {
+        const int o = min(i * 64 + lane, U::T * kTile * PER_ROW - 1), t = o / (kTile * PER_ROW);
+        const int row = (tile * U::R + t % U::R) * kTile + o / PER_ROW % kTile;
+        const uint32_t at = min(row, a.rows - 1) * blocks + c0 / U::B + o % PER_ROW * U::CHUNK;
+        const uint8_t* sc = (U::MATS == 2 && t ? a.sc[1] : a.sc[0]) + expert * a.rows * blocks;
+        // past a row's end other rows' scales are as good, the operand is zero there
+        if (at + U::CHUNK <= end) {
+            __builtin_memcpy(b.d[i], sc + at, U::CHUNK);
+        } else {  // past the array's end there are none: its last dword, shifted
 #pragma unroll
-            for (int i = 0; i < L::SB / 4; ++i) {
-                const uint32_t from = min(at + 4 * i, last);
-                uint32_t d;
-                __builtin_memcpy(&d, sc + from, 4);
-                b.sc[t][i] = d >> (8 * (at + 4 * i - from) & 31);
+            for (int k = 0; k < U::CHUNK / 4; ++k) {
+                const int64_t from = min((int64_t)at + 4 * k, end - 4);
+                uint32_t v;
+                __builtin_memcpy(&v, sc + from, 4);
+                b.d[i][k] = v >> (8 * (int)(at + 4 * k - from) & 31);
             }
         }
     }
+}
+
+template <typename U>
+__device__ __forceinline__ void place_scales(const Scales<U>& b, uint8_t* to, int lane) {
+#pragma unroll
+    for (int i = 0; i < U::LOADS; ++i)
+        if (i * 64 + lane < U::T * kTile * U::ROW / U::CHUNK) __builtin_memcpy(to + (i * 64 + lane) * U::CHUNK, b.d[i], U::CHUNK);
 }
 
 // Exchange the dword index with the lane group: afterwards dword j of lane
@@ -113,67 +140,117 @@ __device__ __forceinline__ v8bf codes_bf16(uint32_t d, float scale) {
     return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], e[0], e[1]};
 }
 
-// acc += the wave's weights times the operand's columns (LDS; `stride` 16-byte
-// units from one 32-column read to the next).
-template <int FMT, bool DOWN, int NS>
-__device__ __forceinline__ void compute(Load<FMT, DOWN, NS>& b, const uint4* in, int stride, int kg, bool live, v4f* acc) {
-    using L = Load<FMT, DOWN, NS>;
+// acc += two steps of weights times the operand's columns (LDS; `stride`
+// 16-byte units from one 32-column read to the next); sc: the lane's row of
+// scales of the steps.
+template <int FMT, bool DOWN, typename U>
+__device__ __forceinline__ void compute(Pair<U::T>& b, const uint4* in, int stride, const uint8_t* sc, int kg, bool live, v4f* acc) {
+    uint32_t e[U::T][U::PAIR / 4];
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
+    for (int t = 0; t < U::T; ++t) {
+        __builtin_memcpy(e[t], __builtin_assume_aligned(sc + t * kTile * U::ROW, U::PAIR), U::PAIR);
+        swap_lane_bit3(b.q[t][0].x, b.q[t][1].x);
+        swap_lane_bit3(b.q[t][0].y, b.q[t][1].y);
+        swap_lane_bit3(b.q[t][0].z, b.q[t][1].z);
+        swap_lane_bit3(b.q[t][0].w, b.q[t][1].w);
+    }
 #pragma unroll
-        for (int t = 0; t < L::T; ++t) {
-            if (s % 2 == 0) {
-                swap_lane_bit3(b.q[t][s].x, b.q[t][s + 1].x);
-                swap_lane_bit3(b.q[t][s].y, b.q[t][s + 1].y);
-                swap_lane_bit3(b.q[t][s].z, b.q[t][s + 1].z);
-                swap_lane_bit3(b.q[t][s].w, b.q[t][s + 1].w);
-            }
-            if constexpr (FMT == kNV) transpose_groups(b.q[t][s]);
+    for (int s = 0; s < 2; ++s) {
+        if constexpr (FMT == kNV) {
+#pragma unroll
+            for (int t = 0; t < U::T; ++t) transpose_groups(b.q[t][s]);
         }
-        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint4 v = in[(s * 4 + j) * stride];
             if constexpr (FMT == kNV) v = live ? v : make_uint4(0, 0, 0, 0);
             const v8bf x = __builtin_bit_cast(v8bf, v);
 #pragma unroll
-            for (int t = 0; t < L::T; ++t) {
+            for (int t = 0; t < U::T; ++t) {
                 const uint32_t d[4] = {b.q[t][s].x, b.q[t][s].y, b.q[t][s].z, b.q[t][s].w};
                 if constexpr (FMT == kMX) {
                     // byte kg of the step's dword into the exponent field
-                    const uint32_t e = __builtin_amdgcn_alignbit(b.sc[t][s], b.sc[t][s], (uint32_t)(8 * kg + 9));
-                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, codes_bf16(d[j], as_f32(e)), acc[t], 0, 0, 0);
+                    const uint32_t f = __builtin_amdgcn_alignbit(e[t][s], e[t][s], (uint32_t)(8 * kg + 9));
+                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, codes_bf16(d[j], as_f32(f)), acc[t], 0, 0, 0);
                 } else {
                     const v4f D = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, codes_bf16(d[j], 1.0f), v4f{0.0f, 0.0f, 0.0f, 0.0f},
                                                                           0, 0, 0);
                     const int i = s * 8 + 2 * j;
-                    const v2f sc = i % 4 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(b.sc[t][i / 4], 1.0f, true)
-                                         : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(b.sc[t][i / 4], 1.0f, false);
-                    float f = __builtin_fmaf(sc.y, D[1], __builtin_fmaf(sc.x, D[0], acc[t][0]));
-                    if constexpr (DOWN) f = __builtin_fmaf(sc.y, D[3], __builtin_fmaf(sc.x, D[2], f));
-                    acc[t][0] = f;
+                    const v2f f = i % 4 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(e[t][i / 4], 1.0f, true)
+                                        : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(e[t][i / 4], 1.0f, false);
+                    float r = __builtin_fmaf(f.y, D[1], __builtin_fmaf(f.x, D[0], acc[t][0]));
+                    if constexpr (DOWN) r = __builtin_fmaf(f.y, D[3], __builtin_fmaf(f.x, D[2], r));
+                    acc[t][0] = r;
                 }
             }
             if constexpr (FMT == kNV) {
                 // keep the sums where they are: taken later, every result of
                 // the matrix instruction would wait for them in registers
 #pragma unroll
-                for (int t = 0; t < L::T; ++t) asm volatile("" : "+v"(acc[t][0]));
+                for (int t = 0; t < U::T; ++t) asm volatile("" : "+v"(acc[t][0]));
             }
         }
     }
 }
 
+__device__ __forceinline__ int ceil_step(int n, int step) { return (n + step - 1) / step * step; }
+
 // bf16 value nearest to f, as an f32.
 __device__ __forceinline__ float head_bf16(float f) { return as_f32(bf16_of_scaled(1.0f, as_u32(f)) << 16); }
 
+// A tile's sums over the waves that share its columns, and its outputs: every
+// wave calls it as often.
+template <int FMT, bool DOWN, typename U>
+__device__ __forceinline__ void finish(const MoeArgs& a, int expert, int tile, int member, int count, float* sums, v4f* acc) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+#pragma unroll
+    for (int t = 0; t < U::T; ++t) {
+        sums[(wave * U::T + t) * 64 + lane] = DOWN && FMT == kMX ? acc[t][0] + (acc[t][1] + acc[t][2]) : acc[t][0];
+        acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    __syncthreads();
+    for (int r = wave; r < U::R; r += waves) {
+        const int row = (tile * U::R + r) * kTile + (lane & 15), of = (lane >> 4) / (4 / U::PER);
+        float v[U::MATS];
+#pragma unroll
+        for (int m = 0; m < U::MATS; ++m) {
+            for (int w = 0; w < waves; ++w) {
+                const float* p = sums + (w * U::T + m * U::R + r) * 64;
+                const float x = U::PER == 2 ? p[lane] + p[lane ^ 16] : p[lane];
+                v[m] = w == 0 ? x : v[m] + x;
+            }
+            if (a.top[m]) v[m] *= a.top[m][expert];
+        }
+        const int sl = __shfl(member, of & 63);
+        if (row >= a.rows || of >= count) continue;
+        if constexpr (DOWN) {
+            if (U::PER == 4 || !(lane & 16)) a.part[(int64_t)sl * a.rows + row] = v[0];
+        } else {
+            float g1 = v[0], u = v[U::MATS - 1];
+            if (a.limit > 0.0f) {
+                g1 = fminf(g1, a.limit);
+                u = fminf(fmaxf(u, -a.limit), a.limit);
+            }
+            float h = g1 / (1.0f + expf(-g1)) * u;
+            uint16_t* to = a.pieces + (int64_t)sl * kPieces * a.rows + row;
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p) {
+                const float bf = head_bf16(h);
+                to[(int64_t)p * a.rows] = (uint16_t)(as_u32(bf) >> 16);
+                h -= bf;
+            }
+        }
+    }
+}
+
 template <int FMT, bool DOWN, int NS>
 __global__ __launch_bounds__(64 * kWaves, 3) void k_moe(MoeArgs a) {
-    using L = Load<FMT, DOWN, NS>;
-    constexpr int CHUNKS = NS * 16;  // 16-byte reads of an operand row
-    extern __shared__ uint4 lds[];   // each wave's operand rows, then the waves' sums
+    using U = Unit<FMT, DOWN, NS>;
+    constexpr int SLICE = U::SLICE;
+    extern __shared__ uint4 lds[];  // the operand, the waves' block scales and their sums
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, n = lane & 15, kg = lane >> 4;
-    const int slot = blockIdx.y, tile = blockIdx.x;
+    const int slot = blockIdx.y, tiles = (a.rows + kTile * U::R - 1) / (kTile * U::R);
+    const int end = min((int)(blockIdx.x + 1) * a.turns, tiles);
 
     // The slots of this slot's expert; the workgroup is theirs if `slot` is
     // the first, or (a.most)-th, ... of them.
@@ -199,120 +276,114 @@ __global__ __launch_bounds__(64 * kWaves, 3) void k_moe(MoeArgs a) {
     }
     if (before % a.most != 0) return;
 
-    const int rows_in = a.most * L::LANES, live_rows = count * L::LANES;
-    uint4* own = lds + wave * CHUNKS * rows_in;
+    int tile = blockIdx.x * a.turns, c0 = wave * SLICE;
+    Pair<U::T> b[NS / 2];
+    Scales<U> sr;
+#pragma unroll
+    for (int s = 0; s < NS / 2; ++s) issue<U>(b[s], a, expert, tile, lane, c0 + 2 * s * kStep);
+    issue_scales<U>(sr, a, expert, tile, lane, c0);
+
+    // The operand: [step][32 columns][lane group][row], zeros past the last
+    // column; a wave reads only the slices that it has staged itself.
+    const int rows_in = a.most * U::LANES, live_rows = count * U::LANES;
+    for (int p0 = c0; p0 < a.cols; p0 += waves * SLICE)
+        for (int r0 = 0; r0 < live_rows; r0 += 4)
+            for (int i = 0; i < NS * 16; i += 64) {
+                uint4 v[4];
+                const int o = i + lane, k = o % 4, j = o / 4 % 4;
+                const int c = p0 + o / 16 * kStep + (FMT == kMX ? 32 * k + 8 * j : 32 * j + 8 * k);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const int r = min(r0 + p, live_rows - 1), sl = __builtin_amdgcn_readlane(member, r / U::LANES);
+                    const int64_t at = DOWN ? (int64_t)sl * kPieces + r % kPieces : (int64_t)(sl / a.K);
+                    v[p] = c < a.cols ? load_global16(a.in + at * a.cols + c) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                    if (r0 + p < live_rows && o < NS * 16) lds[(p0 / 8 + o) * rows_in + r0 + p] = v[p];
+            }
+    // the wave's own lanes read what the others wrote
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+
     int row_in;  // the lane's operand row
     if constexpr (!DOWN) row_in = n >> 2;
     else if constexpr (FMT == kMX) row_in = kPieces * (n >> 2) + min(n & 3, 2);
     else row_in = kPieces * (n >> 3) + min((n & 7) >> 1, 2);
-    const uint4* in = own + kg * rows_in + min(row_in, rows_in - 1);
+    const uint4* in = lds + kg * rows_in + min(row_in, rows_in - 1);
     // NVFP4: an operand row holds one 16-column block of each 32 columns, row
     // bit 0 says which; a down operand's rows 6 and 7 of 8 hold nothing.
     const bool live = (kg >> 1) == (n & 1) && (!DOWN || (n & 7) < 6);
+    const int64_t operand = ceil_step(a.cols, SLICE) / 8 * (int64_t)rows_in;
+    uint8_t* const scales = reinterpret_cast<uint8_t*>(lds + operand) + wave * U::T * kTile * U::ROW;  // [wave][tile][row][block]
+    float* const sums = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(lds + operand) + waves * U::T * kTile * U::ROW);
 
-    v4f acc[L::T];
+    v4f acc[U::T];
 #pragma unroll
-    for (int t = 0; t < L::T; ++t) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < U::T; ++t) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-    for (int c0 = wave * NS * kStep; c0 < a.cols; c0 += waves * NS * kStep) {
-        L b;
-        issue<FMT, DOWN, NS>(b, a, expert, tile, lane, c0);
-        // The operand: [step][j][lane group][row], zeros past the last column.
-        constexpr int AT_ONCE = CHUNKS < 64 ? 64 / CHUNKS : 1, TIMES = CHUNKS < 64 ? 1 : CHUNKS / 64;  // rows, loads
-        constexpr int BATCH = 4 / TIMES * AT_ONCE;                                                   // rows of four loads
-        for (int r0 = 0; r0 < live_rows; r0 += BATCH) {
-            uint4 v[4];
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const int r = r0 + p / TIMES * AT_ONCE + lane / CHUNKS, o = (p % TIMES * 64 + lane) % CHUNKS;
-                const int sl = __shfl(member, min(r / L::LANES, count - 1)), k = o % 4, j = o / 4 % 4;
-                const int64_t at = DOWN ? (int64_t)sl * kPieces + r % kPieces : (int64_t)(sl / a.K);
-                const int c = c0 + o / 16 * kStep + (FMT == kMX ? 32 * k + 8 * j : 32 * j + 8 * k);
-                v[p] = make_uint4(0, 0, 0, 0);
-                if (c < a.cols && r < live_rows) v[p] = load_global16(a.in + at * a.cols + c);
-            }
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const int r = r0 + p / TIMES * AT_ONCE + lane / CHUNKS, o = (p % TIMES * 64 + lane) % CHUNKS;
-                if (r < live_rows) own[o * rows_in + r] = v[p];
-            }
-        }
-        // the wave's own lanes read what the others wrote
+    for (int turn = 0; tile < end;) {
+        int t1 = tile, c1 = c0 + waves * SLICE;
+        if (c1 >= a.cols) c1 = wave * SLICE, ++t1;
+        place_scales<U>(sr, scales, lane);
+        if (t1 < end) issue_scales<U>(sr, a, expert, t1, lane, c1);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        compute<FMT, DOWN, NS>(b, in, 4 * rows_in, kg, live, acc);
+#pragma unroll
+        for (int s = 0; s < NS / 2; ++s) {
+            compute<FMT, DOWN, U>(b[s], in + (c0 / 8 + 32 * s) * rows_in, 4 * rows_in, scales + n * U::ROW + s * U::PAIR, kg,
+                                  live, acc);
+            if (t1 < end) issue<U>(b[s], a, expert, t1, lane, c1 + 2 * s * kStep);
+        }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-    }
-
-    float* sums = reinterpret_cast<float*>(lds + waves * CHUNKS * rows_in);  // [wave][tile][lane]
-#pragma unroll
-    for (int t = 0; t < L::T; ++t)
-        sums[(wave * L::T + t) * 64 + lane] = DOWN && FMT == kMX ? acc[t][0] + (acc[t][1] + acc[t][2]) : acc[t][0];
-    __syncthreads();
-    for (int o = threadIdx.x; o < L::R * 64; o += blockDim.x) {
-        const int l = o & 63, r = o / 64;
-        const int row = (tile * L::R + r) * kTile + (l & 15), of = (l >> 4) / (4 / L::PER);
-        float v[L::MATS];
-#pragma unroll
-        for (int m = 0; m < L::MATS; ++m) {
-            for (int w = 0; w < waves; ++w) {
-                const float* p = sums + (w * L::T + m * L::R + r) * 64;
-                const float x = L::PER == 2 ? p[l] + p[l ^ 16] : p[l];
-                v[m] = w == 0 ? x : v[m] + x;
-            }
-            if (a.top[m]) v[m] *= a.top[m][expert];
-        }
-        const int sl = __shfl(member, of & 63);
-        if (row >= a.rows || of >= count) continue;
-        if constexpr (DOWN) {
-            if (L::PER == 4 || !(l & 16)) a.part[(int64_t)sl * a.rows + row] = v[0];
-        } else {
-            float g1 = v[0], u = v[L::MATS - 1];
-            if (a.limit > 0.0f) {
-                g1 = fminf(g1, a.limit);
-                u = fminf(fmaxf(u, -a.limit), a.limit);
-            }
-            float h = g1 / (1.0f + expf(-g1)) * u;
-            uint16_t* to = a.pieces + (int64_t)sl * kPieces * a.rows + row;
-#pragma unroll
-            for (int p = 0; p < kPieces; ++p) {
-                const float bf = head_bf16(h);
-                to[(int64_t)p * a.rows] = (uint16_t)(as_u32(bf) >> 16);
-                h -= bf;
-            }
-        }
+        c0 = c1;
+        if (t1 == tile) continue;
+        finish<FMT, DOWN, U>(a, expert, tile, member, count, sums + (turn & 1) * waves * U::T * 64, acc);
+        tile = t1;
+        ++turn;
     }
 }
 
-// y = base + the weighted sum of a token's experts, in order of k.
-__global__ __launch_bounds__(256) void k_moe_sum(const float* __restrict__ part, const int32_t* __restrict__ ids,
-                                                 const float* __restrict__ weights, const float* base, int64_t experts,
-                                                 int hidden, int K, float* y) {
-    const int m = blockIdx.y, c = (blockIdx.x * 256 + threadIdx.x) * 4;
+// y = base + the weighted sum of a token's experts, in order of k. All loads
+// are issued before the first is used: a choice that is none reads what lies
+// in its place and leaves it.
+__global__ __launch_bounds__(64) void k_moe_sum(const float* __restrict__ part, const int32_t* __restrict__ ids,
+                                                const float* __restrict__ weights, const float* base, int64_t experts,
+                                                int hidden, int K, float* y) {
+    const int m = blockIdx.y, c = (blockIdx.x * 64 + threadIdx.x) * 4;
     if (c >= hidden) return;
     const int64_t o = (int64_t)m * hidden + c;
     v4f s = base ? *reinterpret_cast<const v4f*>(base + o) : v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k = 0; k < K; ++k) {
-        const int slot = m * K + k, e = ids[slot];
-        if (e < 0 || e >= experts) continue;
-        const v4f v = *reinterpret_cast<const v4f*>(part + (int64_t)slot * hidden + c);
-        const float w = weights[slot];
+    for (int k0 = 0; k0 < K; k0 += 8) {
+        v4f v[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = __builtin_fmaf(w, v[i], s[i]);
+        for (int k = 0; k < 8; ++k)
+            v[k] = *reinterpret_cast<const v4f*>(part + (int64_t)(m * K + min(k0 + k, K - 1)) * hidden + c);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int slot = m * K + min(k0 + k, K - 1), e = ids[slot];
+            const float w = weights[slot];
+            if (k0 + k >= K || e < 0 || e >= experts) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] = __builtin_fmaf(w, v[k][i], s[i]);
+        }
     }
     *reinterpret_cast<v4f*>(y + o) = s;
 }
 
 template <int FMT, bool DOWN, int NS>
 void launch_steps(MoeArgs a, hipStream_t s) {
-    using L = Load<FMT, DOWN, NS>;
-    a.most = a.slots / a.K < L::PER ? a.slots / a.K : L::PER;
-    const int64_t slices = ceil_div(a.cols, NS * kStep);
+    using U = Unit<FMT, DOWN, NS>;
+    const int64_t slices = ceil_div(a.cols, NS * kStep), tiles = ceil_div(a.rows, kTile * U::R);
     const int waves = (int)(slices < kWaves ? slices : kWaves);
-    const size_t lds = (size_t)waves * (NS * 256 * a.most * L::LANES + L::T * 256);
-    const dim3 grid((unsigned)ceil_div(a.rows, kTile * L::R), (unsigned)a.slots);
-    k_moe<FMT, DOWN, NS><<<grid, 64 * waves, lds, s>>>(a);
+    const int64_t row_bytes = slices * NS * kStep * 2 * U::LANES;
+    a.most = a.slots / a.K < U::PER ? a.slots / a.K : U::PER;
+    while (a.most > 1 && a.most * row_bytes > 64 * 1024) a.most /= 2;
+    const int64_t turns = tiles * a.slots / kGroups;
+    a.turns = (int)(turns < 1 ? 1 : turns > kTurns ? kTurns : turns);
+    const dim3 grid((unsigned)ceil_div(tiles, a.turns), (unsigned)a.slots);
+    k_moe<FMT, DOWN, NS><<<grid, 64 * waves, (size_t)(a.most * row_bytes + waves * U::T * (kTile * U::ROW + 512)), s>>>(a);
 }
 
 template <int FMT, bool DOWN>
@@ -327,12 +398,12 @@ void run(const fp4_moe_layer& l, const uint16_t* x, int M, const int32_t* ids, c
          const float* base, float* y, uint16_t* pieces, float* part, hipStream_t s) {
     const int H = (int)l.hidden, I = (int)l.inter;
     MoeArgs a = {{l.gate, l.up}, {l.gate_scales, l.up_scales}, {l.gate_global, l.up_global}, x, ids, pieces, nullptr,
-                 l.experts, I, H, M * K, K, 1, l.limit};
+                 l.experts, I, H, M * K, K, 1, 1, l.limit};
     launch<FMT, false>(a, s);
     a = {{l.down, nullptr}, {l.down_scales, nullptr}, {l.down_global, nullptr}, pieces, ids, nullptr, part,
-         l.experts, H, I, M * K, K, 1, 0.0f};
+         l.experts, H, I, M * K, K, 1, 1, 0.0f};
     launch<FMT, true>(a, s);
-    k_moe_sum<<<dim3((unsigned)ceil_div(H, 1024), (unsigned)M), 256, 0, s>>>(part, ids, weights, base, l.experts, H, K, y);
+    k_moe_sum<<<dim3((unsigned)ceil_div(H, 256), (unsigned)M), 64, 0, s>>>(part, ids, weights, base, l.experts, H, K, y);
 }
 
 bool width_ok(int64_t n, int64_t most) { return n >= 32 && n <= most && n % 32 == 0; }
