@@ -1,4 +1,17 @@
 // Router: the experts each token goes to and their weights, in 64 bits.
+//
+// A choice is a decision, and neighbours around the border have to fall the
+// same way wherever they are computed, so the logits are sums in 64 bits of
+// products that are exact (bf16 x bf16), on v_mfma_f64_16x16x4_f64: 16 tokens
+// by 16 experts. That instruction is the bound of a large panel (64 cycles for
+// 2048 flop: 74 TFLOP/s); a few tokens are bound by latency.
+//
+// Order of a logit, whatever the panel: chunks of 128 columns, each a chain
+// of matrix instructions from 0; four sums over the chunks c % 4 = 0, 1, 2, 3
+// in order; then (s0 + s1) + (s2 + s3). Few tiles: every chunk is a wave of
+// its own, the chunks' sums go to the workspace, and the kernel that chooses
+// adds them. Many tiles: the four waves of a workgroup each walk a quarter of
+// the chunks and add in LDS.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -9,95 +22,290 @@
 namespace fp8blk {
 namespace {
 
-constexpr size_t kRouteAlign = 256;
+typedef double v4d __attribute__((ext_vector_type(4)));
+
+constexpr int64_t kRouteAlign = 256;
+constexpr int kTile = 16, kStepCols = 32, kChunkCols = 128;
+constexpr int kSplitTiles = 256;  // up to so many 16 x 16 tiles each chunk has a wave of its own
+
+inline int route_chunks(int64_t cols) { return (int)ceil_div(cols, kChunkCols); }
+inline bool route_split(int64_t experts, int64_t M) { return ceil_div(experts, kTile) * ceil_div(M, kTile) <= kSplitTiles; }
 
 struct RouteArgs {
+    const uint16_t* w;
+    const uint16_t* x;
     const float* bias;
-    const double* logits;  // [M, E]
+    double* logits;  // [M, E], or [chunk][M, E] where the chunks are added later
     int32_t* ids;
     float* weights;
-    int32_t E, K, score, normalize;
+    int32_t E, M, cols, K, score, normalize, chunks;
     float scale;
 };
 
-__device__ __forceinline__ double shfl_xor64(double v, int m) {
+// 8 bf16 values as f64.
+struct Eight {
+    double v[8];
+};
+__device__ __forceinline__ Eight widen(const uint4& d) {
+    float f[8];
+    widen8_bf16(d, f);
+    Eight e;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e.v[i] = (double)f[i];
+    return e;
+}
+
+// Lane (n, k) of a wave holds 8 columns, k-th of four, of token or expert n in
+// a 32-column step; instruction j takes column j of each. The loads of AHEAD
+// steps are in flight.
+constexpr int kSteps = kChunkCols / kStepCols;
+template <int R, int AHEAD>
+struct Steps {
+    const uint16_t *x[R], *w[R];
+    uint4 xd[AHEAD][R], wd[AHEAD][R];
+    int cols, kg;
+
+    __device__ __forceinline__ void load(int slot, int c) {
+        const int at = min(c + 8 * kg, cols - 8);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            xd[slot][i] = load_global16(x[i] + at);
+            wd[slot][i] = load_global16(w[i] + at);
+        }
+    }
+    __device__ __forceinline__ Eight take(const uint4& d, int c) const {  // zeros past the last column
+        const uint32_t keep = c + 8 * kg < cols ? ~0u : 0u;
+        return widen(make_uint4(d.x & keep, d.y & keep, d.z & keep, d.w & keep));
+    }
+    // acc += the step in `slot`, columns c on; that slot then takes the step at `next`.
+    __device__ __forceinline__ void multiply(int slot, int c, bool more, int next, v4d (&acc)[R][R]) {
+        Eight xe[R], we[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) xe[i] = take(xd[slot][i], c), we[i] = take(wd[slot][i], c);
+        if (more) load(slot, next);
+        __builtin_amdgcn_sched_barrier(0);  // the loads go out before the products, not where they are used
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int j = 0; j < R; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f64_16x16x4f64(xe[i].v[k], we[j].v[k], acc[i][j], 0, 0, 0);
+    }
+};
+
+// Register i of lane l of a result tile is token 4 i + l / 16, expert l % 16.
+template <int R, bool SPLIT>
+__global__ __launch_bounds__(256) void k_route_logits(RouteArgs a) {
+    __shared__ double sums[SPLIT ? 1 : 3][SPLIT ? 1 : R * R * 4 * 64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, kg = lane >> 4;
+    const int e0 = blockIdx.x * R * kTile, m0 = blockIdx.y * R * kTile;
+    constexpr int AHEAD = SPLIT ? kSteps : 2;
+    Steps<R, AHEAD> steps;
+    steps.cols = a.cols;
+    steps.kg = kg;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        steps.x[i] = a.x + (int64_t)min(m0 + i * kTile + n, a.M - 1) * a.cols;
+        steps.w[i] = a.w + (int64_t)min(e0 + i * kTile + n, a.E - 1) * a.cols;
+    }
+    v4d total[R][R];
+    const auto clear = [](v4d(&t)[R][R]) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < R; ++j) t[i][j] = v4d{0.0, 0.0, 0.0, 0.0};
+    };
+    clear(total);
+    double* out = a.logits;
+    if constexpr (SPLIT) {
+        const int chunk = blockIdx.z * 4 + wave, c0 = chunk * kChunkCols;
+        if (chunk >= a.chunks) return;
+        out += (int64_t)chunk * a.M * a.E;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) steps.load(s, c0 + s * kStepCols);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) steps.multiply(s, c0 + s * kStepCols, false, 0, total);
+    } else {
+        v4d acc[R][R];
+        steps.load(0, wave * kChunkCols);
+        steps.load(1, wave * kChunkCols + kStepCols);
+        for (int chunk = wave; chunk < a.chunks; chunk += 4) {
+            clear(acc);
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const int c = chunk * kChunkCols + s * kStepCols;
+                steps.multiply(s % 2, c, true, s + 2 < kSteps ? c + 2 * kStepCols : c + (2 - kSteps) * kStepCols + 4 * kChunkCols, acc);
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int j = 0; j < R; ++j) total[i][j] += acc[i][j];
+        }
+        if (wave > 0)
+#pragma unroll
+            for (int t = 0; t < R * R * 4; ++t) sums[wave - 1][t * 64 + lane] = total[t / 4 / R][t / 4 % R][t % 4];
+        __syncthreads();
+        if (wave > 0) return;
+#pragma unroll
+        for (int t = 0; t < R * R * 4; ++t) {
+            const int o = t * 64 + lane;
+            const double s = total[t / 4 / R][t / 4 % R][t % 4];
+            total[t / 4 / R][t / 4 % R][t % 4] = (s + sums[0][o]) + (sums[1][o] + sums[2][o]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int m = m0 + i * kTile + 4 * k + kg, e = e0 + j * kTile + n;
+                if (m < a.M && e < a.E) out[(int64_t)m * a.E + e] = total[i][j][k];
+            }
+}
+
+template <int CTRL>
+__device__ __forceinline__ double dpp64(double v) {
     const uint64_t u = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = (uint32_t)__shfl_xor((int)(uint32_t)u, m), hi = (uint32_t)__shfl_xor((int)(uint32_t)(u >> 32), m);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// One wave per (expert, token).
-__global__ __launch_bounds__(64) void k_route_logits(const uint16_t* __restrict__ w, const uint16_t* __restrict__ x,
-                                                     int cols, int E, double* __restrict__ logits) {
-    const int64_t e = blockIdx.x, m = blockIdx.y;
-    double s = 0.0;
-    for (int c = threadIdx.x; c < cols; c += 64)
-        s = __builtin_fma((double)as_f32((uint32_t)w[e * cols + c] << 16), (double)as_f32((uint32_t)x[m * cols + c] << 16), s);
-    for (int h = 32; h >= 1; h >>= 1) s += shfl_xor64(s, h);
-    if (threadIdx.x == 0) logits[m * E + e] = s;
+// A reduction over the wave, the same bits in every lane.
+template <typename F>
+__device__ __forceinline__ double reduce64(double v, F f) {
+    const auto halves = [&](bool by32) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        const uint32_t lo = (uint32_t)u, hi = (uint32_t)(u >> 32);
+        const auto a = by32 ? __builtin_amdgcn_permlane32_swap(lo, lo, false, false) : __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+        const auto b = by32 ? __builtin_amdgcn_permlane32_swap(hi, hi, false, false) : __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+        return f(__builtin_bit_cast(double, (uint64_t)b[0] << 32 | a[0]), __builtin_bit_cast(double, (uint64_t)b[1] << 32 | a[1]));
+    };
+    v = halves(true);
+    v = halves(false);
+    v = f(v, dpp64<kRowRor8>(v));
+    v = f(v, dpp64<kRowRor4>(v));
+    v = f(v, dpp64<kQuadXor2>(v));
+    v = f(v, dpp64<kQuadXor1>(v));
+    return v;
 }
 
-// One wave per token; lane l holds experts l, l + 64, ...
-template <int NE>
-__global__ __launch_bounds__(64) void k_route_choose(RouteArgs a) {
-    const int64_t m = blockIdx.x;
-    const int lane = threadIdx.x;
+__device__ __forceinline__ double lane_value64(double v, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// A logit from its chunks' sums, 32 loads at a time.
+__device__ __forceinline__ double add_chunks(const RouteArgs& a, int64_t at) {
+    const int64_t n = (int64_t)a.M * a.E;
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    for (int c = 0; c < a.chunks; c += 32) {
+        double v[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = a.logits[at + min(c + k, a.chunks - 1) * n];
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            if (c + k < a.chunks) s[k % 4] += v[k];
+    }
+    return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+// sigmoid(l) or sqrt(log(1 + exp(l))).
+__device__ __forceinline__ double own_score(int score, double l) {
+    const double t = exp(-fabs(l));  // at most 1
+    if (score == FP8BLK_SCORE_SIGMOID) return l >= 0.0 ? 1.0 / (1.0 + t) : t / (1.0 + t);
+    return sqrt((l > 0.0 ? l : 0.0) + log1p(t));
+}
+
+// One wave per token; lane l holds experts l, l + 64, ... WIDE: the logits are
+// first added by a workgroup.
+template <int NE, bool WIDE>
+__global__ __launch_bounds__(256) void k_route_choose(RouteArgs a) {
+    __shared__ double whole[WIDE ? FP8BLK_MAX_EXPERTS : 1];
+    const int lane = threadIdx.x & 63;
+    const int64_t m = WIDE ? blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     const double lowest = -__builtin_inf();
-    double s[NE], pick[NE], top = lowest;
+    if constexpr (WIDE) {
+        for (int e = threadIdx.x; e < a.E; e += 256) {
+            const double l = add_chunks(a, m * a.E + e);
+            whole[e] = a.score == FP8BLK_SCORE_SOFTMAX ? l : own_score(a.score, l);
+        }
+        __syncthreads();
+        if (threadIdx.x >= 64) return;
+    }
+    if (m >= a.M) return;
+    double s[NE], pick[NE];
+    float bias[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) bias[i] = a.bias ? a.bias[min(lane + 64 * i, a.E - 1)] : 0.0f;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
         const int e = lane + 64 * i;
-        s[i] = e < a.E ? a.logits[m * a.E + e] : lowest;
-        top = s[i] > top ? s[i] : top;
+        if constexpr (WIDE) s[i] = e < a.E ? whole[e] : lowest;
+        else s[i] = e < a.E ? a.logits[m * a.E + e] : lowest;
     }
     if (a.score == FP8BLK_SCORE_SOFTMAX) {
-        for (int h = 32; h >= 1; h >>= 1) top = fmax(top, shfl_xor64(top, h));
-        double sum = 0.0;
+        double top = lowest, sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) top = s[i] > top ? s[i] : top;
+        top = reduce64(top, [](double p, double q) { return p > q ? p : q; });
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
             s[i] = exp(s[i] - top);
             sum += lane + 64 * i < a.E ? s[i] : 0.0;
         }
-        for (int h = 32; h >= 1; h >>= 1) sum += shfl_xor64(sum, h);
+        sum = reduce64(sum, [](double p, double q) { return p + q; });
 #pragma unroll
         for (int i = 0; i < NE; ++i) s[i] /= sum;
-    } else {
+    } else if (!WIDE) {
 #pragma unroll
-        for (int i = 0; i < NE; ++i)
-            s[i] = a.score == FP8BLK_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-s[i]))
-                                                   : sqrt(fmax(s[i], 0.0) + log1p(exp(-fabs(s[i]))));
+        for (int i = 0; i < NE; ++i) s[i] = own_score(a.score, s[i]);
     }
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
         const int e = lane + 64 * i;
-        pick[i] = e < a.E ? s[i] + (a.bias ? (double)a.bias[e] : 0.0) : lowest;
+        pick[i] = e < a.E ? s[i] + (double)bias[i] : lowest;
         if (!(pick[i] > lowest)) pick[i] = lowest;  // NaN: never chosen
     }
     double mine = 0.0, total = 0.0;  // lane k: the k-th choice's score
     int my_id = -1;
     for (int k = 0; k < a.K; ++k) {
         double best = lowest, score = 0.0;
-        int id = 0x7fffffff;
+        int id = FP8BLK_MAX_EXPERTS;
 #pragma unroll
         for (int i = 0; i < NE; ++i)
             if (pick[i] > best) best = pick[i], score = s[i], id = lane + 64 * i;
-        for (int h = 32; h >= 1; h >>= 1) {
-            const double b = shfl_xor64(best, h), sc = shfl_xor64(score, h);
-            const int j = __shfl_xor(id, h);
-            if (b > best || (b == best && j < id)) best = b, score = sc, id = j;
+        const double most = reduce64(best, [](double p, double q) { return p > q ? p : q; });
+        if (!(most > lowest)) break;  // nothing left
+        uint64_t who = __ballot(best == most);
+        int at = __builtin_ctzll(who), least = __builtin_amdgcn_readlane(id, at);
+        for (who &= who - 1; who; who &= who - 1) {  // a tie: the lowest index
+            const int l = __builtin_ctzll(who), other = __builtin_amdgcn_readlane(id, l);
+            if (other < least) least = other, at = l;
         }
-        const bool none = !(best > lowest);
+        const double p = lane_value64(score, at);
 #pragma unroll
         for (int i = 0; i < NE; ++i)
-            if (id == lane + 64 * i) pick[i] = lowest;
-        if (lane == k) mine = none ? 0.0 : score, my_id = none ? -1 : id;
-        total += none ? 0.0 : score;
+            if (least == lane + 64 * i) pick[i] = lowest;
+        if (lane == k) mine = p, my_id = least;
+        total += p;
     }
     if (lane < a.K) {
         if (a.normalize) mine = total > 0.0 ? mine / total : 0.0;
         a.ids[m * a.K + lane] = my_id;
         a.weights[m * a.K + lane] = (float)(mine * (double)a.scale);
     }
+}
+
+template <int NE>
+void choose(const RouteArgs& a, bool wide, hipStream_t s) {
+    if (wide) k_route_choose<NE, true><<<(unsigned)a.M, 256, 0, s>>>(a);
+    else k_route_choose<NE, false><<<(unsigned)ceil_div(a.M, 4), 256, 0, s>>>(a);
 }
 
 bool route_shape_ok(int64_t experts, int64_t cols, int64_t M) {
@@ -108,7 +316,8 @@ bool route_shape_ok(int64_t experts, int64_t cols, int64_t M) {
 
 size_t route_workspace_bytes(int64_t experts, int64_t cols, int64_t M) {
     if (!route_shape_ok(experts, cols, M)) return 0;
-    return (size_t)ceil_div(M * experts * (int64_t)sizeof(double), kRouteAlign) * kRouteAlign;
+    const int64_t n = M * experts * (route_split(experts, M) ? route_chunks(cols) : 1);
+    return (size_t)(ceil_div(n * (int64_t)sizeof(double), kRouteAlign) * kRouteAlign);
 }
 
 }  // namespace fp8blk
@@ -125,13 +334,22 @@ extern "C" int fp8blk_moe_route(const uint16_t* w_bf16, const float* bias, int64
         !aligned(ids, 4) || !aligned(weights, 4))
         return FP8BLK_ERR_ARG;
     if (!ws || !aligned(ws, kRouteAlign) || ws_bytes < route_workspace_bytes(experts, cols, M)) return FP8BLK_ERR_WORKSPACE;
-    double* logits = static_cast<double*>(ws);
+    RouteArgs a = {w_bf16, x_bf16, bias, static_cast<double*>(ws), ids, weights, (int32_t)experts, (int32_t)M, (int32_t)cols,
+                   top_k, score, normalize != 0, route_chunks(cols), scale};
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     (void)hipGetLastError();
-    k_route_logits<<<dim3((unsigned)experts, (unsigned)M), 64, 0, s>>>(w_bf16, x_bf16, (int)cols, (int)experts, logits);
-    const RouteArgs a = {bias, logits, ids, weights, (int32_t)experts, top_k, score, normalize != 0, scale};
-    if (experts <= 64) k_route_choose<1><<<(unsigned)M, 64, 0, s>>>(a);
-    else if (experts <= 256) k_route_choose<4><<<(unsigned)M, 64, 0, s>>>(a);
-    else k_route_choose<16><<<(unsigned)M, 64, 0, s>>>(a);
+    const bool split = route_split(experts, M);
+    const int64_t te = ceil_div(experts, kTile), tm = ceil_div(M, kTile);
+    if (split) {
+        k_route_logits<1, true><<<dim3((unsigned)te, (unsigned)tm, (unsigned)ceil_div(a.chunks, 4)), 256, 0, s>>>(a);
+    } else {
+        // two by two tiles a wave halve its reads, where that leaves two waves a SIMD
+        if (te * tm >= 2048) k_route_logits<2, false><<<dim3((unsigned)ceil_div(te, 2), (unsigned)ceil_div(tm, 2)), 256, 0, s>>>(a);
+        else k_route_logits<1, false><<<dim3((unsigned)te, (unsigned)tm), 256, 0, s>>>(a);
+    }
+    if (experts <= 64) choose<1>(a, split, s);
+    else if (experts <= 128) choose<2>(a, split, s);
+    else if (experts <= 256) choose<4>(a, split, s);
+    else choose<16>(a, split, s);
     return launch_status();
 }
