@@ -855,28 +855,37 @@ def fp4_expert_sequence(seq, stream=None, check=True):
 
 # --- around the linears: norms, router, expert layer, 4-bit linear ------------------
 
-class _On:
-    """The device and stream of one call: every tensor has to be on `device`,
-    and `stream` (or that device's current stream) belongs to it."""
+_kinds = None
 
-    def __init__(self, device, stream):
-        import torch
-        self.device = device
-        s = torch.cuda.current_stream(device) if stream is None else stream
-        if s.device_index != device:
-            raise ValueError(f"the stream belongs to device {s.device_index}, the tensors are on device {device}")
-        self.stream = s.cuda_stream
 
-    def __call__(self, fn, args, name, check):
+def _dtypes():
+    """(f32, bf16 patterns, bytes, i32), each a tuple of dtypes that are taken."""
+    global _kinds
+    if _kinds is None:
         import torch
-        if torch.cuda.current_device() == self.device:
-            st = fn(*args, self.stream)
-        else:
-            with torch.cuda.device(self.device):
-                st = fn(*args, self.stream)
-        if check and st != OK:
-            raise Fp8BlkError(st, name)
-        return st
+        _kinds = ((torch.float32,), _bf16_dtypes(), (torch.uint8,), (torch.int32,))
+    return _kinds
+
+
+def _enqueue(fn, device, args, stream, name, check):
+    """Call fn(*args, stream) on `device`, whose current stream is taken unless
+    one is named, which has to be that device's."""
+    from torch import _C
+    if stream is None:
+        raw = _C._cuda_getCurrentRawStream(device)
+    elif stream.device_index == device:
+        raw = stream.cuda_stream
+    else:
+        raise ValueError(f"the stream belongs to device {stream.device_index}, the tensors are on device {device}")
+    if _C._cuda_getDevice() == device:
+        st = fn(*args, raw)
+    else:
+        import torch
+        with torch.cuda.device(device):
+            st = fn(*args, raw)
+    if check and st != OK:
+        raise Fp8BlkError(st, name)
+    return st
 
 
 def _buf(t, device, dtypes, shape, name):
@@ -913,16 +922,15 @@ def _need(name, **tensors):
 def _workspace(ws, device):
     if ws is None:
         return None, 0
-    if ws.get_device() != device:
-        raise ValueError(f"ws must be on device {device}, it is on {ws.device}")
-    return _dev(ws, None, "ws"), ws.numel() * ws.element_size()
+    if ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous and on device {device}, it is on {ws.device}")
+    return ws.data_ptr(), ws.nbytes
 
 
 def _block_norm_args(resid, y, post_w, gate, scale, resid_out, pre_w, eps, x_next):
-    import torch
     dev, N, cols = _matrix(resid, "resid")
-    f32, bf16 = (torch.float32,), _bf16_dtypes()
-    if resid.dtype is torch.float32:
+    f32, bf16, _, _ = _dtypes()
+    if resid.dtype in f32:
         kind, types = TYPE_F32, f32
     else:
         kind, types = TYPE_BF16, bf16
@@ -947,19 +955,18 @@ def fp8blk_block_norm(resid, y, post_w, gate, scale, resid_out, pre_w, eps, x_ne
     None for what is left out: post_w (no norm of y), gate, y with post_w, gate
     and resid_out (only the norm of resid), pre_w with x_next (only the sum)."""
     dev, args = _block_norm_args(resid, y, post_w, gate, scale, resid_out, pre_w, eps, x_next)
-    return _On(dev, stream)(load().fp8blk_block_norm, args, "fp8blk_block_norm", check)
+    return _enqueue(load().fp8blk_block_norm, dev, args, stream, "fp8blk_block_norm", check)
 
 
 def _moe_route_args(w_bf16, bias, x_bf16, score, normalize, scale, ids, weights, ws):
-    import torch
     dev, E, cols = _matrix(w_bf16, "w_bf16")
     _, M, K = _matrix(ids, "ids")
-    bf16, f32 = _bf16_dtypes(), (torch.float32,)
+    f32, bf16, _, i32 = _dtypes()
     _need("fp8blk_moe_route", x_bf16=x_bf16, weights=weights)
     wsp, wsb = _workspace(ws, dev)
     return dev, (_buf(w_bf16, dev, bf16, (E, cols), "w_bf16"), _buf(bias, dev, f32, (E,), "bias"), E, cols,
                  _buf(x_bf16, dev, bf16, (M, cols), "x_bf16"), M, score, K, bool(normalize), scale,
-                 _buf(ids, dev, (torch.int32,), (M, K), "ids"), _buf(weights, dev, f32, (M, K), "weights"), wsp, wsb)
+                 _buf(ids, dev, i32, (M, K), "ids"), _buf(weights, dev, f32, (M, K), "weights"), wsp, wsb)
 
 
 def fp8blk_moe_route(w_bf16, bias, x_bf16, score, normalize, scale, ids, weights, ws, stream=None, check=True):
@@ -968,7 +975,7 @@ def fp8blk_moe_route(w_bf16, bias, x_bf16, score, normalize, scale, ids, weights
     score + bias (f32 [experts] or None), weighted by score. ws:
     fp8blk_workspace_bytes(OP_MOE_ROUTE, experts, cols, M) bytes."""
     dev, args = _moe_route_args(w_bf16, bias, x_bf16, score, normalize, scale, ids, weights, ws)
-    return _On(dev, stream)(load().fp8blk_moe_route, args, "fp8blk_moe_route", check)
+    return _enqueue(load().fp8blk_moe_route, dev, args, stream, "fp8blk_moe_route", check)
 
 
 class MoeLayer:
@@ -999,7 +1006,7 @@ def fp4_moe_weights(fmt, gate, gate_scales, gate_global, up, up_scales, up_globa
         if t.dim() != 3:
             raise ValueError(f"{name} must be [experts, rows, cols/2], got shape {tuple(t.shape)}")
     E, inter, hidden, dev = gate.shape[0], gate.shape[1], 2 * gate.shape[2], gate.get_device()
-    u8, f32 = (torch.uint8,), (torch.float32,)
+    f32, _, u8, _ = _dtypes()
     _need("fp4_moe_weights", gate_scales=gate_scales, up=up, up_scales=up_scales, down_scales=down_scales)
     h = Fp4MoeLayer(experts=E, hidden=hidden, inter=inter, fmt=fmt, limit=limit)
     for name, codes, scales, top, rows, cols in (("gate", gate, gate_scales, gate_global, inter, hidden),
@@ -1016,15 +1023,15 @@ def fp4_moe_bytes(inter: int, M: int, top_k: int) -> int:
 
 
 def _moe_args(layer, x_bf16, ids, weights, base, y, ws):
-    import torch
     dev, M, K = _matrix(ids, "ids")
     if dev != layer.device:
         raise ValueError(f"ids must be on the layer's device {layer.device}, they are on {dev}")
-    f32, panel = (torch.float32,), (M, layer.hidden)
+    f32, bf16, _, i32 = _dtypes()
+    panel = (M, layer.hidden)
     _need("fp4_moe", x_bf16=x_bf16, weights=weights, y=y)
     wsp, wsb = _workspace(ws, dev)
-    return dev, (ctypes.byref(layer.handle), _buf(x_bf16, dev, _bf16_dtypes(), panel, "x_bf16"), M,
-                 _buf(ids, dev, (torch.int32,), (M, K), "ids"), _buf(weights, dev, f32, (M, K), "weights"), K,
+    return dev, (ctypes.byref(layer.handle), _buf(x_bf16, dev, bf16, panel, "x_bf16"), M,
+                 _buf(ids, dev, i32, (M, K), "ids"), _buf(weights, dev, f32, (M, K), "weights"), K,
                  _buf(base, dev, f32, panel, "base"), _buf(y, dev, f32, panel, "y"), wsp, wsb)
 
 
@@ -1034,21 +1041,20 @@ def fp4_moe(layer, x_bf16, ids, weights, base, y, ws, stream=None, check=True):
     weights f32 [M, K] as fp8blk_moe_route writes them. ws:
     fp4_moe_bytes(inter, M, K) bytes."""
     dev, args = _moe_args(layer, x_bf16, ids, weights, base, y, ws)
-    return _On(dev, stream)(load().fp4_moe, args, "fp4_moe", check)
+    return _enqueue(load().fp4_moe, dev, args, stream, "fp4_moe", check)
 
 
 def _int4_args(codes, scales_bf16, zeros, group, x_bf16, y):
-    import torch
     dev, rows, half = _matrix(codes, "codes")
     _, M, cols = _matrix(x_bf16, "x_bf16")
-    u8, bf16 = (torch.uint8,), _bf16_dtypes()
+    f32, bf16, u8, _ = _dtypes()
     if cols != 2 * half:
         raise ValueError(f"x_bf16 must be [M, cols={2 * half}], got shape {tuple(x_bf16.shape)}")
     _need("int4_gemv", scales_bf16=scales_bf16, y=y)
     grid = (rows, cols // group if group in (32, 64, 128) else 0)
     return dev, (_buf(codes, dev, u8, (rows, half), "codes"), _buf(scales_bf16, dev, bf16, grid, "scales_bf16"),
                  _buf(zeros, dev, u8, grid, "zeros"), group, rows, cols, _buf(x_bf16, dev, bf16, (M, cols), "x_bf16"), M,
-                 _buf(y, dev, (torch.float32,), (M, rows), "y"))
+                 _buf(y, dev, f32, (M, rows), "y"))
 
 
 def int4_gemv(codes, scales_bf16, zeros, group, x_bf16, y, stream=None, check=True):
@@ -1056,7 +1062,7 @@ def int4_gemv(codes, scales_bf16, zeros, group, x_bf16, y, stream=None, check=Tr
     q [rows, cols/2], bf16 scales and uint8 zero points (None: 8) [rows,
     cols/group], group 32, 64 or 128."""
     dev, args = _int4_args(codes, scales_bf16, zeros, group, x_bf16, y)
-    return _On(dev, stream)(load().int4_gemv, args, "int4_gemv", check)
+    return _enqueue(load().int4_gemv, dev, args, stream, "int4_gemv", check)
 
 
 def raw_call(name: str, *args):
@@ -1082,8 +1088,8 @@ def prepared(name: str, *tensors_and_sizes, stream=None):
               "int4_gemv": _int4_args}.get(name)
     if around is not None:
         dev, args = around(*tensors_and_sizes)
-        on = _On(dev, stream)
-        return lambda: on(fn, args, name, False)
+        stream = torch.cuda.current_stream(dev) if stream is None else stream
+        return lambda: _enqueue(fn, dev, args, stream, name, False)
     s = _stream(stream)
     if name == "fp8blk_gemv":
         codes, grid, x, y = tensors_and_sizes
