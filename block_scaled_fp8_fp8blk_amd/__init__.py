@@ -855,22 +855,22 @@ def fp4_expert_sequence(seq, stream=None, check=True):
 
 # --- around the linears: norms, router, expert layer, 4-bit linear ------------------
 
-_kinds = None
+_torch = None
 
 
-def _dtypes():
-    """(f32, bf16 patterns, bytes, i32), each a tuple of dtypes that are taken."""
-    global _kinds
-    if _kinds is None:
-        import torch
-        _kinds = ((torch.float32,), _bf16_dtypes(), (torch.uint8,), (torch.int32,))
-    return _kinds
+def _load_torch():
+    """What the calls below look up of torch, once: these launches take a few
+    microseconds, and imports and tuples inside them would be a good part."""
+    global _torch, _C, _f32, _bf16, _u8, _i32
+    import torch
+    from torch import _C
+    _f32, _bf16, _u8, _i32 = (torch.float32,), _bf16_dtypes(), (torch.uint8,), (torch.int32,)
+    _torch = torch
 
 
 def _enqueue(fn, device, args, stream, name, check):
     """Call fn(*args, stream) on `device`, whose current stream is taken unless
     one is named, which has to be that device's."""
-    from torch import _C
     if stream is None:
         raw = _C._cuda_getCurrentRawStream(device)
     elif stream.device_index == device:
@@ -880,18 +880,20 @@ def _enqueue(fn, device, args, stream, name, check):
     if _C._cuda_getDevice() == device:
         st = fn(*args, raw)
     else:
-        import torch
-        with torch.cuda.device(device):
+        with _torch.cuda.device(device):
             st = fn(*args, raw)
-    if check and st != OK:
+    if st and check:
         raise Fp8BlkError(st, name)
     return st
 
 
-def _buf(t, device, dtypes, shape, name):
-    """Pointer of a contiguous tensor on `device` that has this shape; None stays None."""
-    if t is None:
+def _buf(t, device, dtypes, shape, name, need=True):
+    """Pointer of a contiguous tensor on `device` that has this shape; None,
+    where that may be."""
+    if t is None and not need:
         return None
+    if t is None:
+        raise ValueError(f"{name} is needed")
     if t.get_device() != device:
         raise ValueError(f"{name} must be on device {device}, it is on {t.device}")
     if t.dtype not in dtypes:
@@ -905,18 +907,13 @@ def _buf(t, device, dtypes, shape, name):
 
 def _matrix(t, name):
     """Device and the two sizes of a matrix that is on a GPU."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if _torch is None:
+        _load_torch()
+    if not isinstance(t, _torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, got shape {tuple(t.shape)}")
     return (t.get_device(), *t.shape)
-
-
-def _need(name, **tensors):
-    for k, t in tensors.items():
-        if t is None:
-            raise ValueError(f"{name}: {k} is needed")
 
 
 def _workspace(ws, device):
@@ -929,22 +926,21 @@ def _workspace(ws, device):
 
 def _block_norm_args(resid, y, post_w, gate, scale, resid_out, pre_w, eps, x_next):
     dev, N, cols = _matrix(resid, "resid")
-    f32, bf16, _, _ = _dtypes()
-    if resid.dtype in f32:
-        kind, types = TYPE_F32, f32
-    else:
-        kind, types = TYPE_BF16, bf16
+    kind, types = (TYPE_F32, _f32) if resid.dtype in _f32 else (TYPE_BF16, _bf16)
     panel, row = (N, cols), (cols,)
-    gate_rows = 0
+    gate_rows, gate_shape = 0, None
     if gate is not None:
-        gate_rows = gate.shape[0] if gate.dim() == 2 else 1
-        if gate_rows not in (1, N):
-            raise ValueError(f"gate must be [cols], [1, cols] or [N, cols], got shape {tuple(gate.shape)}")
-    gate_shape = row if gate is not None and gate.dim() == 1 else (gate_rows, cols)
-    return dev, (_buf(resid, dev, types, panel, "resid"), kind, _buf(y, dev, f32, panel, "y"), N, cols,
-                 _buf(post_w, dev, bf16, row, "post_w"), _buf(gate, dev, bf16, gate_shape, "gate"), gate_rows, scale,
-                 _buf(resid_out, dev, types, panel, "resid_out"), _buf(pre_w, dev, bf16, row, "pre_w"), eps,
-                 _buf(x_next, dev, bf16, panel, "x_next"))
+        gate_shape = gate.shape
+        if gate_shape == row:
+            gate_rows = 1
+        elif gate_shape == panel or gate_shape == (1, cols):
+            gate_rows = gate_shape[0]
+        else:
+            raise ValueError(f"gate must be [cols], [1, cols] or [N, cols], got shape {tuple(gate_shape)}")
+    return dev, (_buf(resid, dev, types, panel, "resid"), kind, _buf(y, dev, _f32, panel, "y", False), N, cols,
+                 _buf(post_w, dev, _bf16, row, "post_w", False), _buf(gate, dev, _bf16, gate_shape, "gate", False), gate_rows,
+                 scale, _buf(resid_out, dev, types, panel, "resid_out", False),
+                 _buf(pre_w, dev, _bf16, row, "pre_w", False), eps, _buf(x_next, dev, _bf16, panel, "x_next", False))
 
 
 def fp8blk_block_norm(resid, y, post_w, gate, scale, resid_out, pre_w, eps, x_next, stream=None, check=True):
@@ -961,12 +957,10 @@ def fp8blk_block_norm(resid, y, post_w, gate, scale, resid_out, pre_w, eps, x_ne
 def _moe_route_args(w_bf16, bias, x_bf16, score, normalize, scale, ids, weights, ws):
     dev, E, cols = _matrix(w_bf16, "w_bf16")
     _, M, K = _matrix(ids, "ids")
-    f32, bf16, _, i32 = _dtypes()
-    _need("fp8blk_moe_route", x_bf16=x_bf16, weights=weights)
     wsp, wsb = _workspace(ws, dev)
-    return dev, (_buf(w_bf16, dev, bf16, (E, cols), "w_bf16"), _buf(bias, dev, f32, (E,), "bias"), E, cols,
-                 _buf(x_bf16, dev, bf16, (M, cols), "x_bf16"), M, score, K, bool(normalize), scale,
-                 _buf(ids, dev, i32, (M, K), "ids"), _buf(weights, dev, f32, (M, K), "weights"), wsp, wsb)
+    return dev, (_buf(w_bf16, dev, _bf16, (E, cols), "w_bf16"), _buf(bias, dev, _f32, (E,), "bias", False), E, cols,
+                 _buf(x_bf16, dev, _bf16, (M, cols), "x_bf16"), M, score, K, 1 if normalize else 0, scale,
+                 _buf(ids, dev, _i32, (M, K), "ids"), _buf(weights, dev, _f32, (M, K), "weights"), wsp, wsb)
 
 
 def fp8blk_moe_route(w_bf16, bias, x_bf16, score, normalize, scale, ids, weights, ws, stream=None, check=True):
@@ -984,6 +978,7 @@ class MoeLayer:
 
     def __init__(self, handle, device, keep):
         self.handle = handle
+        self.pointer = ctypes.byref(handle)
         self.device = device
         self.keep = keep
         self.hidden, self.inter = handle.hidden, handle.inter
@@ -996,25 +991,23 @@ def fp4_moe_weights(fmt, gate, gate_scales, gate_global, up, up_scales, up_globa
     /B in place of /2 (B = 32 for FMT_MXFP4, 16 for FMT_NVFP4), global scales
     f32 [experts] or None; limit > 0 clamps gate and up. Checked here, once;
     the tensors must stay as they are while the layer is used."""
-    import torch
+    _load_torch()
     B = {FMT_MXFP4: 32, FMT_NVFP4: 16}.get(fmt)
     if B is None:
         raise ValueError(f"fmt {fmt} is not FMT_MXFP4 or FMT_NVFP4")
     for name, t in (("gate", gate), ("down", down)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        if not isinstance(t, _torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
         if t.dim() != 3:
             raise ValueError(f"{name} must be [experts, rows, cols/2], got shape {tuple(t.shape)}")
     E, inter, hidden, dev = gate.shape[0], gate.shape[1], 2 * gate.shape[2], gate.get_device()
-    f32, _, u8, _ = _dtypes()
-    _need("fp4_moe_weights", gate_scales=gate_scales, up=up, up_scales=up_scales, down_scales=down_scales)
     h = Fp4MoeLayer(experts=E, hidden=hidden, inter=inter, fmt=fmt, limit=limit)
     for name, codes, scales, top, rows, cols in (("gate", gate, gate_scales, gate_global, inter, hidden),
                                                  ("up", up, up_scales, up_global, inter, hidden),
                                                  ("down", down, down_scales, down_global, hidden, inter)):
-        setattr(h, name, _buf(codes, dev, u8, (E, rows, cols // 2), name))
-        setattr(h, name + "_scales", _buf(scales, dev, u8, (E, rows, cols // B), name + "_scales"))
-        setattr(h, name + "_global", _buf(top, dev, f32, (E,), name + "_global"))
+        setattr(h, name, _buf(codes, dev, _u8, (E, rows, cols // 2), name))
+        setattr(h, name + "_scales", _buf(scales, dev, _u8, (E, rows, cols // B), name + "_scales"))
+        setattr(h, name + "_global", _buf(top, dev, _f32, (E,), name + "_global", False))
     return MoeLayer(h, dev, (gate, gate_scales, gate_global, up, up_scales, up_global, down, down_scales, down_global))
 
 
@@ -1026,13 +1019,11 @@ def _moe_args(layer, x_bf16, ids, weights, base, y, ws):
     dev, M, K = _matrix(ids, "ids")
     if dev != layer.device:
         raise ValueError(f"ids must be on the layer's device {layer.device}, they are on {dev}")
-    f32, bf16, _, i32 = _dtypes()
     panel = (M, layer.hidden)
-    _need("fp4_moe", x_bf16=x_bf16, weights=weights, y=y)
     wsp, wsb = _workspace(ws, dev)
-    return dev, (ctypes.byref(layer.handle), _buf(x_bf16, dev, bf16, panel, "x_bf16"), M,
-                 _buf(ids, dev, i32, (M, K), "ids"), _buf(weights, dev, f32, (M, K), "weights"), K,
-                 _buf(base, dev, f32, panel, "base"), _buf(y, dev, f32, panel, "y"), wsp, wsb)
+    return dev, (layer.pointer, _buf(x_bf16, dev, _bf16, panel, "x_bf16"), M, _buf(ids, dev, _i32, (M, K), "ids"),
+                 _buf(weights, dev, _f32, (M, K), "weights"), K, _buf(base, dev, _f32, panel, "base", False),
+                 _buf(y, dev, _f32, panel, "y"), wsp, wsb)
 
 
 def fp4_moe(layer, x_bf16, ids, weights, base, y, ws, stream=None, check=True):
@@ -1047,14 +1038,12 @@ def fp4_moe(layer, x_bf16, ids, weights, base, y, ws, stream=None, check=True):
 def _int4_args(codes, scales_bf16, zeros, group, x_bf16, y):
     dev, rows, half = _matrix(codes, "codes")
     _, M, cols = _matrix(x_bf16, "x_bf16")
-    f32, bf16, u8, _ = _dtypes()
     if cols != 2 * half:
         raise ValueError(f"x_bf16 must be [M, cols={2 * half}], got shape {tuple(x_bf16.shape)}")
-    _need("int4_gemv", scales_bf16=scales_bf16, y=y)
-    grid = (rows, cols // group if group in (32, 64, 128) else 0)
-    return dev, (_buf(codes, dev, u8, (rows, half), "codes"), _buf(scales_bf16, dev, bf16, grid, "scales_bf16"),
-                 _buf(zeros, dev, u8, grid, "zeros"), group, rows, cols, _buf(x_bf16, dev, bf16, (M, cols), "x_bf16"), M,
-                 _buf(y, dev, f32, (M, rows), "y"))
+    grid = (rows, cols // group if group > 0 else 0)
+    return dev, (_buf(codes, dev, _u8, (rows, half), "codes"), _buf(scales_bf16, dev, _bf16, grid, "scales_bf16"),
+                 _buf(zeros, dev, _u8, grid, "zeros", False), group, rows, cols,
+                 _buf(x_bf16, dev, _bf16, (M, cols), "x_bf16"), M, _buf(y, dev, _f32, (M, rows), "y"))
 
 
 def int4_gemv(codes, scales_bf16, zeros, group, x_bf16, y, stream=None, check=True):

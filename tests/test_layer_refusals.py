@@ -151,7 +151,9 @@ class _Gpu0:
 def test_binding_checks_a_buffer():
     t = _Gpu0((2, 32), torch.float32)
     f32 = (torch.float32,)
-    assert fb._buf(None, 0, f32, (2, 32), "t") is None and fb._buf(t, 0, f32, (2, 32), "t") == P
+    assert fb._buf(None, 0, f32, (2, 32), "t", False) is None and fb._buf(t, 0, f32, (2, 32), "t") == P
+    with pytest.raises(ValueError, match="needed"):
+        fb._buf(None, 0, f32, (2, 32), "t")
     with pytest.raises(ValueError, match="device 1"):
         fb._buf(t, 1, f32, (2, 32), "t")
     with pytest.raises(TypeError, match="dtype"):
