@@ -193,6 +193,25 @@ __device__ __forceinline__ double reduce64(double v, F f) {
     return v;
 }
 
+// Largest of one value per lane, the same in every lane.
+__device__ __forceinline__ uint32_t most_of_wave(uint32_t v) {
+    const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = max(a[0], a[1]);
+    const auto b = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max(b[0], b[1]);
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kRowRor8, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kRowRor4, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kQuadXor2, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kQuadXor1, 0xF, 0xF, false));
+    return v;
+}
+
+// A number as an unsigned one that orders the same way, never 0.
+__device__ __forceinline__ uint64_t rank_of(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0);  // -0 as 0
+    return u >> 63 ? ~u : u | 0x8000000000000000ull;
+}
+
 __device__ __forceinline__ double lane_value64(double v, int lane) {
     const uint64_t u = __builtin_bit_cast(uint64_t, v);
     const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
@@ -239,7 +258,8 @@ __global__ __launch_bounds__(256) void k_route_choose(RouteArgs a) {
         if (threadIdx.x >= 64) return;
     }
     if (m >= a.M) return;
-    double s[NE], pick[NE];
+    double s[NE];
+    uint64_t pick[NE];  // ranks; 0: not to be chosen
     float bias[NE];
 #pragma unroll
     for (int i = 0; i < NE; ++i) bias[i] = a.bias ? a.bias[min(lane + 64 * i, a.E - 1)] : 0.0f;
@@ -268,21 +288,25 @@ __global__ __launch_bounds__(256) void k_route_choose(RouteArgs a) {
     }
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-        const int e = lane + 64 * i;
-        pick[i] = e < a.E ? s[i] + (double)bias[i] : lowest;
-        if (!(pick[i] > lowest)) pick[i] = lowest;  // NaN: never chosen
+        const double c = s[i] + (double)bias[i];
+        pick[i] = lane + 64 * i < a.E && c > lowest ? rank_of(c) : 0;  // NaN and -inf: never chosen
     }
     double mine = 0.0, total = 0.0;  // lane k: the k-th choice's score
     int my_id = -1;
     for (int k = 0; k < a.K; ++k) {
-        double best = lowest, score = 0.0;
+        uint64_t best = 0;
+        double score = 0.0;
         int id = FP8BLK_MAX_EXPERTS;
 #pragma unroll
         for (int i = 0; i < NE; ++i)
             if (pick[i] > best) best = pick[i], score = s[i], id = lane + 64 * i;
-        const double most = reduce64(best, [](double p, double q) { return p > q ? p : q; });
-        if (!(most > lowest)) break;  // nothing left
-        uint64_t who = __ballot(best == most);
+        const uint32_t hi = (uint32_t)(best >> 32), most = most_of_wave(hi);
+        if (most == 0) break;  // nothing left
+        uint64_t who = __ballot(hi == most);
+        if (who & (who - 1)) {  // the high halves do not tell
+            const uint32_t lo = hi == most ? (uint32_t)best : 0;
+            who &= __ballot(lo == most_of_wave(lo));
+        }
         int at = __builtin_ctzll(who), least = __builtin_amdgcn_readlane(id, at);
         for (who &= who - 1; who; who &= who - 1) {  // a tie: the lowest index
             const int l = __builtin_ctzll(who), other = __builtin_amdgcn_readlane(id, l);
@@ -291,7 +315,7 @@ __global__ __launch_bounds__(256) void k_route_choose(RouteArgs a) {
         const double p = lane_value64(score, at);
 #pragma unroll
         for (int i = 0; i < NE; ++i)
-            if (least == lane + 64 * i) pick[i] = lowest;
+            if (least == lane + 64 * i) pick[i] = 0;
         if (lane == k) mine = p, my_id = least;
         total += p;
     }
