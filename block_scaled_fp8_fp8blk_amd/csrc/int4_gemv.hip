@@ -115,15 +115,16 @@ __device__ __forceinline__ void load_groups(Groups<N>& g, const uint16_t* s, con
     }
 }
 
-// One wave's loads of a tile's 512 columns.
-template <int G>
+// One wave's loads of a tile's 512 columns; WIDE: without the scales, which
+// come as a block (below).
+template <int G, bool WIDE>
 struct Load {
     uint4 q[kSteps];
-    Groups<kSuper / G> g;
+    Groups<WIDE ? 2 : kSuper / G> g;
 };
 
-template <int G, bool ZERO>
-__device__ __forceinline__ void issue(Load<G>& b, const Int4Args& a, const uint8_t* lo, const uint8_t* hi, int64_t row,
+template <int G, bool ZERO, bool WIDE>
+__device__ __forceinline__ void issue(Load<G, WIDE>& b, const Int4Args& a, const uint8_t* lo, const uint8_t* hi, int64_t row,
                                       int lane, int c0) {
 #pragma unroll
     for (int s = 0; s < kSteps; s += 2) {  // columns past the end meet zeros of the panel: any code will do
@@ -131,13 +132,66 @@ __device__ __forceinline__ void issue(Load<G>& b, const Int4Args& a, const uint8
         b.q[s] = load_stream16(lo + c);
         b.q[s + 1] = load_stream16(hi + c);
     }
-    const int64_t g = row * (a.cols / G) + c0 / G;
-    load_groups<kSuper / G, ZERO>(b.g, a.scales + g, ZERO ? a.zeros + g : nullptr, (a.cols - c0) / G);
+    if constexpr (!WIDE) {
+        const int64_t g = row * (a.cols / G) + c0 / G;
+        load_groups<kSuper / G, ZERO>(b.g, a.scales + g, ZERO ? a.zeros + g : nullptr, (a.cols - c0) / G);
+    }
+}
+
+// The scales and zero points of 32 groups of a tile's 16 rows, 64 and 32 bytes
+// a row. Read row by row where they are used, they would ask for 16 lines with
+// every load, and for each line many times; so a wave reads a block as it lies
+// and hands it out through its own part of LDS.
+constexpr int kBlockGroups = 32, kBlockScales = 16 * 2 * kBlockGroups, kBlockBytes = kBlockScales + 16 * kBlockGroups;
+struct Block {
+    uint32_t s[4], z[2];  // lane: 8 groups of row lane / 4
+};
+
+template <int N>
+__device__ __forceinline__ void load_inside(uint32_t* d, const uint8_t* p, int64_t at, int64_t end) {
+    if (at + 4 * N <= end) {
+        __builtin_memcpy(d, p + at, 4 * N);
+    } else {  // across the array's end: its last dword, shifted
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int64_t from = min(at + 4 * k, end - 4);
+            uint32_t v;
+            __builtin_memcpy(&v, p + from, 4);
+            d[k] = v >> (8 * (int)(at + 4 * k - from) & 31);
+        }
+    }
+}
+
+template <bool ZERO>
+__device__ __forceinline__ void issue_block(Block& b, const Int4Args& a, int groups, int64_t row0, int lane, int first) {
+    const int64_t at = min(row0 + (lane >> 2), a.rows - 1) * groups + first + 8 * (lane & 3), end = a.rows * groups;
+    load_inside<4>(b.s, reinterpret_cast<const uint8_t*>(a.scales), 2 * at, 2 * end);
+    if constexpr (ZERO) load_inside<2>(b.z, a.zeros, at, end);
+}
+
+// Zeros past the row's last group, whose neighbours are another row's.
+template <bool ZERO>
+__device__ __forceinline__ void place_block(const Block& b, uint8_t* to, int groups, int lane, int first) {
+    const int left = groups - first - 8 * (lane & 3);
+    uint32_t s[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[k] = left >= 2 * k + 2 ? b.s[k] : left == 2 * k + 1 ? b.s[k] & 0xFFFFu : 0;
+    *reinterpret_cast<uint4*>(to + 16 * lane) = make_uint4(s[0], s[1], s[2], s[3]);
+    if constexpr (ZERO) *reinterpret_cast<uint2*>(to + kBlockScales + 8 * lane) = make_uint2(b.z[0], b.z[1]);
 }
 
 // acc += the 512 columns of b times the panel's columns from x on (LDS).
-template <int G, bool ZERO, int NI>
-__device__ __forceinline__ void compute(Load<G>& b, const uint4* x, const float* xsum, float (&acc)[NI]) {
+template <int G, bool ZERO, int NI, bool WIDE>
+__device__ __forceinline__ void compute(Load<G, WIDE>& b, const uint4* x, const float* xsum, const uint8_t* sb, const uint8_t* zb,
+                                        float (&acc)[NI]) {
+    constexpr int N = kSuper / G;
+    Groups<N> gr;
+    if constexpr (WIDE) {  // the lane's row of the block, from these columns' groups on
+        __builtin_memcpy(gr.s, __builtin_assume_aligned(sb, 8), 2 * N);
+        if constexpr (ZERO) __builtin_memcpy(gr.z, __builtin_assume_aligned(zb, 4), N);
+    } else {
+        gr = b.g;
+    }
     constexpr int per_step = kStep / G;  // groups of a step
     constexpr int per_group = 4 / per_step;
 #pragma unroll
@@ -159,9 +213,9 @@ __device__ __forceinline__ void compute(Load<G>& b, const uint4* x, const float*
                 D = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, codes_bf16(d[j]), D, 0, 0, 0);
             }
             const int i = s * per_step + g;
-            const uint32_t sc = b.g.s[i / 2];
+            const uint32_t sc = gr.s[i / 2];
             const float scale = as_f32(i % 2 ? sc & 0xFFFF0000u : sc << 16);
-            const float zero = ZERO ? (float)((b.g.z[i / 4] >> (8 * (i % 4))) & 0xFFu) : 8.0f;
+            const float zero = ZERO ? (float)((gr.z[i / 4] >> (8 * (i % 4))) & 0xFFu) : 8.0f;
 #pragma unroll
             for (int k = 0; k < NI; ++k)
                 acc[k] = __builtin_fmaf(scale, __builtin_fmaf(-zero, xsum[i * 4 * NI + k], D[k]), acc[k]);
@@ -172,7 +226,7 @@ __device__ __forceinline__ void compute(Load<G>& b, const uint4* x, const float*
 // NI: registers of a result tile that hold tokens. The instruction's operand
 // row n carries token 4 (n % NI) + n / 4 (rows repeat where NI < 4), so that
 // token t ends in register t / 4 of lane group t % 4.
-template <int G, bool ZERO, int NI>
+template <int G, bool ZERO, int NI, bool WIDE>
 __global__ __launch_bounds__(1024) void k_int4(Int4Args a) {
     extern __shared__ uint4 lds[];  // the panel's piece: [step][j][lane group][token]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
@@ -183,6 +237,14 @@ __global__ __launch_bounds__(1024) void k_int4(Int4Args a) {
     float* const xsums = reinterpret_cast<float*>(lds + a.piece / 8 * 4 * NI);  // [group][lane group][NI]
     float* const sums = xsums + a.piece / G * 4 * NI;
     const float* xsum = xsums + kg * NI;
+    // WIDE (split == 1): the wave's block of scales
+    uint8_t* const block = reinterpret_cast<uint8_t*>(sums) + wave * kBlockBytes;
+    constexpr int SPAN = kBlockGroups * G;  // its columns
+    const int groups = a.cols / G;
+    Block next;
+    if constexpr (WIDE)
+        if ((int64_t)blockIdx.x * across + side < tiles)
+            issue_block<ZERO>(next, a, groups, ((int64_t)blockIdx.x * across + side) * kTile, lane, 0);
     const int pieces = (a.cols + a.piece - 1) / a.piece;
 
     auto stage = [&](int p0, int cols) {
@@ -217,8 +279,8 @@ __global__ __launch_bounds__(1024) void k_int4(Int4Args a) {
         for (int p = 0; p < pieces; ++p) {
             const int p0 = p * a.piece, p1 = min(p0 + a.piece, a.cols);
             int c0 = p0 + part * kSuper;
-            Load<G> A, B;
-            if (c0 < p1) issue<G, ZERO>(A, a, lo, hi, row, lane, c0);
+            Load<G, WIDE> A, B;
+            if (c0 < p1) issue<G, ZERO, WIDE>(A, a, lo, hi, row, lane, c0);
             if (pieces > 1 || first == (int64_t)blockIdx.x * across) {
                 if (pieces > 1) __syncthreads();
                 stage(p0, (p1 - p0 + kSuper - 1) / kSuper * kSuper);
@@ -227,15 +289,29 @@ __global__ __launch_bounds__(1024) void k_int4(Int4Args a) {
             const int stride = a.split * kSuper;
             while (c0 < p1) {
                 const int c1 = c0 + stride;
-                if (c1 < p1) issue<G, ZERO>(B, a, lo, hi, row, lane, c1);
-                compute<G, ZERO, NI>(A, x + (c0 - p0) / 8 * 4 * NI, xsum + (c0 - p0) / G * 4 * NI, acc);
+                if (c1 < p1) issue<G, ZERO, WIDE>(B, a, lo, hi, row, lane, c1);
+                if constexpr (WIDE)
+                    if (c0 % SPAN == 0) {  // the next block: this row's, or the next tile's first
+                        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                        __builtin_amdgcn_wave_barrier();
+                        place_block<ZERO>(next, block, groups, lane, c0 / G);
+                        const bool more = c0 + SPAN < a.cols;
+                        const int64_t t = more ? tile : tile + (int64_t)gridDim.x * across;
+                        if (t < tiles) issue_block<ZERO>(next, a, groups, t * kTile, lane, more ? (c0 + SPAN) / G : 0);
+                        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                        __builtin_amdgcn_wave_barrier();
+                    }
+                const uint8_t *sb = block + n * 2 * kBlockGroups, *zb = block + kBlockScales + n * kBlockGroups;
+                compute<G, ZERO, NI, WIDE>(A, x + (c0 - p0) / 8 * 4 * NI, xsum + (c0 - p0) / G * 4 * NI, sb + c0 % SPAN / G * 2,
+                                           zb + c0 % SPAN / G, acc);
                 if (c1 >= p1) break;
                 c0 = c1 + stride;
-                if (c0 < p1) issue<G, ZERO>(A, a, lo, hi, row, lane, c0);
-                compute<G, ZERO, NI>(B, x + (c1 - p0) / 8 * 4 * NI, xsum + (c1 - p0) / G * 4 * NI, acc);
+                if (c0 < p1) issue<G, ZERO, WIDE>(A, a, lo, hi, row, lane, c0);
+                compute<G, ZERO, NI, WIDE>(B, x + (c1 - p0) / 8 * 4 * NI, xsum + (c1 - p0) / G * 4 * NI, sb + c1 % SPAN / G * 2,
+                                           zb + c1 % SPAN / G, acc);
             }
         }
-        if (a.split > 1) {
+        if (!WIDE && a.split > 1) {
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < NI; ++i) sums[(wave * NI + i) * 64 + lane] = acc[i];
@@ -367,11 +443,13 @@ void launch(Int4Args a, int cus, hipStream_t s) {
     a.split = p.split;
     const int64_t padded = (int64_t)supers * kSuper, most = kPanelBytes / (8 * NI);
     a.piece = (int)(padded < most ? padded : most);
+    const int waves = p.split * p.across;
     const size_t lds = (size_t)a.piece * 8 * NI + (size_t)(a.piece / G) * 16 * NI +
-                       (p.split > 1 ? (size_t)p.split * p.across * NI * 256 : 0);
+                       (p.split > 1 ? (size_t)waves * NI * 256 : (size_t)waves * kBlockBytes);
     const int64_t groups = ceil_div(tiles, p.across);
     const int grid = (int)(groups < cus ? groups : cus);
-    k_int4<G, ZERO, NI><<<grid, 64 * p.split * p.across, lds, s>>>(a);
+    if (p.split > 1) k_int4<G, ZERO, NI, false><<<grid, 64 * waves, lds, s>>>(a);
+    else k_int4<G, ZERO, NI, true><<<grid, 64 * waves, lds, s>>>(a);
 }
 
 template <int G, bool ZERO>

@@ -44,7 +44,24 @@ def test_odd_numbers_of_groups(gpu, cols):
     assert_within(_run(gpu, *c), *int4(*c), f"g64 cols={2 * cols}")
 
 
-@pytest.mark.parametrize("rows,cols", [(100, 2080), (4096, 4096), (700, 8192)])
+@pytest.mark.parametrize("M,rows,cols,group", [(3, 8209, 1056, 32), (16, 16400, 544, 32), (5, 70001, 352, 32), (1, 70001, 2080, 32),
+                                               (9, 33000, 1088, 64), (16, 20000, 4160, 64), (12, 66003, 192, 64),
+                                               (2, 66003, 4224, 64), (4, 9000, 8320, 128), (16, 66003, 128, 128),
+                                               (16, 66000, 4096, 32), (8, 66000, 8192, 32), (16, 66003, 5248, 128)])
+def test_many_rows(gpu, M, rows, cols, group):
+    """Persistent workgroups: the first and last rows and 300 between them."""
+    rng = np.random.default_rng(rows + cols)
+    print("int4", group, M, rows, cols, flush=True)
+    for zeros in (True, False):
+        c = _case(rows + cols + M, M, rows, cols, group, zeros)
+        y = _run(gpu, *c)
+        at = torch.from_numpy(np.unique(np.r_[0:40, rng.integers(0, rows, 300), rows - 40:rows]))
+        some = (c[0][at], c[1][at], None if c[2] is None else c[2][at], group, c[4])
+        assert_within(y[:, at.to(DEV)], *int4(*some), f"g{group} {M}x{rows}x{cols} zeros {zeros}")
+        assert torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("rows,cols", [(100, 2080), (4096, 4096), (700, 8192), (12288, 1056), (70000, 352)])
 def test_rows_do_not_depend_on_the_panel(gpu, rows, cols):
     codes, scales, z, g, x = _case(7, 16, rows, cols, 32)
     y = _run(gpu, codes, scales, z, g, x)
@@ -75,13 +92,14 @@ def test_codes_at_the_zero_point_give_nothing(gpu):
     assert (y[:, 5] == 0).all() and (y[:, 20] == 0).all() and (y[:, 6] != 0).all()
 
 
-def test_values_that_are_not_finite_stay_in_their_row(gpu):
-    codes, scales, z, g, x = _case(23, 5, 50, 640, 128)
+@pytest.mark.parametrize("rows,cols,group", [(50, 640, 128), (50, 2080, 32), (70000, 352, 32), (70000, 640, 128)])
+def test_values_that_are_not_finite_stay_in_their_row(gpu, rows, cols, group):
+    codes, scales, z, g, x = _case(23, 5, rows, cols, group)
     clean = _run(gpu, codes, scales, z, g, x)
-    x[1, 77], x[3, 600] = float("nan"), float("inf")
+    x[1, 77], x[3, 300] = float("nan"), float("inf")
     y = _run(gpu, codes, scales, z, g, x)
     assert torch.equal(y[[0, 2, 4]], clean[[0, 2, 4]]) and y[1].isnan().all() and not torch.isfinite(y[3]).any()
-    scales[7, 2] = float("nan")
+    scales[7, 0] = float("nan")
     y = _run(gpu, codes, scales, z, g, x)
     assert y[:, 7].isnan().all() and torch.equal(y[0, :7], clean[0, :7]) and torch.equal(y[0, 8:], clean[0, 8:])
 
