@@ -79,14 +79,30 @@ __device__ __forceinline__ v8bf even_odd(const uint4& v) {
     return __builtin_bit_cast(v8bf, o);
 }
 
-// Exchange the dword index with the lane group: afterwards dword j of lane
-// group k is what dword k of lane group j was.
-__device__ __forceinline__ void transpose_groups(uint4& v) {
-    const auto a = __builtin_amdgcn_permlane32_swap(v.x, v.z, false, false);
-    const auto b = __builtin_amdgcn_permlane32_swap(v.y, v.w, false, false);
-    const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-    const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-    v = make_uint4(c[0], c[1], d[0], d[1]);
+// Hand the lane groups (k = lane / 16, each with 32 columns of a step) dwords
+// of 8 columns so that dword j of all four lies in one group of G columns.
+// G = 128: nothing to do. G = 64: the upper two lane groups' first two dwords
+// change places with the lower two's last two. G = 32: the dword index changes
+// places with the lane group.
+template <int G>
+__device__ __forceinline__ void gather_groups(uint4& v) {
+    if constexpr (G < kStep) {
+        const auto a = __builtin_amdgcn_permlane32_swap(v.x, v.z, false, false);
+        const auto b = __builtin_amdgcn_permlane32_swap(v.y, v.w, false, false);
+        v = make_uint4(a[0], b[0], a[1], b[1]);
+    }
+    if constexpr (G < 64) {
+        const auto a = __builtin_amdgcn_permlane16_swap(v.x, v.y, false, false);
+        const auto b = __builtin_amdgcn_permlane16_swap(v.z, v.w, false, false);
+        v = make_uint4(a[0], a[1], b[0], b[1]);
+    }
+}
+// The first column, in a step, of dword j of lane group k after that.
+template <int G>
+__device__ __forceinline__ int gathered_column(int j, int k) {
+    if constexpr (G == kStep) return 32 * k + 8 * j;
+    if constexpr (G == 64) return 64 * (j >> 1) + 8 * (j & 1) + 32 * (k & 1) + 16 * (k >> 1);
+    return 32 * j + 8 * k;
 }
 
 // The scales and zero points of N groups of a row; zeros past the row's end.
@@ -202,7 +218,7 @@ __device__ __forceinline__ void compute(Load<G, WIDE>& b, const uint4* x, const 
             swap_lane_bit3(b.q[s].z, b.q[s + 1].z);
             swap_lane_bit3(b.q[s].w, b.q[s + 1].w);
         }
-        if constexpr (G != kStep) transpose_groups(b.q[s]);
+        gather_groups<G>(b.q[s]);
         const uint32_t d[4] = {b.q[s].x, b.q[s].y, b.q[s].z, b.q[s].w};
 #pragma unroll
         for (int g = 0; g < per_step; ++g) {
@@ -250,7 +266,7 @@ __global__ __launch_bounds__(1024) void k_int4(Int4Args a) {
     auto stage = [&](int p0, int cols) {
         for (int o = threadIdx.x; o < cols / 8 * 4 * NI; o += blockDim.x) {
             const int t = o % (4 * NI), k = o / (4 * NI) % 4, j = o / (16 * NI) % 4, s = o / (64 * NI);
-            const int c = p0 + s * kStep + (G == kStep ? 32 * k + 8 * j : 32 * j + 8 * k);
+            const int c = p0 + s * kStep + gathered_column<G>(j, k);
             uint4 v = make_uint4(0, 0, 0, 0);
             if (t < a.M && c < a.cols) v = load_global16(a.x + (int64_t)t * a.cols + c);
             lds[o] = __builtin_bit_cast(uint4, even_odd(v));
@@ -363,8 +379,7 @@ __global__ __launch_bounds__(1024) void k_int4_shot(Int4Args a) {
         for (int s = 0; s < NS; ++s)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                v[s][j] = load_global16(x + (G == kStep ? min(c0 + s * kStep + 32 * kg, last) + 8 * j
-                                                        : min(c0 + s * kStep + 32 * j, last) + 8 * kg));
+                v[s][j] = load_global16(x + min(c0 + s * kStep + gathered_column<G>(j, kg), a.cols - 8));
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
             if (s % 2 == 0) {
@@ -373,7 +388,7 @@ __global__ __launch_bounds__(1024) void k_int4_shot(Int4Args a) {
                 swap_lane_bit3(q[s].z, q[s + 1].z);
                 swap_lane_bit3(q[s].w, q[s + 1].w);
             }
-            if constexpr (G != kStep) transpose_groups(q[s]);
+            gather_groups<G>(q[s]);
             const uint32_t d[4] = {q[s].x, q[s].y, q[s].z, q[s].w};
 #pragma unroll
             for (int h = 0; h < per_step; ++h) {
