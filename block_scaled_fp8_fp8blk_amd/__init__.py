@@ -45,7 +45,7 @@ MAX_CHAIN = 65536
 CHAIN_COLS = (1024, 2048, 3072, 4096)
 ARM_FP8, ARM_BF16, ARM_FP8_MFMA, ARM_BF16_MFMA, ARM_MXFP4, ARM_NVFP4 = 0, 1, 2, 3, 4, 5
 FMT_MXFP4, FMT_NVFP4 = 0, 1
-MAX_EXPERTS, MAX_TOP_K, MAX_INTER = 1024, 16, 24576
+MAX_EXPERTS, MAX_TOP_K, MAX_INTER = 1024, 16, 20480
 SCORE_SOFTMAX, SCORE_SIGMOID, SCORE_SQRT_SOFTPLUS = 0, 1, 2
 TYPE_F32, TYPE_BF16 = 0, 1
 

@@ -24,6 +24,14 @@ constexpr int kStep = 128;  // columns of one 16-byte load per lane
 constexpr int kWaves = 8;   // of a workgroup, at most
 constexpr int kTurns = 4;   // tiles that a workgroup takes one after another, at most,
 constexpr int kGroups = 2048;  // and only where there are this many workgroups even so
+// Up to so many weights of down (tokens x experts of a token x slab), down and
+// the sum over the experts are one launch: it saves about 3 us of launch and
+// start, but has few workgroups and lets tokens read an expert that they share
+// once each. Measured, one launch against two: 3 tokens, 4 of 1440x736 experts
+// (13e6) 15.3 against 16.6 us; 6 tokens (25e6) 20.4 against 22.0; 4 tokens, 6
+// of 2048x1024 (50e6) 26.2 against 23.3; 1 token, 8 of 4096x2048 (67e6) 35.0
+// against 32.5.
+constexpr int64_t kFewWeights = 1 << 25;
 constexpr int kPieces = 3;  // bf16 values that hold an f32 h
 constexpr int kSlots = FP8BLK_MAX_M * FP8BLK_MAX_TOP_K;
 
@@ -64,18 +72,28 @@ struct Pair {
     uint4 q[T][2];
 };
 
+// Where tile t of a unit lies. A workgroup of one expert takes tiles side by
+// side, one of one token the same rows of the experts that it goes to.
+struct Where {
+    int expert, row;  // rows of this expert's from this one on
+};
 template <typename U>
-__device__ __forceinline__ void issue(Pair<U::T>& b, const MoeArgs& a, int64_t expert, int tile, int lane, int c0) {
+struct SideBySide {
+    int expert, tile;
+    __device__ __forceinline__ Where operator()(int t) const { return {expert, (tile * U::R + t % U::R) * kTile}; }
+};
+
+template <typename U, typename F>
+__device__ __forceinline__ void issue(Pair<U::T>& b, const MoeArgs& a, const F& where, int lane, int c0) {
     const uint32_t wide = a.cols / 2;  // bytes of a row: an expert's slab is less than 2^31 bytes
-    const int64_t slab = expert * a.rows * wide;
     // columns past the end meet zeros of the operand: any code will do
     const uint32_t c = min(c0 + 16 * (lane & 8) + 32 * (lane >> 4), a.cols - 32) / 2;
 #pragma unroll
     for (int t = 0; t < U::T; ++t) {
-        const int r0 = (tile * U::R + t % U::R) * kTile;
-        const uint8_t* w = a.w[t / U::R] + slab;
-        b.q[t][0] = load_stream16(w + (min(r0 + (lane & 7), a.rows - 1) * wide + c));
-        b.q[t][1] = load_stream16(w + (min(r0 + 8 + (lane & 7), a.rows - 1) * wide + c));
+        const Where at = where(t);
+        const uint8_t* w = a.w[t / U::R] + (int64_t)at.expert * a.rows * wide;
+        b.q[t][0] = load_stream16(w + (min(at.row + (lane & 7), a.rows - 1) * wide + c));
+        b.q[t][1] = load_stream16(w + (min(at.row + 8 + (lane & 7), a.rows - 1) * wide + c));
     }
 }
 
@@ -88,17 +106,18 @@ struct Scales {
     uint32_t d[U::LOADS][U::CHUNK / 4];
 };
 
-template <typename U>
-__device__ __forceinline__ void issue_scales(Scales<U>& b, const MoeArgs& a, int64_t expert, int tile, int lane, int c0) {
+template <typename U, typename F>
+__device__ __forceinline__ void issue_scales(Scales<U>& b, const MoeArgs& a, const F& where, int lane, int c0) {
     constexpr int PER_ROW = U::ROW / U::CHUNK;
     const uint32_t blocks = a.cols / U::B;
-    const int64_t end = (a.experts - expert) * a.rows * blocks;  // of the array, from this expert's scales
 #pragma unroll
     for (int i = 0; i < U::LOADS; ++i) {
         const int o = min(i * 64 + lane, U::T * kTile * PER_ROW - 1), t = o / (kTile * PER_ROW);
-        const int row = (tile * U::R + t % U::R) * kTile + o / PER_ROW % kTile;
-        const uint32_t at = min(row, a.rows - 1) * blocks + c0 / U::B + o % PER_ROW * U::CHUNK;
-        const uint8_t* sc = (U::MATS == 2 && t ? a.sc[1] : a.sc[0]) + expert * a.rows * blocks;
+        const Where w = where(t);
+        const int row = min(w.row + o / PER_ROW % kTile, a.rows - 1);
+        const uint8_t* sc = (U::MATS == 2 && t ? a.sc[1] : a.sc[0]) + (int64_t)w.expert * a.rows * blocks;
+        const uint32_t at = row * blocks + c0 / U::B + o % PER_ROW * U::CHUNK;
+        const int64_t end = (a.experts - w.expert) * a.rows * blocks;  // of the array, from this expert's scales
         // past a row's end other rows' scales are as good, the operand is zero there
         if (at + U::CHUNK <= end) {
             __builtin_memcpy(b.d[i], sc + at, U::CHUNK);
@@ -142,8 +161,9 @@ __device__ __forceinline__ v8bf codes_bf16(uint32_t d, float scale) {
 
 // acc += two steps of weights times the operand's columns (LDS; `stride`
 // 16-byte units from one 32-column read to the next); sc: the lane's row of
-// scales of the steps.
-template <int FMT, bool DOWN, typename U>
+// scales of the steps. OWN: every tile has an operand of its own, kPieces rows
+// from one to the next.
+template <int FMT, bool DOWN, typename U, bool OWN = false>
 __device__ __forceinline__ void compute(Pair<U::T>& b, const uint4* in, int stride, const uint8_t* sc, int kg, bool live, v4f* acc) {
     uint32_t e[U::T][U::PAIR / 4];
 #pragma unroll
@@ -163,10 +183,12 @@ __device__ __forceinline__ void compute(Pair<U::T>& b, const uint4* in, int stri
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint4 v = in[(s * 4 + j) * stride];
-            if constexpr (FMT == kNV) v = live ? v : make_uint4(0, 0, 0, 0);
-            const v8bf x = __builtin_bit_cast(v8bf, v);
 #pragma unroll
             for (int t = 0; t < U::T; ++t) {
+                if constexpr (OWN)
+                    if (t > 0) v = in[(s * 4 + j) * stride + t * kPieces];
+                if (FMT == kNV && (OWN || t == 0)) v = live ? v : make_uint4(0, 0, 0, 0);
+                const v8bf x = __builtin_bit_cast(v8bf, v);
                 const uint32_t d[4] = {b.q[t][s].x, b.q[t][s].y, b.q[t][s].z, b.q[t][s].w};
                 if constexpr (FMT == kMX) {
                     // byte kg of the step's dword into the exponent field
@@ -280,8 +302,8 @@ __global__ __launch_bounds__(64 * kWaves, 3) void k_moe(MoeArgs a) {
     Pair<U::T> b[NS / 2];
     Scales<U> sr;
 #pragma unroll
-    for (int s = 0; s < NS / 2; ++s) issue<U>(b[s], a, expert, tile, lane, c0 + 2 * s * kStep);
-    issue_scales<U>(sr, a, expert, tile, lane, c0);
+    for (int s = 0; s < NS / 2; ++s) issue<U>(b[s], a, SideBySide<U>{expert, tile}, lane, c0 + 2 * s * kStep);
+    issue_scales<U>(sr, a, SideBySide<U>{expert, tile}, lane, c0);
 
     // The operand: [step][32 columns][lane group][row], zeros past the last
     // column; a wave reads only the slices that it has staged itself.
@@ -326,14 +348,14 @@ __global__ __launch_bounds__(64 * kWaves, 3) void k_moe(MoeArgs a) {
         int t1 = tile, c1 = c0 + waves * SLICE;
         if (c1 >= a.cols) c1 = wave * SLICE, ++t1;
         place_scales<U>(sr, scales, lane);
-        if (t1 < end) issue_scales<U>(sr, a, expert, t1, lane, c1);
+        if (t1 < end) issue_scales<U>(sr, a, SideBySide<U>{expert, t1}, lane, c1);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int s = 0; s < NS / 2; ++s) {
             compute<FMT, DOWN, U>(b[s], in + (c0 / 8 + 32 * s) * rows_in, 4 * rows_in, scales + n * U::ROW + s * U::PAIR, kg,
                                   live, acc);
-            if (t1 < end) issue<U>(b[s], a, expert, t1, lane, c1 + 2 * s * kStep);
+            if (t1 < end) issue<U>(b[s], a, SideBySide<U>{expert, t1}, lane, c1 + 2 * s * kStep);
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -343,6 +365,100 @@ __global__ __launch_bounds__(64 * kWaves, 3) void k_moe(MoeArgs a) {
         tile = t1;
         ++turn;
     }
+}
+
+// Down and the weighted sum in one, for a few tokens: a workgroup takes 16
+// rows of the output of one token and walks the experts that it goes to, four
+// at a time, so that their sum stays in the workgroup. Every sum is taken as
+// k_moe and k_moe_sum take it. (Tokens read an expert that they share once
+// each, which is why many tokens go the other way.)
+template <int FMT, int NS>
+__global__ __launch_bounds__(64 * kWaves, 2) void k_moe_token(MoeArgs a, const float* __restrict__ weights, const float* base,
+                                                              float* y) {
+    using U = Unit<FMT, true, NS>;
+    constexpr int ROWS = U::T * kPieces;  // operand rows in LDS
+    extern __shared__ uint4 lds[];        // the waves' operands, block scales and sums
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, n = lane & 15, kg = lane >> 4;
+    const int m = blockIdx.y, row0 = blockIdx.x * kTile, c0 = wave * U::SLICE;
+    uint4* const own = lds + wave * NS * 16 * ROWS;
+    uint8_t* const scales = reinterpret_cast<uint8_t*>(lds + waves * NS * 16 * ROWS) + wave * U::T * kTile * U::ROW;
+    float* const sums = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(lds + waves * NS * 16 * ROWS) +
+                                                 waves * U::T * kTile * U::ROW);  // [wave][k][lane group 0, 1][row]
+    // A choice that is none takes part as expert 0 and is left out of the sum.
+    const auto from = [&](int k0) {
+        return [&a, m, row0, k0](int t) {
+            const int e = a.ids[m * a.K + min(k0 + t, a.K - 1)];
+            return Where{e >= 0 && e < a.experts ? e : 0, row0};
+        };
+    };
+    Pair<U::T> b[NS / 2];
+    Scales<U> sr;
+#pragma unroll
+    for (int s = 0; s < NS / 2; ++s) issue<U>(b[s], a, from(0), lane, c0 + 2 * s * kStep);
+    issue_scales<U>(sr, a, from(0), lane, c0);
+
+    const uint4* in = own + kg * ROWS + (FMT == kMX ? min(n & 3, 2) : min((n & 7) >> 1, 2));
+    const bool live = (kg >> 1) == (n & 1) && (n & 7) < 6;  // as in k_moe
+    for (int k0 = 0; k0 < a.K; k0 += U::T) {
+#pragma unroll
+        for (int t = 0; t < U::T; ++t) {
+            const int64_t slot = m * a.K + min(k0 + t, a.K - 1);
+            const uint16_t* src = a.in + slot * kPieces * a.cols;
+#pragma unroll
+            for (int i = 0; i < (NS * 16 + 63) / 64; ++i) {
+                const int o = i * 64 + lane, k = o % 4, j = o / 4 % 4;
+                const int c = c0 + o / 16 * kStep + (FMT == kMX ? 32 * k + 8 * j : 32 * j + 8 * k);
+                if (o >= NS * 16) continue;
+#pragma unroll
+                for (int p = 0; p < kPieces; ++p)
+                    own[o * ROWS + t * kPieces + p] =
+                        c < a.cols ? load_global16(src + (int64_t)p * a.cols + c) : make_uint4(0, 0, 0, 0);
+            }
+        }
+        place_scales<U>(sr, scales, lane);
+        const bool more = k0 + U::T < a.K;
+        if (more) issue_scales<U>(sr, a, from(k0 + U::T), lane, c0);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        v4f acc[U::T];
+#pragma unroll
+        for (int t = 0; t < U::T; ++t) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < NS / 2; ++s) {
+            compute<FMT, true, U, true>(b[s], in + 32 * s * ROWS, 4 * ROWS, scales + n * U::ROW + s * U::PAIR, kg, live, acc);
+            if (more) issue<U>(b[s], a, from(k0 + U::T), lane, c0 + 2 * s * kStep);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int t = 0; t < U::T; ++t)
+            if (lane < 32 && k0 + t < a.K)
+                sums[(wave * FP8BLK_MAX_TOP_K + k0 + t) * 32 + lane] =
+                    FMT == kMX ? acc[t][0] + (acc[t][1] + acc[t][2]) : acc[t][0];
+    }
+    __syncthreads();
+    // The k-th expert's value of row n, in place of the first wave's sum.
+    for (int o = threadIdx.x; o < a.K * kTile; o += blockDim.x) {
+        const int k = o / kTile, r = o % kTile, e = a.ids[m * a.K + k];
+        if (e < 0 || e >= a.experts) continue;
+        float v = 0.0f;
+        for (int w = 0; w < waves; ++w) {
+            const float* p = sums + (w * FP8BLK_MAX_TOP_K + k) * 32;
+            const float f = U::PER == 2 ? p[r] + p[r + 16] : p[r];
+            v = w == 0 ? f : v + f;
+        }
+        if (a.top[0]) v *= a.top[0][e];
+        sums[k * 32 + r] = v;
+    }
+    __syncthreads();
+    const int row = row0 + threadIdx.x;
+    if (threadIdx.x >= kTile || row >= a.rows) return;
+    float s = base ? base[(int64_t)m * a.rows + row] : 0.0f;
+    for (int k = 0; k < a.K; ++k) {
+        const int slot = m * a.K + k, e = a.ids[slot];
+        if (e >= 0 && e < a.experts) s = __builtin_fmaf(weights[slot], sums[k * 32 + threadIdx.x], s);
+    }
+    y[(int64_t)m * a.rows + row] = s;
 }
 
 // y = base + the weighted sum of a token's experts, in order of k. All loads
@@ -378,6 +494,10 @@ void launch_steps(MoeArgs a, hipStream_t s) {
     const int64_t slices = ceil_div(a.cols, NS * kStep), tiles = ceil_div(a.rows, kTile * U::R);
     const int waves = (int)(slices < kWaves ? slices : kWaves);
     const int64_t row_bytes = slices * NS * kStep * 2 * U::LANES;
+    // The widest operands (1 row of FP8BLK_MAX_COLS columns of x, 3 of
+    // FP8BLK_MAX_INTER of h) leave 30 KB of LDS for the waves' scales and sums.
+    static_assert((DOWN ? FP8BLK_MAX_INTER : FP8BLK_MAX_COLS) * 2 * U::LANES + kWaves * U::T * (kTile * U::ROW + 512) <= 160 * 1024,
+                  "LDS of a workgroup");
     a.most = a.slots / a.K < U::PER ? a.slots / a.K : U::PER;
     while (a.most > 1 && a.most * row_bytes > 64 * 1024) a.most /= 2;
     const int64_t turns = tiles * a.slots / kGroups;
@@ -393,6 +513,14 @@ void launch(const MoeArgs& a, hipStream_t s) {
     else launch_steps<FMT, DOWN, NS>(a, s);
 }
 
+template <int FMT, int NS>
+void launch_token(const MoeArgs& a, int M, const float* weights, const float* base, float* y, hipStream_t s) {
+    using U = Unit<FMT, true, NS>;
+    const int waves = (int)ceil_div(a.cols, U::SLICE);
+    const size_t lds = (size_t)waves * (NS * 256 * U::T * kPieces + U::T * kTile * U::ROW + FP8BLK_MAX_TOP_K * 128);
+    k_moe_token<FMT, NS><<<dim3((unsigned)ceil_div(a.rows, kTile), (unsigned)M), 64 * waves, lds, s>>>(a, weights, base, y);
+}
+
 template <int FMT>
 void run(const fp4_moe_layer& l, const uint16_t* x, int M, const int32_t* ids, const float* weights, int K,
          const float* base, float* y, uint16_t* pieces, float* part, hipStream_t s) {
@@ -402,6 +530,11 @@ void run(const fp4_moe_layer& l, const uint16_t* x, int M, const int32_t* ids, c
     launch<FMT, false>(a, s);
     a = {{l.down, nullptr}, {l.down_scales, nullptr}, {l.down_global, nullptr}, pieces, ids, nullptr, part,
          l.experts, H, I, M * K, K, 1, 1, 0.0f};
+    if ((int64_t)M * K * H * I <= kFewWeights && I <= kWaves * 4 * kStep) {
+        if (I <= 2 * 4 * kStep) launch_token<FMT, 2>(a, M, weights, base, y, s);
+        else launch_token<FMT, 4>(a, M, weights, base, y, s);
+        return;
+    }
     launch<FMT, true>(a, s);
     k_moe_sum<<<dim3((unsigned)ceil_div(H, 256), (unsigned)M), 64, 0, s>>>(part, ids, weights, base, l.experts, H, K, y);
 }

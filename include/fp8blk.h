@@ -771,7 +771,7 @@ int fp8blk_moe_route(const uint16_t *w_bf16, const float *bias, int64_t experts,
  *     bad sizes); its contents on entry do not matter.
  * Enqueued on `stream`; does not wait.
  */
-#define FP8BLK_MAX_INTER 24576
+#define FP8BLK_MAX_INTER 20480
 typedef struct fp4_moe_layer {
     const uint8_t *gate, *gate_scales;
     const uint8_t *up, *up_scales;

@@ -48,7 +48,9 @@ class Layer:
 @pytest.mark.parametrize("M,K,E,hidden,inter", [(1, 1, 1, 32, 32), (1, 2, 8, 64, 96), (1, 8, 16, 1024, 512), (2, 4, 5, 160, 1056),
                                                 (3, 4, 32, 1440, 736), (5, 8, 12, 544, 256), (8, 2, 4, 256, 2080),
                                                 (13, 6, 9, 416, 320), (16, 8, 24, 512, 384), (16, 16, 16, 96, 64),
-                                                (16, 1, 2, 2080, 128)])
+                                                (16, 1, 2, 2080, 128), (16, 8, 10, 1440, 736), (12, 6, 7, 1056, 2080),
+                                                (16, 5, 4, 2080, 352), (9, 4, 20, 2592, 416), (1, 1, 2, 64, 20480),
+                                                (2, 1, 2, 65536, 32), (1, 2, 3, 8224, 4128)])
 def test_matches_plain(gpu, fmt, M, K, E, hidden, inter):
     print("moe", fmt, M, K, E, hidden, inter, flush=True)
     L = Layer(gpu, fmt, E, hidden, inter, M * hidden + inter + fmt, limit=(0.0, 3.0)[M % 2])
@@ -64,8 +66,9 @@ def test_workload_shape(gpu, fmt):
 
 
 @pytest.mark.parametrize("fmt", [MX, NV])
-def test_ids_without_an_expert_add_nothing(gpu, fmt):
-    L = Layer(gpu, fmt, 6, 288, 160, 5)
+@pytest.mark.parametrize("hidden,inter", [(288, 160), (1056, 1600)])
+def test_ids_without_an_expert_add_nothing(gpu, fmt, hidden, inter):
+    L = Layer(gpu, fmt, 6, hidden, inter, 5)
     x, ids, p, base = L.tokens(5, 4)
     ids[0] = -1
     ids[1] = torch.tensor([6, 2, -1, 100])
@@ -79,9 +82,10 @@ def test_ids_without_an_expert_add_nothing(gpu, fmt):
 
 @pytest.mark.parametrize("fmt", [MX, NV])
 @pytest.mark.parametrize("M,K", [(1, 16), (16, 16), (7, 5)])
-def test_the_same_expert_many_times(gpu, fmt, M, K):
+@pytest.mark.parametrize("hidden,inter", [(160, 96), (1056, 544)])
+def test_the_same_expert_many_times(gpu, fmt, M, K, hidden, inter):
     """Every choice the same expert (up to 256 of one), and two experts in turn."""
-    L = Layer(gpu, fmt, 3, 160, 96, 8)
+    L = Layer(gpu, fmt, 3, hidden, inter, 8)
     x, ids, p, base = L.tokens(M, K)
     ids[:] = 1
     L.check(gpu, x, ids, p, base, "one expert")
@@ -117,8 +121,10 @@ def test_extreme_block_scales(gpu, fmt, lo, hi):
     L.check(gpu, x, ids, p, base, f"{fmt} scales {lo}..{hi}")
 
 
-def test_values_that_are_not_finite_stay_in_their_token(gpu):
-    L = Layer(gpu, MX, 4, 160, 96, 41)
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("hidden,inter", [(160, 96), (1440, 1376)])
+def test_values_that_are_not_finite_stay_in_their_token(gpu, fmt, hidden, inter):
+    L = Layer(gpu, fmt, 4, hidden, inter, 41)
     x, ids, p, base = L.tokens(6, 3)
     clean = L.run(gpu, x, ids, p, base)
     x[2, 9], p[4, 1] = float("nan"), float("inf")

@@ -79,7 +79,7 @@ def _moe(lib, layer=None, **kw):
 
 @pytest.mark.parametrize("layer", [
     dict(fmt=2), dict(fmt=-1), dict(experts=0), dict(experts=fb.MAX_EXPERTS + 1), dict(hidden=16), dict(hidden=80),
-    dict(hidden=65568), dict(inter=0), dict(inter=48), dict(inter=65568), dict(limit=-1.0), dict(limit=float("inf")),
+    dict(hidden=65568), dict(inter=0), dict(inter=48), dict(inter=fb.MAX_INTER + 32), dict(limit=-1.0), dict(limit=float("inf")),
     dict(limit=float("nan")), dict(gate=None), dict(up_scales=None), dict(down=None), dict(gate=P + 8), dict(up=P + 4),
     dict(down_scales=P + 4), dict(gate_scales=P + 2), dict(fmt=fb.FMT_MXFP4, up_scales=P + 2), dict(gate_global=P + 2)])
 def test_moe_layer_refusals(lib, layer):
@@ -103,7 +103,7 @@ def test_moe_workspace(lib):
     assert _moe(lib, ws=None) == fb.ERR_WORKSPACE
     assert _moe(lib, ws=P + 128) == fb.ERR_WORKSPACE
     assert _moe(lib, wsb=need - 1) == fb.ERR_WORKSPACE
-    for bad in ((16, 1, 1), (48, 1, 1), (65568, 1, 1), (64, 0, 1), (64, 17, 1), (64, 1, 0), (64, 1, 17)):
+    for bad in ((16, 1, 1), (48, 1, 1), (fb.MAX_INTER + 32, 1, 1), (64, 0, 1), (64, 17, 1), (64, 1, 0), (64, 1, 17)):
         assert fb.fp4_moe_bytes(*bad) == 0
 
 
