@@ -249,9 +249,9 @@ __device__ __forceinline__ void finish(const MoeArgs& a, int expert, int tile, i
             if (U::PER == 4 || !(lane & 16)) a.part[(int64_t)sl * a.rows + row] = v[0];
         } else {
             float g1 = v[0], u = v[U::MATS - 1];
-            if (a.limit > 0.0f) {
-                g1 = fminf(g1, a.limit);
-                u = fminf(fmaxf(u, -a.limit), a.limit);
+            if (a.limit > 0.0f) {  // a NaN stays one
+                g1 = g1 > a.limit ? a.limit : g1;
+                u = u > a.limit ? a.limit : u < -a.limit ? -a.limit : u;
             }
             float h = g1 / (1.0f + expf(-g1)) * u;
             uint16_t* to = a.pieces + (int64_t)sl * kPieces * a.rows + row;
@@ -259,7 +259,7 @@ __device__ __forceinline__ void finish(const MoeArgs& a, int expert, int tile, i
             for (int p = 0; p < kPieces; ++p) {
                 const float bf = head_bf16(h);
                 to[(int64_t)p * a.rows] = (uint16_t)(as_u32(bf) >> 16);
-                h -= bf;
+                h = fabsf(bf) < __builtin_inff() ? h - bf : 0.0f;  // an infinity or NaN is its first piece
             }
         }
     }

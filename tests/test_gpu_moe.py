@@ -133,6 +133,32 @@ def test_values_that_are_not_finite_stay_in_their_token(gpu, fmt, hidden, inter)
     assert torch.equal(y[ok], clean[ok]) and y[2].isnan().all() and not torch.isfinite(y[4]).any()
 
 
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("limit", [0.0, 2.0])
+def test_a_nan_passes_the_limit(gpu, fmt, limit):
+    """Also with a limit, which an infinite gate or up is brought down to, a
+    NaN in x gives NaN."""
+    L = Layer(gpu, fmt, 3, 96, 64, 43, limit=limit)
+    x, ids, p, base = L.tokens(3, 2)
+    x[1, 40] = float("nan")
+    y = L.run(gpu, x, ids, p, base)
+    assert y[1].isnan().all() and torch.isfinite(y[[0, 2]]).all()
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("inter", [64, 4128])
+def test_an_infinite_h_gives_infinite_outputs(gpu, fmt, inter):
+    """h past the largest f32: h times a weight is infinite, with its sign."""
+    L = Layer(gpu, fmt, 1, 64, inter, 47, with_global=False, scale_range=(120, 120) if fmt == MX else (56, 56))
+    for slab, code in ((L.gate, 0x22), (L.up, 0x22), (L.down, 0xAA)):  # 1, 1, -1
+        slab.codes[:] = code
+    L.handle = gpu.fp4_moe_weights(fmt, *L.gate.on(DEV), *L.up.on(DEV), *L.down.on(DEV))
+    x = torch.full((2, 64), 2.0 ** 70).bfloat16()
+    x[1] = 0.0
+    y = L.run(gpu, x, torch.zeros((2, 1), dtype=torch.int32), torch.ones(2, 1), None)
+    assert (y[0] == -float("inf")).all() and (y[1] == 0).all()
+
+
 def test_large_gates(gpu):
     """silu far from 0: exp(-g) overflows to infinity and h is 0, or h is g u."""
     L = Layer(gpu, MX, 2, 96, 64, 51, scale_range=(127, 131))
