@@ -223,7 +223,7 @@ __device__ __forceinline__ float head_bf16(float f) { return as_f32(bf16_of_scal
 // A tile's sums over the waves that share its columns, and its outputs: every
 // wave calls it as often.
 template <int FMT, bool DOWN, typename U>
-__device__ __forceinline__ void finish(const MoeArgs& a, int expert, int tile, int member, int count, float* sums, v4f* acc) {
+__device__ __forceinline__ void finish(const MoeArgs& a, const float (&top)[U::MATS], int tile, int member, int count, float* sums, v4f* acc) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
 #pragma unroll
     for (int t = 0; t < U::T; ++t) {
@@ -241,7 +241,7 @@ __device__ __forceinline__ void finish(const MoeArgs& a, int expert, int tile, i
                 const float x = U::PER == 2 ? p[lane] + p[lane ^ 16] : p[lane];
                 v[m] = w == 0 ? x : v[m] + x;
             }
-            if (a.top[m]) v[m] *= a.top[m][expert];
+            v[m] *= top[m];
         }
         const int sl = __shfl(member, of & 63);
         if (row >= a.rows || of >= count) continue;
@@ -276,14 +276,22 @@ __global__ __launch_bounds__(64 * kWaves, 3) void k_moe(MoeArgs a) {
 
     // The slots of this slot's expert; the workgroup is theirs if `slot` is
     // the first, or (a.most)-th, ... of them.
-    const int expert = a.ids[slot];
+    int ids[kSlots / 64];
+#pragma unroll
+    for (int q = 0; q < kSlots / 64; ++q) ids[q] = 64 * q < a.slots ? a.ids[min(64 * q + lane, a.slots - 1)] : 0;
+    int expert = 0;
+#pragma unroll
+    for (int q = 0; q < kSlots / 64; ++q)
+        if (slot >> 6 == q) expert = __builtin_amdgcn_readlane(ids[q], slot & 63);
     if (expert < 0 || expert >= a.experts) return;
+    float top[U::MATS];  // the global scales
+#pragma unroll
+    for (int m = 0; m < U::MATS; ++m) top[m] = a.top[m] ? a.top[m][expert] : 1.0f;
     int before = 0, count = 0, member = 0;  // member: lane t holds the t-th slot
 #pragma unroll
     for (int q = 0; q < kSlots / 64; ++q) {
         if (64 * q >= a.slots) continue;
-        const int s = 64 * q + lane;
-        uint64_t same = __ballot(s < a.slots && a.ids[min(s, a.slots - 1)] == expert);
+        uint64_t same = __ballot(64 * q + lane < a.slots && ids[q] == expert);
         if (slot >= 64 * q) {
             const uint64_t below = slot - 64 * q < 64 ? (1ull << (slot - 64 * q)) - 1 : ~0ull;
             before += __popcll(same & below);
@@ -361,7 +369,7 @@ __global__ __launch_bounds__(64 * kWaves, 3) void k_moe(MoeArgs a) {
         __builtin_amdgcn_wave_barrier();
         c0 = c1;
         if (t1 == tile) continue;
-        finish<FMT, DOWN, U>(a, expert, tile, member, count, sums + (turn & 1) * waves * U::T * 64, acc);
+        finish<FMT, DOWN, U>(a, top, tile, member, count, sums + (turn & 1) * waves * U::T * 64, acc);
         tile = t1;
         ++turn;
     }
@@ -506,10 +514,18 @@ void launch_steps(MoeArgs a, hipStream_t s) {
     k_moe<FMT, DOWN, NS><<<grid, 64 * waves, (size_t)(a.most * row_bytes + waves * U::T * (kTile * U::ROW + 512)), s>>>(a);
 }
 
+// Steps a wave takes at a time: half as many where the columns are few. Down:
+// wherever 8 waves then cover the row, which for one token is more waves than
+// 4 steps give (1 token, 8 of 4096x2048: 36.3 against 37.8 us NVFP4, 32.2
+// against 32.8 MXFP4; 16 tokens 235 against 233, 199 against 198). Gate and
+// up only up to 2048 columns (the same token with 4 steps over 4096 columns:
+// 39.3 against 37.9 us).
+inline bool half_steps(bool down, int cols) { return cols <= (down ? 2 * kStep * kWaves : 16 * kStep); }
+
 template <int FMT, bool DOWN>
 void launch(const MoeArgs& a, hipStream_t s) {
     constexpr int NS = DOWN ? 4 : 8;
-    if (a.cols <= 2 * NS * kStep) launch_steps<FMT, DOWN, NS / 2>(a, s);
+    if (half_steps(DOWN, a.cols)) launch_steps<FMT, DOWN, NS / 2>(a, s);
     else launch_steps<FMT, DOWN, NS>(a, s);
 }
 
@@ -531,7 +547,7 @@ void run(const fp4_moe_layer& l, const uint16_t* x, int M, const int32_t* ids, c
     a = {{l.down, nullptr}, {l.down_scales, nullptr}, {l.down_global, nullptr}, pieces, ids, nullptr, part,
          l.experts, H, I, M * K, K, 1, 1, 0.0f};
     if ((int64_t)M * K * H * I <= kFewWeights && I <= kWaves * 4 * kStep) {
-        if (I <= 2 * 4 * kStep) launch_token<FMT, 2>(a, M, weights, base, y, s);
+        if (half_steps(true, I)) launch_token<FMT, 2>(a, M, weights, base, y, s);
         else launch_token<FMT, 4>(a, M, weights, base, y, s);
         return;
     }
