@@ -3,15 +3,23 @@
 // A choice is a decision, and neighbours around the border have to fall the
 // same way wherever they are computed, so the logits are sums in 64 bits of
 // products that are exact (bf16 x bf16), on v_mfma_f64_16x16x4_f64: 16 tokens
-// by 16 experts. That instruction is the bound of a large panel (64 cycles for
-// 2048 flop: 74 TFLOP/s); a few tokens are bound by latency.
+// by 16 experts. What bounds it:
+//   - a large panel: that instruction. Alone it runs in 74 cycles with two or
+//     more waves a SIMD (86 with one), and the conversion of its inputs to 64
+//     bits is not hidden behind it: 2 more vector instructions for each make it
+//     88. 2048 tokens, 256 experts, 4096 columns: 80 us, 54 TFLOP/s (a library's
+//     64-bit product of inputs that are converted already: 125 us; of 4096^3:
+//     71 TFLOP/s).
+//   - a few tokens: latency, of two launches, a chain of 32 instructions and a
+//     choice (1 token, 256 experts, 4096 columns: 9.6 us, of which an empty
+//     launch takes 2.6 each).
 //
 // Order of a logit, whatever the panel: chunks of 128 columns, each a chain
-// of matrix instructions from 0; four sums over the chunks c % 4 = 0, 1, 2, 3
-// in order; then (s0 + s1) + (s2 + s3). Few tiles: every chunk is a wave of
-// its own, the chunks' sums go to the workspace, and the kernel that chooses
-// adds them. Many tiles: the four waves of a workgroup each walk a quarter of
-// the chunks and add in LDS.
+// of matrix instructions from 0; eight sums over the chunks c % 8 = 0 .. 7 in
+// order; then their tree. Few tiles: every chunk is a wave of its own, the
+// chunks' sums go to the workspace, and the kernel that chooses adds them.
+// Many tiles: the eight waves of a workgroup each walk an eighth of the chunks
+// and add in LDS.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -26,7 +34,12 @@ typedef double v4d __attribute__((ext_vector_type(4)));
 
 constexpr int64_t kRouteAlign = 256;
 constexpr int kTile = 16, kStepCols = 32, kChunkCols = 128;
-constexpr int kSplitTiles = 256;  // up to so many 16 x 16 tiles each chunk has a wave of its own
+constexpr int kWaves = 8;       // sums of a logit, and waves that share a tile's chunks
+constexpr int kSplitWaves = 4;  // chunks of a workgroup where each has a wave of its own
+// Up to so many 16 x 16 tiles each chunk has a wave of its own: 256 experts of
+// 4096 columns, against eight waves a tile, 128 tokens (128 tiles) 15.8 against
+// about 19 us, 200 tokens 20.9 against 19.5, 256 tokens 23.1 against 19.6.
+constexpr int kSplitTiles = 128;
 
 inline int route_chunks(int64_t cols) { return (int)ceil_div(cols, kChunkCols); }
 inline bool route_split(int64_t experts, int64_t M) { return ceil_div(experts, kTile) * ceil_div(M, kTile) <= kSplitTiles; }
@@ -42,128 +55,133 @@ struct RouteArgs {
     float scale;
 };
 
-// 8 bf16 values as f64.
-struct Eight {
-    double v[8];
-};
-__device__ __forceinline__ Eight widen(const uint4& d) {
-    float f[8];
-    widen8_bf16(d, f);
-    Eight e;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e.v[i] = (double)f[i];
-    return e;
+__device__ __forceinline__ double tree(const double (&s)[kWaves]) {
+    return ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
 }
 
-// Lane (n, k) of a wave holds 8 columns, k-th of four, of token or expert n in
-// a 32-column step; instruction j takes column j of each. The loads of AHEAD
-// steps are in flight.
+// The inputs of RX by RW tiles (tokens by experts). Lane (n, k) of a wave holds
+// 8 columns, k-th of four, of token or expert n in a 32-column step;
+// instruction j takes column j of each. The loads of AHEAD steps are in flight.
 constexpr int kSteps = kChunkCols / kStepCols;
-template <int R, int AHEAD>
+template <int RX, int RW, int AHEAD>
 struct Steps {
-    const uint16_t *x[R], *w[R];
-    uint4 xd[AHEAD][R], wd[AHEAD][R];
+    const uint8_t *x, *w;        // the first rows
+    uint32_t xrow[RX], wrow[RW];  // the lane's rows from there, in bytes
+    uint4 xd[AHEAD][RX], wd[AHEAD][RW];
     int cols, kg;
 
-    __device__ __forceinline__ void load(int slot, int c) {
-        const int at = min(c + 8 * kg, cols - 8);
+    __device__ __forceinline__ void start(const RouteArgs& a, int m0, int e0, int lane) {
+        x = reinterpret_cast<const uint8_t*>(a.x + (int64_t)m0 * a.cols);
+        w = reinterpret_cast<const uint8_t*>(a.w + (int64_t)e0 * a.cols);
+        cols = a.cols;
+        kg = lane >> 4;
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            xd[slot][i] = load_global16(x[i] + at);
-            wd[slot][i] = load_global16(w[i] + at);
-        }
+        for (int i = 0; i < RX; ++i) xrow[i] = 2u * a.cols * min(i * kTile + (lane & 15), a.M - 1 - m0);
+#pragma unroll
+        for (int i = 0; i < RW; ++i) wrow[i] = 2u * a.cols * min(i * kTile + (lane & 15), a.E - 1 - e0);
     }
-    __device__ __forceinline__ Eight take(const uint4& d, int c) const {  // zeros past the last column
-        const uint32_t keep = c + 8 * kg < cols ? ~0u : 0u;
-        return widen(make_uint4(d.x & keep, d.y & keep, d.z & keep, d.w & keep));
+    __device__ __forceinline__ void load(int slot, int c) {
+        // a last step has 16 columns, which both halves of the wave then read
+        const uint32_t in = c + kStepCols <= cols ? 16 * kg : 16 * (kg & 1);
+        const int64_t at = 2 * (c < cols ? c : 0);
+#pragma unroll
+        for (int i = 0; i < RX; ++i) xd[slot][i] = load_global16(x + at + (xrow[i] + in));
+#pragma unroll
+        for (int i = 0; i < RW; ++i) wd[slot][i] = load_global16(w + at + (wrow[i] + in));
+    }
+    static __device__ __forceinline__ double value(const uint4& d, int k) {
+        const uint32_t q[4] = {d.x, d.y, d.z, d.w};
+        return (double)as_f32(k % 2 ? q[k / 2] & 0xFFFF0000u : q[k / 2] << 16);
     }
     // acc += the step in `slot`, columns c on; that slot then takes the step at `next`.
-    __device__ __forceinline__ void multiply(int slot, int c, bool more, int next, v4d (&acc)[R][R]) {
-        Eight xe[R], we[R];
+    __device__ __forceinline__ void multiply(int slot, int c, bool more, int next, v4d (&acc)[RX][RW]) {
+        if (c + kStepCols > cols) {  // zeros past the last column
+            const uint32_t keep = c + 8 * kg < cols ? ~0u : 0u;
 #pragma unroll
-        for (int i = 0; i < R; ++i) xe[i] = take(xd[slot][i], c), we[i] = take(wd[slot][i], c);
-        if (more) load(slot, next);
-        __builtin_amdgcn_sched_barrier(0);  // the loads go out before the products, not where they are used
+            for (int i = 0; i < RX; ++i)
+                xd[slot][i] = make_uint4(xd[slot][i].x & keep, xd[slot][i].y & keep, xd[slot][i].z & keep, xd[slot][i].w & keep);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+            for (int i = 0; i < RW; ++i)
+                wd[slot][i] = make_uint4(wd[slot][i].x & keep, wd[slot][i].y & keep, wd[slot][i].z & keep, wd[slot][i].w & keep);
+        }
 #pragma unroll
-            for (int i = 0; i < R; ++i)
+        for (int k = 0; k < 8; ++k) {
+            double xe[RX], we[RW];
 #pragma unroll
-                for (int j = 0; j < R; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f64_16x16x4f64(xe[i].v[k], we[j].v[k], acc[i][j], 0, 0, 0);
+            for (int i = 0; i < RX; ++i) xe[i] = value(xd[slot][i], k);
+#pragma unroll
+            for (int i = 0; i < RW; ++i) we[i] = value(wd[slot][i], k);
+            if (k == 7) {
+                if (more) load(slot, next);
+                __builtin_amdgcn_sched_barrier(0);  // the loads go out here, not where they are used
+            }
+#pragma unroll
+            for (int i = 0; i < RX; ++i)
+#pragma unroll
+                for (int j = 0; j < RW; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f64_16x16x4f64(xe[i], we[j], acc[i][j], 0, 0, 0);
+        }
     }
 };
 
 // Register i of lane l of a result tile is token 4 i + l / 16, expert l % 16.
-template <int R, bool SPLIT>
-__global__ __launch_bounds__(256) void k_route_logits(RouteArgs a) {
-    __shared__ double sums[SPLIT ? 1 : 3][SPLIT ? 1 : R * R * 4 * 64];
+template <int RX, int RW, bool SPLIT>
+__global__ __launch_bounds__(64 * kWaves) void k_route_logits(RouteArgs a) {
+    constexpr int T = RX * RW;
+    __shared__ double sums[SPLIT ? 1 : kWaves][SPLIT ? 1 : T * 4 * 64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, kg = lane >> 4;
-    const int e0 = blockIdx.x * R * kTile, m0 = blockIdx.y * R * kTile;
-    constexpr int AHEAD = SPLIT ? kSteps : 2;
-    Steps<R, AHEAD> steps;
-    steps.cols = a.cols;
-    steps.kg = kg;
+    const int e0 = blockIdx.x * RW * kTile, m0 = blockIdx.y * RX * kTile;
+    constexpr int AHEAD = T < 4 ? kSteps : 2;
+    Steps<RX, RW, AHEAD> steps;
+    steps.start(a, m0, e0, lane);
+    v4d acc[RX][RW], total[RX][RW];
+    const auto clear = [](v4d(&t)[RX][RW]) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        steps.x[i] = a.x + (int64_t)min(m0 + i * kTile + n, a.M - 1) * a.cols;
-        steps.w[i] = a.w + (int64_t)min(e0 + i * kTile + n, a.E - 1) * a.cols;
-    }
-    v4d total[R][R];
-    const auto clear = [](v4d(&t)[R][R]) {
+        for (int i = 0; i < RX; ++i)
 #pragma unroll
-        for (int i = 0; i < R; ++i)
-#pragma unroll
-            for (int j = 0; j < R; ++j) t[i][j] = v4d{0.0, 0.0, 0.0, 0.0};
+            for (int j = 0; j < RW; ++j) t[i][j] = v4d{0.0, 0.0, 0.0, 0.0};
     };
-    clear(total);
-    double* out = a.logits;
+    const auto store = [&](double* out, int tile, int k, double v) {
+        const int m = m0 + tile / RW * kTile + 4 * k + kg, e = e0 + tile % RW * kTile + n;
+        if (m < a.M && e < a.E) out[(int64_t)m * a.E + e] = v;
+    };
     if constexpr (SPLIT) {
-        const int chunk = blockIdx.z * 4 + wave, c0 = chunk * kChunkCols;
+        const int chunk = blockIdx.z * kSplitWaves + wave, c0 = chunk * kChunkCols;
         if (chunk >= a.chunks) return;
-        out += (int64_t)chunk * a.M * a.E;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) steps.load(s, c0 + s * kStepCols);
         __builtin_amdgcn_sched_barrier(0);
+        clear(acc);
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) steps.multiply(s, c0 + s * kStepCols, false, 0, total);
+        for (int s = 0; s < kSteps; ++s) steps.multiply(s, c0 + s * kStepCols, false, 0, acc);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) store(a.logits + (int64_t)chunk * a.M * a.E, 0, k, acc[0][0][k]);
     } else {
-        v4d acc[R][R];
-        steps.load(0, wave * kChunkCols);
-        steps.load(1, wave * kChunkCols + kStepCols);
-        for (int chunk = wave; chunk < a.chunks; chunk += 4) {
+        clear(total);
+#pragma unroll
+        for (int s = 0; s < AHEAD; ++s) steps.load(s, wave * kChunkCols + s * kStepCols);
+        for (int chunk = wave; chunk < a.chunks; chunk += kWaves) {
             clear(acc);
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
-                const int c = chunk * kChunkCols + s * kStepCols;
-                steps.multiply(s % 2, c, true, s + 2 < kSteps ? c + 2 * kStepCols : c + (2 - kSteps) * kStepCols + 4 * kChunkCols, acc);
+                const int t = s + AHEAD, c0 = chunk * kChunkCols;
+                steps.multiply(s % AHEAD, c0 + s * kStepCols, true, c0 + t / kSteps * kWaves * kChunkCols + t % kSteps * kStepCols, acc);
             }
 #pragma unroll
-            for (int i = 0; i < R; ++i)
+            for (int i = 0; i < RX; ++i)
 #pragma unroll
-                for (int j = 0; j < R; ++j) total[i][j] += acc[i][j];
+                for (int j = 0; j < RW; ++j) total[i][j] += acc[i][j];
         }
-        if (wave > 0)
 #pragma unroll
-            for (int t = 0; t < R * R * 4; ++t) sums[wave - 1][t * 64 + lane] = total[t / 4 / R][t / 4 % R][t % 4];
+        for (int t = 0; t < T * 4; ++t) sums[wave][t * 64 + lane] = total[t / 4 / RW][t / 4 % RW][t % 4];
         __syncthreads();
-        if (wave > 0) return;
+        for (int t = wave; t < T * 4; t += kWaves) {
+            double s[kWaves];
 #pragma unroll
-        for (int t = 0; t < R * R * 4; ++t) {
-            const int o = t * 64 + lane;
-            const double s = total[t / 4 / R][t / 4 % R][t % 4];
-            total[t / 4 / R][t / 4 % R][t % 4] = (s + sums[0][o]) + (sums[1][o] + sums[2][o]);
+            for (int v = 0; v < kWaves; ++v) s[v] = sums[v][t * 64 + lane];
+            store(a.logits, t / 4, t % 4, tree(s));
         }
     }
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int j = 0; j < R; ++j)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int m = m0 + i * kTile + 4 * k + kg, e = e0 + j * kTile + n;
-                if (m < a.M && e < a.E) out[(int64_t)m * a.E + e] = total[i][j][k];
-            }
 }
 
 template <int CTRL>
@@ -222,16 +240,16 @@ __device__ __forceinline__ double lane_value64(double v, int lane) {
 // A logit from its chunks' sums, 32 loads at a time.
 __device__ __forceinline__ double add_chunks(const RouteArgs& a, int64_t at) {
     const int64_t n = (int64_t)a.M * a.E;
-    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    double s[kWaves] = {};
     for (int c = 0; c < a.chunks; c += 32) {
         double v[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) v[k] = a.logits[at + min(c + k, a.chunks - 1) * n];
 #pragma unroll
         for (int k = 0; k < 32; ++k)
-            if (c + k < a.chunks) s[k % 4] += v[k];
+            if (c + k < a.chunks) s[k % kWaves] += v[k];
     }
-    return (s[0] + s[1]) + (s[2] + s[3]);
+    return tree(s);
 }
 
 // sigmoid(l) or sqrt(log(1 + exp(l))).
@@ -332,6 +350,31 @@ void choose(const RouteArgs& a, bool wide, hipStream_t s) {
     else k_route_choose<NE, false><<<(unsigned)ceil_div(a.M, 4), 256, 0, s>>>(a);
 }
 
+// The tiles of a workgroup. Every matrix instruction waits for the conversions
+// of its inputs (they share the 64-bit units), which more tiles share; fewer
+// fill the compute units more evenly. So: the least of the rounds of workgroups
+// over the compute units times the measured us of one round at 4096 columns.
+// By 256 experts of 4096 columns, us for 4x2, 2x2, 2x1, 1x1 tiles: 2048 tokens
+// 80 83 91 99, 1500 tokens 79 82 71 77, 1024 tokens 77 46 50 54, 700 tokens
+// 77 45 50 43, 300 tokens 75 44 29 31.
+void logits(const RouteArgs& a, int64_t te, int64_t tm, int cus, hipStream_t s) {
+    const struct {
+        int rx, rw;
+        double us;
+    } forms[] = {{4, 2, 74.5}, {2, 2, 39.0}, {2, 1, 21.5}, {1, 1, 11.8}};
+    int best = 0;
+    double least = 1e300;
+    for (int f = 0; f < 4; ++f) {
+        const double us = forms[f].us * (double)ceil_div(ceil_div(te, forms[f].rw) * ceil_div(tm, forms[f].rx), cus);
+        if (us < least) least = us, best = f;
+    }
+    const dim3 grid((unsigned)ceil_div(te, forms[best].rw), (unsigned)ceil_div(tm, forms[best].rx));
+    if (best == 0) k_route_logits<4, 2, false><<<grid, 64 * kWaves, 0, s>>>(a);
+    else if (best == 1) k_route_logits<2, 2, false><<<grid, 64 * kWaves, 0, s>>>(a);
+    else if (best == 2) k_route_logits<2, 1, false><<<grid, 64 * kWaves, 0, s>>>(a);
+    else k_route_logits<1, 1, false><<<grid, 64 * kWaves, 0, s>>>(a);
+}
+
 bool route_shape_ok(int64_t experts, int64_t cols, int64_t M) {
     return experts >= 1 && experts <= FP8BLK_MAX_EXPERTS && M >= 1 && M <= FP8BLK_MAX_PANEL && shape_ok(experts, cols);
 }
@@ -360,17 +403,16 @@ extern "C" int fp8blk_moe_route(const uint16_t* w_bf16, const float* bias, int64
     if (!ws || !aligned(ws, kRouteAlign) || ws_bytes < route_workspace_bytes(experts, cols, M)) return FP8BLK_ERR_WORKSPACE;
     RouteArgs a = {w_bf16, x_bf16, bias, static_cast<double*>(ws), ids, weights, (int32_t)experts, (int32_t)M, (int32_t)cols,
                    top_k, score, normalize != 0, route_chunks(cols), scale};
+    const int cus = device_cus();
+    if (cus < 1) return FP8BLK_ERR_HIP;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     (void)hipGetLastError();
     const bool split = route_split(experts, M);
     const int64_t te = ceil_div(experts, kTile), tm = ceil_div(M, kTile);
-    if (split) {
-        k_route_logits<1, true><<<dim3((unsigned)te, (unsigned)tm, (unsigned)ceil_div(a.chunks, 4)), 256, 0, s>>>(a);
-    } else {
-        // two by two tiles a wave halve its reads, where that leaves two waves a SIMD
-        if (te * tm >= 2048) k_route_logits<2, false><<<dim3((unsigned)ceil_div(te, 2), (unsigned)ceil_div(tm, 2)), 256, 0, s>>>(a);
-        else k_route_logits<1, false><<<dim3((unsigned)te, (unsigned)tm), 256, 0, s>>>(a);
-    }
+    if (split)
+        k_route_logits<1, 1, true><<<dim3((unsigned)te, (unsigned)tm, (unsigned)ceil_div(a.chunks, kSplitWaves)), 64 * kSplitWaves, 0, s>>>(a);
+    else
+        logits(a, te, tm, cus, s);
     if (experts <= 64) choose<1>(a, split, s);
     else if (experts <= 128) choose<2>(a, split, s);
     else if (experts <= 256) choose<4>(a, split, s);

@@ -132,6 +132,22 @@ def test_tokens_do_not_depend_on_the_panel(gpu):
             assert torch.equal(i1, ids[:n]) and torch.equal(p1, p[:n]), (E, n)
 
 
+@pytest.mark.parametrize("M,E,cols", [(200, 250, 336), (515, 250, 1552), (990, 250, 336), (2030, 250, 336), (4100, 250, 1040)])
+def test_large_panels(gpu, M, E, cols):
+    """1, 2, 4 and 8 tiles a workgroup, with rows and experts missing from the
+    last, and the same tokens alone."""
+    x, w, b = _inputs(M + cols, M, E, cols, True)
+    ids, p = _run(gpu, x, w, b, 1, 6, True, 1.5)
+    want, q, _ = route(x, w, b, 1, 6, True, 1.5)
+    v = (torch.sigmoid(x.double() @ w.double().t()) + b.double()).sort(dim=1, descending=True).values
+    clear = ((v[:, :6] - v[:, 1:7]) > 1e-11).all(1)  # of so many choices some may tie
+    assert clear.float().mean() > 0.999 and torch.equal(ids[clear].long(), want[clear])
+    assert ((p.double() - q).abs() <= (U + 1e-12) * q.abs() + 2.0 ** -150)[clear].all()
+    for at in (0, M // 2, M - 1):
+        i1, p1 = _run(gpu, x[at:at + 1], w, b, 1, 6, True, 1.5)
+        assert torch.equal(i1, ids[at:at + 1]) and torch.equal(p1, p[at:at + 1]), at
+
+
 def test_largest_panel(gpu):
     x, w, b = _inputs(14, 65536, 9, 16, True)
     ids, p = _run(gpu, x, w, b, 1, 2, True, 1.0)
