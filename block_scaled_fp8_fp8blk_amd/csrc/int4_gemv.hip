@@ -15,18 +15,25 @@
 // bytes and one scaled conversion turns two of them into bf16: 7 instructions
 // for 8 weights.
 //
-// The token panel lies in LDS in the order the instruction's operand takes it,
-// so that a step's four reads are 16 bytes per lane without bank conflicts;
-// panels larger than kPanelBytes are staged in pieces. Workgroups are
-// persistent, one or more per compute unit; a wave takes a tile of 16 weight
-// rows x 512 columns at a time: lane (n, k) = (l % 16, l / 16) loads 16 bytes,
-// 32 codes, of row n in each 128-column step, and the loads of its next
-// 512 columns are in flight while it computes. Where a group is shorter than
-// a step, an exchange of the lane group with the dword index hands lane group
-// k the k-th eighth of each 32-column block, so that one instruction stays
-// inside a group. `split` waves share a row tile's columns, in turn, and add
-// their sums in wave order through LDS; split depends on rows and cols alone,
-// so a token's bits do not depend on M.
+// Many rows (k_int4): the token panel lies in LDS in the order the
+// instruction's operand takes it, so that a step's four reads are 16 bytes per
+// lane without bank conflicts; panels larger than kPanelBytes are staged in
+// pieces. Workgroups are persistent, one per compute unit; a wave takes a tile
+// of 16 weight rows x 512 columns at a time: lane (n, k) = (l % 16, l / 16)
+// loads 16 bytes, 32 codes, of row n in each 128-column step, and the loads of
+// its next 512 columns are in flight while it computes. Where a group is
+// shorter than a step, dwords change places between lane groups so that one
+// instruction stays inside a group (gather_groups). `split` waves share a row
+// tile's columns, in turn, and add their sums in wave order through LDS. Few
+// rows (k_int4_shot): a workgroup a tile, no staging. Which way, and split,
+// depend on rows, cols and group alone, so a token's bits do not depend on M.
+//
+// What bounds it: one token, the codes' way from memory (129280 x 4096 in
+// groups of 128: 51 us, 5.4 TB/s; a plain read of that much reaches 6 TB/s);
+// 16 tokens, besides, 21 vector instructions for each matrix instruction (in
+// groups of 64: 65 us, 4.5 TB/s; of 32: 79 us, 3.9 TB/s); few rows, the launch
+// and one chain of load, sum, join and store (4096 x 4096, 1 token: 5.8 us, 1.5
+// TB/s, 16 tokens 8.0 us).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -421,7 +428,11 @@ __global__ __launch_bounds__(1024) void k_int4_shot(Int4Args a) {
 
 // How a workgroup's waves share the tiles: `split` waves per tile, `across`
 // tiles at once. Chosen for the least work of the busiest of kPlanCUs compute
-// units, counted in tiles x 512 columns.
+// units, counted in tiles x 512 columns, of which one with fewer than kWaves
+// waves does less at a time; a join counts as two. Always 16 tiles across takes
+// 21.9 us where this takes 10.9 (12288 rows x 4096, 1 token), 26.1 against 17.0
+// (16384 rows, 16 tokens); always 4 waves a tile 64 us against 51 (129280
+// rows, 1 token), 54 against 43 (28672 x 8192, 16 tokens).
 struct Plan {
     int split, across;
 };
@@ -446,12 +457,24 @@ template <int G, bool ZERO, int NI>
 void launch(Int4Args a, int cus, hipStream_t s) {
     const int64_t tiles = ceil_div(a.rows, kTile);
     const int supers = (int)ceil_div(a.cols, kSuper);
+    // Up to two tiles a compute unit, a workgroup for each tile: there is too
+    // little for a persistent one to run through (1 token, 8192 rows x 4096: 8.1
+    // us against 8.5; 16 tokens x 2048 columns 7.8 against 10.0; but 16 tokens
+    // x 4096 13.7 against 12.9), and beyond that the other way round (12288
+    // rows x 4096, 16 tokens 19.8 against 16.1; 16384 rows, 1 token 14.5
+    // against 12.5, 16 tokens 24.8 against 17.0).
     if (tiles <= 2 * kPlanCUs) {
-        const int64_t w2 = ceil_div(a.cols, 2 * kStep), w4 = ceil_div(a.cols, 4 * kStep);
-        if (tiles * w2 <= 8 * kPlanCUs)
-            k_int4_shot<G, ZERO, NI, 2><<<(int)tiles, 64 * (int)(w2 < kWaves ? w2 : kWaves), 0, s>>>(a);
-        else
-            k_int4_shot<G, ZERO, NI, 4><<<(int)tiles, 64 * (int)(w4 < kWaves ? w4 : kWaves), 0, s>>>(a);
+        // Of 4 steps a wave where that gives at least 4 waves that all have 4 and
+        // few scales (2048 rows x 2048 columns in groups of 128: 3.7 us against
+        // 3.9 with 2 steps, 1024 x 7168 6.4 against 7.0, 4096 x 4096 5.8 against
+        // 5.9 and of 16 tokens 8.0 against 9.0), else 2 (2001 x 2080 in groups
+        // of 32 4.9 against 5.8, 2880 x 2880 in groups of 64 5.0 against 6.4,
+        // 8192 x 1024 3.8 against 4.2, 4096 x 4096 in groups of 32 6.2 against 6.6).
+        const bool two = a.cols % kSuper != 0 || supers < 4 || (G == 32 && supers <= 8);
+        const int64_t w = ceil_div(a.cols, (two ? 2 : 4) * kStep);
+        const int grid = (int)tiles, threads = 64 * (int)(w < kWaves ? w : kWaves);
+        if (two) k_int4_shot<G, ZERO, NI, 2><<<grid, threads, 0, s>>>(a);
+        else k_int4_shot<G, ZERO, NI, 4><<<grid, threads, 0, s>>>(a);
         return;
     }
     const Plan p = plan(tiles, supers);
@@ -463,6 +486,9 @@ void launch(Int4Args a, int cus, hipStream_t s) {
                        (p.split > 1 ? (size_t)waves * NI * 256 : (size_t)waves * kBlockBytes);
     const int64_t groups = ceil_div(tiles, p.across);
     const int grid = (int)(groups < cus ? groups : cus);
+    // A wave that has a tile to itself reads its scales as blocks: 57399 rows x
+    // 352 in groups of 32 8.1 us against 10.1 row by row, 129280 x 4096 in
+    // groups of 128 51 against 56, of 64 with 16 tokens 65 against 69.
     if (p.split > 1) k_int4<G, ZERO, NI, false><<<grid, 64 * waves, lds, s>>>(a);
     else k_int4<G, ZERO, NI, true><<<grid, 64 * waves, lds, s>>>(a);
 }
