@@ -1,6 +1,28 @@
-// A whole mixture-of-experts layer over FP4 experts for a few tokens: two
-// launches of one kernel template (gate and up with silu; down), and the
-// weighted sum over a token's experts.
+// A whole mixture-of-experts layer over FP4 experts for a few tokens: gate and
+// up with silu, down, and the weighted sum over a token's experts.
+//
+// A choice of an expert by a token is a slot. Gate and up, and down, are two
+// launches of one kernel (k_moe): a workgroup takes an expert's tiles of 16
+// weight rows for up to four slots that go to it, so that the tokens that share
+// an expert read it once; which slots those are every workgroup finds from the
+// ids, and those that are not the first of theirs end at once. No list of
+// tokens by expert is built, and nothing goes to the host.
+//
+// The sums are v_mfma_f32_16x16x32_bf16 on weights widened to bf16, exact for
+// both formats. MXFP4: with their scale, a power of two, in the conversion. An
+// operand of 16 rows holds 4 slots, and for down every slot's h as three bf16
+// pieces, the f32 value to its last bit or so: h never loses more than f32
+// does. NVFP4: an e4m3 scale times a code is a bf16 value, but a conversion
+// takes powers of two only, so the instruction runs on the codes, with the
+// 16-column blocks of 32 columns in rows of their own (the operand's other
+// half zero), and f32 scales its results. More instructions for every byte,
+// hence NVFP4's distance from MXFP4 below.
+//
+// What bounds it: the experts' weights. 16 tokens, 8 of 128 experts of
+// 4096x2048 MXFP4, 1.1 GB: 196 us, 5.6 TB/s (a plain read of that much
+// reaches 6 to 6.9); NVFP4 232 us, 5.0 TB/s. One token, 8 of 64: 31.4 and 35.6
+// us, 3.4 and 3.2 TB/s, where the three launches' starts and ends are half.
+// Small layers are latency (2 tokens, 2 of 8 of 512x512: 9.6 us).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -22,8 +44,7 @@ constexpr int64_t kMoeAlign = 256;
 constexpr int kTile = 16;   // weight rows of a matrix instruction
 constexpr int kStep = 128;  // columns of one 16-byte load per lane
 constexpr int kWaves = 8;   // of a workgroup, at most
-constexpr int kTurns = 4;   // tiles that a workgroup takes one after another, at most,
-constexpr int kGroups = 2048;  // and only where there are this many workgroups even so
+constexpr int kBusy = 512;  // workgroups with work: two a compute unit
 // Up to so many weights of down (tokens x experts of a token x slab), down and
 // the sum over the experts are one launch: it saves about 3 us of launch and
 // start, but has few workgroups and lets tokens read an expert that they share
@@ -496,22 +517,43 @@ __global__ __launch_bounds__(64) void k_moe_sum(const float* __restrict__ part, 
     *reinterpret_cast<v4f*>(y + o) = s;
 }
 
+// How many slots' workgroups have something to do, to be expected of tokens
+// that choose freely: one for every expert that is chosen, or for every `most`
+// slots where they are more.
+inline double busy_slots(const MoeArgs& a) {
+    const double idle = a.K < a.experts ? 1.0 - (double)a.K / (double)a.experts : 0.0;
+    double none = 1.0;  // that no token goes to an expert
+    for (int m = 0; m < a.slots / a.K; ++m) none *= idle;
+    const double chosen = (double)a.experts * (1.0 - none), full = (double)a.slots / a.most;
+    return chosen > full ? chosen : full;
+}
+
 template <int FMT, bool DOWN, int NS>
 void launch_steps(MoeArgs a, hipStream_t s) {
     using U = Unit<FMT, DOWN, NS>;
     const int64_t slices = ceil_div(a.cols, NS * kStep), tiles = ceil_div(a.rows, kTile * U::R);
     const int waves = (int)(slices < kWaves ? slices : kWaves);
     const int64_t row_bytes = slices * NS * kStep * 2 * U::LANES;
-    // The widest operands (1 row of FP8BLK_MAX_COLS columns of x, 3 of
-    // FP8BLK_MAX_INTER of h) leave 30 KB of LDS for the waves' scales and sums.
+    // LDS for the operand, besides the waves' scales and sums: at least 1 row of
+    // FP8BLK_MAX_COLS columns of x or 3 of FP8BLK_MAX_INTER of h. All of it goes
+    // to slots that share an expert's weights, although fewer workgroups then
+    // fit a compute unit (16 tokens, 4 of 8 experts of 2048x4096 MXFP4: 72 us,
+    // 85 with at most 64 KB; 8 tokens, 6 of 32 of 5120x8192 NVFP4: 477 against 548).
+    const int64_t own = waves * U::T * (kTile * U::ROW + 512), room = 160 * 1024 - own;
     static_assert((DOWN ? FP8BLK_MAX_INTER : FP8BLK_MAX_COLS) * 2 * U::LANES + kWaves * U::T * (kTile * U::ROW + 512) <= 160 * 1024,
                   "LDS of a workgroup");
     a.most = a.slots / a.K < U::PER ? a.slots / a.K : U::PER;
-    while (a.most > 1 && a.most * row_bytes > 64 * 1024) a.most /= 2;
-    const int64_t turns = tiles * a.slots / kGroups;
-    a.turns = (int)(turns < 1 ? 1 : turns > kTurns ? kTurns : turns);
+    while (a.most > 1 && a.most * row_bytes > room) a.most /= 2;
+    // Several tiles a workgroup, for whose operand and start it pays once while
+    // the next tile's loads are in flight, where about two workgroups with work
+    // for each compute unit are left. us for 1, 2, 4 and 8 tiles at most: 16
+    // tokens, 8 of 128 experts of 4096x2048 MXFP4 240, 203, 196, 207; 4 tokens,
+    // 8 of 128 of 4096x1536 NVFP4 92, 84, 73, 73; where it leaves too few, 14
+    // tokens, 5 of 6 of 2560x1024 NVFP4, 4 tiles 60 and this rule's 2 48.
+    const double turns = (double)tiles * busy_slots(a) / kBusy;
+    a.turns = turns >= 3.0 ? 4 : turns >= 1.5 ? 2 : 1;
     const dim3 grid((unsigned)ceil_div(tiles, a.turns), (unsigned)a.slots);
-    k_moe<FMT, DOWN, NS><<<grid, 64 * waves, (size_t)(a.most * row_bytes + waves * U::T * (kTile * U::ROW + 512)), s>>>(a);
+    k_moe<FMT, DOWN, NS><<<grid, 64 * waves, (size_t)(a.most * row_bytes + own), s>>>(a);
 }
 
 // Steps a wave takes at a time: half as many where the columns are few. Down:
