@@ -46,13 +46,13 @@ constexpr int kStep = 128;  // columns of one 16-byte load per lane
 constexpr int kWaves = 8;   // of a workgroup, at most
 constexpr int kBusy = 512;  // workgroups with work: two a compute unit
 // Up to so many weights of down (tokens x experts of a token x slab), down and
-// the sum over the experts are one launch: it saves about 3 us of launch and
-// start, but has few workgroups and lets tokens read an expert that they share
-// once each. Measured, one launch against two: 3 tokens, 4 of 1440x736 experts
-// (13e6) 15.3 against 16.6 us; 6 tokens (25e6) 20.4 against 22.0; 4 tokens, 6
-// of 2048x1024 (50e6) 26.2 against 23.3; 1 token, 8 of 4096x2048 (67e6) 35.0
-// against 32.5.
-constexpr int64_t kFewWeights = 1 << 25;
+// the sum over the experts are one launch, which saves a launch's start and end
+// but lets tokens read an expert that they share once each. One launch against
+// two, us: 2 tokens, 2 of 8 experts of 512x512 MXFP4 7.9, 10.8; 6 tokens, 4 of
+// 32 of 1440x736 (25e6 weights) 20.1, 23.0; 4 tokens, 8 of 128 of 2048x768
+// (50e6) 24.9, 27.5, NVFP4 28.0, 30.7; 4 tokens, 2 of 8 of 4096x2048 (67e6)
+// 36.7, 31.1; 8 tokens, 6 of 64 of 2048x1024 (101e6) 43.2, 38.2.
+constexpr int64_t kFewWeights = 50 << 20;
 constexpr int kPieces = 3;  // bf16 values that hold an f32 h
 constexpr int kSlots = FP8BLK_MAX_M * FP8BLK_MAX_TOP_K;
 
@@ -396,10 +396,10 @@ __global__ __launch_bounds__(64 * kWaves, 3) void k_moe(MoeArgs a) {
     }
 }
 
-// Down and the weighted sum in one, for a few tokens: a workgroup takes 16
-// rows of the output of one token and walks the experts that it goes to, four
-// at a time, so that their sum stays in the workgroup. Every sum is taken as
-// k_moe and k_moe_sum take it. (Tokens read an expert that they share once
+// Down and the weighted sum in one, for a few tokens: a workgroup takes 16 rows
+// of the output of one token, of all its experts at once, a wave four of them
+// and a slice of columns, so that their sum stays in the workgroup. Every sum is taken
+// as k_moe and k_moe_sum take it. (Tokens read an expert that they share once
 // each, which is why many tokens go the other way.)
 template <int FMT, int NS>
 __global__ __launch_bounds__(64 * kWaves, 2) void k_moe_token(MoeArgs a, const float* __restrict__ weights, const float* base,
@@ -407,87 +407,87 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_moe_token(MoeArgs a, const f
     using U = Unit<FMT, true, NS>;
     constexpr int ROWS = U::T * kPieces;  // operand rows in LDS
     extern __shared__ uint4 lds[];        // the waves' operands, block scales and sums
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, n = lane & 15, kg = lane >> 4;
-    const int m = blockIdx.y, row0 = blockIdx.x * kTile, c0 = wave * U::SLICE;
+    const int lane = threadIdx.x, n = lane & 15, kg = lane >> 4, slices = blockDim.y, waves = blockDim.z * slices;
+    const int slice = __builtin_amdgcn_readfirstlane(threadIdx.y), group = __builtin_amdgcn_readfirstlane(threadIdx.z);
+    const int wave = group * slices + slice;
+    const int m = blockIdx.y, row0 = blockIdx.x * kTile, c0 = slice * U::SLICE, k0 = group * U::T;
     uint4* const own = lds + wave * NS * 16 * ROWS;
     uint8_t* const scales = reinterpret_cast<uint8_t*>(lds + waves * NS * 16 * ROWS) + wave * U::T * kTile * U::ROW;
     float* const sums = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(lds + waves * NS * 16 * ROWS) +
-                                                 waves * U::T * kTile * U::ROW);  // [wave][k][lane group 0, 1][row]
+                                                 waves * U::T * kTile * U::ROW);  // [slice][k][lane group 0, 1][row]
+    const int padded = blockDim.z * U::T;  // K, up to whole waves' experts
     // A choice that is none takes part as expert 0 and is left out of the sum.
-    const auto from = [&](int k0) {
-        return [&a, m, row0, k0](int t) {
-            const int e = a.ids[m * a.K + min(k0 + t, a.K - 1)];
-            return Where{e >= 0 && e < a.experts ? e : 0, row0};
-        };
+    const auto from = [&](int t) {
+        const int e = a.ids[m * a.K + min(k0 + t, a.K - 1)];
+        return Where{e >= 0 && e < a.experts ? e : 0, row0};
     };
+    const uint4* in = own + kg * ROWS + (FMT == kMX ? min(n & 3, 2) : min((n & 7) >> 1, 2));
+    const bool live = (kg >> 1) == (n & 1) && (n & 7) < 6;  // as in k_moe
+    uint4 v[U::T][kPieces];
+    const int k = lane % 4, j = lane / 4 % 4, c = c0 + lane / 16 * kStep + (FMT == kMX ? 32 * k + 8 * j : 32 * j + 8 * k);
+    const bool mine = lane < NS * 16;
+#pragma unroll
+    for (int t = 0; t < U::T; ++t)
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p)
+            v[t][p] = load_global16(a.in + (int64_t)((m * a.K + min(k0 + t, a.K - 1)) * kPieces + p) * a.cols + min(c, a.cols - 8));
     Pair<U::T> b[NS / 2];
     Scales<U> sr;
 #pragma unroll
-    for (int s = 0; s < NS / 2; ++s) issue<U>(b[s], a, from(0), lane, c0 + 2 * s * kStep);
-    issue_scales<U>(sr, a, from(0), lane, c0);
-
-    const uint4* in = own + kg * ROWS + (FMT == kMX ? min(n & 3, 2) : min((n & 7) >> 1, 2));
-    const bool live = (kg >> 1) == (n & 1) && (n & 7) < 6;  // as in k_moe
-    for (int k0 = 0; k0 < a.K; k0 += U::T) {
-#pragma unroll
-        for (int t = 0; t < U::T; ++t) {
-            const int64_t slot = m * a.K + min(k0 + t, a.K - 1);
-            const uint16_t* src = a.in + slot * kPieces * a.cols;
-#pragma unroll
-            for (int i = 0; i < (NS * 16 + 63) / 64; ++i) {
-                const int o = i * 64 + lane, k = o % 4, j = o / 4 % 4;
-                const int c = c0 + o / 16 * kStep + (FMT == kMX ? 32 * k + 8 * j : 32 * j + 8 * k);
-                if (o >= NS * 16) continue;
-#pragma unroll
-                for (int p = 0; p < kPieces; ++p)
-                    own[o * ROWS + t * kPieces + p] =
-                        c < a.cols ? load_global16(src + (int64_t)p * a.cols + c) : make_uint4(0, 0, 0, 0);
-            }
-        }
-        place_scales<U>(sr, scales, lane);
-        const bool more = k0 + U::T < a.K;
-        if (more) issue_scales<U>(sr, a, from(k0 + U::T), lane, c0);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        v4f acc[U::T];
-#pragma unroll
-        for (int t = 0; t < U::T; ++t) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int s = 0; s < NS / 2; ++s) {
-            compute<FMT, true, U, true>(b[s], in + 32 * s * ROWS, 4 * ROWS, scales + n * U::ROW + s * U::PAIR, kg, live, acc);
-            if (more) issue<U>(b[s], a, from(k0 + U::T), lane, c0 + 2 * s * kStep);
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
+    for (int s = 0; s < NS / 2; ++s) issue<U>(b[s], a, from, lane, c0 + 2 * s * kStep);
+    issue_scales<U>(sr, a, from, lane, c0);
+    __builtin_amdgcn_sched_barrier(0);  // every load goes out before the first is waited for
+    if (mine)
 #pragma unroll
         for (int t = 0; t < U::T; ++t)
-            if (lane < 32 && k0 + t < a.K)
-                sums[(wave * FP8BLK_MAX_TOP_K + k0 + t) * 32 + lane] =
-                    FMT == kMX ? acc[t][0] + (acc[t][1] + acc[t][2]) : acc[t][0];
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p) own[lane * ROWS + t * kPieces + p] = c < a.cols ? v[t][p] : make_uint4(0, 0, 0, 0);
+    place_scales<U>(sr, scales, lane);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    v4f acc[U::T];
+#pragma unroll
+    for (int t = 0; t < U::T; ++t) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int s = 0; s < NS / 2; ++s)
+        compute<FMT, true, U, true>(b[s], in + 32 * s * ROWS, 4 * ROWS, scales + n * U::ROW + s * U::PAIR, kg, live, acc);
+#pragma unroll
+    for (int t = 0; t < U::T; ++t)
+        if (lane < 32) sums[(slice * padded + k0 + t) * 32 + lane] = FMT == kMX ? acc[t][0] + (acc[t][1] + acc[t][2]) : acc[t][0];
+    // The first wave joins: lane (k, row) the slices of expert k of every four,
+    // then the first 16 lanes the experts.
+    constexpr int ROUNDS = FP8BLK_MAX_TOP_K / U::T;
+    const int row = row0 + n;
+    bool is[ROUNDS];
+    float top[ROUNDS], weight[ROUNDS];
+#pragma unroll
+    for (int i = 0; i < ROUNDS; ++i) {
+        if (i * U::T >= a.K) break;
+        const int slot = m * a.K + min(i * U::T + kg, a.K - 1), e = a.ids[slot];
+        is[i] = e >= 0 && e < a.experts;
+        top[i] = a.top[0] && is[i] ? a.top[0][e] : 1.0f;
+        weight[i] = weights[slot];
     }
+    float s = base && row < a.rows ? base[(int64_t)m * a.rows + row] : 0.0f;
     __syncthreads();
-    // The k-th expert's value of row n, in place of the first wave's sum.
-    for (int o = threadIdx.x; o < a.K * kTile; o += blockDim.x) {
-        const int k = o / kTile, r = o % kTile, e = a.ids[m * a.K + k];
-        if (e < 0 || e >= a.experts) continue;
-        float v = 0.0f;
-        for (int w = 0; w < waves; ++w) {
-            const float* p = sums + (w * FP8BLK_MAX_TOP_K + k) * 32;
-            const float f = U::PER == 2 ? p[r] + p[r + 16] : p[r];
-            v = w == 0 ? f : v + f;
+    if (wave > 0) return;
+#pragma unroll
+    for (int i = 0; i < ROUNDS; ++i) {
+        if (i * U::T >= a.K) break;
+        float f = 0.0f;
+        for (int w = 0; w < slices; ++w) {
+            const float* p = sums + (w * padded + i * U::T + kg) * 32 + n;
+            const float g = U::PER == 2 ? p[0] + p[16] : p[0];
+            f = w == 0 ? g : f + g;
         }
-        if (a.top[0]) v *= a.top[0][e];
-        sums[k * 32 + r] = v;
+        f *= top[i];
+#pragma unroll
+        for (int t = 0; t < U::T; ++t) {
+            const float ft = __shfl(f, kTile * t + n), wt = __shfl(weight[i], kTile * t);
+            if (__shfl((int)is[i], kTile * t) && i * U::T + t < a.K) s = __builtin_fmaf(wt, ft, s);
+        }
     }
-    __syncthreads();
-    const int row = row0 + threadIdx.x;
-    if (threadIdx.x >= kTile || row >= a.rows) return;
-    float s = base ? base[(int64_t)m * a.rows + row] : 0.0f;
-    for (int k = 0; k < a.K; ++k) {
-        const int slot = m * a.K + k, e = a.ids[slot];
-        if (e >= 0 && e < a.experts) s = __builtin_fmaf(weights[slot], sums[k * 32 + threadIdx.x], s);
-    }
-    y[(int64_t)m * a.rows + row] = s;
+    if (lane < kTile && row < a.rows) y[(int64_t)m * a.rows + row] = s;
 }
 
 // y = base + the weighted sum of a token's experts, in order of k. All loads
@@ -574,9 +574,9 @@ void launch(const MoeArgs& a, hipStream_t s) {
 template <int FMT, int NS>
 void launch_token(const MoeArgs& a, int M, const float* weights, const float* base, float* y, hipStream_t s) {
     using U = Unit<FMT, true, NS>;
-    const int waves = (int)ceil_div(a.cols, U::SLICE);
-    const size_t lds = (size_t)waves * (NS * 256 * U::T * kPieces + U::T * kTile * U::ROW + FP8BLK_MAX_TOP_K * 128);
-    k_moe_token<FMT, NS><<<dim3((unsigned)ceil_div(a.rows, kTile), (unsigned)M), 64 * waves, lds, s>>>(a, weights, base, y);
+    const dim3 block(64, (unsigned)ceil_div(a.cols, U::SLICE), (unsigned)ceil_div(a.K, U::T));
+    const size_t lds = (size_t)(block.y * block.z) * (NS * 256 * U::T * kPieces + U::T * kTile * U::ROW + U::T * 128);
+    k_moe_token<FMT, NS><<<dim3((unsigned)ceil_div(a.rows, kTile), (unsigned)M), block, lds, s>>>(a, weights, base, y);
 }
 
 template <int FMT>
@@ -588,8 +588,10 @@ void run(const fp4_moe_layer& l, const uint16_t* x, int M, const int32_t* ids, c
     launch<FMT, false>(a, s);
     a = {{l.down, nullptr}, {l.down_scales, nullptr}, {l.down_global, nullptr}, pieces, ids, nullptr, part,
          l.experts, H, I, M * K, K, 1, 1, 0.0f};
-    if ((int64_t)M * K * H * I <= kFewWeights && I <= kWaves * 4 * kStep) {
-        if (half_steps(true, I)) launch_token<FMT, 2>(a, M, weights, base, y, s);
+    const int NS = half_steps(true, I) ? 2 : 4;
+    const int64_t waves = ceil_div(I, NS * kStep) * ceil_div(K, Unit<FMT, true, 4>::T);
+    if ((int64_t)M * K * H * I <= kFewWeights && waves <= kWaves) {
+        if (NS == 2) launch_token<FMT, 2>(a, M, weights, base, y, s);
         else launch_token<FMT, 4>(a, M, weights, base, y, s);
         return;
     }
