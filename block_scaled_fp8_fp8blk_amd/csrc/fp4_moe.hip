@@ -291,7 +291,8 @@ __global__ __launch_bounds__(64 * kWaves, 3) void k_moe(MoeArgs a) {
     using U = Unit<FMT, DOWN, NS>;
     constexpr int SLICE = U::SLICE;
     extern __shared__ uint4 lds[];  // the operand, the waves' block scales and their sums
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, n = lane & 15, kg = lane >> 4;
+    const int lane = threadIdx.x & 63, n = lane & 15, kg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int slot = blockIdx.y, tiles = (a.rows + kTile * U::R - 1) / (kTile * U::R);
     const int end = min((int)(blockIdx.x + 1) * a.turns, tiles);
 
@@ -328,30 +329,51 @@ __global__ __launch_bounds__(64 * kWaves, 3) void k_moe(MoeArgs a) {
     if (before % a.most != 0) return;
 
     int tile = blockIdx.x * a.turns, c0 = wave * SLICE;
+    // The operand: [step][32 columns][lane group][row], zeros past the last
+    // column; a wave reads only the slices that it has staged itself. Its first
+    // rows are asked for before the weights and so are there before them.
+    const int rows_in = a.most * U::LANES, live_rows = count * U::LANES;
+    const auto operand_at = [&](int p0, int o) {  // column of 8 that unit o of a slice holds
+        const int k = o % 4, j = o / 4 % 4;
+        return p0 + o / 16 * kStep + (FMT == kMX ? 32 * k + 8 * j : 32 * j + 8 * k);
+    };
+    const auto load_operand = [&](int r, int c) {
+        const int sl = __builtin_amdgcn_readlane(member, r / U::LANES);
+        const int64_t at = DOWN ? (int64_t)sl * kPieces + r % kPieces : (int64_t)(sl / a.K);
+        return load_global16(a.in + at * a.cols + min(c, a.cols - 8));
+    };
+    constexpr int FIRST = DOWN ? kPieces : 2, ROUNDS = (NS * 16 + 63) / 64;
+    uint4 first[ROUNDS][FIRST];
+#pragma unroll
+    for (int i = 0; i < ROUNDS; ++i)
+#pragma unroll
+        for (int r = 0; r < FIRST; ++r)
+            if (DOWN || r < live_rows) first[i][r] = load_operand(r, operand_at(c0, i * 64 + lane));
     Pair<U::T> b[NS / 2];
     Scales<U> sr;
+    issue_scales<U>(sr, a, SideBySide<U>{expert, tile}, lane, c0);
 #pragma unroll
     for (int s = 0; s < NS / 2; ++s) issue<U>(b[s], a, SideBySide<U>{expert, tile}, lane, c0 + 2 * s * kStep);
-    issue_scales<U>(sr, a, SideBySide<U>{expert, tile}, lane, c0);
-
-    // The operand: [step][32 columns][lane group][row], zeros past the last
-    // column; a wave reads only the slices that it has staged itself.
-    const int rows_in = a.most * U::LANES, live_rows = count * U::LANES;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < ROUNDS; ++i) {
+        const int o = i * 64 + lane;
+        const bool in = operand_at(c0, o) < a.cols;
+#pragma unroll
+        for (int r = 0; r < FIRST; ++r)
+            if (o < NS * 16 && (DOWN || r < live_rows)) lds[(c0 / 8 + o) * rows_in + r] = in ? first[i][r] : make_uint4(0, 0, 0, 0);
+    }
     for (int p0 = c0; p0 < a.cols; p0 += waves * SLICE)
-        for (int r0 = 0; r0 < live_rows; r0 += 4)
+        for (int r0 = p0 == c0 ? FIRST : 0; r0 < live_rows; r0 += 4)
             for (int i = 0; i < NS * 16; i += 64) {
                 uint4 v[4];
-                const int o = i + lane, k = o % 4, j = o / 4 % 4;
-                const int c = p0 + o / 16 * kStep + (FMT == kMX ? 32 * k + 8 * j : 32 * j + 8 * k);
+                const int o = i + lane, c = operand_at(p0, o);
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const int r = min(r0 + p, live_rows - 1), sl = __builtin_amdgcn_readlane(member, r / U::LANES);
-                    const int64_t at = DOWN ? (int64_t)sl * kPieces + r % kPieces : (int64_t)(sl / a.K);
-                    v[p] = c < a.cols ? load_global16(a.in + at * a.cols + c) : make_uint4(0, 0, 0, 0);
-                }
+                for (int p = 0; p < 4; ++p) v[p] = load_operand(min(r0 + p, live_rows - 1), c);
 #pragma unroll
                 for (int p = 0; p < 4; ++p)
-                    if (r0 + p < live_rows && o < NS * 16) lds[(p0 / 8 + o) * rows_in + r0 + p] = v[p];
+                    if (r0 + p < live_rows && o < NS * 16)
+                        lds[(p0 / 8 + o) * rows_in + r0 + p] = c < a.cols ? v[p] : make_uint4(0, 0, 0, 0);
             }
     // the wave's own lanes read what the others wrote
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -433,9 +455,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_moe_token(MoeArgs a, const f
             v[t][p] = load_global16(a.in + (int64_t)((m * a.K + min(k0 + t, a.K - 1)) * kPieces + p) * a.cols + min(c, a.cols - 8));
     Pair<U::T> b[NS / 2];
     Scales<U> sr;
+    issue_scales<U>(sr, a, from, lane, c0);
 #pragma unroll
     for (int s = 0; s < NS / 2; ++s) issue<U>(b[s], a, from, lane, c0 + 2 * s * kStep);
-    issue_scales<U>(sr, a, from, lane, c0);
     __builtin_amdgcn_sched_barrier(0);  // every load goes out before the first is waited for
     if (mine)
 #pragma unroll
