@@ -32,7 +32,7 @@
 // groups of 128: 51 us, 5.4 TB/s; a plain read of that much reaches 6 TB/s);
 // 16 tokens, besides, 21 vector instructions for each matrix instruction (in
 // groups of 64: 65 us, 4.5 TB/s; of 32: 79 us, 3.9 TB/s); few rows, the launch
-// and one chain of load, sum, join and store (4096 x 4096, 1 token: 5.8 us, 1.5
+// and one chain of load, sum, join and store (4096 x 4096, 1 token: 5.7 us, 1.5
 // TB/s, 16 tokens 8.0 us).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -374,19 +374,32 @@ __global__ __launch_bounds__(1024) void k_int4_shot(Int4Args a) {
     for (int c0 = wave * NS * kStep; c0 < a.cols; c0 += waves * NS * kStep) {
         uint4 q[NS], v[NS][4];
         Groups<N> g;
+        const auto load_codes = [&]() {
 #pragma unroll
-        for (int s = 0; s < NS; s += 2) {
-            const int c = min(c0 + s * kStep + 16 * (lane & 8) + 32 * kg, last) / 2;
-            q[s] = load_stream16(lo + c);
-            q[s + 1] = load_stream16(hi + c);
-        }
+            for (int s = 0; s < NS; s += 2) {
+                const int c = min(c0 + s * kStep + 16 * (lane & 8) + 32 * kg, last) / 2;
+                q[s] = load_stream16(lo + c);
+                q[s + 1] = load_stream16(hi + c);
+            }
+        };
+        const auto load_x = [&]() {
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[s][j] = load_global16(x + min(c0 + s * kStep + gathered_column<G>(j, kg), a.cols - 8));
+        };
+        // Loads arrive in order: 4 steps' codes are asked for last, to be used one
+        // by one as they come (16 tokens, 8192 rows x 4096: 12.7 us against 13.7,
+        // 4096 x 16384 23.6 against 25.6); 2 steps' first, being the longest wait
+        // (2001 x 2080 4.9 against 5.2).
+        if constexpr (NS == 2) load_codes();
+        else load_x();
         const int64_t g0 = row * (a.cols / G) + c0 / G;
         load_groups<N, ZERO>(g, a.scales + g0, ZERO ? a.zeros + g0 : nullptr, (a.cols - c0) / G);
-#pragma unroll
-        for (int s = 0; s < NS; ++s)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[s][j] = load_global16(x + min(c0 + s * kStep + gathered_column<G>(j, kg), a.cols - 8));
+        if constexpr (NS == 2) load_x();
+        else load_codes();
+        if constexpr (NS == 4) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
             if (s % 2 == 0) {
@@ -459,14 +472,14 @@ void launch(Int4Args a, int cus, hipStream_t s) {
     const int supers = (int)ceil_div(a.cols, kSuper);
     // Up to two tiles a compute unit, a workgroup for each tile: there is too
     // little for a persistent one to run through (1 token, 8192 rows x 4096: 8.1
-    // us against 8.5; 16 tokens x 2048 columns 7.8 against 10.0; but 16 tokens
-    // x 4096 13.7 against 12.9), and beyond that the other way round (12288
-    // rows x 4096, 16 tokens 19.8 against 16.1; 16384 rows, 1 token 14.5
-    // against 12.5, 16 tokens 24.8 against 17.0).
+    // us against 8.5, 16 tokens 12.7 against 13.0; 16 tokens x 2048 columns 7.7
+    // against 10.0), and beyond that the other way round (12288 rows x 4096, 16
+    // tokens 19.8 against 16.1; 16384 rows, 1 token 14.5 against 12.5, 16
+    // tokens 24.8 against 17.0).
     if (tiles <= 2 * kPlanCUs) {
         // Of 4 steps a wave where that gives at least 4 waves that all have 4 and
         // few scales (2048 rows x 2048 columns in groups of 128: 3.7 us against
-        // 3.9 with 2 steps, 1024 x 7168 6.4 against 7.0, 4096 x 4096 5.8 against
+        // 3.9 with 2 steps, 1024 x 7168 6.4 against 7.0, 4096 x 4096 5.7 against
         // 5.9 and of 16 tokens 8.0 against 9.0), else 2 (2001 x 2080 in groups
         // of 32 4.9 against 5.8, 2880 x 2880 in groups of 64 5.0 against 6.4,
         // 8192 x 1024 3.8 against 4.2, 4096 x 4096 in groups of 32 6.2 against 6.6).
