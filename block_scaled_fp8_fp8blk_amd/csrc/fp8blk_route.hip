@@ -237,16 +237,20 @@ __device__ __forceinline__ double lane_value64(double v, int lane) {
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// A logit from its chunks' sums, 32 loads at a time.
-__device__ __forceinline__ double add_chunks(const RouteArgs& a, int64_t at) {
+// A logit from its chunks' sums, N loads at a time, and behind the first of
+// them its expert's bias.
+template <int N>
+__device__ __forceinline__ double add_chunks(const RouteArgs& a, int64_t at, int e, float& bias) {
     const int64_t n = (int64_t)a.M * a.E;
     double s[kWaves] = {};
-    for (int c = 0; c < a.chunks; c += 32) {
-        double v[32];
+    for (int c = 0; c < a.chunks; c += N) {
+        double v[N];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = a.logits[at + min(c + k, a.chunks - 1) * n];
+        for (int k = 0; k < N; ++k) v[k] = a.logits[at + min(c + k, a.chunks - 1) * n];
+        if (c == 0 && a.bias) bias = a.bias[e];
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
+        for (int k = 0; k < N; ++k)
             if (c + k < a.chunks) s[k % kWaves] += v[k];
     }
     return tree(s);
@@ -260,16 +264,20 @@ __device__ __forceinline__ double own_score(int score, double l) {
 }
 
 // One wave per token; lane l holds experts l, l + 64, ... WIDE: the logits are
-// first added by a workgroup.
+// first added by a workgroup, a thread each.
 template <int NE, bool WIDE>
-__global__ __launch_bounds__(256) void k_route_choose(RouteArgs a) {
+__global__ __launch_bounds__(WIDE ? FP8BLK_MAX_EXPERTS : 256) void k_route_choose(RouteArgs a) {
     __shared__ double whole[WIDE ? FP8BLK_MAX_EXPERTS : 1];
+    __shared__ float biases[WIDE ? FP8BLK_MAX_EXPERTS : 1];
     const int lane = threadIdx.x & 63;
     const int64_t m = WIDE ? blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     const double lowest = -__builtin_inf();
     if constexpr (WIDE) {
-        for (int e = threadIdx.x; e < a.E; e += 256) {
-            const double l = add_chunks(a, m * a.E + e);
+        const int e = threadIdx.x;
+        if (e < a.E) {
+            float b = 0.0f;
+            const double l = a.chunks > 16 ? add_chunks<32>(a, m * a.E + e, e, b) : add_chunks<16>(a, m * a.E + e, e, b);
+            biases[e] = b;
             whole[e] = a.score == FP8BLK_SCORE_SOFTMAX ? l : own_score(a.score, l);
         }
         __syncthreads();
@@ -280,7 +288,11 @@ __global__ __launch_bounds__(256) void k_route_choose(RouteArgs a) {
     uint64_t pick[NE];  // ranks; 0: not to be chosen
     float bias[NE];
 #pragma unroll
-    for (int i = 0; i < NE; ++i) bias[i] = a.bias ? a.bias[min(lane + 64 * i, a.E - 1)] : 0.0f;
+    for (int i = 0; i < NE; ++i) {
+        const int e = min(lane + 64 * i, a.E - 1);
+        if constexpr (WIDE) bias[i] = biases[e];
+        else bias[i] = a.bias ? a.bias[e] : 0.0f;
+    }
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
         const int e = lane + 64 * i;
@@ -346,7 +358,7 @@ __global__ __launch_bounds__(256) void k_route_choose(RouteArgs a) {
 
 template <int NE>
 void choose(const RouteArgs& a, bool wide, hipStream_t s) {
-    if (wide) k_route_choose<NE, true><<<(unsigned)a.M, 256, 0, s>>>(a);
+    if (wide) k_route_choose<NE, true><<<(unsigned)a.M, 64 * NE, 0, s>>>(a);
     else k_route_choose<NE, false><<<(unsigned)ceil_div(a.M, 4), 256, 0, s>>>(a);
 }
 
