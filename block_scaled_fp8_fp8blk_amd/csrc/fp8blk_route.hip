@@ -11,10 +11,11 @@
 //     64-bit product of inputs that are converted already: 125 us; of 4096^3:
 //     71 TFLOP/s).
 //   - a few tokens: latency, of two launches, a chain of 32 instructions and a
-//     choice (1 token, 256 experts, 4096 columns: 9.6 us, of which an empty
+//     choice (1 token, 256 experts, 4096 columns: 8.7 us, of which an empty
 //     launch takes 2.6 each).
 //
-// Order of a logit, whatever the panel: chunks of 128 columns, each a chain
+// Order of a logit, whatever the panel: chunks of 128 columns (of 64, 1 token
+// takes 10.7 us for the chunks to add, of 256 9.5 for the chain), each a chain
 // of matrix instructions from 0; eight sums over the chunks c % 8 = 0 .. 7 in
 // order; then their tree. Few tiles: every chunk is a wave of its own, the
 // chunks' sums go to the workspace, and the kernel that chooses adds them.
@@ -266,7 +267,7 @@ __device__ __forceinline__ double own_score(int score, double l) {
 // One wave per token; lane l holds experts l, l + 64, ... WIDE: the logits are
 // first added by a workgroup, a thread each.
 template <int NE, bool WIDE>
-__global__ __launch_bounds__(WIDE ? FP8BLK_MAX_EXPERTS : 256) void k_route_choose(RouteArgs a) {
+__global__ __launch_bounds__(WIDE ? 64 * NE : 256) void k_route_choose(RouteArgs a) {
     __shared__ double whole[WIDE ? FP8BLK_MAX_EXPERTS : 1];
     __shared__ float biases[WIDE ? FP8BLK_MAX_EXPERTS : 1];
     const int lane = threadIdx.x & 63;
@@ -425,9 +426,12 @@ extern "C" int fp8blk_moe_route(const uint16_t* w_bf16, const float* bias, int64
         k_route_logits<1, 1, true><<<dim3((unsigned)te, (unsigned)tm, (unsigned)ceil_div(a.chunks, kSplitWaves)), 64 * kSplitWaves, 0, s>>>(a);
     else
         logits(a, te, tm, cus, s);
+    // As many logits a lane as there are, up to a power of two (2048 tokens, 384
+    // experts of 2048 columns: 72 us with 8, 77 with 16; 1 token of 7168 13.4, 15.1).
     if (experts <= 64) choose<1>(a, split, s);
     else if (experts <= 128) choose<2>(a, split, s);
     else if (experts <= 256) choose<4>(a, split, s);
+    else if (experts <= 512) choose<8>(a, split, s);
     else choose<16>(a, split, s);
     return launch_status();
 }
