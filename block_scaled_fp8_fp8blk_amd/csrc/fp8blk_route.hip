@@ -7,7 +7,7 @@
 //   - a large panel: that instruction. Alone it runs in 74 cycles with two or
 //     more waves a SIMD (86 with one), and the conversion of its inputs to 64
 //     bits is not hidden behind it: 2 more vector instructions for each make it
-//     88. 2048 tokens, 256 experts, 4096 columns: 80 us, 54 TFLOP/s (a library's
+//     88. 2048 tokens, 256 experts, 4096 columns: 78 us, 55 TFLOP/s (a library's
 //     64-bit product of inputs that are converted already: 125 us; of 4096^3:
 //     71 TFLOP/s).
 //   - a few tokens: latency, of two launches, a chain of 32 instructions and a
@@ -131,7 +131,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_logits(RouteArgs a) {
     constexpr int T = RX * RW;
     __shared__ double sums[SPLIT ? 1 : kWaves][SPLIT ? 1 : T * 4 * 64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, kg = lane >> 4;
-    const int e0 = blockIdx.x * RW * kTile, m0 = blockIdx.y * RX * kTile;
+    // Many tiles: workgroups that follow each other, on one L2 after the other,
+    // take other tokens, so that an L2 reads its tokens once (2048 tokens 79.6 ->
+    // 78.3 us; 146 -> 34 MB read).
+    const int e0 = (SPLIT ? blockIdx.x : blockIdx.y) * RW * kTile, m0 = (SPLIT ? blockIdx.y : blockIdx.x) * RX * kTile;
     constexpr int AHEAD = T < 4 ? kSteps : 2;
     Steps<RX, RW, AHEAD> steps;
     steps.start(a, m0, e0, lane);
@@ -381,7 +384,7 @@ void logits(const RouteArgs& a, int64_t te, int64_t tm, int cus, hipStream_t s) 
         const double us = forms[f].us * (double)ceil_div(ceil_div(te, forms[f].rw) * ceil_div(tm, forms[f].rx), cus);
         if (us < least) least = us, best = f;
     }
-    const dim3 grid((unsigned)ceil_div(te, forms[best].rw), (unsigned)ceil_div(tm, forms[best].rx));
+    const dim3 grid((unsigned)ceil_div(tm, forms[best].rx), (unsigned)ceil_div(te, forms[best].rw));
     if (best == 0) k_route_logits<4, 2, false><<<grid, 64 * kWaves, 0, s>>>(a);
     else if (best == 1) k_route_logits<2, 2, false><<<grid, 64 * kWaves, 0, s>>>(a);
     else if (best == 2) k_route_logits<2, 1, false><<<grid, 64 * kWaves, 0, s>>>(a);

@@ -768,7 +768,9 @@ int fp8blk_moe_route(const uint16_t *w_bf16, const float *bias, int64_t experts,
  *   codes, x_bf16, base, y: device, 16-byte aligned; scales: device, 4-byte
  *   (MXFP4) or 8-byte (NVFP4) aligned.
  *   ws: device, 256-byte aligned, >= fp4_moe_bytes(inter, M, top_k) bytes (0:
- *     bad sizes); its contents on entry do not matter.
+ *     bad sizes), which is enough for every hidden; its contents on entry do
+ *     not matter.
+ * A NaN passes the limit; an h past the largest f32 is infinite.
  * Enqueued on `stream`; does not wait.
  */
 #define FP8BLK_MAX_INTER 20480
@@ -797,8 +799,11 @@ int fp4_moe(const fp4_moe_layer *layer, const uint16_t *x_bf16, int64_t M, const
  *   rows >= 1; 1 <= M <= FP8BLK_MAX_M.
  *   codes, x_bf16: device, 16-byte aligned; scales_bf16: 2-byte aligned; y:
  *   4-byte aligned.
- * Every code, zero point and x is exact in the products; sums are f32. Row m
- * of an M-row call equals the 1-row call on x[m] bit for bit. y must not
+ * Every code, zero point and x is exact in the products; sums are f32. A
+ * group's sum is formed as s * (sum q x - z * sum x), so it is good to a few
+ * roundings of |s| * sum (q + z) |x|, and an infinite x (or one whose group's
+ * sum of 15 |x| is no f32) gives NaN. Row m of an M-row call equals the 1-row
+ * call on x[m] bit for bit. y must not
  * overlap the inputs. No workspace. Enqueued on `stream`; does not wait.
  */
 int int4_gemv(const uint8_t *codes, const uint16_t *scales_bf16, const uint8_t *zeros, int group, int64_t rows,

@@ -50,7 +50,8 @@ class Layer:
                                                 (13, 6, 9, 416, 320), (16, 8, 24, 512, 384), (16, 16, 16, 96, 64),
                                                 (16, 1, 2, 2080, 128), (16, 8, 10, 1440, 736), (12, 6, 7, 1056, 2080),
                                                 (16, 5, 4, 2080, 352), (9, 4, 20, 2592, 416), (1, 1, 2, 64, 20480),
-                                                (2, 1, 2, 65536, 32), (1, 2, 3, 8224, 4128)])
+                                                (2, 1, 2, 65536, 32), (1, 2, 3, 8224, 4128), (4, 2, 2, 64, 5632),
+                                                (4, 2, 2, 96, 10752), (4, 1, 1, 16384, 32)])
 def test_matches_plain(gpu, fmt, M, K, E, hidden, inter):
     print("moe", fmt, M, K, E, hidden, inter, flush=True)
     L = Layer(gpu, fmt, E, hidden, inter, M * hidden + inter + fmt, limit=(0.0, 3.0)[M % 2])
