@@ -722,7 +722,8 @@ int fp8blk_block_norm(const void *resid, int resid_type, const float *y, int64_t
  *     ids are -1 and their weights 0. Every other id is in [0, experts), and
  *     a token's ids are distinct, whatever the inputs hold.
  *   w_bf16 [experts, cols], x_bf16 [M, cols]: device, 16-byte aligned;
- *   ids int32 [M, top_k], weights f32 [M, top_k], bias: device, 4-byte aligned.
+ *   ids int32 [M, top_k], weights f32 [M, top_k], bias: device, 4-byte aligned;
+ *   ids, weights and ws overlap nothing else.
  *   1 <= experts <= FP8BLK_MAX_EXPERTS; 1 <= top_k <= min(experts,
  *   FP8BLK_MAX_TOP_K); 1 <= M <= FP8BLK_MAX_PANEL; cols as for fp8blk_gemv.
  *   ws: device, 256-byte aligned, >= fp8blk_workspace_bytes(FP8BLK_OP_MOE_ROUTE,
