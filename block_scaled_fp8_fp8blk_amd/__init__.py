@@ -905,15 +905,18 @@ def _buf(t, device, dtypes, shape, name, need=True):
     return t.data_ptr()
 
 
-def _matrix(t, name):
-    """Device and the two sizes of a matrix that is on a GPU."""
-    if _torch is None:
-        _load_torch()
+def _matrix(t, dtypes, name):
+    """Device, pointer and the two sizes of a contiguous matrix on a GPU."""
     if not isinstance(t, _torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, got shape {tuple(t.shape)}")
-    return (t.get_device(), *t.shape)
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have two dimensions, got shape {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.get_device(), t.data_ptr(), *shape
 
 
 def _workspace(ws, device):
@@ -925,7 +928,9 @@ def _workspace(ws, device):
 
 
 def _block_norm_args(resid, y, post_w, gate, scale, resid_out, pre_w, eps, x_next):
-    dev, N, cols = _matrix(resid, "resid")
+    if _torch is None:
+        _load_torch()
+    dev, resid_p, N, cols = _matrix(resid, _f32 + _bf16, "resid")
     kind, types = (TYPE_F32, _f32) if resid.dtype in _f32 else (TYPE_BF16, _bf16)
     panel, row = (N, cols), (cols,)
     gate_rows, gate_shape = 0, None
@@ -937,7 +942,7 @@ def _block_norm_args(resid, y, post_w, gate, scale, resid_out, pre_w, eps, x_nex
             gate_rows = gate_shape[0]
         else:
             raise ValueError(f"gate must be [cols], [1, cols] or [N, cols], got shape {tuple(gate_shape)}")
-    return dev, (_buf(resid, dev, types, panel, "resid"), kind, _buf(y, dev, _f32, panel, "y", False), N, cols,
+    return dev, (resid_p, kind, _buf(y, dev, _f32, panel, "y", False), N, cols,
                  _buf(post_w, dev, _bf16, row, "post_w", False), _buf(gate, dev, _bf16, gate_shape, "gate", False), gate_rows,
                  scale, _buf(resid_out, dev, types, panel, "resid_out", False),
                  _buf(pre_w, dev, _bf16, row, "pre_w", False), eps, _buf(x_next, dev, _bf16, panel, "x_next", False))
@@ -955,12 +960,15 @@ def fp8blk_block_norm(resid, y, post_w, gate, scale, resid_out, pre_w, eps, x_ne
 
 
 def _moe_route_args(w_bf16, bias, x_bf16, score, normalize, scale, ids, weights, ws):
-    dev, E, cols = _matrix(w_bf16, "w_bf16")
-    _, M, K = _matrix(ids, "ids")
+    if _torch is None:
+        _load_torch()
+    dev, w_p, E, cols = _matrix(w_bf16, _bf16, "w_bf16")
+    on, ids_p, M, K = _matrix(ids, _i32, "ids")
+    if on != dev:
+        raise ValueError(f"ids must be on device {dev}, they are on {on}")
     wsp, wsb = _workspace(ws, dev)
-    return dev, (_buf(w_bf16, dev, _bf16, (E, cols), "w_bf16"), _buf(bias, dev, _f32, (E,), "bias", False), E, cols,
-                 _buf(x_bf16, dev, _bf16, (M, cols), "x_bf16"), M, score, K, 1 if normalize else 0, scale,
-                 _buf(ids, dev, _i32, (M, K), "ids"), _buf(weights, dev, _f32, (M, K), "weights"), wsp, wsb)
+    return dev, (w_p, _buf(bias, dev, _f32, (E,), "bias", False), E, cols, _buf(x_bf16, dev, _bf16, (M, cols), "x_bf16"), M,
+                 score, K, 1 if normalize else 0, scale, ids_p, _buf(weights, dev, _f32, (M, K), "weights"), wsp, wsb)
 
 
 def fp8blk_moe_route(w_bf16, bias, x_bf16, score, normalize, scale, ids, weights, ws, stream=None, check=True):
@@ -1016,12 +1024,12 @@ def fp4_moe_bytes(inter: int, M: int, top_k: int) -> int:
 
 
 def _moe_args(layer, x_bf16, ids, weights, base, y, ws):
-    dev, M, K = _matrix(ids, "ids")
+    dev, ids_p, M, K = _matrix(ids, _i32, "ids")
     if dev != layer.device:
         raise ValueError(f"ids must be on the layer's device {layer.device}, they are on {dev}")
     panel = (M, layer.hidden)
     wsp, wsb = _workspace(ws, dev)
-    return dev, (layer.pointer, _buf(x_bf16, dev, _bf16, panel, "x_bf16"), M, _buf(ids, dev, _i32, (M, K), "ids"),
+    return dev, (layer.pointer, _buf(x_bf16, dev, _bf16, panel, "x_bf16"), M, ids_p,
                  _buf(weights, dev, _f32, (M, K), "weights"), K, _buf(base, dev, _f32, panel, "base", False),
                  _buf(y, dev, _f32, panel, "y"), wsp, wsb)
 
@@ -1036,14 +1044,18 @@ def fp4_moe(layer, x_bf16, ids, weights, base, y, ws, stream=None, check=True):
 
 
 def _int4_args(codes, scales_bf16, zeros, group, x_bf16, y):
-    dev, rows, half = _matrix(codes, "codes")
-    _, M, cols = _matrix(x_bf16, "x_bf16")
+    if _torch is None:
+        _load_torch()
+    dev, codes_p, rows, half = _matrix(codes, _u8, "codes")
+    on, x_p, M, cols = _matrix(x_bf16, _bf16, "x_bf16")
+    if on != dev:
+        raise ValueError(f"x_bf16 must be on device {dev}, it is on {on}")
     if cols != 2 * half:
         raise ValueError(f"x_bf16 must be [M, cols={2 * half}], got shape {tuple(x_bf16.shape)}")
     grid = (rows, cols // group if group > 0 else 0)
-    return dev, (_buf(codes, dev, _u8, (rows, half), "codes"), _buf(scales_bf16, dev, _bf16, grid, "scales_bf16"),
+    return dev, (codes_p, _buf(scales_bf16, dev, _bf16, grid, "scales_bf16"),
                  _buf(zeros, dev, _u8, grid, "zeros", False), group, rows, cols,
-                 _buf(x_bf16, dev, _bf16, (M, cols), "x_bf16"), M, _buf(y, dev, _f32, (M, rows), "y"))
+                 x_p, M, _buf(y, dev, _f32, (M, rows), "y"))
 
 
 def int4_gemv(codes, scales_bf16, zeros, group, x_bf16, y, stream=None, check=True):
