@@ -95,9 +95,10 @@ def test_the_same_expert_many_times(gpu, fmt, M, K, hidden, inter):
 
 
 @pytest.mark.parametrize("fmt", [MX, NV])
-def test_tokens_do_not_depend_on_the_panel(gpu, fmt):
-    L = Layer(gpu, fmt, 7, 1056, 544, 15)
-    x, ids, p, base = L.tokens(16, 5)
+@pytest.mark.parametrize("hidden,inter,K", [(1056, 544, 5), (2080, 544, 4), (1056, 2080, 4), (2080, 768, 6)])
+def test_tokens_do_not_depend_on_the_panel(gpu, fmt, hidden, inter, K):
+    L = Layer(gpu, fmt, 7, hidden, inter, 15)
+    x, ids, p, base = L.tokens(16, K)
     y = L.run(gpu, x, ids, p, base)
     for n in (1, 3, 6, 9):
         for at in (0, 16 - n):
