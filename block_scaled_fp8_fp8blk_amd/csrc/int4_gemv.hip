@@ -138,6 +138,20 @@ __device__ __forceinline__ void load_groups(Groups<N>& g, const uint16_t* s, con
     }
 }
 
+// A lane's two weight rows of a tile (rows past the last are the last): bytes
+// from the tile's first, which is the same for the whole wave.
+struct Rows {
+    const uint8_t* codes;
+    uint32_t lo, hi;
+    __device__ __forceinline__ Rows(const Int4Args& a, int64_t row0, int lane) {
+        const uint32_t wide = a.cols / 2;
+        const int last = (int)min(a.rows - 1 - row0, (int64_t)kTile);
+        codes = a.codes + row0 * wide;
+        lo = min(lane & 7, last) * wide;
+        hi = min(8 + (lane & 7), last) * wide;
+    }
+};
+
 // One wave's loads of a tile's 512 columns; WIDE: without the scales, which
 // come as a block (below).
 template <int G, bool WIDE>
@@ -147,13 +161,12 @@ struct Load {
 };
 
 template <int G, bool ZERO, bool WIDE>
-__device__ __forceinline__ void issue(Load<G, WIDE>& b, const Int4Args& a, const uint8_t* lo, const uint8_t* hi, int64_t row,
-                                      int lane, int c0) {
+__device__ __forceinline__ void issue(Load<G, WIDE>& b, const Int4Args& a, const Rows& rows, int64_t row, int lane, int c0) {
 #pragma unroll
     for (int s = 0; s < kSteps; s += 2) {  // columns past the end meet zeros of the panel: any code will do
-        const int c = min(c0 + s * kStep + 16 * (lane & 8) + 32 * (lane >> 4), a.cols - 32) / 2;
-        b.q[s] = load_stream16(lo + c);
-        b.q[s + 1] = load_stream16(hi + c);
+        const uint32_t c = min(c0 + s * kStep + 16 * (lane & 8) + 32 * (lane >> 4), a.cols - 32) / 2;
+        b.q[s] = load_stream16(rows.codes + (rows.lo + c));
+        b.q[s + 1] = load_stream16(rows.codes + (rows.hi + c));
     }
     if constexpr (!WIDE) {
         const int64_t g = row * (a.cols / G) + c0 / G;
@@ -252,7 +265,7 @@ __device__ __forceinline__ void compute(Load<G, WIDE>& b, const uint4* x, const 
 template <int G, bool ZERO, int NI, bool WIDE>
 __global__ __launch_bounds__(1024) void k_int4(Int4Args a) {
     extern __shared__ uint4 lds[];  // the panel's piece: [step][j][lane group][token]
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int n = lane & 15, kg = lane >> 4;
     const int side = wave / a.split, part = wave % a.split, across = waves / a.split;  // across: tiles a workgroup takes at once
     const int64_t tiles = (a.rows + kTile - 1) / kTile;
@@ -294,8 +307,7 @@ __global__ __launch_bounds__(1024) void k_int4(Int4Args a) {
     for (int64_t first = (int64_t)blockIdx.x * across; first < tiles; first += (int64_t)gridDim.x * across) {
         const int64_t tile = first + side;
         const int64_t row0 = min(tile, tiles - 1) * kTile, row = min(row0 + n, a.rows - 1);
-        const uint8_t* lo = a.codes + min(row0 + (lane & 7), a.rows - 1) * (a.cols / 2);
-        const uint8_t* hi = a.codes + min(row0 + 8 + (lane & 7), a.rows - 1) * (a.cols / 2);
+        const Rows rows(a, row0, lane);
         float acc[NI];
 #pragma unroll
         for (int i = 0; i < NI; ++i) acc[i] = 0.0f;
@@ -303,7 +315,7 @@ __global__ __launch_bounds__(1024) void k_int4(Int4Args a) {
             const int p0 = p * a.piece, p1 = min(p0 + a.piece, a.cols);
             int c0 = p0 + part * kSuper;
             Load<G, WIDE> A, B;
-            if (c0 < p1) issue<G, ZERO, WIDE>(A, a, lo, hi, row, lane, c0);
+            if (c0 < p1) issue<G, ZERO, WIDE>(A, a, rows, row, lane, c0);
             if (pieces > 1 || first == (int64_t)blockIdx.x * across) {
                 if (pieces > 1) __syncthreads();
                 stage(p0, (p1 - p0 + kSuper - 1) / kSuper * kSuper);
@@ -312,7 +324,7 @@ __global__ __launch_bounds__(1024) void k_int4(Int4Args a) {
             const int stride = a.split * kSuper;
             while (c0 < p1) {
                 const int c1 = c0 + stride;
-                if (c1 < p1) issue<G, ZERO, WIDE>(B, a, lo, hi, row, lane, c1);
+                if (c1 < p1) issue<G, ZERO, WIDE>(B, a, rows, row, lane, c1);
                 if constexpr (WIDE)
                     if (c0 % SPAN == 0) {  // the next block: this row's, or the next tile's first
                         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -329,7 +341,7 @@ __global__ __launch_bounds__(1024) void k_int4(Int4Args a) {
                                            zb + c0 % SPAN / G, acc);
                 if (c1 >= p1) break;
                 c0 = c1 + stride;
-                if (c0 < p1) issue<G, ZERO, WIDE>(A, a, lo, hi, row, lane, c0);
+                if (c0 < p1) issue<G, ZERO, WIDE>(A, a, rows, row, lane, c0);
                 compute<G, ZERO, NI, WIDE>(B, x + (c1 - p0) / 8 * 4 * NI, xsum + (c1 - p0) / G * 4 * NI, sb + c1 % SPAN / G * 2,
                                            zb + c1 % SPAN / G, acc);
             }
