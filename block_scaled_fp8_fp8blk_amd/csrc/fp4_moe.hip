@@ -578,19 +578,26 @@ void launch_steps(MoeArgs a, hipStream_t s) {
     k_moe<FMT, DOWN, NS><<<grid, 64 * waves, (size_t)(a.most * row_bytes + own), s>>>(a);
 }
 
-// Steps a wave takes at a time: half as many where the columns are few. Down:
+// Steps a wave takes at a time: fewer where the columns are few. Down: 2
 // wherever 8 waves then cover the row, which for one token is more waves than
 // 4 steps give (1 token, 8 of 4096x2048: 36.3 against 37.8 us NVFP4, 32.2
-// against 32.8 MXFP4; 16 tokens 235 against 233, 199 against 198). Gate and
-// up only up to 2048 columns (the same token with 4 steps over 4096 columns:
-// 39.3 against 37.9 us).
-inline bool half_steps(bool down, int cols) { return cols <= (down ? 2 * kStep * kWaves : 16 * kStep); }
+// against 32.8 MXFP4; 16 tokens 235 against 233, 199 against 198). Gate and up:
+// 2 up to 1024 columns (16 tokens, 8 of 64 experts of 512x256 MXFP4 12.7 us, with 4
+// 13.7; 8 of 2048x1408, though, 69.7, with 4 63.0), 4 up to 2048, else 8 (1 token,
+// 8 of 4096x2048 37.9 us, with 4 39.3).
+constexpr int down_steps(int cols) { return cols <= 2 * kStep * kWaves ? 2 : 4; }
 
-template <int FMT, bool DOWN>
-void launch(const MoeArgs& a, hipStream_t s) {
-    constexpr int NS = DOWN ? 4 : 8;
-    if (half_steps(DOWN, a.cols)) launch_steps<FMT, DOWN, NS / 2>(a, s);
-    else launch_steps<FMT, DOWN, NS>(a, s);
+template <int FMT>
+void launch_up(const MoeArgs& a, hipStream_t s) {
+    if (a.cols <= 8 * kStep) launch_steps<FMT, false, 2>(a, s);
+    else if (a.cols <= 16 * kStep) launch_steps<FMT, false, 4>(a, s);
+    else launch_steps<FMT, false, 8>(a, s);
+}
+
+template <int FMT>
+void launch_down(const MoeArgs& a, hipStream_t s) {
+    if (down_steps(a.cols) == 2) launch_steps<FMT, true, 2>(a, s);
+    else launch_steps<FMT, true, 4>(a, s);
 }
 
 template <int FMT, int NS>
@@ -607,17 +614,17 @@ void run(const fp4_moe_layer& l, const uint16_t* x, int M, const int32_t* ids, c
     const int H = (int)l.hidden, I = (int)l.inter;
     MoeArgs a = {{l.gate, l.up}, {l.gate_scales, l.up_scales}, {l.gate_global, l.up_global}, x, ids, pieces, nullptr,
                  l.experts, I, H, M * K, K, 1, 1, l.limit};
-    launch<FMT, false>(a, s);
+    launch_up<FMT>(a, s);
     a = {{l.down, nullptr}, {l.down_scales, nullptr}, {l.down_global, nullptr}, pieces, ids, nullptr, part,
          l.experts, H, I, M * K, K, 1, 1, 0.0f};
-    const int NS = half_steps(true, I) ? 2 : 4;
+    const int NS = down_steps(I);
     const int64_t waves = ceil_div(I, NS * kStep) * ceil_div(K, Unit<FMT, true, 4>::T);
     if ((int64_t)M * K * H * I <= kFewWeights && waves <= kWaves) {
         if (NS == 2) launch_token<FMT, 2>(a, M, weights, base, y, s);
         else launch_token<FMT, 4>(a, M, weights, base, y, s);
         return;
     }
-    launch<FMT, true>(a, s);
+    launch_down<FMT>(a, s);
     k_moe_sum<<<dim3((unsigned)ceil_div(H, 256), (unsigned)M), 64, 0, s>>>(part, ids, weights, base, l.experts, H, K, y);
 }
 
