@@ -19,10 +19,10 @@
 // hence NVFP4's distance from MXFP4 below.
 //
 // What bounds it: the experts' weights. 16 tokens, 8 of 128 experts of
-// 4096x2048 MXFP4, 1.1 GB: 196 us, 5.6 TB/s (a plain read of that much
-// reaches 6 to 6.9); NVFP4 232 us, 5.0 TB/s. One token, 8 of 64: 31.4 and 35.6
-// us, 3.4 and 3.2 TB/s, where the three launches' starts and ends are half.
-// Small layers are latency (2 tokens, 2 of 8 of 512x512: 9.6 us).
+// 4096x2048 MXFP4, 1.1 GB: 194 us, 5.7 TB/s (a plain read of that much
+// reaches 6 to 6.9); NVFP4 229 us, 5.1 TB/s. One token, 8 of 64: 29.4 and 34.0
+// us, 3.6 and 3.3 TB/s, where the three launches' starts and ends are half.
+// Small layers are latency (2 tokens, 2 of 8 of 512x512: 7.3 us).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -48,7 +48,7 @@ constexpr int kBusy = 512;  // workgroups with work: two a compute unit
 // Up to so many weights of down (tokens x experts of a token x slab), down and
 // the sum over the experts are one launch, which saves a launch's start and end
 // but lets tokens read an expert that they share once each. One launch against
-// two, us: 2 tokens, 2 of 8 experts of 512x512 MXFP4 7.9, 10.8; 6 tokens, 4 of
+// two, us: 2 tokens, 2 of 8 experts of 512x512 MXFP4 7.6, 10.8; 6 tokens, 4 of
 // 32 of 1440x736 (25e6 weights) 20.1, 23.0; 4 tokens, 8 of 128 of 2048x768
 // (50e6) 24.9, 27.5, NVFP4 28.0, 30.7; 4 tokens, 2 of 8 of 4096x2048 (67e6)
 // 36.7, 31.1; 8 tokens, 6 of 64 of 2048x1024 (101e6) 43.2, 38.2.
