@@ -139,7 +139,7 @@ __device__ __forceinline__ void issue_scales(Scales<U>& b, const MoeArgs& a, con
         const uint8_t* sc = (U::MATS == 2 && t ? a.sc[1] : a.sc[0]) + (int64_t)w.expert * a.rows * blocks;
         const uint32_t at = row * blocks + c0 / U::B + o % PER_ROW * U::CHUNK;
         const int64_t end = (a.experts - w.expert) * a.rows * blocks;  // of the array, from this expert's scales
-        // past a row's end other rows' scales are as good, the operand is zero there
+        // past a row's end come other rows' scales, which place_scales leaves out
         if (at + U::CHUNK <= end) {
             __builtin_memcpy(b.d[i], sc + at, U::CHUNK);
         } else {  // past the array's end there are none: its last dword, shifted
@@ -154,8 +154,20 @@ __device__ __forceinline__ void issue_scales(Scales<U>& b, const MoeArgs& a, con
     }
 }
 
+// left: blocks of the row from the slice's first on. The columns past the end
+// are codes times a zero operand, but a code times a scale that was not chosen
+// for it may be infinite: there the scale is the smallest (code 0).
 template <typename U>
-__device__ __forceinline__ void place_scales(const Scales<U>& b, uint8_t* to, int lane) {
+__device__ __forceinline__ void place_scales(Scales<U>& b, uint8_t* to, int lane, int left) {
+    if (left < U::ROW) {
+#pragma unroll
+        for (int i = 0; i < U::LOADS; ++i)
+#pragma unroll
+            for (int k = 0; k < U::CHUNK / 4; ++k) {
+                const int in = left - (i * 64 + lane) % (U::ROW / U::CHUNK) * U::CHUNK - 4 * k;
+                b.d[i][k] = in >= 4 ? b.d[i][k] : in > 0 ? b.d[i][k] & ((1u << 8 * in) - 1) : 0;
+            }
+    }
 #pragma unroll
     for (int i = 0; i < U::LOADS; ++i)
         if (i * 64 + lane < U::T * kTile * U::ROW / U::CHUNK) __builtin_memcpy(to + (i * 64 + lane) * U::CHUNK, b.d[i], U::CHUNK);
@@ -398,7 +410,7 @@ __global__ __launch_bounds__(64 * kWaves, 3) void k_moe(MoeArgs a) {
     for (int turn = 0; tile < end;) {
         int t1 = tile, c1 = c0 + waves * SLICE;
         if (c1 >= a.cols) c1 = wave * SLICE, ++t1;
-        place_scales<U>(sr, scales, lane);
+        place_scales<U>(sr, scales, lane, (a.cols - c0) / U::B);
         if (t1 < end) issue_scales<U>(sr, a, SideBySide<U>{expert, t1}, lane, c1);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -464,7 +476,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_moe_token(MoeArgs a, const f
         for (int t = 0; t < U::T; ++t)
 #pragma unroll
             for (int p = 0; p < kPieces; ++p) own[lane * ROWS + t * kPieces + p] = c < a.cols ? v[t][p] : make_uint4(0, 0, 0, 0);
-    place_scales<U>(sr, scales, lane);
+    place_scales<U>(sr, scales, lane, (a.cols - c0) / U::B);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     v4f acc[U::T];

@@ -189,3 +189,23 @@ def test_experts_past_32_bit_offsets(gpu):
     torch.cuda.synchronize()
     near = torch.tensor([[0, 1], [1, -1]])
     assert_within(y, *moe(*small, x, near, p, None, 0.0), "experts past 2^32")
+
+
+@pytest.mark.parametrize("high", [253, 254])
+@pytest.mark.parametrize("M,K,hidden,inter", [(3, 2, 96, 96), (1, 1, 64, 64), (5, 4, 1056, 160), (3, 5, 96, 2080), (16, 6, 2080, 544)])
+def test_block_scales_past_a_rows_end_do_not_count(gpu, high, M, K, hidden, inter):
+    """MXFP4 scale codes of 253 and 254 stand beside small codes only (here 0),
+    and times the 6 at the end of a row before, or of their own row, they would
+    be infinite. Down and the sum in one launch, and in two."""
+    L = Layer(gpu, MX, 8, hidden, inter, 53)
+    for slab in (L.gate, L.up, L.down):
+        slab.codes[..., :16] = slab.codes[..., -32:-16] = 0x00
+        slab.scales[..., 0] = slab.scales[..., -2] = high
+        slab.values[..., :32] = slab.values[..., -64:-32] = 0.0
+        slab.codes[..., -16:], slab.scales[..., -1], slab.values[..., -32:] = 0x77, 121, 6 * 2.0 ** -6
+        codes, scales, _ = slab.on(DEV)
+        ws = torch.empty(gpu.fp8blk_workspace_bytes(gpu.OP_LOAD_CHECK, 8, 64), dtype=torch.uint8, device=DEV)
+        for c, s in zip(codes, scales):
+            assert gpu.fp4_load_check(MX, c, s, ws)[0] == gpu.OK
+    L.handle = gpu.fp4_moe_weights(MX, *L.gate.on(DEV), *L.up.on(DEV), *L.down.on(DEV))
+    L.check(gpu, *L.tokens(M, K), f"scale codes {high}")
