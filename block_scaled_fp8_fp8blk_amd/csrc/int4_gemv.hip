@@ -398,8 +398,13 @@ __global__ __launch_bounds__(1024) void k_int4_shot(Int4Args a) {
 #pragma unroll
             for (int s = 0; s < NS; ++s)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    v[s][j] = load_global16(x + min(c0 + s * kStep + gathered_column<G>(j, kg), a.cols - 8));
+                for (int j = 0; j < 4; ++j) {
+                    // A group past the row's end reads the last one, whose columns it
+                    // so holds once each: its sums are f32s where that group's are,
+                    // and its scale of 0 leaves nothing of them.
+                    const int at = gathered_column<G>(j, kg);
+                    v[s][j] = load_global16(x + min(c0 + s * kStep + at, a.cols - G + at % G));
+                }
         };
         // Loads arrive in order: 4 steps' codes are asked for last, to be used one
         // by one as they come (16 tokens, 8192 rows x 4096: 12.7 us against 13.7,

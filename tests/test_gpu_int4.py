@@ -134,3 +134,15 @@ def test_codes_past_32_bit_offsets(gpu):
     assert_within(y[:, at], *int4(c, s, None, g, x), "rows past 2^32")
     y[:, at] = 0
     assert (y == 0).all()
+
+
+@pytest.mark.parametrize("rows", [40, 9001])
+@pytest.mark.parametrize("cols,group", [(128, 128), (384, 128), (416, 32), (320, 64), (2176, 128)])
+def test_large_last_columns(gpu, rows, cols, group):
+    """The last 8 columns near the end of the range, the same for few and for
+    many rows: no column counts twice."""
+    codes, scales, z, g, x = _case(41, 3, rows, cols, group)
+    codes[:, -4:] = 0xFF
+    x[:, -8:] = 2e36  # 15 sum |x| = 2.4e38
+    c = codes, scales.abs(), z, g, x
+    assert_within(_run(gpu, *c), *int4(*c), f"{rows}x{cols} in groups of {group}")
