@@ -802,10 +802,12 @@ int fp4_moe(const fp4_moe_layer *layer, const uint16_t *x_bf16, int64_t M, const
  *   4-byte aligned.
  * Every code, zero point and x is exact in the products; sums are f32. A
  * group's sum is formed as s * (sum q x - z * sum x), so it is good to a few
- * roundings of |s| * sum (q + z) |x|, and an infinite x (or one whose group's
- * sum of 15 |x| is no f32) gives NaN. Row m of an M-row call equals the 1-row
- * call on x[m] bit for bit. y must not
- * overlap the inputs. No workspace. Enqueued on `stream`; does not wait.
+ * roundings of |s| * sum (q + z) |x|: of x that share an offset, or z far from
+ * the codes, more is lost than in sums of (q - z) x. It needs max(15, z) *
+ * sum |x| over the group to be an f32; past that, y may be infinite or NaN, as
+ * it is for an infinite x. Row m of an M-row call equals the 1-row call on x[m]
+ * bit for bit. y must not overlap the inputs. No workspace. Enqueued on
+ * `stream`; does not wait.
  */
 int int4_gemv(const uint8_t *codes, const uint16_t *scales_bf16, const uint8_t *zeros, int group, int64_t rows,
               int64_t cols, const uint16_t *x_bf16, int64_t M, float *y, fp8blk_stream_t stream);

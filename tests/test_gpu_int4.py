@@ -146,3 +146,25 @@ def test_large_last_columns(gpu, rows, cols, group):
     x[:, -8:] = 2e36  # 15 sum |x| = 2.4e38
     c = codes, scales.abs(), z, g, x
     assert_within(_run(gpu, *c), *int4(*c), f"{rows}x{cols} in groups of {group}")
+
+
+@pytest.mark.parametrize("rows,cols,group", [(33, 384, 128), (9001, 416, 32)])
+def test_largest_values_beside_any_zero_point(gpu, rows, cols, group):
+    """Zero points up to 255, with sums of max(15, z) |x| over a group just in f32's range."""
+    codes, scales, z, g, x = _case(43, 3, rows, cols, group)
+    z = torch.from_numpy(np.random.default_rng(43).integers(0, 256, z.shape, dtype=np.uint8))
+    z[0] = 255
+    x = (x.sign() * 1.2e38 / (128 * 255) * 2.5).bfloat16()  # 255 sum |x| is at most 3e38
+    x[:, ::2] = x[:, ::2].abs()
+    c = codes, (scales * 2.0 ** -20), z, g, x
+    assert_within(_run(gpu, *c), *int4(*c), f"{rows}x{cols} in groups of {group}")
+
+
+@pytest.mark.parametrize("rows,cols,group", [(130, 2176, 128), (4096, 4096, 64), (9001, 1056, 32)])
+def test_activations_with_an_offset(gpu, rows, cols, group):
+    """Activations that share an offset, and zero points far above the codes:
+    both sums are large beside their difference, and the bound counts them."""
+    codes, scales, z, g, x = _case(47, 4, rows, cols, group)
+    z = z + 200
+    c = codes, scales, z, g, (x.float() + 30).bfloat16()
+    assert_within(_run(gpu, *c), *int4(*c), f"{rows}x{cols} in groups of {group}")
