@@ -11,12 +11,12 @@
 // The sums are v_mfma_f32_16x16x32_bf16 on weights widened to bf16, exact for
 // both formats. MXFP4: with their scale, a power of two, in the conversion. An
 // operand of 16 rows holds 4 slots, and for down every slot's h as three bf16
-// pieces, the f32 value to its last bit or so: h never loses more than f32
-// does. NVFP4: an e4m3 scale times a code is a bf16 value, but a conversion
-// takes powers of two only, so the instruction runs on the codes, with the
-// 16-column blocks of 32 columns in rows of their own (the operand's other
-// half zero), and f32 scales its results. More instructions for every byte,
-// hence NVFP4's distance from MXFP4 below.
+// pieces, which hold all its bits (below 2^-110, where the last piece is a
+// subnormal bf16, all down to 2^-133). NVFP4: an e4m3 scale times a code is a
+// bf16 value, but a conversion takes powers of two only, so the instruction
+// runs on the codes, with the 16-column blocks of 32 columns in rows of their
+// own (the operand's other half zero), and f32 scales its results. More
+// instructions for every byte, hence NVFP4's distance from MXFP4 below.
 //
 // What bounds it: the experts' weights. 16 tokens, 8 of 128 experts of
 // 4096x2048 MXFP4, 1.1 GB: 194 us, 5.7 TB/s (a plain read of that much

@@ -748,7 +748,8 @@ int fp8blk_moe_route(const uint16_t *w_bf16, const float *bias, int64_t experts,
  *   h = g / (1 + exp(-g)) * u
  *   y_m = base_m + sum_k weights[m, k] * (Wdown_e h)
  * W is e2m1(code) * block scale * global scale, as for fp4_expert_gemv, on
- * bf16 activations as they are. Sums are f32 and h is held to f32 accuracy.
+ * bf16 activations as they are. Sums are f32 and h is held to f32 accuracy (one
+ * below 2^-110 to 2^-134).
  * The sum over k is taken in order of k; row m of an M-row call equals the
  * 1-row call on token m bit for bit.
  *   layer (HOST struct): gate, up: codes [experts, inter, hidden/2], scales

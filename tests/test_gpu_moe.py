@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from block_scaled_fp8_fp8blk_amd import inputs as I
-from layer_plain import Slab, assert_within, moe, normal
+from layer_plain import Slab, U, assert_within, moe, normal
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -209,3 +209,62 @@ def test_block_scales_past_a_rows_end_do_not_count(gpu, high, M, K, hidden, inte
             assert gpu.fp4_load_check(MX, c, s, ws)[0] == gpu.OK
     L.handle = gpu.fp4_moe_weights(MX, *L.gate.on(DEV), *L.up.on(DEV), *L.down.on(DEV))
     L.check(gpu, *L.tokens(M, K), f"scale codes {high}")
+
+
+class Picking(Layer):
+    """A layer whose outputs are h itself: tokens of one column each, so that
+    gate and up are exact, and rows of down that hold a single 1."""
+
+    def __init__(self, gpu, fmt, hidden, inter, seed, top=(1.0, 1.0)):
+        super().__init__(gpu, fmt, 3, hidden, inter, seed, with_global=False)
+        self.at = self.rng.integers(0, inter, (3, hidden))
+        self.down.codes[:], self.down.scales[:] = 0, 127 if fmt == MX else 0x38
+        e, r = np.ogrid[:3, :hidden]
+        self.down.codes[e, r, self.at // 2] = np.where(self.at % 2, 0x20, 0x02)
+        self.gate.top, self.up.top = (np.full(3, t, dtype=np.float32) for t in top)
+        self.handle = gpu.fp4_moe_weights(fmt, *self.gate.on(DEV), *self.up.on(DEV), *self.down.on(DEV))
+
+    def one_column_tokens(self, M, K, size):
+        """Each token's first choice is an expert, the others are none."""
+        col = torch.from_numpy(self.rng.integers(0, self.hidden, M))
+        x = torch.zeros(M, self.hidden).bfloat16()
+        x[torch.arange(M), col] = torch.from_numpy(self.rng.uniform(0.5, 1.0, M) * size).bfloat16()
+        ids = torch.full((M, K), -1, dtype=torch.int32)
+        ids[:, 0] = torch.from_numpy(self.rng.integers(0, 3, M))
+        return x, ids, torch.ones(M, K), col
+
+    def h(self, x, ids, col):
+        """The h that every output picks, in 64 bits."""
+        out = torch.empty(x.shape[0], self.hidden, dtype=torch.float64)
+        for m, e in enumerate(ids[:, 0].tolist()):
+            v = float(x[m, col[m]])
+            g, u = (s.values[e][:, col[m]] * v * float(s.top[e]) for s in (self.gate, self.up))
+            out[m] = (g * torch.sigmoid(g) * u)[torch.from_numpy(self.at[e])]
+        return out
+
+
+@pytest.mark.parametrize("fmt,size", [(MX, 4.0), (NV, 0.25)])
+@pytest.mark.parametrize("top", [0, -60, -112, 110])
+@pytest.mark.parametrize("K,hidden,inter", [(2, 256, 96), (5, 256, 2080), (3, 96, 512)])
+def test_h_keeps_all_its_bits(gpu, fmt, size, top, K, hidden, inter):
+    """h to f32 accuracy from its three bf16 pieces, across its range. exp is
+    good to 2 f32 steps, 4 U, which 1 + exp passes on at most whole; that sum,
+    the division and the product by u round once each: 7 U, and 12 with room.
+    Two pieces would leave up to 128 U. Below 2^-110 the last piece is a
+    subnormal bf16, good to 2^-134."""
+    L = Picking(gpu, fmt, hidden, inter, 71 + inter, top=(1.0, 2.0 ** top))
+    x, ids, p, col = L.one_column_tokens(16, K, size)
+    want = L.h(x, ids, col)
+    assert_within(L.run(gpu, x, ids, p, None), want, 12 * U * want.abs() + 2.0 ** -134, f"h around 2^{top}")
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_subnormal_weights_reach_the_output(gpu, fmt):
+    """Block scales of the smallest codes, their weights subnormal in bf16 for
+    MXFP4, on activations that bring gate and up back to ordinary sizes."""
+    L = Layer(gpu, fmt, 4, 192, 128, 33, scale_range=(0, 6), with_global=False)
+    L.down = Slab(L.rng, fmt, 4, 192, 128, with_global=False)
+    L.handle = gpu.fp4_moe_weights(fmt, *L.gate.on(DEV), *L.up.on(DEV), *L.down.on(DEV))
+    x, ids, p, base = L.tokens(5, 3)
+    x *= 2.0 ** (120 if fmt == MX else 4)
+    L.check(gpu, x, ids, p, base * 0.125, f"{fmt} scales 0..6")
