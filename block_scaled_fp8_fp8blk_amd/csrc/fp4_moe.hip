@@ -288,11 +288,14 @@ __device__ __forceinline__ void finish(const MoeArgs& a, const float (&top)[U::M
             }
             float h = g1 / (1.0f + expf(-g1)) * u;
             uint16_t* to = a.pieces + (int64_t)sl * kPieces * a.rows + row;
+            const bool number = fabsf(h) < __builtin_inff();
 #pragma unroll
             for (int p = 0; p < kPieces; ++p) {
-                const float bf = head_bf16(h);
+                float bf = head_bf16(h);
+                // bf16's largest, where the nearest would be an infinity
+                if (p == 0 && number) bf = __builtin_amdgcn_fmed3f(bf, as_f32(0xFF7F0000u), as_f32(0x7F7F0000u));
                 to[(int64_t)p * a.rows] = (uint16_t)(as_u32(bf) >> 16);
-                h = fabsf(bf) < __builtin_inff() ? h - bf : 0.0f;  // an infinity or NaN is its first piece
+                h = p > 0 || number ? h - bf : 0.0f;  // an infinity or NaN is its first piece
             }
         }
     }

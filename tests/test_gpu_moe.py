@@ -268,3 +268,20 @@ def test_subnormal_weights_reach_the_output(gpu, fmt):
     x, ids, p, base = L.tokens(5, 3)
     x *= 2.0 ** (120 if fmt == MX else 4)
     L.check(gpu, x, ids, p, base * 0.125, f"{fmt} scales 0..6")
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("K,hidden,inter", [(1, 64, 64), (5, 64, 2080)])
+def test_an_h_past_bf16s_largest_is_a_number(gpu, fmt, K, hidden, inter):
+    """(2 - 2^-10) 2^127 is an f32, and nearer to infinity than to bf16's
+    largest value: h stays that number, exactly."""
+    L = Picking(gpu, fmt, hidden, inter, 83, top=(2.0 ** 64, (2.0 - 2.0 ** -10) * 2.0 ** 63))
+    for slab in (L.gate, L.up):  # 1, before the global scales
+        slab.codes[:], slab.scales[:] = 0x22, 127 if fmt == MX else 0x38
+    L.handle = gpu.fp4_moe_weights(fmt, *L.gate.on(DEV), *L.up.on(DEV), *L.down.on(DEV))
+    ids = torch.full((2, K), -1, dtype=torch.int32)
+    ids[:, 0] = torch.tensor([0, 2])
+    x = torch.zeros(2, hidden).bfloat16()
+    x[:, 7] = torch.tensor([1.0, 0.5]).bfloat16()
+    y = L.run(gpu, x, ids, torch.ones(2, K), None).cpu()
+    assert (y[0] == (2.0 - 2.0 ** -10) * 2.0 ** 127).all() and (y[1] == (2.0 - 2.0 ** -10) * 2.0 ** 125).all()
