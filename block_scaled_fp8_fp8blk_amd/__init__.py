@@ -1074,9 +1074,9 @@ def raw_call(name: str, *args):
 
 def prepared(name: str, *tensors_and_sizes, stream=None):
     """Marshal an entry point's arguments once and return a zero-argument
-    callable that enqueues it and returns its status. For launch-bound loops
-    (benchmarks, graph capture), where per-call tensor inspection would
-    dominate. Supported: "fp8blk_gemv" and "fp8blk_gemv_mfma" (codes,
+    callable that enqueues it and returns its status, and that keeps the tensors
+    alive. For launch-bound loops (benchmarks, graph capture), where per-call
+    tensor inspection would dominate. Supported: "fp8blk_gemv" and "fp8blk_gemv_mfma" (codes,
     scales_f32, x_bf16, y), "bf16_gemv_twin" and "bf16_gemv_twin_mfma" (w_bf16,
     x_bf16, y), the grouped launches (members, x_bf16), the scaled-input
     launches (codes, scales_f32, src_f32, c, y) and (members, src_f32, c), the
@@ -1085,12 +1085,14 @@ def prepared(name: str, *tensors_and_sizes, stream=None):
     "fp8blk_block_norm", "fp8blk_moe_route", "fp4_moe" and "int4_gemv" with their own arguments."""
     import torch
     fn = getattr(load(), name)
+    # what the marshalled pointers point into (a group's list may change later)
+    keep = [list(a) if isinstance(a, (list, tuple)) else a for a in tensors_and_sizes]
     around = {"fp8blk_block_norm": _block_norm_args, "fp8blk_moe_route": _moe_route_args, "fp4_moe": _moe_args,
               "int4_gemv": _int4_args}.get(name)
     if around is not None:
         dev, args = around(*tensors_and_sizes)
         stream = torch.cuda.current_stream(dev) if stream is None else stream
-        return lambda: _enqueue(fn, dev, args, stream, name, False)
+        return lambda keep=keep: _enqueue(fn, dev, args, stream, name, False)
     s = _stream(stream)
     if name == "fp8blk_gemv":
         codes, grid, x, y = tensors_and_sizes
@@ -1153,4 +1155,4 @@ def prepared(name: str, *tensors_and_sizes, stream=None):
         args = (ctypes.byref(seq.handle), s)
     else:
         raise ValueError(f"prepared: unsupported entry point {name!r}")
-    return lambda: fn(*args)
+    return lambda keep=keep: fn(*args)

@@ -1,6 +1,9 @@
 """GPU: the norms, router, expert layer and 4-bit linear run together as a
 decode or verify step runs them, eager, on another stream, and captured in a
 HIP graph."""
+import gc
+import weakref
+
 import numpy as np
 import pytest
 import torch
@@ -157,3 +160,48 @@ def test_prepared_calls(gpu):
     assert [c() for c in calls] == [gpu.OK] * 5
     torch.cuda.synchronize()
     assert _same(s.outputs(), want)
+
+
+def test_prepared_calls_keep_their_tensors(gpu):
+    """A prepared call is the only owner of what it was given."""
+    s = Step(gpu, 3, seed=91)
+    s.run()
+    torch.cuda.synchronize()
+    want, d = s.outputs(), s.d
+    outs = {k: torch.full_like(d[k], -5 if k == "ids" else float("nan")) for k in ("x", "ids", "p", "y", "out", "next")}
+    mine = lambda t: None if t is None else t.clone()
+    layer = lambda: gpu.fp4_moe_weights(s.fmt, *[mine(t) for t in s.layer.keep], limit=7.0)
+    args = [("fp8blk_block_norm", d["resid"].clone(), None, None, None, 0.0, None, d["w1"].clone(), EPS, outs["x"]),
+            ("fp8blk_moe_route", d["router"].clone(), d["bias"].clone(), outs["x"], gpu.SCORE_SIGMOID, True, 1.5, outs["ids"],
+             outs["p"], s.ws1.clone()),
+            ("int4_gemv", d["codes"].clone(), d["scales"].clone(), None, 32, outs["x"], outs["y"]),
+            ("fp4_moe", layer(), outs["x"], outs["ids"], outs["p"], outs["y"], outs["y"], s.ws2.clone()),
+            ("fp8blk_block_norm", d["resid"].clone(), outs["y"], d["w2"].clone(), d["gate"].clone(), 0.5, outs["out"],
+             d["w3"].clone(), EPS, outs["next"])]
+    owned = [t for a in args for t in a if isinstance(t, torch.Tensor)] + [t for t in args[3][1].keep if t is not None]
+    refs = [weakref.ref(t) for t in owned]
+    calls = [gpu.prepared(*a) for a in args]
+    del args, owned
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    assert [c() for c in calls] == [gpu.OK] * 5
+    torch.cuda.synchronize()
+    assert _same([outs[k] for k in ("x", "ids", "p", "y", "out", "next")], want)
+
+
+def test_prepared_linears_keep_their_tensors(gpu):
+    """The same of a linear and of a group's list of members."""
+    codes = torch.full((32, 128), 0x38, dtype=torch.uint8, device=DEV)  # 1
+    grid, x = torch.ones(1, 1, device=DEV), torch.ones(1, 128, dtype=torch.bfloat16, device=DEV)
+    y = [torch.zeros(1, 32, device=DEV) for _ in range(2)]
+    members = [(codes.clone(), grid.clone(), y[1])]
+    one = [codes.clone(), grid.clone(), x.clone(), y[0]]
+    refs = [weakref.ref(t) for t in one + list(members[0])]
+    calls = [gpu.prepared("fp8blk_gemv", *one), gpu.prepared("fp8blk_gemv_grouped", members, x.clone())]
+    members.clear()
+    one.clear()
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    assert [c() for c in calls] == [gpu.OK] * 2
+    torch.cuda.synchronize()
+    assert (y[0] == 128).all() and (y[1] == 128).all()
