@@ -260,10 +260,12 @@ __device__ __forceinline__ double add_chunks(const RouteArgs& a, int64_t at, int
     return tree(s);
 }
 
-// sigmoid(l) or sqrt(log(1 + exp(l))).
+// sigmoid(l) or sqrt(log(1 + exp(l))), which is exp(l / 2) to the last bit far
+// below 0, where exp(l) is no normal number any more but its root still is.
 __device__ __forceinline__ double own_score(int score, double l) {
     const double t = exp(-fabs(l));  // at most 1
     if (score == FP8BLK_SCORE_SIGMOID) return l >= 0.0 ? 1.0 / (1.0 + t) : t / (1.0 + t);
+    if (l < -700.0) return exp(0.5 * l);
     return sqrt((l > 0.0 ? l : 0.0) + log1p(t));
 }
 

@@ -158,3 +158,23 @@ def test_largest_panel(gpu):
     clear = ((v[:, :2] - v[:, 1:3]) > 1e-11).all(1)
     assert clear.float().mean() > 0.999
     assert torch.equal(ids[clear].long(), want[clear])
+
+
+@pytest.mark.parametrize("M", [1, 20, 2100])
+def test_small_softplus_scores_keep_their_order(gpu, M):
+    """sqrt(log(1 + exp(l))) is exp(l / 2) for l far below 0, in 64 bits a
+    normal number down to l = -1416, though exp(l) is none below -708."""
+    l = torch.tensor([-760.0, -748.0, -800.0, -752.0, -1408.0, -744.0, -712.0, -1440.0, -4992.0] + [-6016.0] * 7)
+    w = torch.zeros(16, 16).bfloat16()
+    w[:, 3] = l.bfloat16()  # exact
+    assert torch.equal(w[:, 3].float(), l)
+    x = torch.zeros(M, 16).bfloat16()
+    x[:, 3] = 1.0
+    ids, p = _run(gpu, x, w, None, 2, 7, True, 2.0)
+    assert (ids == torch.tensor([6, 5, 1, 3, 0, 2, 4])).all()
+    want = torch.exp((l[[6, 5, 1, 3, 0, 2, 4]].double() + 712) / 2)
+    want = 2.0 * want / want.sum()
+    assert ((p.double() - want).abs() <= (U + 1e-12) * want + 2.0 ** -150).all()
+    x[:, 3] = 2.0 ** -1  # -372 .. -3008: no underflow before -1416
+    ids, p = _run(gpu, x, w, None, 2, 4, True, 2.0)
+    assert (ids == torch.tensor([6, 5, 1, 3])).all()
