@@ -682,8 +682,9 @@ int fp4_expert_sequence(const fp8blk_sequence *seq, fp8blk_stream_t stream);
  * y is a block's f32 output (a linear's y), resid the residual stream before
  * it, r' the stream after it and x_next the next block's input. Statistics and
  * products are f32; r' is rounded once, to resid's type, and x_next is formed
- * from the unrounded f32 r'. Squares are summed in f32: a row with a value
- * beyond about 1e18 overflows them.
+ * from the unrounded f32 r'. Squares are summed in f32: a row whose sum of
+ * squares is no f32 (4096 values of 3e17) gives zeros or NaN, and beside an eps
+ * of 0 one whose values are all below about 1e-18 loses digits or gives infinities.
  *   resid, resid_out: [N, cols], f32 or bf16 (resid_type FP8BLK_F32 or
  *     FP8BLK_BF16, the same for both); resid_out may be resid itself.
  *   y: f32 [N, cols]. NULL: the first norm of a model (r' = resid); then

@@ -118,3 +118,15 @@ def test_many_rows_past_32_bit_offsets(gpu):
     torch.cuda.synchronize()
     _check(dict(c, y=None), 0.0, 1e-6, None, x[at], "rows past 2^31")
     assert (x[12345] == 0).all() and (x[N - 2] == 0).all()
+
+
+@pytest.mark.parametrize("spread,eps", [(2.0 ** 54, 1e-6), (2.0 ** -58, 0.0)])
+def test_the_range_of_the_squares(gpu, spread, eps):
+    """Rows near both ends of what f32 sums of squares hold: 4096 of 2^112, and
+    squares around 2^-112 beside an eps of 0."""
+    c = _case(27, 3, 4096, "f32", "none", True, spread)
+    first = dict(c, y=None, post_w=None)
+    none, x = _run(gpu, first, 0.0, eps)
+    _check(first, 0.0, eps, None, x, f"{spread}")
+    out, x = _run(gpu, c, 0.25 * spread, eps)
+    _check(c, 0.25 * spread, eps, out, x, f"{spread}")
