@@ -205,3 +205,49 @@ def test_prepared_linears_keep_their_tensors(gpu):
     assert [c() for c in calls] == [gpu.OK] * 2
     torch.cuda.synchronize()
     assert (y[0] == 128).all() and (y[1] == 128).all()
+
+
+def _offset(t, bytes_off):
+    """A copy of t that lies that many bytes behind an aligned address."""
+    n = t.element_size()
+    room = torch.empty(t.numel() + bytes_off // n, dtype=t.dtype, device=DEV)
+    room[bytes_off // n:].copy_(t.reshape(-1))
+    return room[bytes_off // n:].view(t.shape)
+
+
+@pytest.mark.parametrize("fmt", [I.MXFP4, I.NVFP4])
+@pytest.mark.parametrize("M,hidden,inter", [(1, 1056, 352), (6, 1056, 352), (6, 160, 2080)])
+def test_smallest_alignments(gpu, fmt, M, hidden, inter):
+    """Every buffer that need not be 16-byte aligned, at its smallest alignment."""
+    s = Step(gpu, M, fmt, K=5, hidden=hidden, inter=inter, seed=97)
+    s.run()
+    torch.cuda.synchronize()
+    want, d = s.outputs(), s.d
+    keep = list(s.layer.keep)
+    for i in (1, 4, 7):  # block scales
+        keep[i] = _offset(keep[i], 4 if fmt == I.MXFP4 else 8)
+    for i in (2, 5, 8):  # global scales
+        keep[i] = keep[i] if keep[i] is None else _offset(keep[i], 4)
+    s.layer = gpu.fp4_moe_weights(fmt, *keep, limit=7.0)
+    for k in ("bias", "ids", "p"):
+        d[k] = _offset(d[k], 4)
+    d["scales"] = _offset(d["scales"], 2)
+    for k in ("x", "p", "y", "out", "next"):
+        d[k].fill_(float("nan"))
+    s.run()
+    torch.cuda.synchronize()
+    assert _same(s.outputs(), want)
+
+
+@pytest.mark.parametrize("M,rows,cols,group", [(1, 45, 2080, 32), (5, 9001, 2080, 32), (3, 9001, 1088, 64), (16, 20001, 384, 128)])
+def test_smallest_alignments_of_a_4_bit_linear(gpu, M, rows, cols, group):
+    rng = np.random.default_rng(rows)
+    codes = torch.from_numpy(rng.integers(0, 256, (rows, cols // 2), dtype=np.uint8)).to(DEV)
+    scales = (normal(rng, rows, cols // group) * 0.01).bfloat16().to(DEV)
+    zeros = torch.from_numpy(rng.integers(0, 16, (rows, cols // group), dtype=np.uint8)).to(DEV)
+    x = normal(rng, M, cols).bfloat16().to(DEV)
+    y, z = torch.empty(M, rows, device=DEV), _offset(torch.full((M, rows), float("nan"), device=DEV), 4)
+    gpu.int4_gemv(codes, scales, zeros, group, x, y)
+    gpu.int4_gemv(codes, _offset(scales, 2), _offset(zeros, 1), group, x, z)
+    torch.cuda.synchronize()
+    assert torch.equal(y, z)
