@@ -19,10 +19,16 @@
 // instructions for every byte, hence NVFP4's distance from MXFP4 below.
 //
 // What bounds it: the experts' weights. 16 tokens, 8 of 128 experts of
-// 4096x2048 MXFP4, 1.1 GB: 194 us, 5.7 TB/s (a plain read of that much
-// reaches 6 to 6.9); NVFP4 229 us, 5.1 TB/s. One token, 8 of 64: 29.4 and 34.0
-// us, 3.6 and 3.3 TB/s, where the three launches' starts and ends are half.
-// Small layers are latency (2 tokens, 2 of 8 of 512x512: 7.3 us).
+// 4096x2048 MXFP4, 1.1 GB: 196 us, 5.6 TB/s (a plain read of that much
+// reaches 6 to 6.9); NVFP4 230 us, 5.0 TB/s. One token, 8 of 64: 29.5 and 33.7
+// us, 3.6 and 3.4 TB/s, where gate/up and down each ask for all that they read
+// at once, and the sum is a launch of its own. Tokens that share experts: a
+// workgroup takes 4 slots of an expert (2 in NVFP4's down), as many as the
+// operand holds, so its weights are read, exchanged and widened again for every
+// 4 (16 tokens, 4 of 8 of 2048x4096 MXFP4: 70 us, 21 by its bytes; 14 tokens, 5
+// of 6 of 2560x1024 NVFP4: 47 us, 5 by its bytes; the waves wait half of their
+// time, vector units are 18 to 28% busy). Small layers are latency (2 tokens, 2
+// of 8 of 512x512: 7.7 us).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -48,10 +54,10 @@ constexpr int kBusy = 512;  // workgroups with work: two a compute unit
 // Up to so many weights of down (tokens x experts of a token x slab), down and
 // the sum over the experts are one launch, which saves a launch's start and end
 // but lets tokens read an expert that they share once each. One launch against
-// two, us: 2 tokens, 2 of 8 experts of 512x512 MXFP4 7.6, 10.8; 6 tokens, 4 of
-// 32 of 1440x736 (25e6 weights) 20.1, 23.0; 4 tokens, 8 of 128 of 2048x768
-// (50e6) 24.9, 27.5, NVFP4 28.0, 30.7; 4 tokens, 2 of 8 of 4096x2048 (67e6)
-// 36.7, 31.1; 8 tokens, 6 of 64 of 2048x1024 (101e6) 43.2, 38.2.
+// two, us: 2 tokens, 2 of 8 experts of 512x512 MXFP4 7.7, 10.3; 6 tokens, 4 of
+// 32 of 1440x736 (25e6 weights) 18.8, 21.6; 4 tokens, 8 of 128 of 2048x768
+// (50e6) 23.9, 26.2, NVFP4 26.9, 29.3; 4 tokens, 2 of 8 of 4096x2048 (67e6)
+// 32.7, 28.1; 8 tokens, 6 of 64 of 2048x1024 (101e6) 40.4, 36.7.
 constexpr int64_t kFewWeights = 50 << 20;
 constexpr int kPieces = 3;  // bf16 values that hold an f32 h
 constexpr int kSlots = FP8BLK_MAX_M * FP8BLK_MAX_TOP_K;
@@ -574,8 +580,8 @@ void launch_steps(MoeArgs a, hipStream_t s) {
     // LDS for the operand, besides the waves' scales and sums: at least 1 row of
     // FP8BLK_MAX_COLS columns of x or 3 of FP8BLK_MAX_INTER of h. All of it goes
     // to slots that share an expert's weights, although fewer workgroups then
-    // fit a compute unit (16 tokens, 4 of 8 experts of 2048x4096 MXFP4: 72 us,
-    // 85 with at most 64 KB; 8 tokens, 6 of 32 of 5120x8192 NVFP4: 477 against 548).
+    // fit a compute unit (16 tokens, 4 of 8 experts of 2048x4096 MXFP4: 70 us,
+    // 82 with at most 64 KB; 8 tokens, 6 of 32 of 5120x8192 NVFP4: 458 against 493).
     const int64_t own = waves * U::T * (kTile * U::ROW + 512), room = 160 * 1024 - own;
     static_assert((DOWN ? FP8BLK_MAX_INTER : FP8BLK_MAX_COLS) * 2 * U::LANES + kWaves * U::T * (kTile * U::ROW + 512) <= 160 * 1024,
                   "LDS of a workgroup");
@@ -584,22 +590,27 @@ void launch_steps(MoeArgs a, hipStream_t s) {
     // Several tiles a workgroup, for whose operand and start it pays once while
     // the next tile's loads are in flight, where about two workgroups with work
     // for each compute unit are left. us for 1, 2, 4 and 8 tiles at most: 16
-    // tokens, 8 of 128 experts of 4096x2048 MXFP4 240, 203, 196, 207; 4 tokens,
-    // 8 of 128 of 4096x1536 NVFP4 92, 84, 73, 73; where it leaves too few, 14
-    // tokens, 5 of 6 of 2560x1024 NVFP4, 4 tiles 60 and this rule's 2 48.
+    // tokens, 8 of 128 experts of 4096x2048 MXFP4 228, 195, 196, 202; 4 tokens,
+    // 8 of 128 of 4096x1536 NVFP4 82, 83, 74, 74; where it leaves too few, 14
+    // tokens, 5 of 6 of 2560x1024 NVFP4, 4 tiles 59 and this rule's 2 47.
     const double turns = (double)tiles * busy_slots(a) / kBusy;
     a.turns = turns >= 3.0 ? 4 : turns >= 1.5 ? 2 : 1;
     const dim3 grid((unsigned)ceil_div(tiles, a.turns), (unsigned)a.slots);
     k_moe<FMT, DOWN, NS><<<grid, 64 * waves, (size_t)(a.most * row_bytes + own), s>>>(a);
 }
 
-// Steps a wave takes at a time: fewer where the columns are few. Down: 2
-// wherever 8 waves then cover the row, which for one token is more waves than
-// 4 steps give (1 token, 8 of 4096x2048: 36.3 against 37.8 us NVFP4, 32.2
-// against 32.8 MXFP4; 16 tokens 235 against 233, 199 against 198). Gate and up:
-// 2 up to 1024 columns (16 tokens, 8 of 64 experts of 512x256 MXFP4 12.7 us, with 4
-// 13.7; 8 of 2048x1408, though, 69.7, with 4 63.0), 4 up to 2048, else 8 (1 token,
-// 8 of 4096x2048 37.9 us, with 4 39.3).
+// Steps a wave takes at a time: fewer where the columns are few. us for both
+// sides, of experts of 4096x2048 where no other size is named.
+// Down: 2 wherever 8 waves then cover the row, else 4. With 4 there too, 1 token,
+// 8 of 64 NVFP4 35.0 against 33.8, MXFP4 29.9 against 29.6; 4 tokens NVFP4 89.2
+// against 87.7; from 8 tokens on the other way round or the same (NVFP4 128.6
+// against 131.6; 16 tokens, 8 of 128 229 against 233, MXFP4 197 against 198), but
+// a token's bits are those of any panel, so the tokens do not choose.
+// Gate and up: 2 up to 1024 columns (16 tokens, 8 of 64 of 512x256 MXFP4 13.3,
+// with 4 14.1), 4 up to 2048 (8 of 64 of 2048x1408 73.5, with 2 79.1), else 8
+// (16 tokens, 8 of 128 MXFP4 196, with 4 207, NVFP4 228 and 236; 4 tokens, 6 of
+// 32 of 5120x1536 MXFP4 62.9 and 68.1, NVFP4 71.8 and 71.6; 1 token, 8 of 64
+// MXFP4 the same, NVFP4 34.6 and 33.8).
 constexpr int down_steps(int cols) { return cols <= 2 * kStep * kWaves ? 2 : 4; }
 
 template <int FMT>

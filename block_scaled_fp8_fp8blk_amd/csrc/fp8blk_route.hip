@@ -9,7 +9,10 @@
 //     bits is not hidden behind it: 2 more vector instructions for each make it
 //     88. 2048 tokens, 256 experts, 4096 columns: 78 us, 55 TFLOP/s (a library's
 //     64-bit product of inputs that are converted already: 125 us; of 4096^3:
-//     71 TFLOP/s).
+//     74 TFLOP/s).
+//   - some hundred tokens: rounds of whole tiles over the compute units, each
+//     tile with all its columns (300 tokens 31 us, 700 44, 1024 46, 1500 74: 1.6
+//     to 3.6 times their products at 74 TFLOP/s).
 //   - a few tokens: latency, of two launches, a chain of 32 instructions and a
 //     choice (1 token, 256 experts, 4096 columns: 8.7 us, of which an empty
 //     launch takes 2.6 each).
