@@ -11,8 +11,8 @@ Tensors must be contiguous CUDA (HIP) tensors of these dtypes:
   scales_f32, y           torch.float32
   x_bf16, w_bf16, out     torch.bfloat16, torch.int16 or torch.uint16 (bf16 bit patterns)
   ws                      any dtype, or None when the op needs no workspace
-The norms, router, expert layer and 4-bit linear at the end of this file take
-tensors of any one device, and run on that device's current stream unless
+The norms, router, expert layer, 4-bit linear, rotary positions and attention at
+the end of this file take tensors of any one device, and run on that device's current stream unless
 `stream` names another one of it.
 """
 from __future__ import annotations
@@ -38,7 +38,8 @@ EXPORTS = ("fp8blk_abi_version", "fp8blk_strerror", "fp8blk_workspace_bytes", "f
            "bf16_gemv_twin_mfma_sequence", "fp8blk_gemm_staged", "bf16_gemm_twin", "fp8blk_act_quant",
            "fp4_load_check", "fp4_dequant_bf16", "fp4_expert_gemv", "fp4_expert_sequence_init",
            "fp4_expert_sequence", "fp8blk_chain_bytes", "fp8blk_chain_init", "fp8blk_gemv_chain",
-           "fp8blk_chain_status", "fp8blk_block_norm", "fp8blk_moe_route", "fp4_moe_bytes", "fp4_moe", "int4_gemv")
+           "fp8blk_chain_status", "fp8blk_block_norm", "fp8blk_moe_route", "fp4_moe_bytes", "fp4_moe", "int4_gemv",
+           "fp8blk_rope_freqs", "fp8blk_rope_append", "fp8blk_attn_bytes", "fp8blk_paged_attn", "fp8blk_latent_attn")
 MAX_GROUP = 8
 MAX_SEQ = 65536
 MAX_CHAIN = 65536
@@ -47,7 +48,8 @@ ARM_FP8, ARM_BF16, ARM_FP8_MFMA, ARM_BF16_MFMA, ARM_MXFP4, ARM_NVFP4 = 0, 1, 2, 
 FMT_MXFP4, FMT_NVFP4 = 0, 1
 MAX_EXPERTS, MAX_TOP_K, MAX_INTER = 1024, 16, 20480
 SCORE_SOFTMAX, SCORE_SIGMOID, SCORE_SQRT_SOFTPLUS = 0, 1, 2
-TYPE_F32, TYPE_BF16 = 0, 1
+TYPE_F32, TYPE_BF16, TYPE_E4M3 = 0, 1, 2
+MAX_PAGE, MAX_HEADS, MAX_HEAD_COLS, MAX_ROT = 65536, 1024, 1024, 256
 
 
 class Linear(ctypes.Structure):
@@ -95,6 +97,33 @@ class Fp4MoeLayer(ctypes.Structure):
                                                "gate_global", "up_global", "down_global")] + [
         ("experts", ctypes.c_int64), ("hidden", ctypes.c_int64), ("inter", ctypes.c_int64), ("fmt", ctypes.c_int32),
         ("limit", ctypes.c_float)]
+
+
+class CacheRecord(ctypes.Structure):
+    """fp8blk_cache: a paged cache's buffers, strides in values, and type."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("pages", "page_size", "heads", "k_cols", "v_cols", "k_page", "k_slot", "k_head",
+                                      "v_page", "v_slot", "v_head")] + [
+        ("type", ctypes.c_int32), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class RopeRecord(ctypes.Structure):
+    """fp8blk_rope: which columns rotate how fast."""
+    _fields_ = [("freqs", ctypes.c_void_p), ("rot", ctypes.c_int64), ("interleaved", ctypes.c_int32),
+                ("rot_first", ctypes.c_int32), ("mscale", ctypes.c_float)]
+
+
+class HeadsRecord(ctypes.Structure):
+    """fp8blk_heads: q, k or v of the tokens, in one or two parts."""
+    _fields_ = [("pass_", ctypes.c_void_p), ("rot", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("pass_token", "pass_head", "rot_token", "rot_head", "heads", "pass_cols",
+                                      "norm_cols")] + [("norm", ctypes.c_void_p), ("type", ctypes.c_int32)]
+
+
+class BatchRecord(ctypes.Structure):
+    """fp8blk_batch: the sequences of an attention call."""
+    _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("starts", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("seqs", "max_pages", "max_new", "max_len")]
 
 
 _lib = None
@@ -187,6 +216,14 @@ def load():
     L.fp4_moe.argtypes = [ctypes.POINTER(Fp4MoeLayer), vp, i64, vp, vp, i32, vp, vp, vp, sz, vp]
     L.fp4_moe.restype = i32
     L.int4_gemv.argtypes, L.int4_gemv.restype = [vp, vp, vp, i32, i64, i64, vp, i64, vp, vp], i32
+    f64, f32 = ctypes.c_double, ctypes.c_float
+    L.fp8blk_rope_freqs.argtypes, L.fp8blk_rope_freqs.restype = [i64, f64, f64, f64, f64, f64, vp], i32
+    L.fp8blk_rope_append.argtypes = [vp, vp, i64, vp, vp, i64, i64, vp, vp, vp, vp, f32, vp]
+    L.fp8blk_rope_append.restype = i32
+    L.fp8blk_attn_bytes.argtypes, L.fp8blk_attn_bytes.restype = [vp, i64, i64, i64, i64, i64], sz
+    for attend in (L.fp8blk_paged_attn, L.fp8blk_latent_attn):
+        attend.argtypes = [vp, vp, i64, i64, i64, i64, vp, f32, i32, i64, vp, vp, i64, i64, vp, sz, vp]
+        attend.restype = i32
     _lib = L
     return L
 
@@ -1066,6 +1103,244 @@ def int4_gemv(codes, scales_bf16, zeros, group, x_bf16, y, stream=None, check=Tr
     return _enqueue(load().int4_gemv, dev, args, stream, "int4_gemv", check)
 
 
+# --- between the q and kv linears and o: positions, paged cache, attention -----------
+
+def fp8blk_rope_freqs(rot, base=10000.0, factor=1.0, original=4096, fast=32.0, slow=1.0):
+    """Radians a position of the rot / 2 pairs, float64 on the CPU: base^(-2i/rot),
+    for factor > 1 divided by it by parts, as the header says."""
+    import torch
+    out = torch.empty(max(rot, 0) // 2, dtype=torch.float64)
+    st = load().fp8blk_rope_freqs(rot, base, factor, original, fast, slow, out.data_ptr())
+    if st != OK:
+        raise Fp8BlkError(st, "fp8blk_rope_freqs")
+    return out
+
+
+class Rope:
+    """Rotary positions (fp8blk_rope): `handle` is the record that
+    fp8blk_rope_append takes, `freqs` the tensor it points at."""
+
+    def __init__(self, handle, freqs):
+        self.handle, self.freqs = handle, freqs
+        self.pointer = ctypes.byref(handle)
+        self.device, self.rot, self.rot_first = freqs.get_device(), handle.rot, bool(handle.rot_first)
+
+
+def fp8blk_rope(freqs, interleaved=False, rot_first=True, mscale=1.0):
+    """What fp8blk_rope_append rotates: freqs float64 [rot / 2] on the GPU (radians
+    a position of each pair), pairs (2i, 2i + 1) if interleaved, else (i, i +
+    rot / 2); rot_first: the rotated columns are a head's first, else its last;
+    mscale multiplies them. freqs must stay as they are while this is used."""
+    _load_torch()
+    if not isinstance(freqs, _torch.Tensor) or not freqs.is_cuda:
+        raise TypeError("freqs must be a CUDA tensor")
+    if freqs.dim() != 1:
+        raise ValueError(f"freqs must be [rot / 2], got shape {tuple(freqs.shape)}")
+    p = _buf(freqs, freqs.get_device(), (_torch.float64,), freqs.shape, "freqs")
+    return Rope(RopeRecord(p, 2 * freqs.shape[0], interleaved, rot_first, mscale), freqs)
+
+
+class PagedCache:
+    """A paged cache (fp8blk_cache): `handle` is the record that
+    fp8blk_rope_append and the attention calls take, `keep` the tensors it
+    points at."""
+
+    def __init__(self, handle, device, keep):
+        self.handle, self.device, self.keep = handle, device, keep
+        self.pointer = ctypes.byref(handle)
+        self.heads, self.k_cols, self.v_cols, self.latent = handle.heads, handle.k_cols, handle.v_cols, handle.v is None
+
+
+def _strided(t, device, dims, name):
+    """Pointer of a tensor on `device` whose last dimension is contiguous."""
+    if not isinstance(t, _torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on device {device}, it is on {t.device}")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
+    if t.stride(dims - 1) != 1 and t.shape[dims - 1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr()
+
+
+def _outer(t, step):
+    """Strides of all dimensions but the last; those of dimensions of one, which
+    say nothing, as one row's, rounded up to `step`."""
+    row = -(-t.shape[-1] // step) * step
+    return [row if n == 1 else s for n, s in zip(t.shape[:-1], t.stride()[:-1])]
+
+
+def fp8blk_cache(k, v, k_scale=1.0, v_scale=1.0, v_cols=None):
+    """A paged cache of keys k [pages, page_size, heads, k_cols] and values v
+    [pages, page_size, heads, v_cols], bfloat16, or float8_e4m3fn with their
+    scales; any strides (multiples of 16) of the first three dimensions, so a
+    transposed view of pages that hold heads of slots is one too. v None: a latent
+    cache, the values being the first v_cols columns of k (None: all). Checked here, once;
+    the tensors must stay where they are while the cache is used."""
+    _load_torch()
+    kinds = {_torch.bfloat16: TYPE_BF16, _torch.float8_e4m3fn: TYPE_E4M3}
+    if not isinstance(k, _torch.Tensor) or not k.is_cuda:
+        raise TypeError("k must be a CUDA tensor")
+    dev = k.get_device()
+    h = CacheRecord(k_scale=k_scale, v_scale=v_scale)
+    for name, t in (("k", k), ("v", v)):
+        if t is None:
+            continue
+        if isinstance(t, _torch.Tensor) and (t.dtype not in kinds or t.dtype != k.dtype):
+            raise TypeError(f"{name}: dtype {t.dtype}, k and v must both be bfloat16 or float8_e4m3fn")
+        setattr(h, name, _strided(t, dev, 4, name))
+        if t.shape[:3] != k.shape[:3]:
+            raise ValueError(f"v must have k's pages, slots and heads {tuple(k.shape[:3])}, got shape {tuple(t.shape)}")
+        for part, stride in zip(("page", "slot", "head"), _outer(t, 16)):
+            setattr(h, f"{name}_{part}", stride)
+    if v is not None and v_cols is not None:
+        raise ValueError("v_cols belongs to a cache without v")
+    h.type, h.v_cols = kinds[k.dtype], k.shape[3] if v is None and v_cols is None else v_cols if v is None else v.shape[3]
+    h.pages, h.page_size, h.heads, h.k_cols = k.shape
+    return PagedCache(h, dev, (k, v))
+
+
+def _heads(parts, device, N, rot, norm, rot_first, name):
+    """fp8blk_heads of (pass, rot), each [N, heads, cols] or None, and its heads
+    and columns."""
+    first, turned = parts
+    h = HeadsRecord()
+    kind = None
+    for part, field, t in (("pass", "pass_", first), ("rot", "rot", turned)):
+        if t is None:
+            continue
+        setattr(h, field, _strided(t, device, 3, name))
+        if t.dtype not in _f32 + _bf16 or kind not in (None, t.dtype):
+            raise TypeError(f"{name}: dtype {t.dtype}, both parts must be float32, or both bfloat16")
+        kind = t.dtype
+        if t.shape[0] != N or (h.heads and t.shape[1] != h.heads) or (part == "rot" and t.shape[2] != rot):
+            raise ValueError(f"{name} must be [N={N}, heads, cols] and [N, heads, rot={rot}], got shape {tuple(t.shape)}")
+        h.heads = t.shape[1]
+        token, head = _outer(t, 8)
+        setattr(h, part + "_token", token)
+        setattr(h, part + "_head", head)
+    if kind is None or (rot and turned is None):
+        raise ValueError(f"{name} is needed")
+    h.type = TYPE_F32 if kind in _f32 else TYPE_BF16
+    h.pass_cols = 0 if first is None else first.shape[2]
+    cols = h.pass_cols + rot
+    if norm is not None:
+        if norm.dim() != 1 or norm.shape[0] not in (cols, h.pass_cols):
+            raise ValueError(f"{name}'s norm must be [{cols}] or [{h.pass_cols}], got shape {tuple(norm.shape)}")
+        h.norm, h.norm_cols = _buf(norm, device, _bf16, norm.shape, name + "_norm"), norm.shape[0]
+    return h, h.heads, cols
+
+
+def _rope_append_args(rope, positions, q, q_out, k, v, cache, slots, q_norm=None, k_norm=None, eps=1e-6):
+    if _torch is None:
+        _load_torch()
+    dev, rot = rope.device, rope.rot
+    if positions.dim() != 1:
+        raise ValueError(f"positions must be [N], got shape {tuple(positions.shape)}")
+    N = positions.shape[0]
+    positions_p = _buf(positions, dev, _i32, (N,), "positions")
+    hq = out_p = hk = hv = slots_p = None
+    out_strides = (0, 0)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out belong together")
+    if q is not None:
+        hq, heads, cols = _heads(q, dev, N, rot, q_norm, rope.rot_first, "q")
+        out_p = _strided(q_out, dev, 3, "q_out")
+        if q_out.dtype not in _bf16:
+            raise TypeError(f"q_out: dtype {q_out.dtype} not in {_bf16}")
+        if q_out.shape != (N, heads, cols):
+            raise ValueError(f"q_out must be {(N, heads, cols)}, got shape {tuple(q_out.shape)}")
+        out_strides = _outer(q_out, 8)
+    elif q_norm is not None:
+        raise ValueError("q_norm without q")
+    if k is None:
+        if v is not None or cache is not None or slots is not None or k_norm is not None:
+            raise ValueError("v, cache, slots and k_norm belong to k")
+    else:
+        if cache is None or slots is None:
+            raise ValueError("k needs a cache and slots")
+        if cache.device != dev:
+            raise ValueError(f"the cache is on device {cache.device}, the frequencies are on {dev}")
+        hk, heads, cols = _heads(k, dev, N, rot, k_norm, rope.rot_first, "k")
+        if (heads, cols) != (cache.heads, cache.k_cols):
+            raise ValueError(f"k must have the cache's {cache.heads} heads of {cache.k_cols}, got {heads} of {cols}")
+        slots_p = _buf(slots, dev, _i32, (N,), "slots")
+        if (v is None) != cache.latent:
+            raise ValueError("v is needed, but for a latent cache, which has none")
+        if v is not None:
+            hv, heads, cols = _heads((v, None), dev, N, 0, None, True, "v")
+            if (heads, cols) != (cache.heads, cache.v_cols):
+                raise ValueError(f"v must have the cache's {cache.heads} heads of {cache.v_cols}, got {heads} of {cols}")
+    ref = lambda h: None if h is None else ctypes.byref(h)  # noqa: E731
+    return dev, (rope.pointer, positions_p, N, ref(hq), out_p, *out_strides, ref(hk), ref(hv),
+                 None if cache is None else cache.pointer, slots_p, eps)
+
+
+def fp8blk_rope_append(rope, positions, q, q_out, k, v, cache, slots, q_norm=None, k_norm=None, eps=1e-6, stream=None,
+                       check=True):
+    """Rotate q into q_out and k into the cache at positions int32 [N], and v beside
+    it, in one launch. q and k: pairs (pass, rot) of float32 or bfloat16 [N, heads,
+    cols] and [N, heads, rot], the columns that stay and those that `rope`
+    (fp8blk_rope) rotates, either with any strides that are multiples of 8 (slices
+    of one linear's output, or a part that every head shares by expand); pass None
+    where all rotate. v: [N, heads, v_cols], None for a latent cache. slots int32
+    [N]: where in the cache (page * page_size + slot, -1: nowhere). q_norm, k_norm:
+    bfloat16 RMS norm weights of the written row, or of pass alone. q with q_out, or
+    k with v, cache and slots, may be None."""
+    dev, args = _rope_append_args(rope, positions, q, q_out, k, v, cache, slots, q_norm, k_norm, eps)
+    return _enqueue(load().fp8blk_rope_append, dev, args, stream, "fp8blk_rope_append", check)
+
+
+def fp8blk_attn_bytes(cache, heads, seqs, max_new, max_len, window=0):
+    """Bytes of workspace of fp8blk_paged_attn and fp8blk_latent_attn (0: none)."""
+    return load().fp8blk_attn_bytes(cache.pointer, heads, seqs, max_new, max_len, window)
+
+
+def _attn_args(cache, q, table, lens, starts, max_new, max_len, scale, out, ws, causal=True, window=0, sinks=None):
+    dev = cache.device
+    q_p, out_p = _strided(q, dev, 3, "q"), _strided(out, dev, 3, "out")
+    for name, t in (("q", q), ("out", out)):
+        if t.dtype not in _bf16:
+            raise TypeError(f"{name}: dtype {t.dtype} not in {_bf16}")
+    N, heads, cols = q.shape
+    if cols != cache.k_cols:
+        raise ValueError(f"q must be [N, heads, {cache.k_cols}], got shape {tuple(q.shape)}")
+    if out.shape != (N, heads, cache.v_cols):
+        raise ValueError(f"out must be {(N, heads, cache.v_cols)}, got shape {tuple(out.shape)}")
+    if table.dim() != 2:
+        raise ValueError(f"table must be [seqs, pages], got shape {tuple(table.shape)}")
+    S = table.shape[0]
+    batch = BatchRecord(_buf(table, dev, _i32, table.shape, "table"), _buf(lens, dev, _i32, (S,), "lens"),
+                        _buf(starts, dev, _i32, (S + 1,), "starts"), S, table.shape[1], max_new, max_len)
+    wsp, wsb = _workspace(ws, dev)
+    return dev, (cache.pointer, q_p, *_outer(q, 8), N, heads, ctypes.byref(batch), scale, 1 if causal else 0, window,
+                 _buf(sinks, dev, _f32, (heads,), "sinks", False), out_p, *_outer(out, 8), wsp, wsb)
+
+
+def fp8blk_paged_attn(cache, q, table, lens, starts, max_new, max_len, scale, out, ws, causal=True, window=0, sinks=None,
+                      stream=None, check=True):
+    """Attention of new tokens q [N, heads, k_cols] into out [N, heads, v_cols],
+    bfloat16, over a paged cache (fp8blk_cache): sequence s has lens[s] tokens in
+    the pages table[s] (int32 [seqs, pages]), the last starts[s + 1] - starts[s]
+    of them being rows starts[s] .. of q (int32 [seqs + 1]). max_new and max_len
+    are the most new tokens and tokens of a sequence, on the host. causal; window >
+    0: only the last `window` keys; sinks f32 [heads] or None: a logit in the sum
+    below. ws: fp8blk_attn_bytes(...) bytes. Key and value columns 64, 64; 128,
+    128; 192, 128 or 256, 256."""
+    dev, args = _attn_args(cache, q, table, lens, starts, max_new, max_len, scale, out, ws, causal, window, sinks)
+    return _enqueue(load().fp8blk_paged_attn, dev, args, stream, "fp8blk_paged_attn", check)
+
+
+def fp8blk_latent_attn(cache, q, table, lens, starts, max_new, max_len, scale, out, ws, causal=True, window=0, sinks=None,
+                       stream=None, check=True):
+    """fp8blk_paged_attn over a latent cache: one bfloat16 row of 512 or 576 columns a
+    token for all heads, its first 512 the values too; q [N, heads, 512 or 576]
+    and out [N, heads, 512] in the latent space."""
+    dev, args = _attn_args(cache, q, table, lens, starts, max_new, max_len, scale, out, ws, causal, window, sinks)
+    return _enqueue(load().fp8blk_latent_attn, dev, args, stream, "fp8blk_latent_attn", check)
+
+
 def raw_call(name: str, *args):
     """Call an exported symbol with raw ctypes arguments (pointers as ints).
     Used by tests that exercise the C ABI's argument checks directly."""
@@ -1082,13 +1357,15 @@ def prepared(name: str, *tensors_and_sizes, stream=None):
     launches (codes, scales_f32, src_f32, c, y) and (members, src_f32, c), the
     next-input launches (codes, scales_f32, x_bf16, y, c, x_next) and
     (members, x_bf16, k, c, x_next), the staged GEMMs (..., ws), the sequence launches (a planned Sequence), and
-    "fp8blk_block_norm", "fp8blk_moe_route", "fp4_moe" and "int4_gemv" with their own arguments."""
+    "fp8blk_block_norm", "fp8blk_moe_route", "fp4_moe", "int4_gemv", "fp8blk_rope_append", "fp8blk_paged_attn" and
+    "fp8blk_latent_attn" with their own arguments."""
     import torch
     fn = getattr(load(), name)
     # what the marshalled pointers point into (a group's list may change later)
     keep = [list(a) if isinstance(a, (list, tuple)) else a for a in tensors_and_sizes]
     around = {"fp8blk_block_norm": _block_norm_args, "fp8blk_moe_route": _moe_route_args, "fp4_moe": _moe_args,
-              "int4_gemv": _int4_args}.get(name)
+              "int4_gemv": _int4_args, "fp8blk_rope_append": _rope_append_args, "fp8blk_paged_attn": _attn_args,
+              "fp8blk_latent_attn": _attn_args}.get(name)
     if around is not None:
         dev, args = around(*tensors_and_sizes)
         stream = torch.cuda.current_stream(dev) if stream is None else stream

@@ -78,4 +78,9 @@ size_t gemm_workspace_bytes(int op, int64_t rows, int64_t cols);
 // Workspace of the router (fp8blk_route.hip); 0 for a bad shape.
 size_t route_workspace_bytes(int64_t experts, int64_t cols, int64_t M);
 
+// Whether a paged cache is as documented, and the bytes from its first key (value)
+// to its last (fp8blk_rope.hip).
+bool cache_ok(const fp8blk_cache& c);
+int64_t cache_span(const fp8blk_cache& c, bool values);
+
 }  // namespace fp8blk

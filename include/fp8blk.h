@@ -814,6 +814,168 @@ int fp4_moe(const fp4_moe_layer *layer, const uint16_t *x_bf16, int64_t M, const
 int int4_gemv(const uint8_t *codes, const uint16_t *scales_bf16, const uint8_t *zeros, int group, int64_t rows,
               int64_t cols, const uint16_t *x_bf16, int64_t M, float *y, fp8blk_stream_t stream);
 
+/*
+ * Between a layer's q and kv linears and its o linear: rotary positions, a
+ * paged cache of keys and values, and attention over it. As above, nothing
+ * allocates, waits or keeps state, everything may be captured in a HIP graph,
+ * and calls that overlap in time need workspaces of their own.
+ */
+
+/*
+ * A paged cache (HOST struct). Key row (page p, slot i, head h) is k_cols values
+ * at k + p * k_page + i * k_slot + h * k_head, strides in values, so pages may
+ * hold slots of heads or heads of slots, and keys and values may share one
+ * buffer; likewise v. v NULL: a latent cache, whose values are the first v_cols
+ * columns of the key rows.
+ *   type FP8BLK_BF16: values as they are, k_scale and v_scale 1.
+ *   type FP8BLK_E4M3: e4m3 codes, value = code * k_scale (v_scale); the scales
+ *     are finite and above 0, and not below 2^-100 nor above 2^100.
+ *   page_size: a power of two, 1 .. FP8BLK_MAX_PAGE; pages >= 1; pages *
+ *   page_size < 2^31; 1 <= heads <= FP8BLK_MAX_HEADS; k_cols, v_cols: multiples
+ *   of 16 up to FP8BLK_MAX_HEAD_COLS (v_cols <= k_cols in a latent cache).
+ *   k, v: device, 16-byte aligned; strides: multiples of 16, at least the row's
+ *   columns.
+ */
+#define FP8BLK_E4M3 2
+#define FP8BLK_MAX_PAGE 65536
+#define FP8BLK_MAX_HEADS 1024
+#define FP8BLK_MAX_HEAD_COLS 1024
+typedef struct fp8blk_cache {
+    void *k, *v;
+    int64_t pages, page_size, heads, k_cols, v_cols;
+    int64_t k_page, k_slot, k_head;
+    int64_t v_page, v_slot, v_head;
+    int32_t type;
+    float k_scale, v_scale;
+} fp8blk_cache;
+
+/*
+ * Radians a position of the pairs of `rot` rotated columns (HOST, 64 bits):
+ *   freqs[i] = base^(-2 i / rot), i < rot / 2
+ * and, with factor > 1 (a context `factor` times the `original` one), by parts
+ * (the YaRN paper's "NTK-by-parts"): with t = original * freqs[i] / (2 pi) turns
+ * in the original context, freqs[i] stays where t > fast, is divided by factor
+ * where t < slow, and changes in between as w + (1 - w) / factor, w = (t - slow)
+ * / (fast - slow). fast == slow: at t >= fast it stays.
+ *   rot: a multiple of 8, 8 .. FP8BLK_MAX_ROT; base > 0; factor >= 1; original
+ *   >= 1 where factor > 1; 0 <= slow <= fast; all finite.
+ * Pure host function.
+ */
+#define FP8BLK_MAX_ROT 256
+int fp8blk_rope_freqs(int64_t rot, double base, double factor, double original, double fast, double slow,
+                      double *freqs);
+
+/*
+ * Rotary positions, and new keys and values into a paged cache, in one launch.
+ * For token n at position p, every head of q and k:
+ *   x: pass_cols columns as they come beside rot columns to rotate; in the row
+ *     that is written the rotated ones come first (rot_first) or last
+ *   with norm: x = x / sqrt(mean x^2 + eps) * norm over the whole row
+ *     (norm_cols = pass_cols + rot, weights in the order of the written row) or
+ *     over the pass_cols columns alone (norm_cols = pass_cols)
+ *   pair i of the rotated columns, (2 i, 2 i + 1) if interleaved, else (i, i +
+ *     rot / 2): (a, b) -> mscale * (a cos t - b sin t, a sin t + b cos t),
+ *     t = p * freqs[i]
+ * q's rows are written to q_out as bf16, k's and v's to the cache's slot
+ * slots[n] (page slots[n] / page_size), bf16 or e4m3(value / scale), values past
+ * +-448 to +-448. A slot outside [0, pages * page_size) is not written (padding);
+ * the others are distinct (of two tokens with one slot either may be left, in
+ * parts). Angles are formed and reduced in 64 bits, cos and sin rounded to f32;
+ * norms and rotation are f32, rounded once at the end.
+ *   heads (HOST structs): pass [N, heads, pass_cols] and rot [N, heads, rot],
+ *     both f32 or bf16 (type), each with a token and a head stride in values (0:
+ *     the same for all); NULL: none, pass_cols 0 or no rotated columns (v has
+ *     none and no norm). heads: 1 .. FP8BLK_MAX_HEADS; pass_cols: a multiple of
+ *     8; pass_cols + rot <= FP8BLK_MAX_HEAD_COLS.
+ *   rope: freqs f64 [rot / 2], device, 8-byte aligned; rot as for
+ *     fp8blk_rope_freqs; mscale finite.
+ *   positions, slots: int32 [N], device, 4-byte aligned; 1 <= N <=
+ *     FP8BLK_MAX_PANEL. eps >= 0 and finite.
+ *   q and q_out may be NULL together; k, cache and slots too, and v is NULL with
+ *     them or where the cache is a latent one. k has the cache's heads and k_cols
+ *     columns, v the cache's heads and v_cols.
+ *   q_out: [N, heads, cols] with strides q_token and q_head in values.
+ *   All buffers: device; values 16-byte aligned, strides multiples of 8, an
+ *   output's at least its columns. q_out and the cache overlap no input and not
+ *   each other (else FP8BLK_ERR_ARG, for the span from first to last byte).
+ * A token's bits do not depend on the others. Enqueued on `stream`; does not wait.
+ */
+typedef struct fp8blk_rope {
+    const double *freqs;
+    int64_t rot;
+    int32_t interleaved, rot_first;
+    float mscale;
+} fp8blk_rope;
+
+typedef struct fp8blk_heads {
+    const void *pass, *rot;
+    int64_t pass_token, pass_head, rot_token, rot_head;
+    int64_t heads, pass_cols, norm_cols;
+    const uint16_t *norm;
+    int32_t type; /* FP8BLK_F32 or FP8BLK_BF16 */
+} fp8blk_heads;
+
+int fp8blk_rope_append(const fp8blk_rope *rope, const int32_t *positions, int64_t N, const fp8blk_heads *q,
+                       uint16_t *q_out, int64_t q_token, int64_t q_head, const fp8blk_heads *k, const fp8blk_heads *v,
+                       const fp8blk_cache *cache, const int32_t *slots, float eps, fp8blk_stream_t stream);
+
+/*
+ * Attention of new tokens over a paged cache: one token a sequence (decode), a
+ * few (verify) or a prompt's chunk, of several sequences at once. Sequence s has
+ * lens[s] tokens in the cache, the new ones among them (append first), and its
+ * new tokens are rows starts[s] .. starts[s + 1] - 1 of q and out, the last of
+ * its tokens in order: row i stands at position p = lens[s] - starts[s + 1] + i.
+ * Key j lies at slot j % page_size of page table[s, j / page_size]. For each row
+ * and head h, over the keys j < lens[s] that it sees:
+ *   z[j] = scale * q . k[j];  out = sum_j exp(z[j]) v[j] / (sum_j exp(z[j]) + exp(sinks[h]))
+ * It sees j <= p if causal, and j > p - window if window > 0. sinks: f32 [heads]
+ * or NULL (no such term). A row that sees nothing, or only scores of -inf, gives
+ * 0. What a row does not see does not touch it, infinities and NaN in it
+ * included. Head h reads key head h / (heads / cache heads).
+ *   table: int32 [seqs, max_pages]; a page outside [0, pages) or past max_pages
+ *     holds no keys. lens: int32 [seqs], starts: int32 [seqs + 1], not falling, in
+ *     [0, N]; device, 4-byte aligned. A sequence may have no new tokens; rows
+ *     outside of all are left as they were.
+ *   max_new, max_len (host): at least every sequence's new tokens and lens. A
+ *     sequence's tokens past max_new get no output; lens past max_len only take
+ *     longer.
+ *   q: bf16 [N, heads, k_cols], out: bf16 [N, heads, v_cols], each with a token
+ *     and a head stride in values (multiples of 8; out's at least v_cols);
+ *     device, 16-byte aligned. out overlaps neither q nor the cache (else
+ *     FP8BLK_ERR_ARG, for the span from first to last byte). heads: a multiple of
+ *     the cache's, up to FP8BLK_MAX_HEADS; scale finite.
+ *   fp8blk_paged_attn: a cache with v of k_cols, v_cols = 64, 64; 128, 128; 192,
+ *     128 or 256, 256, bf16 or e4m3 (with heads = cache heads and 192, 128 this is
+ *     latent attention in its expanded form).
+ *   fp8blk_latent_attn: a latent cache (v NULL), bf16, one head, v_cols 512 and
+ *     k_cols 512 or 576 (latent attention in its absorbed form).
+ *   1 <= N, seqs, max_new, max_pages <= FP8BLK_MAX_PANEL (max_pages: 2^30);
+ *   1 <= max_len < 2^30; 0 <= window < 2^30.
+ *   ws: device, 256-byte aligned, >= fp8blk_attn_bytes(...) bytes (0: none needed,
+ *     or bad sizes; ws may then be NULL); its contents on entry do not matter.
+ * Sums and the softmax's statistics are f32, the weights exp(z - max) are rounded
+ * to bf16 for their product with v (the sum below them is of the unrounded ones).
+ * With max_new <= FP8BLK_MAX_M a row's bits depend on its own sequence up to its
+ * position, on seqs, max_len, window and the heads, and on nothing else: the rows of a
+ * verify panel equal those of single-token calls, bit for bit.
+ * Enqueued on `stream`; does not wait.
+ */
+typedef struct fp8blk_batch {
+    const int32_t *table, *lens, *starts;
+    int64_t seqs, max_pages, max_new, max_len;
+} fp8blk_batch;
+
+size_t fp8blk_attn_bytes(const fp8blk_cache *cache, int64_t heads, int64_t seqs, int64_t max_new, int64_t max_len,
+                         int64_t window);
+int fp8blk_paged_attn(const fp8blk_cache *cache, const uint16_t *q, int64_t q_token, int64_t q_head, int64_t N,
+                      int64_t heads, const fp8blk_batch *batch, float scale, int causal, int64_t window,
+                      const float *sinks, uint16_t *out, int64_t out_token, int64_t out_head, void *ws, size_t ws_bytes,
+                      fp8blk_stream_t stream);
+int fp8blk_latent_attn(const fp8blk_cache *cache, const uint16_t *q, int64_t q_token, int64_t q_head, int64_t N,
+                       int64_t heads, const fp8blk_batch *batch, float scale, int causal, int64_t window,
+                       const float *sinks, uint16_t *out, int64_t out_token, int64_t out_head, void *ws,
+                       size_t ws_bytes, fp8blk_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
