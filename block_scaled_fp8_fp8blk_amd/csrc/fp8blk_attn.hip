@@ -1,8 +1,297 @@
 // Attention of new tokens over a paged cache of keys and values.
 #include "fp8blk_attn.hpp"
 
+#include <algorithm>
+
 namespace fp8blk {
 namespace {
+
+// --- few rows: decode and verify ----------------------------------------------------
+//
+// Rows of one sequence whose heads share a key head are 32 columns of a tile (row r:
+// token r / group, head r % group), which few rows leave partly empty: bound by the
+// cache's bytes, the matrix cores wait. A workgroup takes a split of the keys, its
+// four waves tiles 0, 4, ...; 1, 5, ...; each with buffers, maximum, sum and outputs
+// of its own, so that nothing waits for another wave before the end, where the four
+// are joined in order. While a wave forms scores its values are on their way, and
+// while it sums values the next tile's keys are.
+template <int DK, int DV>
+struct FewLds {
+    static constexpr int kK = kTile * DK * 2, kV = kTile * DV * 2, kPages = 256;
+    static constexpr int kWave = kK + kV + kPages, kBytes = 4 * kWave;
+    static_assert(kK + kV >= kTile * DV * 4, "a wave's outputs take the place of its tile");
+};
+
+// Byte offsets of a tile's rows: lane l has those of key l % 32.
+struct TileRows {
+    int64_t k, v;
+    uint32_t held;  // bit: a key that a page holds and the workgroup's rows may see
+};
+__device__ __forceinline__ TileRows tile_rows(const AttnArgs& a, int page, int base, int lo, int hi, int lane) {
+    const int j = base + (lane & 31);
+    const bool ok = (uint32_t)page < (uint32_t)a.pages && j >= lo && j < hi;
+    const int64_t p = ok ? page : 0, slot = ok ? j & ((1 << a.page_shift) - 1) : 0;
+    TileRows t;
+    t.k = p * a.k_page + slot * a.k_slot;
+    t.v = p * a.v_page + slot * a.v_slot;
+    t.held = (uint32_t)__ballot(ok);
+    return t;
+}
+__device__ __forceinline__ int64_t of_row(int64_t v, int row) {
+    const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)v, row), hi = (uint32_t)__shfl((int)(v >> 32), row);
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+// The table's entry for key j, or some other where that lies outside.
+__device__ __forceinline__ const int32_t* entry(const AttnArgs& a, int s, int j) {
+    const int64_t i = min((int64_t)(j >> a.page_shift), a.max_pages - 1);
+    return a.table + s * a.max_pages + i;
+}
+
+// 32 rows of COLS bf16 to LDS.
+template <int COLS>
+__device__ __forceinline__ void load_tile(const char* base, int64_t rows, uint32_t lds, int lane) {
+    constexpr int kChunks = COLS / 8;
+#pragma unroll
+    for (int n = 0; n < COLS / 16; ++n) {
+        const int at = 64 * n + lane, row = at / kChunks, c = at % kChunks;
+        load_lds16(base + of_row(rows, row) + (((c & ~7) | ((c & 7) ^ swizzle(row))) << 4), lds + 1024 * n);
+    }
+}
+// 32 rows of COLS e4m3 into registers, and from there widened to LDS.
+template <int COLS>
+struct Codes {
+    uint4 d[COLS / 32];
+};
+template <int COLS>
+__device__ __forceinline__ void load_codes(const char* base, int64_t rows, Codes<COLS>& r, int lane) {
+    constexpr int kChunks = COLS / 16;
+#pragma unroll
+    for (int n = 0; n < COLS / 32; ++n) {
+        const int at = 64 * n + lane;
+        r.d[n] = load_global16(base + of_row(rows, at / kChunks) + at % kChunks * 16);
+    }
+}
+__device__ __forceinline__ uint2 widen4_e4m3(uint32_t d) {
+    return make_uint2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, 1.0f, false)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, 1.0f, true)));
+}
+template <int COLS>
+__device__ __forceinline__ void store_codes(char* lds, const Codes<COLS>& r, int lane) {
+    constexpr int kChunks = COLS / 16;
+#pragma unroll
+    for (int n = 0; n < COLS / 32; ++n) {
+        const int at = 64 * n + lane, row = at / kChunks, c = 2 * (at % kChunks), s = swizzle(row);
+        char* p = lds + row * COLS * 2 + (c >> 3) * 128;
+        const uint2 x = widen4_e4m3(r.d[n].x), y = widen4_e4m3(r.d[n].y), z = widen4_e4m3(r.d[n].z), w = widen4_e4m3(r.d[n].w);
+        *(uint4*)(p + (((c & 7) ^ s) << 4)) = make_uint4(x.x, x.y, y.x, y.y);
+        *(uint4*)(p + (((c & 7) ^ 1 ^ s) << 4)) = make_uint4(z.x, z.y, w.x, w.y);
+    }
+}
+
+// Rows of a tile in LDS that hold no key: zeros, for 0 * what lies there is 0.
+template <int COLS>
+__device__ __forceinline__ void clear_rows(char* lds, uint32_t held, int lane) {
+#pragma unroll 1
+    for (int n = 0; n < COLS / 16; ++n) {
+        const int at = 64 * n + lane;
+        if (!(held >> (at / (COLS / 8)) & 1)) *(uint4*)(lds + at * 16) = make_uint4(0, 0, 0, 0);
+    }
+}
+
+template <int DK, int DV, bool E4M3>
+__global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1)) void k_attn_few(AttnArgs a, int row_tiles, int units) {
+    using L = FewLds<DK, DV>;
+    __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
+    // Workgroup b runs on XCD b % 8: the row tiles of one unit, which read the same keys, on one XCD.
+    const int xcd = blockIdx.x & 7, turn = blockIdx.x >> 3;
+    const int row_tile = turn % row_tiles, unit = turn / row_tiles * 8 + xcd;
+    if (unit >= units) return;
+    const int kv_heads = a.heads / a.group;
+    const int c = unit % a.splits, kv = unit / a.splits % kv_heads, s = unit / a.splits / kv_heads;
+    const Seq seq = sequence(a, s);
+    const int rows = seq.rows * a.group, r0 = row_tile * kTile;
+    if (r0 >= rows) return;
+    const Split split = split_of(a, seq, c);
+    if (c > 0 && c >= split.n) return;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q_row = r0 + (lane & 31);
+    const int t0 = r0 / a.group, t1 = min(r0 + kTile, rows) - 1;  // first token, last row
+    const int token = min(q_row, rows - 1) / a.group, head = kv * a.group + min(q_row, rows - 1) % a.group;
+    const int at0 = seq.at + t0, at1 = seq.at + t1 / a.group;     // positions of the tile's first and last row
+    const int lo = max(split.lo, first_key(a, at0)), hi = min(split.hi, end_key(a, seq, at1));
+    const int own_lo = first_key(a, seq.at + token), own_hi = end_key(a, seq, seq.at + token);
+    const int all_lo = first_key(a, at1), all_hi = end_key(a, seq, at0);  // keys that every row sees
+
+    char* const k_lds = lds + wave * L::kWave;
+    char* const v_lds = k_lds + L::kK;
+    int32_t* const pages = (int32_t*)(v_lds + L::kV);
+    const uint32_t k_at = lds_offset(k_lds), v_at = lds_offset(v_lds), pages_at = lds_offset(pages);
+    const char* const k_base = a.k + kv * a.k_head;
+    const char* const v_base = a.v + kv * a.v_head;
+
+    v8bf q[DK / 16];
+    {
+        const char* p = a.q + (int64_t)(seq.first + token) * a.q_token + head * a.q_head + 16 * (lane >> 5);
+#pragma unroll
+        for (int t = 0; t < DK / 16; ++t) q[t] = q_operand(a, p + 32 * t);
+    }
+    v16f o[DV / 32] = {};
+    Running run = {-INFINITY, 0.0f};
+
+    // The wave's tiles: those of the split whose number is `wave` modulo 4.
+    int tile = (lo - split.lo) / kTile;
+    tile += (wave - tile) & 3;
+    int base = split.lo + tile * kTile;
+    TileRows next, here;
+    Codes<E4M3 ? DK : 32> k_codes;
+    Codes<E4M3 ? DV : 32> v_codes;
+    int next_page = 0;
+    if (base < hi) {
+        next = tile_rows(a, *entry(a, s, base + (lane & 31)), base, lo, hi, lane);
+        const int32_t* later = entry(a, s, base + 4 * kTile + (lane & 31));
+        if constexpr (E4M3) {
+            next_page = *later;
+            load_codes<DK>(k_base, next.k, k_codes, lane);
+            load_codes<DV>(v_base, next.v, v_codes, lane);
+        } else {
+            asm volatile("" ::: "memory");
+            load_lds4((const char*)later, pages_at);
+            load_tile<DK>(k_base, next.k, k_at, lane);
+            load_tile<DV>(v_base, next.v, v_at, lane);
+        }
+    }
+    for (; base < hi; base += 4 * kTile) {
+        const bool more = base + 4 * kTile < hi;
+        here = next;
+        if constexpr (E4M3) store_codes<DK>(k_lds, k_codes, lane);
+        else wait_loads<DV / 16>();
+        v16f z = tile_scores<DK>(k_lds, q, lane);
+        if (more) {
+            if constexpr (!E4M3) next_page = pages[lane & 31];
+            next = tile_rows(a, next_page, base + 4 * kTile, lo, hi, lane);
+            const int32_t* later = entry(a, s, base + 8 * kTile + (lane & 31));
+            if constexpr (E4M3) {
+                next_page = *later;
+                load_codes<DK>(k_base, next.k, k_codes, lane);
+            } else {
+                wait_reads();
+                load_lds4((const char*)later, pages_at);
+                load_tile<DK>(k_base, next.k, k_at, lane);
+            }
+        }
+        const bool edge = base < all_lo || base + kTile > all_hi;
+        const uint32_t seen = edge ? here.held & keys_between(base, own_lo, own_hi) : here.held;
+        if (edge || here.held != ~0u) hide(z, seen, lane);
+        const float keep = tile_weights(z, a.z_scale, run);
+        if (__any(keep != 1.0f))
+#pragma unroll
+            for (int t = 0; t < DV / 32; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[t][i] *= keep;
+        if constexpr (E4M3) store_codes<DV>(v_lds, v_codes, lane);
+        else if (more) wait_loads<DK / 16 + 1>();
+        else wait_loads<0>();
+        if (here.held != ~0u) clear_rows<DV>(v_lds, here.held, lane);
+        if (edge && tile_not_finite<DV>(v_lds, lane)) {
+            tile_add_not_finite<DV>(v_lds, z, seen, o, lane);
+            tile_make_finite<DV>(v_lds, lane);
+        }
+        v8bf p[2];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) p[i >> 3][i & 7] = (__bf16)z[i];
+        tile_sums<DV>(v_lds, p, o, lane);
+        if (more) {
+            if constexpr (E4M3) {
+                load_codes<DV>(v_base, next.v, v_codes, lane);
+            } else {
+                wait_reads();
+                load_tile<DV>(v_base, next.v, v_at, lane);
+            }
+        }
+    }
+
+    // Join the four waves, in order; a wave's outputs lie as rows of DV floats, 16 bytes
+    // at chunk ^ (row % 8).
+    wait_reads();
+    float* const ml = (float*)pages;
+    run.l = bfly32(run.l);
+    if (lane < 32) ml[lane] = run.m;
+    else ml[lane] = run.l;
+    {
+        char* p = k_lds + (lane & 31) * DV * 4;
+#pragma unroll
+        for (int t = 0; t < DV / 32; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int chunk = (8 * t + 2 * j + (lane >> 5)) ^ (lane & 7);
+                *(float4*)(p + chunk * 16) = make_float4(o[t][4 * j], o[t][4 * j + 1], o[t][4 * j + 2], o[t][4 * j + 3]);
+            }
+    }
+    __syncthreads();
+    constexpr int kOnes = DV / 8;  // threads a row
+    for (int r = threadIdx.x / kOnes; r < kTile && r0 + r < rows; r += 256 / kOnes) {
+        const int d = threadIdx.x % kOnes;
+        float m[4], l[4], top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float* of = (const float*)(lds + w * L::kWave + L::kK + L::kV);
+            m[w] = of[r], l[w] = of[32 + r];
+            top = fmaxf(top, m[w]);
+        }
+        const float base = top == -INFINITY ? 0.0f : top;
+        float sum = 0.0f, v[8] = {};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float f = exp2_fast(m[w] - base);
+            sum = __builtin_fmaf(f, l[w], sum);
+            const char* p = lds + w * L::kWave + r * DV * 4;
+            const float4 x = *(const float4*)(p + ((2 * d) ^ (r & 7)) * 16), y = *(const float4*)(p + ((2 * d + 1) ^ (r & 7)) * 16);
+            const float e[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(f, e[i], v[i]);
+        }
+        const int row = r0 + r, i = row / a.group, h = kv * a.group + row % a.group;
+        if (split.n > 1) {
+            const int64_t at = partial(a, s, i, h, c);
+            float* p = a.ws + at * DV + 8 * d;
+            *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
+            *(float4*)(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            if (d == 0) *(float2*)(partial_ml(a, DV) + 2 * at) = make_float2(top, sum);
+        } else {
+            write_out(a, seq.first + i, h, 8 * d, v, top, sum);
+        }
+    }
+}
+
+// The splits of a row and head, in order.
+template <int DV>
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
+    constexpr int kOnes = DV / 8;
+    const int id = blockIdx.x * (256 / kOnes) + threadIdx.x / kOnes, d = threadIdx.x % kOnes;
+    const int head = id % a.heads, i = id / a.heads % a.max_new, s = id / a.heads / a.max_new;
+    if (s >= a.seqs) return;
+    const Seq seq = sequence(a, s);
+    if (i >= seq.rows) return;
+    const int n = split_of(a, seq, 0).n;
+    if (n <= 1) return;
+    const int64_t at = partial(a, s, i, head, 0);
+    const float2* ml = (const float2*)partial_ml(a, DV) + at;
+    float top = -INFINITY;
+    for (int c = 0; c < n; ++c) top = fmaxf(top, ml[c].x);
+    const float base = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f, v[8] = {};
+    for (int c = 0; c < n; ++c) {
+        const float2 t = ml[c];
+        const float f = exp2_fast(t.x - base);
+        sum = __builtin_fmaf(f, t.y, sum);
+        const float4 x = *(const float4*)(a.ws + (at + c) * DV + 8 * d), y = *(const float4*)(a.ws + (at + c) * DV + 8 * d + 4);
+        const float e[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = __builtin_fmaf(f, e[k], v[k]);
+    }
+    write_out(a, seq.first + i, head, 8 * d, v, top, sum);
+}
+
 
 __device__ __forceinline__ float element(const char* row, int i, bool e4m3) {
     if (e4m3) return __builtin_amdgcn_cvt_f32_fp8(((const uint8_t*)row)[i], 0);
@@ -11,7 +300,7 @@ __device__ __forceinline__ float element(const char* row, int i, bool e4m3) {
 
 // One workgroup a row and head, wave w its keys w, w + 4, ...: running maximum and
 // sum of the softmax, each lane columns lane, lane + 64, ...
-__global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a, int seq_of_row_steps, int k_cols, int v_cols, bool e4m3) {
+template <int> __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a, int seq_of_row_steps, int k_cols, int v_cols, bool e4m3) {
     __shared__ float m_w[4], l_w[4], o_w[4][512];
     const int n = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int lo = 0, hi = a.seqs;  // the last sequence that starts at or before the row
@@ -26,7 +315,7 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a, int seq_of_row_st
     float q[16], o[8] = {};
     const char* q_row = a.q + n * a.q_token + h * a.q_head;
 #pragma unroll
-    for (int c = 0; c < 16; ++c) q[c] = c * 64 + lane < k_cols ? element(q_row, c * 64 + lane, false) : 0.0f;
+    for (int c = 0; c < 16; ++c) q[c] = c * 64 + lane < k_cols ? as_f32(((uint32_t)((const uint16_t*)q_row)[c * 64 + lane] << 16 & a.q_and) ^ (a.q_xor & 0x80000000u)) : 0.0f;
     float m = -INFINITY, l = 0.0f;
     for (int j = first_key(a, p) + wave; j < end; j += 4) {
         const int page = page_of(a, lo, j);
@@ -65,6 +354,12 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a, int seq_of_row_st
     }
 }
 
+bool attn_sizes_ok(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, int64_t max_len, int64_t window) {
+    constexpr int64_t kMost = INT64_C(1) << 30;
+    return heads >= 1 && heads <= FP8BLK_MAX_HEADS && heads % c.heads == 0 && seqs >= 1 && seqs <= FP8BLK_MAX_PANEL &&
+           max_new >= 1 && max_new <= FP8BLK_MAX_PANEL && max_len >= 1 && max_len < kMost && window >= 0 && window < kMost;
+}
+
 }  // namespace
 
 int attn_args(AttnArgs& a, const fp8blk_cache* cache, const uint16_t* q, int64_t q_token, int64_t q_head, int64_t N,
@@ -73,10 +368,8 @@ int attn_args(AttnArgs& a, const fp8blk_cache* cache, const uint16_t* q, int64_t
     if (!cache || !batch || !q || !out || !cache_ok(*cache)) return FP8BLK_ERR_ARG;
     const fp8blk_cache& c = *cache;
     const fp8blk_batch& b = *batch;
-    if (N < 1 || N > FP8BLK_MAX_PANEL || heads < 1 || heads > FP8BLK_MAX_HEADS || heads % c.heads) return FP8BLK_ERR_ARG;
-    if (b.seqs < 1 || b.seqs > FP8BLK_MAX_PANEL || b.max_new < 1 || b.max_new > FP8BLK_MAX_PANEL || b.max_pages < 1 ||
-        b.max_pages > (INT64_C(1) << 30) || b.max_len < 1 || b.max_len >= (INT64_C(1) << 30) || window < 0 ||
-        window >= (INT64_C(1) << 30) || !std::isfinite(scale))
+    if (N < 1 || N > FP8BLK_MAX_PANEL || b.max_pages < 1 || b.max_pages > (INT64_C(1) << 30) || !std::isfinite(scale) ||
+        !attn_sizes_ok(c, heads, b.seqs, b.max_new, b.max_len, window))
         return FP8BLK_ERR_ARG;
     if (!b.table || !b.lens || !b.starts) return FP8BLK_ERR_ARG;
     const void* words[] = {b.table, b.lens, b.starts, sinks};
@@ -110,7 +403,12 @@ int attn_args(AttnArgs& a, const fp8blk_cache* cache, const uint16_t* q, int64_t
     a.N = (int32_t)N, a.seqs = (int32_t)b.seqs, a.heads = (int32_t)heads, a.group = (int32_t)(heads / c.heads);
     a.pages = (int32_t)c.pages, a.page_shift = __builtin_ctzll((unsigned long long)c.page_size);
     a.max_new = (int32_t)b.max_new, a.window = (int32_t)window, a.causal = causal != 0;
-    a.z_scale = scale * c.k_scale * kLog2e;
+    a.z_scale = std::fabs(scale) * c.k_scale * kLog2e;
+    a.q_and = a.z_scale > 0.0f ? ~0u : 0u;
+    a.q_xor = a.z_scale > 0.0f && scale < 0.0f ? 0x80008000u : 0u;
+    if (!(a.z_scale > 0.0f)) a.z_scale = 1.0f;
+    a.splits = 1;
+    a.chunk = 1 << 30;
     a.out_scale = latent ? c.k_scale : c.v_scale;
     return FP8BLK_OK;
 }
@@ -119,18 +417,59 @@ int attn_args(AttnArgs& a, const fp8blk_cache* cache, const uint16_t* q, int64_t
 
 using namespace fp8blk;
 
-extern "C" size_t fp8blk_attn_bytes(const fp8blk_cache* cache, int64_t heads, int64_t seqs, int64_t max_new,
-                                    int64_t max_len, int64_t window) {
-    return 0;
+namespace {
+
+struct Plan {
+    int32_t splits, chunk;
+    size_t bytes;
+};
+
+Plan plan(int64_t kv_heads, int64_t heads, int64_t v_cols, int64_t seqs, int64_t max_new, int64_t max_len, int64_t window) {
+    const int64_t seen = window > 0 ? std::min(max_len, window + FP8BLK_MAX_M) : max_len;
+    const int64_t want = std::max<int64_t>(1, 512 / (seqs * kv_heads));
+    const int64_t step = 4 * kTile, most = ceil_div(seen, step), n = std::min(want, most);
+    Plan p;
+    p.chunk = (int32_t)(ceil_div(ceil_div(seen, n), step) * step);
+    p.splits = (int32_t)(ceil_div(seen, p.chunk) + (window > 0 ? 1 : 0));
+    p.bytes = p.splits > 1 ? (size_t)(seqs * max_new * heads * p.splits * (v_cols + 2)) * sizeof(float) : 0;
+    return p;
 }
 
-static int simple(const fp8blk_cache* cache, const AttnArgs& a, hipStream_t s) {
+bool few(int64_t max_new) { return max_new <= FP8BLK_MAX_M; }
+
+template <int DK, int DV, bool E4M3>
+void launch_few(const AttnArgs& a, hipStream_t s) {
+    const int64_t units = (int64_t)a.seqs * (a.heads / a.group) * a.splits;
+    const int64_t tiles = ceil_div((int64_t)a.max_new * a.group, kTile);
+    k_attn_few<DK, DV, E4M3><<<(unsigned)(ceil_div(units, 8) * 8 * tiles), 256, 0, s>>>(a, (int)tiles, (int)units);
+    if (a.splits > 1) {
+        const int64_t rows = (int64_t)a.seqs * a.max_new * a.heads;
+        k_attn_join<DV><<<(unsigned)ceil_div(rows * (DV / 8), 256), 256, 0, s>>>(a);
+    }
+}
+
+template <int DK, int DV>
+void launch_few(const AttnArgs& a, bool e4m3, hipStream_t s) {
+    if (e4m3) launch_few<DK, DV, true>(a, s);
+    else launch_few<DK, DV, false>(a, s);
+}
+
+int simple(const fp8blk_cache* cache, const AttnArgs& a, hipStream_t s) {
     int steps = 0;
     while ((1 << steps) < a.seqs) ++steps;
     (void)hipGetLastError();
-    k_attn_rows<<<dim3((unsigned)a.N, (unsigned)a.heads), 256, 0, s>>>(a, steps + 1, (int)cache->k_cols, (int)cache->v_cols,
+    k_attn_rows<0><<<dim3((unsigned)a.N, (unsigned)a.heads), 256, 0, s>>>(a, steps + 1, (int)cache->k_cols, (int)cache->v_cols,
                                                                        cache->type == FP8BLK_E4M3);
     return launch_status();
+}
+
+}  // namespace
+
+extern "C" size_t fp8blk_attn_bytes(const fp8blk_cache* cache, int64_t heads, int64_t seqs, int64_t max_new,
+                                    int64_t max_len, int64_t window) {
+    if (!cache || !cache_ok(*cache) || !attn_sizes_ok(*cache, heads, seqs, max_new, max_len, window)) return 0;
+    if (!few(max_new) || !cache->v) return 0;
+    return plan(cache->heads, heads, cache->v_cols, seqs, max_new, max_len, window).bytes;
 }
 
 extern "C" int fp8blk_paged_attn(const fp8blk_cache* cache, const uint16_t* q, int64_t q_token, int64_t q_head, int64_t N,
@@ -143,7 +482,19 @@ extern "C" int fp8blk_paged_attn(const fp8blk_cache* cache, const uint16_t* q, i
     if (st) return st;
     const int64_t k = cache->k_cols, v = cache->v_cols;
     if (!cache->v || !((k == v && (k == 64 || k == 128 || k == 256)) || (k == 192 && v == 128))) return FP8BLK_ERR_ARG;
-    return simple(cache, a, reinterpret_cast<hipStream_t>(stream));
+    hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+    if (!few(batch->max_new)) return simple(cache, a, hs);
+    const Plan p = plan(cache->heads, heads, v, batch->seqs, batch->max_new, batch->max_len, window);
+    if (p.bytes && (!ws || ws_bytes < p.bytes || !aligned(ws, 256))) return FP8BLK_ERR_WORKSPACE;
+    a.ws = (float*)ws;
+    a.splits = p.splits, a.chunk = p.chunk;
+    const bool e4m3 = cache->type == FP8BLK_E4M3;
+    (void)hipGetLastError();
+    if (k == 64) launch_few<64, 64>(a, e4m3, hs);
+    else if (k == 128) launch_few<128, 128>(a, e4m3, hs);
+    else if (k == 192) launch_few<192, 128>(a, e4m3, hs);
+    else launch_few<256, 256>(a, e4m3, hs);
+    return launch_status();
 }
 
 extern "C" int fp8blk_latent_attn(const fp8blk_cache* cache, const uint16_t* q, int64_t q_token, int64_t q_head, int64_t N,
