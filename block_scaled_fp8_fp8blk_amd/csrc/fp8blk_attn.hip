@@ -2,6 +2,7 @@
 #include "fp8blk_attn.hpp"
 
 #include <algorithm>
+#include <numeric>
 
 namespace fp8blk {
 namespace {
@@ -47,27 +48,28 @@ __device__ __forceinline__ const int32_t* entry(const AttnArgs& a, int s, int j)
     return a.table + s * a.max_pages + i;
 }
 
-// 32 rows of COLS bf16 to LDS.
-template <int COLS>
+// ROWS rows of COLS bf16 to LDS.
+template <int COLS, int ROWS = kTile>
 __device__ __forceinline__ void load_tile(const char* base, int64_t rows, uint32_t lds, int lane) {
     constexpr int kChunks = COLS / 8;
 #pragma unroll
-    for (int n = 0; n < COLS / 16; ++n) {
+    for (int n = 0; n < COLS * ROWS / 512; ++n) {
         const int at = 64 * n + lane, row = at / kChunks, c = at % kChunks;
         load_lds16(base + of_row(rows, row) + (((c & ~7) | ((c & 7) ^ swizzle(row))) << 4), lds + 1024 * n);
     }
 }
-// 32 rows of COLS e4m3 into registers, and from there widened to LDS.
-template <int COLS>
+// ROWS rows of COLS e4m3 into registers, and from there widened to LDS.
+template <int COLS, int ROWS = kTile>
 struct Codes {
-    uint4 d[COLS / 32];
+    static constexpr int kAll = COLS / 16 * ROWS, kN = (kAll + 63) / 64;  // 16-byte loads
+    uint4 d[kN];
 };
-template <int COLS>
-__device__ __forceinline__ void load_codes(const char* base, int64_t rows, Codes<COLS>& r, int lane) {
+template <int COLS, int ROWS>
+__device__ __forceinline__ void load_codes(const char* base, int64_t rows, Codes<COLS, ROWS>& r, int lane) {
     constexpr int kChunks = COLS / 16;
 #pragma unroll
-    for (int n = 0; n < COLS / 32; ++n) {
-        const int at = 64 * n + lane;
+    for (int n = 0; n < Codes<COLS, ROWS>::kN; ++n) {
+        const int at = min(64 * n + lane, Codes<COLS, ROWS>::kAll - 1);
         r.d[n] = load_global16(base + of_row(rows, at / kChunks) + at % kChunks * 16);
     }
 }
@@ -75,12 +77,13 @@ __device__ __forceinline__ uint2 widen4_e4m3(uint32_t d) {
     return make_uint2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, 1.0f, false)),
                       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, 1.0f, true)));
 }
-template <int COLS>
-__device__ __forceinline__ void store_codes(char* lds, const Codes<COLS>& r, int lane) {
+template <int COLS, int ROWS>
+__device__ __forceinline__ void store_codes(char* lds, const Codes<COLS, ROWS>& r, int lane) {
     constexpr int kChunks = COLS / 16;
 #pragma unroll
-    for (int n = 0; n < COLS / 32; ++n) {
-        const int at = 64 * n + lane, row = at / kChunks, c = 2 * (at % kChunks), s = swizzle(row);
+    for (int n = 0; n < Codes<COLS, ROWS>::kN; ++n) {
+        // lanes past the last load have taken it too and store it once more
+        const int at = min(64 * n + lane, Codes<COLS, ROWS>::kAll - 1), row = at / kChunks, c = 2 * (at % kChunks), s = swizzle(row);
         char* p = lds + row * COLS * 2 + (c >> 3) * 128;
         const uint2 x = widen4_e4m3(r.d[n].x), y = widen4_e4m3(r.d[n].y), z = widen4_e4m3(r.d[n].z), w = widen4_e4m3(r.d[n].w);
         *(uint4*)(p + (((c & 7) ^ s) << 4)) = make_uint4(x.x, x.y, y.x, y.y);
@@ -89,10 +92,10 @@ __device__ __forceinline__ void store_codes(char* lds, const Codes<COLS>& r, int
 }
 
 // Rows of a tile in LDS that hold no key: zeros, for 0 * what lies there is 0.
-template <int COLS>
+template <int COLS, int ROWS = kTile>
 __device__ __forceinline__ void clear_rows(char* lds, uint32_t held, int lane) {
 #pragma unroll 1
-    for (int n = 0; n < COLS / 16; ++n) {
+    for (int n = 0; n < COLS * ROWS / 512; ++n) {
         const int at = 64 * n + lane;
         if (!(held >> (at / (COLS / 8)) & 1)) *(uint4*)(lds + at * 16) = make_uint4(0, 0, 0, 0);
     }
@@ -102,6 +105,7 @@ template <int DK, int DV, bool E4M3>
 __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1)) void k_attn_few(AttnArgs a, int row_tiles, int units) {
     using L = FewLds<DK, DV>;
     __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
+    __shared__ int odd_waves[4];
     // Workgroup b runs on XCD b % 8: the row tiles of one unit, which read the same keys, on one XCD.
     const int xcd = blockIdx.x & 7, turn = blockIdx.x >> 3;
     const int row_tile = turn % row_tiles, unit = turn / row_tiles * 8 + xcd;
@@ -146,13 +150,14 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
     Codes<E4M3 ? DK : 32> k_codes;
     Codes<E4M3 ? DV : 32> v_codes;
     int next_page = 0;
+    bool odd = false;
     if (base < hi) {
         next = tile_rows(a, *entry(a, s, base + (lane & 31)), base, lo, hi, lane);
         const int32_t* later = entry(a, s, base + 4 * kTile + (lane & 31));
         if constexpr (E4M3) {
             next_page = *later;
-            load_codes<DK>(k_base, next.k, k_codes, lane);
-            load_codes<DV>(v_base, next.v, v_codes, lane);
+            load_codes(k_base, next.k, k_codes, lane);
+            load_codes(v_base, next.v, v_codes, lane);
         } else {
             asm volatile("" ::: "memory");
             load_lds4((const char*)later, pages_at);
@@ -163,16 +168,16 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
     for (; base < hi; base += 4 * kTile) {
         const bool more = base + 4 * kTile < hi;
         here = next;
-        if constexpr (E4M3) store_codes<DK>(k_lds, k_codes, lane);
+        if constexpr (E4M3) store_codes(k_lds, k_codes, lane);
         else wait_loads<DV / 16>();
-        v16f z = tile_scores<DK>(k_lds, q, lane);
+        v16f z[1] = {tile_scores<DK>(k_lds, q, lane)};
         if (more) {
             if constexpr (!E4M3) next_page = pages[lane & 31];
             next = tile_rows(a, next_page, base + 4 * kTile, lo, hi, lane);
             const int32_t* later = entry(a, s, base + 8 * kTile + (lane & 31));
             if constexpr (E4M3) {
                 next_page = *later;
-                load_codes<DK>(k_base, next.k, k_codes, lane);
+                load_codes(k_base, next.k, k_codes, lane);
             } else {
                 wait_reads();
                 load_lds4((const char*)later, pages_at);
@@ -180,29 +185,19 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
             }
         }
         const bool edge = base < all_lo || base + kTile > all_hi;
-        const uint32_t seen = edge ? here.held & keys_between(base, own_lo, own_hi) : here.held;
-        if (edge || here.held != ~0u) hide(z, seen, lane);
-        const float keep = tile_weights(z, a.z_scale, run);
-        if (__any(keep != 1.0f))
-#pragma unroll
-            for (int t = 0; t < DV / 32; ++t)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[t][i] *= keep;
-        if constexpr (E4M3) store_codes<DV>(v_lds, v_codes, lane);
+        if (edge || here.held != ~0u) hide(z[0], here.held & keys_between(base, own_lo, own_hi), lane);
+        rescale(o, tile_weights(z, a.z_scale, run));
+        if constexpr (E4M3) store_codes(v_lds, v_codes, lane);
         else if (more) wait_loads<DK / 16 + 1>();
         else wait_loads<0>();
         if (here.held != ~0u) clear_rows<DV>(v_lds, here.held, lane);
-        if (edge && tile_not_finite<DV>(v_lds, lane)) {
-            tile_add_not_finite<DV>(v_lds, z, seen, o, lane);
-            tile_make_finite<DV>(v_lds, lane);
-        }
+        if (edge) odd |= make_finite<DV, kTile>(v_lds, lane);
         v8bf p[2];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) p[i >> 3][i & 7] = (__bf16)z[i];
+        weights_operand(z[0], p);
         tile_sums<DV>(v_lds, p, o, lane);
         if (more) {
             if constexpr (E4M3) {
-                load_codes<DV>(v_base, next.v, v_codes, lane);
+                load_codes(v_base, next.v, v_codes, lane);
             } else {
                 wait_reads();
                 load_tile<DV>(v_base, next.v, v_at, lane);
@@ -217,6 +212,7 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
     run.l = bfly32(run.l);
     if (lane < 32) ml[lane] = run.m;
     else ml[lane] = run.l;
+    if (lane == 0) odd_waves[wave] = odd;
     {
         char* p = k_lds + (lane & 31) * DV * 4;
 #pragma unroll
@@ -251,6 +247,9 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
             for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(f, e[i], v[i]);
         }
         const int row = r0 + r, i = row / a.group, h = kv * a.group + row % a.group;
+        if (odd_waves[0] | odd_waves[1] | odd_waves[2] | odd_waves[3])
+            add_not_finite<kTile>(a, s, v_base, E4M3, 8 * d, split.lo, lo, hi, all_lo, all_hi, first_key(a, seq.at + i),
+                                  end_key(a, seq, seq.at + i), v);
         if (split.n > 1) {
             const int64_t at = partial(a, s, i, h, c);
             float* p = a.ws + at * DV + 8 * d;
@@ -258,9 +257,179 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
             *(float4*)(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
             if (d == 0) *(float2*)(partial_ml(a, DV) + 2 * at) = make_float2(top, sum);
         } else {
-            write_out(a, seq.first + i, h, 8 * d, v, top, sum);
+            write_out(a.out + (seq.first + i) * a.out_token + h * a.out_head + 16 * d, v, out_factor(a, h, top, sum));
         }
     }
+}
+
+// --- many rows: a prompt's chunk ------------------------------------------------------
+//
+// Four waves of 32 rows share tiles of KEYS keys, which they load together, the next
+// one while this one is worked on; one barrier a tile. Bound by the matrix cores,
+// their operands from LDS and the softmax between them, for which a compute unit
+// holds two waves a SIMD where registers and LDS allow.
+template <int DK, int DV>
+struct ChunkLds {
+    static constexpr int kKeys = DK + DV <= 256 ? 64 : 32, kTiles = kKeys / kTile, kRows = kKeys / 4;
+    static constexpr int kK = kKeys * DK * 2, kV = kKeys * DV * 2, kBytes = 2 * (kK + kV) + 64;
+};
+constexpr int kChunkRows = 4 * kTile;
+
+template <int DK, int DV, bool E4M3>
+__global__ __launch_bounds__(256, (DV <= 128 ? 2 : 1)) void k_attn_chunk(AttnArgs a, int row_tiles, int units, int spread) {
+    using L = ChunkLds<DK, DV>;
+    __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
+    // Workgroup b runs on XCD b % 8: a unit's row tiles, which read the same keys, on
+    // `spread` XCDs, those with the most keys first.
+    const int xcd = blockIdx.x & 7, turn = blockIdx.x >> 3, per = (row_tiles + spread - 1) / spread;
+    const int unit = turn / per * (8 / spread) + xcd / spread, row_tile = row_tiles - 1 - (turn % per * spread + xcd % spread);
+    if (unit >= units || row_tile < 0) return;
+    const int kv_heads = a.heads / a.group;
+    const int c = unit % a.splits, kv = unit / a.splits % kv_heads, s = unit / a.splits / kv_heads;
+    const Seq seq = sequence(a, s);
+    const int rows = seq.rows * a.group, r0 = row_tile * kChunkRows;
+    if (r0 >= rows) return;
+    const Split split = split_of(a, seq, c);
+    if (c > 0 && c >= split.n) return;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int w0 = r0 + wave * kTile, q_row = min(w0 + (lane & 31), rows - 1);
+    const int token = q_row / a.group, head = kv * a.group + q_row % a.group;
+    // positions of the first and last row of the workgroup and of the wave
+    const int at0 = seq.at + r0 / a.group, at1 = seq.at + (min(r0 + kChunkRows, rows) - 1) / a.group;
+    const int wave0 = seq.at + min(w0, rows - 1) / a.group, wave1 = seq.at + min(w0 + kTile - 1, rows - 1) / a.group;
+    const int lo = max(split.lo, first_key(a, at0)), hi = min(split.hi, end_key(a, seq, at1));
+    const int all_lo = first_key(a, at1), all_hi = end_key(a, seq, at0);
+    const int wave_lo = first_key(a, wave0), wave_hi = w0 < rows ? end_key(a, seq, wave1) : 0;
+    const int own_lo = first_key(a, seq.at + token), own_hi = end_key(a, seq, seq.at + token);
+
+    const char* const k_base = a.k + kv * a.k_head;
+    const char* const v_base = a.v + kv * a.v_head;
+    v8bf q[DK / 16];
+    {
+        const char* p = a.q + (int64_t)(seq.first + token) * a.q_token + head * a.q_head + 16 * (lane >> 5);
+#pragma unroll
+        for (int t = 0; t < DK / 16; ++t) q[t] = q_operand(a, p + 32 * t);
+    }
+    v16f o[DV / 32] = {};
+    Running run = {-INFINITY, 0.0f};
+
+    // The wave loads rows kRows * wave .. of every tile; its lanes hold their offsets.
+    const int mine = wave * L::kRows;
+    constexpr uint32_t kMine = (uint32_t)(((uint64_t)1 << L::kRows) - 1);
+    int base = split.lo + (lo - split.lo) / L::kKeys * L::kKeys;
+    TileRows next;
+    int page = 0;
+    bool odd = false;
+    Codes<E4M3 ? DK : 64, E4M3 ? L::kRows : 16> k_codes;
+    Codes<E4M3 ? DV : 64, E4M3 ? L::kRows : 16> v_codes;
+    const uint32_t lds_at = lds_offset(lds);
+    auto rows_of = [&](int b) {
+        TileRows t = tile_rows(a, page, b + mine, lo, hi, lane);
+        t.held &= kMine;
+        return t;
+    };
+    auto load = [&](int buffer) {
+        if constexpr (E4M3) {
+            load_codes(k_base, next.k, k_codes, lane);
+            load_codes(v_base, next.v, v_codes, lane);
+        } else {
+            const uint32_t to = lds_at + buffer * (L::kK + L::kV);
+            load_tile<DK, L::kRows>(k_base, next.k, to + mine * DK * 2, lane);
+            load_tile<DV, L::kRows>(v_base, next.v, to + L::kK + mine * DV * 2, lane);
+        }
+    };
+    if (base < hi) {
+        page = *entry(a, s, base + mine + (lane & 31));
+        next = rows_of(base);
+        page = *entry(a, s, base + L::kKeys + mine + (lane & 31));
+        load(0);
+    }
+    for (int buffer = 0; base < hi; base += L::kKeys, buffer ^= 1) {
+        char* const k_lds = lds + buffer * (L::kK + L::kV);
+        char* const v_lds = k_lds + L::kK;
+        if constexpr (E4M3) {
+            store_codes(k_lds + mine * DK * 2, k_codes, lane);
+            store_codes(v_lds + mine * DV * 2, v_codes, lane);
+        } else {
+            wait_loads<0>();
+        }
+        char* const own_v = v_lds + mine * DV * 2;
+        if (next.held != kMine) clear_rows<DV, L::kRows>(own_v, next.held, lane);
+        const bool edge = base < all_lo || base + L::kKeys > all_hi;
+        uint32_t* const said = (uint32_t*)(lds + 2 * (L::kK + L::kV)) + 8 * buffer;  // by each wave: the keys held, and whether some value is not finite
+        if (edge) {
+            const bool some = make_finite<DV, L::kRows>(own_v, lane);
+            if (lane == 0) said[4 + wave] = some;
+        }
+        if (lane == 0) said[wave] = next.held;
+        __syncthreads();
+        uint32_t held[L::kTiles];
+        {
+            const uint4 h = *(const uint4*)said;
+            if constexpr (L::kTiles == 2) held[0] = h.x | h.y << 16, held[1] = h.z | h.w << 16;
+            else held[0] = h.x | h.y << 8 | h.z << 16 | h.w << 24;
+        }
+        if (edge) {
+            const uint4 w = *(const uint4*)(said + 4);
+            odd |= (w.x | w.y | w.z | w.w) != 0;
+        }
+        if (base + L::kKeys < hi) {
+            next = rows_of(base + L::kKeys);
+            page = *entry(a, s, base + 2 * L::kKeys + mine + (lane & 31));
+            load(buffer ^ 1);
+        }
+        const bool active = base < wave_hi && base + L::kKeys > wave_lo;
+        if (!active) continue;
+        v16f z[L::kTiles];
+        uint32_t seen[L::kTiles];
+        bool all = true;
+#pragma unroll
+        for (int t = 0; t < L::kTiles; ++t) {
+            z[t] = tile_scores<DK>(k_lds + t * kTile * DK * 2, q, lane);
+            seen[t] = held[t] & keys_between(base + t * kTile, own_lo, own_hi);
+            all = all && seen[t] == ~0u;
+        }
+        if (!__all(all))
+#pragma unroll
+            for (int t = 0; t < L::kTiles; ++t) hide(z[t], seen[t], lane);
+        rescale(o, tile_weights(z, a.z_scale, run));
+#pragma unroll
+        for (int t = 0; t < L::kTiles; ++t) {
+            v8bf p[2];
+            weights_operand(z[t], p);
+            tile_sums<DV>(v_lds + t * kTile * DV * 2, p, o, lane);
+        }
+    }
+
+    // Lanes of the two halves exchange columns, so that each has 8 in a row.
+    run.l = bfly32(run.l);
+    if (w0 + (lane & 31) >= rows) return;
+    const float factor = out_factor(a, head, run.m, run.l);
+    char* const out = a.out + (seq.first + token) * a.out_token + head * a.out_head;
+    const int64_t part = partial(a, s, token, head, c);
+#pragma unroll
+    for (int t = 0; t < DV / 32; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const auto r = __builtin_amdgcn_permlane32_swap(as_u32(o[t][4 * j + i]), as_u32(o[t][4 * j + 4 + i]), false, false);
+                v[i] = as_f32(r[0]), v[4 + i] = as_f32(r[1]);
+            }
+            const int col = 32 * t + 8 * j + 8 * (lane >> 5);
+            if (odd)
+                add_not_finite<L::kKeys>(a, s, v_base, E4M3, col, split.lo, lo, hi, all_lo, all_hi, own_lo, own_hi, v);
+            if (split.n > 1) {
+                float* p = a.ws + part * DV + col;
+                *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
+                *(float4*)(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+                write_out(out + 2 * col, v, factor);
+            }
+        }
+    if (split.n > 1 && lane < 32) *(float2*)(partial_ml(a, DV) + 2 * part) = make_float2(run.m, run.l);
 }
 
 // The splits of a row and head, in order.
@@ -289,7 +458,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = __builtin_fmaf(f, e[k], v[k]);
     }
-    write_out(a, seq.first + i, head, 8 * d, v, top, sum);
+    write_out(a.out + (seq.first + i) * a.out_token + head * a.out_head + 16 * d, v, out_factor(a, head, top, sum));
 }
 
 
@@ -435,6 +604,18 @@ Plan plan(int64_t kv_heads, int64_t heads, int64_t v_cols, int64_t seqs, int64_t
     return p;
 }
 
+Plan plan_chunk(int64_t kv_heads, int64_t heads, int64_t v_cols, int64_t seqs, int64_t max_new, int64_t max_len, int64_t window) {
+    const int64_t seen = window > 0 ? std::min(max_len, window + max_new) : max_len;
+    const int64_t tiles = seqs * kv_heads * ceil_div(max_new * (heads / kv_heads), kChunkRows);
+    const int64_t want = std::max<int64_t>(1, 256 / tiles), n = std::min(want, ceil_div(seen, 512));
+    Plan p;
+    p.chunk = (int32_t)(ceil_div(ceil_div(seen, n), 64) * 64);
+    p.splits = n > 1 ? (int32_t)(ceil_div(seen, p.chunk) + (window > 0 ? 1 : 0)) : 1;
+    if (p.splits == 1) p.chunk = 1 << 30;
+    p.bytes = p.splits > 1 ? (size_t)(seqs * max_new * heads * p.splits * (v_cols + 2)) * sizeof(float) : 0;
+    return p;
+}
+
 bool few(int64_t max_new) { return max_new <= FP8BLK_MAX_M; }
 
 template <int DK, int DV, bool E4M3>
@@ -442,16 +623,29 @@ void launch_few(const AttnArgs& a, hipStream_t s) {
     const int64_t units = (int64_t)a.seqs * (a.heads / a.group) * a.splits;
     const int64_t tiles = ceil_div((int64_t)a.max_new * a.group, kTile);
     k_attn_few<DK, DV, E4M3><<<(unsigned)(ceil_div(units, 8) * 8 * tiles), 256, 0, s>>>(a, (int)tiles, (int)units);
+}
+
+template <int DK, int DV, bool E4M3>
+void launch_chunk(const AttnArgs& a, hipStream_t s) {
+    const int64_t units = (int64_t)a.seqs * (a.heads / a.group) * a.splits;
+    const int64_t tiles = ceil_div((int64_t)a.max_new * a.group, kChunkRows);
+    const int64_t spread = 8 / std::gcd(units, (int64_t)8), turns = units * spread / 8 * ceil_div(tiles, spread);
+    k_attn_chunk<DK, DV, E4M3><<<(unsigned)(8 * turns), 256, 0, s>>>(a, (int)tiles, (int)units, (int)spread);
+}
+
+template <int DK, int DV>
+void launch(const AttnArgs& a, bool e4m3, hipStream_t s) {
+    if (few(a.max_new)) {
+        if (e4m3) launch_few<DK, DV, true>(a, s);
+        else launch_few<DK, DV, false>(a, s);
+    } else {
+        if (e4m3) launch_chunk<DK, DV, true>(a, s);
+        else launch_chunk<DK, DV, false>(a, s);
+    }
     if (a.splits > 1) {
         const int64_t rows = (int64_t)a.seqs * a.max_new * a.heads;
         k_attn_join<DV><<<(unsigned)ceil_div(rows * (DV / 8), 256), 256, 0, s>>>(a);
     }
-}
-
-template <int DK, int DV>
-void launch_few(const AttnArgs& a, bool e4m3, hipStream_t s) {
-    if (e4m3) launch_few<DK, DV, true>(a, s);
-    else launch_few<DK, DV, false>(a, s);
 }
 
 int simple(const fp8blk_cache* cache, const AttnArgs& a, hipStream_t s) {
@@ -468,8 +662,8 @@ int simple(const fp8blk_cache* cache, const AttnArgs& a, hipStream_t s) {
 extern "C" size_t fp8blk_attn_bytes(const fp8blk_cache* cache, int64_t heads, int64_t seqs, int64_t max_new,
                                     int64_t max_len, int64_t window) {
     if (!cache || !cache_ok(*cache) || !attn_sizes_ok(*cache, heads, seqs, max_new, max_len, window)) return 0;
-    if (!few(max_new) || !cache->v) return 0;
-    return plan(cache->heads, heads, cache->v_cols, seqs, max_new, max_len, window).bytes;
+    if (!cache->v) return 0;
+    return (few(max_new) ? plan : plan_chunk)(cache->heads, heads, cache->v_cols, seqs, max_new, max_len, window).bytes;
 }
 
 extern "C" int fp8blk_paged_attn(const fp8blk_cache* cache, const uint16_t* q, int64_t q_token, int64_t q_head, int64_t N,
@@ -483,17 +677,16 @@ extern "C" int fp8blk_paged_attn(const fp8blk_cache* cache, const uint16_t* q, i
     const int64_t k = cache->k_cols, v = cache->v_cols;
     if (!cache->v || !((k == v && (k == 64 || k == 128 || k == 256)) || (k == 192 && v == 128))) return FP8BLK_ERR_ARG;
     hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
-    if (!few(batch->max_new)) return simple(cache, a, hs);
-    const Plan p = plan(cache->heads, heads, v, batch->seqs, batch->max_new, batch->max_len, window);
+    const Plan p = (few(batch->max_new) ? plan : plan_chunk)(cache->heads, heads, v, batch->seqs, batch->max_new, batch->max_len, window);
     if (p.bytes && (!ws || ws_bytes < p.bytes || !aligned(ws, 256))) return FP8BLK_ERR_WORKSPACE;
     a.ws = (float*)ws;
     a.splits = p.splits, a.chunk = p.chunk;
     const bool e4m3 = cache->type == FP8BLK_E4M3;
     (void)hipGetLastError();
-    if (k == 64) launch_few<64, 64>(a, e4m3, hs);
-    else if (k == 128) launch_few<128, 128>(a, e4m3, hs);
-    else if (k == 192) launch_few<192, 128>(a, e4m3, hs);
-    else launch_few<256, 256>(a, e4m3, hs);
+    if (k == 64) launch<64, 64>(a, e4m3, hs);
+    else if (k == 128) launch<128, 128>(a, e4m3, hs);
+    else if (k == 192) launch<192, 128>(a, e4m3, hs);
+    else launch<256, 256>(a, e4m3, hs);
     return launch_status();
 }
 

@@ -109,6 +109,7 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) char lds_char;
 
 constexpr int kTile = 32;
@@ -153,26 +154,28 @@ __device__ __forceinline__ v16f tile_scores(const char* k, const v8bf (&q)[DK / 
     return c;
 }
 
-// out^T += V^T P^T of a tile: V's rows in LDS, P as tile_scores leaves it. A read
-// gives a lane four rows of one column: lanes 16 g .. 16 g + 15 read four rows of 16
-// columns, and are handed a column each.
+// Values as the operand of a tile's sums: columns 32 t .. and keys 16 k .. of V's rows
+// in LDS, transposed. A read gives a lane four rows of one column: lanes 16 g .. 16 g
+// + 15 read four rows of 16 columns, and are handed a column each.
 template <int DV>
-__device__ __forceinline__ void tile_sums(const char* v, const v8bf (&p)[2], v16f (&o)[DV / 32], int lane) {
+__device__ __forceinline__ v8bf values_operand(const char* v, int t, int k, int lane) {
     const int h = lane >> 5, row = 4 * h + ((lane & 15) >> 2), s = swizzle(row);
     const int chunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-    const char* at = v + row * DV * 2 + (lane & 1) * 8;
+    const char* at = v + row * DV * 2 + (lane & 1) * 8 + (t >> 1) * 128 + (((4 * (t & 1) + chunk) ^ s) << 4) + 16 * k * DV * 2;
+    typedef __attribute__((address_space(3))) v4s lds_v4s;
+    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)at);
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 8 * DV * 2));
+    return __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// out^T += V^T P^T of a tile: V's rows in LDS, P as tile_scores leaves it.
+template <int DV>
+__device__ __forceinline__ void tile_sums(const char* v, const v8bf (&p)[2], v16f (&o)[DV / 32], int lane) {
 #pragma unroll
-    for (int t = 0; t < DV / 32; ++t) {
+    for (int t = 0; t < DV / 32; ++t)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const char* b = at + (t >> 1) * 128 + (((4 * (t & 1) + chunk) ^ s) << 4) + 16 * k * DV * 2;
-            typedef __attribute__((address_space(3))) v4s lds_v4s;
-            const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)b);
-            const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(b + 8 * DV * 2));
-            const v8bf a = __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-            o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, p[k], o[t], 0, 0, 0);
-        }
-    }
+        for (int k = 0; k < 2; ++k)
+            o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values_operand<DV>(v, t, k, lane), p[k], o[t], 0, 0, 0);
 }
 
 __device__ __forceinline__ bool not_finite(uint32_t d) {  // one of two bf16
@@ -184,54 +187,46 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t d) {  // each of two
 }
 
 // A value that is not finite, in a key that some rows of a tile see and others do
-// not, would reach the latter as 0 * inf. Such tiles (found by tile_not_finite) take
-// two steps more: these values times their weights for the rows that see them, and
-// zeros in their place for tile_sums, which then gives every row the bits that
-// it has without them.
-template <int DV>
-__device__ __forceinline__ bool tile_not_finite(const char* v, int lane) {  // for the whole wave
+// not, would reach the latter as 0 * inf. In tiles that not all rows see whole it is
+// made a 0 in LDS before the product, so that every row has the bits that it has
+// without it, and add_not_finite gives it to those that see it at the end.
+template <int DV, int ROWS>
+__device__ __forceinline__ bool make_finite(char* v, int lane) {  // whether there was one, for the whole wave
     bool odd = false;
 #pragma unroll 1
-    for (int n = 0; n < DV * kTile * 2 / 1024; ++n) {
-        const uint4 d = *(const uint4*)(v + n * 1024 + lane * 16);
-        odd = odd || not_finite(d.x) || not_finite(d.y) || not_finite(d.z) || not_finite(d.w);
+    for (int n = 0; n < DV * ROWS * 2 / 1024; ++n) {
+        uint4* p = (uint4*)(v + n * 1024 + lane * 16);
+        const uint4 d = *p;
+        if (not_finite(d.x) || not_finite(d.y) || not_finite(d.z) || not_finite(d.w)) {
+            *p = make_uint4(finite_or_zero(d.x), finite_or_zero(d.y), finite_or_zero(d.z), finite_or_zero(d.w));
+            odd = true;
+        }
     }
     return __any(odd);
 }
-template <int DV>
-__device__ __forceinline__ void tile_make_finite(char* v, int lane) {
+
+// What make_finite took from the tiles of KEYS keys from `from` on that lie in [lo,
+// hi) and not whole in [all_lo, all_hi): infinities and NaN in 8 columns, from `col`,
+// of the keys in [own_lo, own_hi), read again where they come from.
+template <int KEYS>
+__device__ __forceinline__ void add_not_finite(const AttnArgs& a, int s, const char* v_base, bool e4m3, int col, int from, int lo, int hi,
+                                               int all_lo, int all_hi, int own_lo, int own_hi, float (&v)[8]) {
 #pragma unroll 1
-    for (int n = 0; n < DV * kTile * 2 / 1024; ++n) {
-        uint4* p = (uint4*)(v + n * 1024 + lane * 16);
-        const uint4 d = *p;
-        *p = make_uint4(finite_or_zero(d.x), finite_or_zero(d.y), finite_or_zero(d.z), finite_or_zero(d.w));
-    }
-}
-template <int DV>
-__device__ __forceinline__ void tile_add_not_finite(const char* v, v16f w, uint32_t seen, v16f (&o)[DV / 32], int lane) {
-    const int h = lane >> 5;
+    for (int j = max(lo, own_lo); j < min(hi, own_hi); ++j) {
+        const int tile = from + (j - from) / KEYS * KEYS;
+        if (tile >= all_lo && tile + KEYS <= all_hi) {
+            j = tile + KEYS - 1;
+            continue;
+        }
+        const int page = page_of(a, s, j);
+        if (page < 0) continue;
+        const char* p = v_base + page * a.v_page + (j & ((1 << a.page_shift) - 1)) * a.v_slot + (e4m3 ? col : 2 * col);
 #pragma unroll 1
-    for (int i = 0; i < 16; ++i) {  // register i of the weights, which move down one by one
-        const float own = w[0];
+        for (int i = 0; i < 8; ++i) {
+            const float x = e4m3 ? __builtin_amdgcn_cvt_f32_fp8((int)((const uint8_t*)p)[i], 0) : as_f32((uint32_t)((const uint16_t*)p)[i] << 16);
+            if (!__builtin_isfinite(x))
 #pragma unroll
-        for (int r = 0; r < 15; ++r) w[r] = w[r + 1];
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-            const float f = __shfl(own, (lane & 31) + 32 * half);
-            const int row = (i & 3) + 8 * (i >> 2) + 4 * half, s = swizzle(row);
-            if (!(seen >> row & 1)) continue;
-#pragma unroll
-            for (int t = 0; t < DV / 32; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int chunk = 4 * t + j;  // columns 32 t + 8 j + 4 h ..
-                    const uint2 d = *(const uint2*)(v + row * DV * 2 + (chunk >> 3) * 128 + (((chunk & 7) ^ s) << 4) + 8 * h);
-                    if (!not_finite(d.x) && !not_finite(d.y)) continue;
-                    float e[4];
-                    widen2_bf16(d.x, e), widen2_bf16(d.y, e + 2);
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) o[t][4 * j + n] += __builtin_isfinite(e[n]) ? 0.0f : f * e[n];
-                }
+                for (int k = 0; k < 8; ++k) v[k] += k == i ? x : 0.0f;
         }
     }
 }
@@ -243,17 +238,19 @@ __device__ __forceinline__ float max_halves(float v) {
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) { return __builtin_bit_cast(uint32_t, v2bf{(__bf16)lo, (__bf16)hi}); }
 
-// 8 columns of a row's output from its sums v of weights times values and `sum` of
-// weights, both relative to its maximum `top`. A row that sees keys has a weight of 1.
-__device__ __forceinline__ void write_out(const AttnArgs& a, int row, int head, int col, const float (&v)[8], float top, float sum) {
-    const float base = top == -INFINITY ? 0.0f : top;
-    const bool none = sum == 0.0f;
-    if (a.sinks) sum += exp2_fast(__builtin_fmaf(a.sinks[head], kLog2e, -base));
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = none ? 0.0f : v[i] * a.out_scale / sum;
-    *(__attribute__((address_space(1))) v4u*)(a.out + row * a.out_token + head * a.out_head + 2 * col) =
-        v4u{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
+// What a row's sums of weights times values are multiplied by, from its maximum `top`
+// and the sum of its weights, both relative to that. A row that sees keys has a
+// weight of 1; one that sees none has sums of 0.
+__device__ __forceinline__ float out_factor(const AttnArgs& a, int head, float top, float sum) {
+    if (sum == 0.0f) return 0.0f;
+    if (a.sinks) sum += exp2_fast(__builtin_fmaf(a.sinks[head], kLog2e, top == -INFINITY ? 0.0f : -top));
+    return a.out_scale / sum;
+}
+
+// 8 columns of a row's output.
+__device__ __forceinline__ void write_out(char* p, const float (&v)[8], float f) {
+    *(__attribute__((address_space(1))) v4u*)p = v4u{pack_bf16(v[0] * f, v[1] * f), pack_bf16(v[2] * f, v[3] * f),
+                                                     pack_bf16(v[4] * f, v[5] * f), pack_bf16(v[6] * f, v[7] * f)};
 }
 
 // A row's 8 values of q at `p` as an operand.
@@ -277,29 +274,47 @@ __device__ __forceinline__ void hide(v16f& z, uint32_t seen, int lane) {
     for (int i = 0; i < 16; ++i) z[i] = seen >> ((i & 3) + 8 * (i >> 2)) & 1 ? z[i] : -INFINITY;
 }
 
-// A tile's scores become weights: running maximum m and the lane's part l of the
-// running sum; returns the factor of what was summed before.
+// The scores of N tiles become weights: running maximum m (in units of log 2) and
+// the lane's part l of the running sum; returns the factor of what was summed
+// before. scale > 0.
 struct Running {
     float m, l;
 };
-__device__ __forceinline__ float tile_weights(v16f& z, float scale, Running& r) {
+template <int N>
+__device__ __forceinline__ float tile_weights(v16f (&z)[N], float scale, Running& r) {
+    float top = z[0][0];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] *= scale;
-    float top = z[0];
+    for (int n = 0; n < N; ++n)
 #pragma unroll
-    for (int i = 1; i < 16; ++i) top = fmaxf(top, z[i]);
-    top = fmaxf(max_halves(top), r.m);
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, z[n][i]);
+    top = fmaxf(max_halves(top) * scale, r.m);
     const float base = top == -INFINITY ? 0.0f : top;
     const float keep = exp2_fast(r.m - base);
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        z[i] = exp2_fast(z[i] - base);
-        sum += z[i];
-    }
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            z[n][i] = exp2_fast(__builtin_fmaf(z[n][i], scale, -base));
+            sum += z[n][i];
+        }
     r.l = __builtin_fmaf(r.l, keep, sum);
     r.m = top;
     return keep;
+}
+
+template <int T>
+__device__ __forceinline__ void rescale(v16f (&o)[T], float keep) {
+    if (!__any(keep != 1.0f)) return;
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[t][i] *= keep;
+}
+
+__device__ __forceinline__ void weights_operand(const v16f& z, v8bf (&p)[2]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p[i >> 3][i & 7] = (__bf16)z[i];
 }
 
 // Checks the arguments of an attention call and writes its AttnArgs (the workspace
