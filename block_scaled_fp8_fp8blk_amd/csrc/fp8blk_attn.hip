@@ -2,7 +2,6 @@
 #include "fp8blk_attn.hpp"
 
 #include <algorithm>
-#include <numeric>
 
 namespace fp8blk {
 namespace {
@@ -23,41 +22,6 @@ struct FewLds {
     static_assert(kK + kV >= kTile * DV * 4, "a wave's outputs take the place of its tile");
 };
 
-// Byte offsets of a tile's rows: lane l has those of key l % 32.
-struct TileRows {
-    int64_t k, v;
-    uint32_t held;  // bit: a key that a page holds and the workgroup's rows may see
-};
-__device__ __forceinline__ TileRows tile_rows(const AttnArgs& a, int page, int base, int lo, int hi, int lane) {
-    const int j = base + (lane & 31);
-    const bool ok = (uint32_t)page < (uint32_t)a.pages && j >= lo && j < hi;
-    const int64_t p = ok ? page : 0, slot = ok ? j & ((1 << a.page_shift) - 1) : 0;
-    TileRows t;
-    t.k = p * a.k_page + slot * a.k_slot;
-    t.v = p * a.v_page + slot * a.v_slot;
-    t.held = (uint32_t)__ballot(ok);
-    return t;
-}
-__device__ __forceinline__ int64_t of_row(int64_t v, int row) {
-    const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)v, row), hi = (uint32_t)__shfl((int)(v >> 32), row);
-    return (int64_t)((uint64_t)hi << 32 | lo);
-}
-// The table's entry for key j, or some other where that lies outside.
-__device__ __forceinline__ const int32_t* entry(const AttnArgs& a, int s, int j) {
-    const int64_t i = min((int64_t)(j >> a.page_shift), a.max_pages - 1);
-    return a.table + s * a.max_pages + i;
-}
-
-// ROWS rows of COLS bf16 to LDS.
-template <int COLS, int ROWS = kTile>
-__device__ __forceinline__ void load_tile(const char* base, int64_t rows, uint32_t lds, int lane) {
-    constexpr int kChunks = COLS / 8;
-#pragma unroll
-    for (int n = 0; n < COLS * ROWS / 512; ++n) {
-        const int at = 64 * n + lane, row = at / kChunks, c = at % kChunks;
-        load_lds16(base + of_row(rows, row) + (((c & ~7) | ((c & 7) ^ swizzle(row))) << 4), lds + 1024 * n);
-    }
-}
 // ROWS rows of COLS e4m3 into registers, and from there widened to LDS.
 template <int COLS, int ROWS = kTile>
 struct Codes {
@@ -88,16 +52,6 @@ __device__ __forceinline__ void store_codes(char* lds, const Codes<COLS, ROWS>& 
         const uint2 x = widen4_e4m3(r.d[n].x), y = widen4_e4m3(r.d[n].y), z = widen4_e4m3(r.d[n].z), w = widen4_e4m3(r.d[n].w);
         *(uint4*)(p + (((c & 7) ^ s) << 4)) = make_uint4(x.x, x.y, y.x, y.y);
         *(uint4*)(p + (((c & 7) ^ 1 ^ s) << 4)) = make_uint4(z.x, z.y, w.x, w.y);
-    }
-}
-
-// Rows of a tile in LDS that hold no key: zeros, for 0 * what lies there is 0.
-template <int COLS, int ROWS = kTile>
-__device__ __forceinline__ void clear_rows(char* lds, uint32_t held, int lane) {
-#pragma unroll 1
-    for (int n = 0; n < COLS * ROWS / 512; ++n) {
-        const int at = 64 * n + lane;
-        if (!(held >> (at / (COLS / 8)) & 1)) *(uint4*)(lds + at * 16) = make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -159,7 +113,6 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
             load_codes(k_base, next.k, k_codes, lane);
             load_codes(v_base, next.v, v_codes, lane);
         } else {
-            asm volatile("" ::: "memory");
             load_lds4((const char*)later, pages_at);
             load_tile<DK>(k_base, next.k, k_at, lane);
             load_tile<DV>(v_base, next.v, v_at, lane);
@@ -169,7 +122,7 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
         const bool more = base + 4 * kTile < hi;
         here = next;
         if constexpr (E4M3) store_codes(k_lds, k_codes, lane);
-        else wait_loads<DV / 16>();
+        else wait_loads<L::kV / 1024>();
         v16f z[1] = {tile_scores<DK>(k_lds, q, lane)};
         if (more) {
             if constexpr (!E4M3) next_page = pages[lane & 31];
@@ -219,14 +172,16 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
         for (int t = 0; t < DV / 32; ++t)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
+                const v16f& x = o[t];
                 const int chunk = (8 * t + 2 * j + (lane >> 5)) ^ (lane & 7);
-                *(float4*)(p + chunk * 16) = make_float4(o[t][4 * j], o[t][4 * j + 1], o[t][4 * j + 2], o[t][4 * j + 3]);
+                *(float4*)(p + chunk * 16) = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
             }
     }
-    __syncthreads();
     constexpr int kOnes = DV / 8;  // threads a row
+    __syncthreads();
+#pragma unroll 1
     for (int r = threadIdx.x / kOnes; r < kTile && r0 + r < rows; r += 256 / kOnes) {
-        const int d = threadIdx.x % kOnes;
+        const int d = threadIdx.x % kOnes, col = 8 * d;
         float m[4], l[4], top = -INFINITY;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -248,16 +203,16 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
         }
         const int row = r0 + r, i = row / a.group, h = kv * a.group + row % a.group;
         if (odd_waves[0] | odd_waves[1] | odd_waves[2] | odd_waves[3])
-            add_not_finite<kTile>(a, s, v_base, E4M3, 8 * d, split.lo, lo, hi, all_lo, all_hi, first_key(a, seq.at + i),
+            add_not_finite<kTile>(a, s, v_base, E4M3, col, split.lo, lo, hi, all_lo, all_hi, first_key(a, seq.at + i),
                                   end_key(a, seq, seq.at + i), v);
         if (split.n > 1) {
             const int64_t at = partial(a, s, i, h, c);
-            float* p = a.ws + at * DV + 8 * d;
+            float* p = a.ws + at * DV + col;
             *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
             *(float4*)(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-            if (d == 0) *(float2*)(partial_ml(a, DV) + 2 * at) = make_float2(top, sum);
+            if (col == 0) *(float2*)(partial_ml(a, DV) + 2 * at) = make_float2(top, sum);
         } else {
-            write_out(a.out + (seq.first + i) * a.out_token + h * a.out_head + 16 * d, v, out_factor(a, h, top, sum));
+            write_out(a.out + (seq.first + i) * a.out_token + h * a.out_head + 2 * col, v, out_factor(a, h, top, sum));
         }
     }
 }
@@ -432,97 +387,6 @@ __global__ __launch_bounds__(256, (DV <= 128 ? 2 : 1)) void k_attn_chunk(AttnArg
     if (split.n > 1 && lane < 32) *(float2*)(partial_ml(a, DV) + 2 * part) = make_float2(run.m, run.l);
 }
 
-// The splits of a row and head, in order.
-template <int DV>
-__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-    constexpr int kOnes = DV / 8;
-    const int id = blockIdx.x * (256 / kOnes) + threadIdx.x / kOnes, d = threadIdx.x % kOnes;
-    const int head = id % a.heads, i = id / a.heads % a.max_new, s = id / a.heads / a.max_new;
-    if (s >= a.seqs) return;
-    const Seq seq = sequence(a, s);
-    if (i >= seq.rows) return;
-    const int n = split_of(a, seq, 0).n;
-    if (n <= 1) return;
-    const int64_t at = partial(a, s, i, head, 0);
-    const float2* ml = (const float2*)partial_ml(a, DV) + at;
-    float top = -INFINITY;
-    for (int c = 0; c < n; ++c) top = fmaxf(top, ml[c].x);
-    const float base = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f, v[8] = {};
-    for (int c = 0; c < n; ++c) {
-        const float2 t = ml[c];
-        const float f = exp2_fast(t.x - base);
-        sum = __builtin_fmaf(f, t.y, sum);
-        const float4 x = *(const float4*)(a.ws + (at + c) * DV + 8 * d), y = *(const float4*)(a.ws + (at + c) * DV + 8 * d + 4);
-        const float e[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = __builtin_fmaf(f, e[k], v[k]);
-    }
-    write_out(a.out + (seq.first + i) * a.out_token + head * a.out_head + 16 * d, v, out_factor(a, head, top, sum));
-}
-
-
-__device__ __forceinline__ float element(const char* row, int i, bool e4m3) {
-    if (e4m3) return __builtin_amdgcn_cvt_f32_fp8(((const uint8_t*)row)[i], 0);
-    return as_f32((uint32_t)((const uint16_t*)row)[i] << 16);
-}
-
-// One workgroup a row and head, wave w its keys w, w + 4, ...: running maximum and
-// sum of the softmax, each lane columns lane, lane + 64, ...
-template <int> __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a, int seq_of_row_steps, int k_cols, int v_cols, bool e4m3) {
-    __shared__ float m_w[4], l_w[4], o_w[4][512];
-    const int n = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int lo = 0, hi = a.seqs;  // the last sequence that starts at or before the row
-    for (int i = 0; i < seq_of_row_steps; ++i) {
-        const int mid = (lo + hi) >> 1;
-        if (mid > lo) (a.starts[mid] <= n ? lo : hi) = mid;
-    }
-    const Seq s = sequence(a, lo);
-    const int i = n - s.first;
-    if (i < 0 || i >= s.rows) return;
-    const int p = s.at + i, end = end_key(a, s, p);
-    float q[16], o[8] = {};
-    const char* q_row = a.q + n * a.q_token + h * a.q_head;
-#pragma unroll
-    for (int c = 0; c < 16; ++c) q[c] = c * 64 + lane < k_cols ? as_f32(((uint32_t)((const uint16_t*)q_row)[c * 64 + lane] << 16 & a.q_and) ^ (a.q_xor & 0x80000000u)) : 0.0f;
-    float m = -INFINITY, l = 0.0f;
-    for (int j = first_key(a, p) + wave; j < end; j += 4) {
-        const int page = page_of(a, lo, j);
-        if (page < 0) continue;
-        const int64_t slot = j & ((1 << a.page_shift) - 1);
-        const char* k = a.k + page * a.k_page + slot * a.k_slot + (h / a.group) * a.k_head;
-        const char* v = a.v + page * a.v_page + slot * a.v_slot + (h / a.group) * a.v_head;
-        float z = 0.0f;
-#pragma unroll
-        for (int c = 0; c < 16; ++c)
-            if (c * 64 + lane < k_cols) z = __builtin_fmaf(q[c], element(k, c * 64 + lane, e4m3), z);
-        z = tree64(z) * a.z_scale;
-        const float top = z > m ? z : m, base = top == -INFINITY ? 0.0f : top;
-        const float keep = exp2_fast(m - base), w = exp2_fast(z - base);
-        m = top;
-        l = l * keep + w;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            if (c * 64 + lane < v_cols) o[c] = o[c] * keep + w * element(v, c * 64 + lane, e4m3);
-    }
-    if (lane == 0) m_w[wave] = m, l_w[wave] = l;
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-        if (c * 64 + lane < v_cols) o_w[wave][c * 64 + lane] = o[c];
-    __syncthreads();
-    float top = fmaxf(fmaxf(m_w[0], m_w[1]), fmaxf(m_w[2], m_w[3]));
-    const float base = top == -INFINITY ? 0.0f : top;
-    float f[4], sum = 0.0f;
-    for (int w = 0; w < 4; ++w) f[w] = exp2_fast(m_w[w] - base), sum += f[w] * l_w[w];
-    const bool none = sum == 0.0f;  // the largest weight of a row that sees keys is 1
-    if (a.sinks) sum += exp2_fast(a.sinks[h] * kLog2e - base);
-    uint16_t* out = (uint16_t*)(a.out + n * a.out_token + h * a.out_head);
-    for (int c = threadIdx.x; c < v_cols; c += 256) {
-        const float v = f[0] * o_w[0][c] + f[1] * o_w[1][c] + f[2] * o_w[2][c] + f[3] * o_w[3][c];
-        out[c] = __builtin_bit_cast(uint16_t, (__bf16)(none ? 0.0f : v * a.out_scale / sum));
-    }
-}
-
 bool attn_sizes_ok(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, int64_t max_len, int64_t window) {
     constexpr int64_t kMost = INT64_C(1) << 30;
     return heads >= 1 && heads <= FP8BLK_MAX_HEADS && heads % c.heads == 0 && seqs >= 1 && seqs <= FP8BLK_MAX_PANEL &&
@@ -589,34 +453,29 @@ using namespace fp8blk;
 namespace {
 
 struct Plan {
+    bool few;  // rows of a panel beside each other in one tile, the keys dealt to the waves
     int32_t splits, chunk;
     size_t bytes;
 };
 
-Plan plan(int64_t kv_heads, int64_t heads, int64_t v_cols, int64_t seqs, int64_t max_new, int64_t max_len, int64_t window) {
-    const int64_t seen = window > 0 ? std::min(max_len, window + FP8BLK_MAX_M) : max_len;
-    const int64_t want = std::max<int64_t>(1, 512 / (seqs * kv_heads));
-    const int64_t step = 4 * kTile, most = ceil_div(seen, step), n = std::min(want, most);
+// Which kernel a call takes and how its keys are split. Up to FP8BLK_MAX_M new tokens
+// the number of them has no say, so that a row's bits do not depend on it.
+Plan plan(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, int64_t max_len, int64_t window) {
+    const int64_t group = heads / c.heads;
+    const bool panel = max_new <= FP8BLK_MAX_M, latent = !c.v;
     Plan p;
+    p.few = latent ? panel && group <= kTile : panel;
+    const int64_t seen = window > 0 ? std::min(max_len, window + (panel ? FP8BLK_MAX_M : max_new)) : max_len;
+    const int64_t units = seqs * c.heads * (p.few ? 1 : ceil_div(panel ? group : max_new * group, latent ? kLatentRows : kChunkRows));
+    const int64_t step = p.few ? 4 * kTile : 64, least = panel ? 128 : 512;
+    const int64_t want = std::max<int64_t>(1, (p.few && !latent ? 512 : 256) / units);
+    const int64_t n = std::min(want, ceil_div(seen, least));
     p.chunk = (int32_t)(ceil_div(ceil_div(seen, n), step) * step);
     p.splits = (int32_t)(ceil_div(seen, p.chunk) + (window > 0 ? 1 : 0));
-    p.bytes = p.splits > 1 ? (size_t)(seqs * max_new * heads * p.splits * (v_cols + 2)) * sizeof(float) : 0;
+    if (n == 1) p.splits = 1, p.chunk = 1 << 30;
+    p.bytes = p.splits > 1 ? (size_t)(seqs * max_new * heads * p.splits * (c.v_cols + 2)) * sizeof(float) : 0;
     return p;
 }
-
-Plan plan_chunk(int64_t kv_heads, int64_t heads, int64_t v_cols, int64_t seqs, int64_t max_new, int64_t max_len, int64_t window) {
-    const int64_t seen = window > 0 ? std::min(max_len, window + max_new) : max_len;
-    const int64_t tiles = seqs * kv_heads * ceil_div(max_new * (heads / kv_heads), kChunkRows);
-    const int64_t want = std::max<int64_t>(1, 256 / tiles), n = std::min(want, ceil_div(seen, 512));
-    Plan p;
-    p.chunk = (int32_t)(ceil_div(ceil_div(seen, n), 64) * 64);
-    p.splits = n > 1 ? (int32_t)(ceil_div(seen, p.chunk) + (window > 0 ? 1 : 0)) : 1;
-    if (p.splits == 1) p.chunk = 1 << 30;
-    p.bytes = p.splits > 1 ? (size_t)(seqs * max_new * heads * p.splits * (v_cols + 2)) * sizeof(float) : 0;
-    return p;
-}
-
-bool few(int64_t max_new) { return max_new <= FP8BLK_MAX_M; }
 
 template <int DK, int DV, bool E4M3>
 void launch_few(const AttnArgs& a, hipStream_t s) {
@@ -629,32 +488,15 @@ template <int DK, int DV, bool E4M3>
 void launch_chunk(const AttnArgs& a, hipStream_t s) {
     const int64_t units = (int64_t)a.seqs * (a.heads / a.group) * a.splits;
     const int64_t tiles = ceil_div((int64_t)a.max_new * a.group, kChunkRows);
-    const int64_t spread = 8 / std::gcd(units, (int64_t)8), turns = units * spread / 8 * ceil_div(tiles, spread);
-    k_attn_chunk<DK, DV, E4M3><<<(unsigned)(8 * turns), 256, 0, s>>>(a, (int)tiles, (int)units, (int)spread);
+    const Deal d = deal(units, tiles);
+    k_attn_chunk<DK, DV, E4M3><<<d.grid, 256, 0, s>>>(a, (int)tiles, (int)units, d.spread);
 }
 
-template <int DK, int DV>
-void launch(const AttnArgs& a, bool e4m3, hipStream_t s) {
-    if (few(a.max_new)) {
-        if (e4m3) launch_few<DK, DV, true>(a, s);
-        else launch_few<DK, DV, false>(a, s);
-    } else {
-        if (e4m3) launch_chunk<DK, DV, true>(a, s);
-        else launch_chunk<DK, DV, false>(a, s);
-    }
-    if (a.splits > 1) {
-        const int64_t rows = (int64_t)a.seqs * a.max_new * a.heads;
-        k_attn_join<DV><<<(unsigned)ceil_div(rows * (DV / 8), 256), 256, 0, s>>>(a);
-    }
-}
-
-int simple(const fp8blk_cache* cache, const AttnArgs& a, hipStream_t s) {
-    int steps = 0;
-    while ((1 << steps) < a.seqs) ++steps;
-    (void)hipGetLastError();
-    k_attn_rows<0><<<dim3((unsigned)a.N, (unsigned)a.heads), 256, 0, s>>>(a, steps + 1, (int)cache->k_cols, (int)cache->v_cols,
-                                                                       cache->type == FP8BLK_E4M3);
-    return launch_status();
+template <int DK, int DV, bool E4M3>
+void launch(const AttnArgs& a, bool few, hipStream_t s) {
+    if (few) launch_few<DK, DV, E4M3>(a, s);
+    else launch_chunk<DK, DV, E4M3>(a, s);
+    launch_join<DV>(a, s);
 }
 
 }  // namespace
@@ -662,9 +504,32 @@ int simple(const fp8blk_cache* cache, const AttnArgs& a, hipStream_t s) {
 extern "C" size_t fp8blk_attn_bytes(const fp8blk_cache* cache, int64_t heads, int64_t seqs, int64_t max_new,
                                     int64_t max_len, int64_t window) {
     if (!cache || !cache_ok(*cache) || !attn_sizes_ok(*cache, heads, seqs, max_new, max_len, window)) return 0;
-    if (!cache->v) return 0;
-    return (few(max_new) ? plan : plan_chunk)(cache->heads, heads, cache->v_cols, seqs, max_new, max_len, window).bytes;
+    return plan(*cache, heads, seqs, max_new, max_len, window).bytes;
 }
+
+namespace {
+
+// The rest of a call whose arguments have been checked.
+int attend(AttnArgs& a, const fp8blk_cache& c, const fp8blk_batch& b, int64_t heads, int64_t window, void* ws, size_t ws_bytes,
+           fp8blk_stream_t stream) {
+    const Plan p = plan(c, heads, b.seqs, b.max_new, b.max_len, window);
+    if (p.bytes && (!ws || ws_bytes < p.bytes || !aligned(ws, 256))) return FP8BLK_ERR_WORKSPACE;
+    a.ws = (float*)ws;
+    a.splits = p.splits, a.chunk = p.chunk;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    (void)hipGetLastError();
+    const bool e4m3 = c.type == FP8BLK_E4M3;
+    switch (c.k_cols) {
+        case 64: e4m3 ? launch<64, 64, true>(a, p.few, s) : launch<64, 64, false>(a, p.few, s); break;
+        case 128: e4m3 ? launch<128, 128, true>(a, p.few, s) : launch<128, 128, false>(a, p.few, s); break;
+        case 192: e4m3 ? launch<192, 128, true>(a, p.few, s) : launch<192, 128, false>(a, p.few, s); break;
+        case 256: e4m3 ? launch<256, 256, true>(a, p.few, s) : launch<256, 256, false>(a, p.few, s); break;
+        default: launch_latent(a, c.k_cols, p.few, s); break;
+    }
+    return launch_status();
+}
+
+}  // namespace
 
 extern "C" int fp8blk_paged_attn(const fp8blk_cache* cache, const uint16_t* q, int64_t q_token, int64_t q_head, int64_t N,
                                  int64_t heads, const fp8blk_batch* batch, float scale, int causal, int64_t window,
@@ -676,18 +541,7 @@ extern "C" int fp8blk_paged_attn(const fp8blk_cache* cache, const uint16_t* q, i
     if (st) return st;
     const int64_t k = cache->k_cols, v = cache->v_cols;
     if (!cache->v || !((k == v && (k == 64 || k == 128 || k == 256)) || (k == 192 && v == 128))) return FP8BLK_ERR_ARG;
-    hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
-    const Plan p = (few(batch->max_new) ? plan : plan_chunk)(cache->heads, heads, v, batch->seqs, batch->max_new, batch->max_len, window);
-    if (p.bytes && (!ws || ws_bytes < p.bytes || !aligned(ws, 256))) return FP8BLK_ERR_WORKSPACE;
-    a.ws = (float*)ws;
-    a.splits = p.splits, a.chunk = p.chunk;
-    const bool e4m3 = cache->type == FP8BLK_E4M3;
-    (void)hipGetLastError();
-    if (k == 64) launch<64, 64>(a, e4m3, hs);
-    else if (k == 128) launch<128, 128>(a, e4m3, hs);
-    else if (k == 192) launch<192, 128>(a, e4m3, hs);
-    else launch<256, 256>(a, e4m3, hs);
-    return launch_status();
+    return attend(a, *cache, *batch, heads, window, ws, ws_bytes, stream);
 }
 
 extern "C" int fp8blk_latent_attn(const fp8blk_cache* cache, const uint16_t* q, int64_t q_token, int64_t q_head, int64_t N,
@@ -698,8 +552,8 @@ extern "C" int fp8blk_latent_attn(const fp8blk_cache* cache, const uint16_t* q, 
     const int st = attn_args(a, cache, q, q_token, q_head, N, heads, batch, scale, causal, window, sinks, out, out_token,
                              out_head);
     if (st) return st;
-    if (cache->v || cache->type != FP8BLK_BF16 || cache->heads != 1 || cache->v_cols != 512 ||
-        (cache->k_cols != 512 && cache->k_cols != 576))
+    if (cache->v || cache->type != FP8BLK_BF16 || cache->heads != 1 || cache->v_cols != kLatent ||
+        (cache->k_cols != kLatent && cache->k_cols != kLatent + 64))
         return FP8BLK_ERR_ARG;
-    return simple(cache, a, reinterpret_cast<hipStream_t>(stream));
+    return attend(a, *cache, *batch, heads, window, ws, ws_bytes, stream);
 }

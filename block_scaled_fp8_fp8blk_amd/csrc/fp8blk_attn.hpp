@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <cmath>
+#include <numeric>
 
 #include "fp8blk.h"
 #include "fp8blk_device.hpp"
@@ -155,27 +156,27 @@ __device__ __forceinline__ v16f tile_scores(const char* k, const v8bf (&q)[DK / 
 }
 
 // Values as the operand of a tile's sums: columns 32 t .. and keys 16 k .. of V's rows
-// in LDS, transposed. A read gives a lane four rows of one column: lanes 16 g .. 16 g
+// of COLS in LDS, transposed. A read gives a lane four rows of one column: lanes 16 g .. 16 g
 // + 15 read four rows of 16 columns, and are handed a column each.
-template <int DV>
+template <int COLS>
 __device__ __forceinline__ v8bf values_operand(const char* v, int t, int k, int lane) {
     const int h = lane >> 5, row = 4 * h + ((lane & 15) >> 2), s = swizzle(row);
     const int chunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-    const char* at = v + row * DV * 2 + (lane & 1) * 8 + (t >> 1) * 128 + (((4 * (t & 1) + chunk) ^ s) << 4) + 16 * k * DV * 2;
+    const char* at = v + row * COLS * 2 + (lane & 1) * 8 + (t >> 1) * 128 + (((4 * (t & 1) + chunk) ^ s) << 4) + 16 * k * COLS * 2;
     typedef __attribute__((address_space(3))) v4s lds_v4s;
     const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)at);
-    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 8 * DV * 2));
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 8 * COLS * 2));
     return __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// out^T += V^T P^T of a tile: V's rows in LDS, P as tile_scores leaves it.
-template <int DV>
+// out^T += V^T P^T of a tile: V, the first DV of rows of COLS in LDS, P as tile_scores leaves it.
+template <int DV, int COLS = DV>
 __device__ __forceinline__ void tile_sums(const char* v, const v8bf (&p)[2], v16f (&o)[DV / 32], int lane) {
 #pragma unroll
     for (int t = 0; t < DV / 32; ++t)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-            o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values_operand<DV>(v, t, k, lane), p[k], o[t], 0, 0, 0);
+            o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values_operand<COLS>(v, t, k, lane), p[k], o[t], 0, 0, 0);
 }
 
 __device__ __forceinline__ bool not_finite(uint32_t d) {  // one of two bf16
@@ -190,11 +191,11 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t d) {  // each of two
 // not, would reach the latter as 0 * inf. In tiles that not all rows see whole it is
 // made a 0 in LDS before the product, so that every row has the bits that it has
 // without it, and add_not_finite gives it to those that see it at the end.
-template <int DV, int ROWS>
+template <int COLS, int ROWS>
 __device__ __forceinline__ bool make_finite(char* v, int lane) {  // whether there was one, for the whole wave
     bool odd = false;
 #pragma unroll 1
-    for (int n = 0; n < DV * ROWS * 2 / 1024; ++n) {
+    for (int n = 0; n < COLS * ROWS / 512; ++n) {
         uint4* p = (uint4*)(v + n * 1024 + lane * 16);
         const uint4 d = *p;
         if (not_finite(d.x) || not_finite(d.y) || not_finite(d.z) || not_finite(d.w)) {
@@ -228,6 +229,51 @@ __device__ __forceinline__ void add_not_finite(const AttnArgs& a, int s, const c
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] += k == i ? x : 0.0f;
         }
+    }
+}
+
+// Byte offsets of a tile's rows: lane l has those of key l % 32.
+struct TileRows {
+    int64_t k, v;
+    uint32_t held;  // bit: a key that a page holds and the workgroup's rows may see
+};
+__device__ __forceinline__ TileRows tile_rows(const AttnArgs& a, int page, int base, int lo, int hi, int lane) {
+    const int j = base + (lane & 31);
+    const bool ok = (uint32_t)page < (uint32_t)a.pages && j >= lo && j < hi;
+    const int64_t p = ok ? page : 0, slot = ok ? j & ((1 << a.page_shift) - 1) : 0;
+    TileRows t;
+    t.k = p * a.k_page + slot * a.k_slot;
+    t.v = p * a.v_page + slot * a.v_slot;
+    t.held = (uint32_t)__ballot(ok);
+    return t;
+}
+__device__ __forceinline__ int64_t of_row(int64_t v, int row) {
+    const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)v, row), hi = (uint32_t)__shfl((int)(v >> 32), row);
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+// The table's entry for key j, or some other where that lies outside.
+__device__ __forceinline__ const int32_t* entry(const AttnArgs& a, int s, int j) {
+    const int64_t i = min((int64_t)(j >> a.page_shift), a.max_pages - 1);
+    return a.table + s * a.max_pages + i;
+}
+
+// ROWS rows of COLS bf16 to LDS.
+template <int COLS, int ROWS = kTile>
+__device__ __forceinline__ void load_tile(const char* base, int64_t rows, uint32_t lds, int lane) {
+    constexpr int kChunks = COLS / 8;
+#pragma unroll
+    for (int n = 0; n < COLS * ROWS / 512; ++n) {
+        const int at = 64 * n + lane, row = at / kChunks, c = at % kChunks;
+        load_lds16(base + of_row(rows, row) + (((c & ~7) | ((c & 7) ^ swizzle(row))) << 4), lds + 1024 * n);
+    }
+}
+// Rows of a tile in LDS that hold no key: zeros, for 0 * what lies there is 0.
+template <int COLS, int ROWS = kTile>
+__device__ __forceinline__ void clear_rows(char* lds, uint32_t held, int lane) {
+#pragma unroll 1
+    for (int n = 0; n < COLS * ROWS / 512; ++n) {
+        const int at = 64 * n + lane;
+        if (!(held >> (at / (COLS / 8)) & 1)) *(uint4*)(lds + at * 16) = make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -274,9 +320,11 @@ __device__ __forceinline__ void hide(v16f& z, uint32_t seen, int lane) {
     for (int i = 0; i < 16; ++i) z[i] = seen >> ((i & 3) + 8 * (i >> 2)) & 1 ? z[i] : -INFINITY;
 }
 
-// The scores of N tiles become weights: running maximum m (in units of log 2) and
-// the lane's part l of the running sum; returns the factor of what was summed
-// before. scale > 0.
+// The scores of N tiles become weights 2^(z - m): m is the row's maximum (in units of
+// log 2) when it was last set, l the lane's part of the running sum; returns the
+// factor of what was summed before. m follows the maximum only where that has grown
+// by more than 8: weights of up to 2^8 lose nothing, and the outputs are hardly
+// ever multiplied (not at all is what `rescale` checks for). scale > 0.
 struct Running {
     float m, l;
 };
@@ -287,9 +335,10 @@ __device__ __forceinline__ float tile_weights(v16f (&z)[N], float scale, Running
     for (int n = 0; n < N; ++n)
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, z[n][i]);
-    top = fmaxf(max_halves(top) * scale, r.m);
+    top = max_halves(top) * scale;
+    top = top > r.m + 8.0f ? top : r.m;
     const float base = top == -INFINITY ? 0.0f : top;
-    const float keep = exp2_fast(r.m - base);
+    const float keep = top == r.m ? 1.0f : exp2_fast(r.m - base);
     float sum = 0.0f;
 #pragma unroll
     for (int n = 0; n < N; ++n)
@@ -316,6 +365,59 @@ __device__ __forceinline__ void weights_operand(const v16f& z, v8bf (&p)[2]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) p[i >> 3][i & 7] = (__bf16)z[i];
 }
+
+// The splits of a row and head, in order.
+template <int DV>
+static __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
+    constexpr int kOnes = DV / 8;
+    const int id = blockIdx.x * (256 / kOnes) + threadIdx.x / kOnes, d = threadIdx.x % kOnes;
+    const int head = id % a.heads, i = id / a.heads % a.max_new, s = id / a.heads / a.max_new;
+    if (s >= a.seqs) return;
+    const Seq seq = sequence(a, s);
+    if (i >= seq.rows) return;
+    const int n = split_of(a, seq, 0).n;
+    if (n <= 1) return;
+    const int64_t at = partial(a, s, i, head, 0);
+    const float2* ml = (const float2*)partial_ml(a, DV) + at;
+    float top = -INFINITY;
+    for (int c = 0; c < n; ++c) top = fmaxf(top, ml[c].x);
+    const float base = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f, v[8] = {};
+    for (int c = 0; c < n; ++c) {
+        const float2 t = ml[c];
+        const float f = exp2_fast(t.x - base);
+        sum = __builtin_fmaf(f, t.y, sum);
+        const float4 x = *(const float4*)(a.ws + (at + c) * DV + 8 * d), y = *(const float4*)(a.ws + (at + c) * DV + 8 * d + 4);
+        const float e[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = __builtin_fmaf(f, e[k], v[k]);
+    }
+    write_out(a.out + (seq.first + i) * a.out_token + head * a.out_head + 16 * d, v, out_factor(a, head, top, sum));
+}
+
+
+template <int DV>
+void launch_join(const AttnArgs& a, hipStream_t s) {
+    if (a.splits < 2) return;
+    const int64_t rows = (int64_t)a.seqs * a.max_new * a.heads;
+    k_attn_join<DV><<<(unsigned)ceil_div(rows * (DV / 8), 256), 256, 0, s>>>(a);
+}
+
+// A grid of units (splits of a key head's keys) and their row tiles: workgroup b runs
+// on XCD b % 8, and a unit's row tiles, which read the same keys, on as few XCDs as
+// give each the same number.
+struct Deal {
+    unsigned grid;
+    int spread;
+};
+inline Deal deal(int64_t units, int64_t tiles) {
+    const int64_t spread = 8 / std::gcd(units, (int64_t)8);
+    return {(unsigned)(units * spread * ceil_div(tiles, spread)), (int)spread};
+}
+
+// Latent attention (fp8blk_latent.hip): rows of a workgroup, value columns, and the launch.
+constexpr int kLatentRows = 64, kLatent = 512;
+void launch_latent(const AttnArgs& a, int64_t k_cols, bool few, hipStream_t s);
 
 // Checks the arguments of an attention call and writes its AttnArgs (the workspace
 // apart); FP8BLK_OK or what the call returns.
