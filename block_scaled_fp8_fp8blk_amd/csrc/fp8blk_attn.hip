@@ -47,11 +47,11 @@ __device__ __forceinline__ void store_codes(char* lds, const Codes<COLS, ROWS>& 
 #pragma unroll
     for (int n = 0; n < Codes<COLS, ROWS>::kN; ++n) {
         // lanes past the last load have taken it too and store it once more
-        const int at = min(64 * n + lane, Codes<COLS, ROWS>::kAll - 1), row = at / kChunks, c = 2 * (at % kChunks), s = swizzle(row);
-        char* p = lds + row * COLS * 2 + (c >> 3) * 128;
+        const int at = min(64 * n + lane, Codes<COLS, ROWS>::kAll - 1), row = at / kChunks, c = 2 * (at % kChunks);
+        char* p = lds + row_at<COLS>(row);
         const uint2 x = widen4_e4m3(r.d[n].x), y = widen4_e4m3(r.d[n].y), z = widen4_e4m3(r.d[n].z), w = widen4_e4m3(r.d[n].w);
-        *(uint4*)(p + (((c & 7) ^ s) << 4)) = make_uint4(x.x, x.y, y.x, y.y);
-        *(uint4*)(p + (((c & 7) ^ 1 ^ s) << 4)) = make_uint4(z.x, z.y, w.x, w.y);
+        *(uint4*)(p + chunk_at(c, row)) = make_uint4(x.x, x.y, y.x, y.y);
+        *(uint4*)(p + chunk_at(c + 1, row)) = make_uint4(z.x, z.y, w.x, w.y);
     }
 }
 
@@ -60,19 +60,25 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
     using L = FewLds<DK, DV>;
     __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
     __shared__ int odd_waves[4];
-    // Workgroup b runs on XCD b % 8: the row tiles of one unit, which read the same keys, on one XCD.
+    // Workgroup b runs on XCD b % 8: all key heads and row tiles of a split, which read
+    // the same keys or their neighbours in memory, on one XCD, one after the other.
+    const int kv_heads = a.heads / a.group, parts = row_tiles * kv_heads;
     const int xcd = blockIdx.x & 7, turn = blockIdx.x >> 3;
-    const int row_tile = turn % row_tiles, unit = turn / row_tiles * 8 + xcd;
+    const int part = turn % parts, unit = turn / parts * 8 + xcd;
     if (unit >= units) return;
-    const int kv_heads = a.heads / a.group;
-    const int c = unit % a.splits, kv = unit / a.splits % kv_heads, s = unit / a.splits / kv_heads;
+    const int row_tile = part / kv_heads, kv = part % kv_heads, c = unit % a.splits, s = unit / a.splits;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // Without a window the wave's first tile is known before the sequence is: its pages
+    // are asked for at once.
+    const int early = c * a.chunk + wave * kTile;
+    int next_page = a.window > 0 ? 0 : *entry(a, s, early + (lane & 31));
     const Seq seq = sequence(a, s);
     const int rows = seq.rows * a.group, r0 = row_tile * kTile;
     if (r0 >= rows) return;
     const Split split = split_of(a, seq, c);
     if (c > 0 && c >= split.n) return;
 
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q_row = r0 + (lane & 31);
+    const int q_row = r0 + (lane & 31);
     const int t0 = r0 / a.group, t1 = min(r0 + kTile, rows) - 1;  // first token, last row
     const int token = min(q_row, rows - 1) / a.group, head = kv * a.group + min(q_row, rows - 1) % a.group;
     const int at0 = seq.at + t0, at1 = seq.at + t1 / a.group;     // positions of the tile's first and last row
@@ -88,11 +94,7 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
     const char* const v_base = a.v + kv * a.v_head;
 
     v8bf q[DK / 16];
-    {
-        const char* p = a.q + (int64_t)(seq.first + token) * a.q_token + head * a.q_head + 16 * (lane >> 5);
-#pragma unroll
-        for (int t = 0; t < DK / 16; ++t) q[t] = q_operand(a, p + 32 * t);
-    }
+    load_q(a.q + (int64_t)(seq.first + token) * a.q_token + head * a.q_head + 16 * (lane >> 5), 32, q);
     v16f o[DV / 32] = {};
     Running run = {-INFINITY, 0.0f};
 
@@ -103,10 +105,10 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
     TileRows next, here;
     Codes<E4M3 ? DK : 32> k_codes;
     Codes<E4M3 ? DV : 32> v_codes;
-    int next_page = 0;
     bool odd = false;
     if (base < hi) {
-        next = tile_rows(a, *entry(a, s, base + (lane & 31)), base, lo, hi, lane);
+        if (a.window > 0) next_page = *entry(a, s, base + (lane & 31));
+        next = tile_rows(a, next_page, base, lo, hi, lane);
         const int32_t* later = entry(a, s, base + 4 * kTile + (lane & 31));
         if constexpr (E4M3) {
             next_page = *later;
@@ -118,6 +120,7 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
             load_tile<DV>(v_base, next.v, v_at, lane);
         }
     }
+    as_operands(a, q);
     for (; base < hi; base += 4 * kTile) {
         const bool more = base + 4 * kTile < hi;
         here = next;
@@ -261,11 +264,7 @@ __global__ __launch_bounds__(256, (DV <= 128 ? 2 : 1)) void k_attn_chunk(AttnArg
     const char* const k_base = a.k + kv * a.k_head;
     const char* const v_base = a.v + kv * a.v_head;
     v8bf q[DK / 16];
-    {
-        const char* p = a.q + (int64_t)(seq.first + token) * a.q_token + head * a.q_head + 16 * (lane >> 5);
-#pragma unroll
-        for (int t = 0; t < DK / 16; ++t) q[t] = q_operand(a, p + 32 * t);
-    }
+    load_q(a.q + (int64_t)(seq.first + token) * a.q_token + head * a.q_head + 16 * (lane >> 5), 32, q);
     v16f o[DV / 32] = {};
     Running run = {-INFINITY, 0.0f};
 
@@ -300,6 +299,7 @@ __global__ __launch_bounds__(256, (DV <= 128 ? 2 : 1)) void k_attn_chunk(AttnArg
         page = *entry(a, s, base + L::kKeys + mine + (lane & 31));
         load(0);
     }
+    as_operands(a, q);
     for (int buffer = 0; base < hi; base += L::kKeys, buffer ^= 1) {
         char* const k_lds = lds + buffer * (L::kK + L::kV);
         char* const v_lds = k_lds + L::kK;
@@ -479,9 +479,8 @@ Plan plan(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, i
 
 template <int DK, int DV, bool E4M3>
 void launch_few(const AttnArgs& a, hipStream_t s) {
-    const int64_t units = (int64_t)a.seqs * (a.heads / a.group) * a.splits;
-    const int64_t tiles = ceil_div((int64_t)a.max_new * a.group, kTile);
-    k_attn_few<DK, DV, E4M3><<<(unsigned)(ceil_div(units, 8) * 8 * tiles), 256, 0, s>>>(a, (int)tiles, (int)units);
+    const int64_t units = (int64_t)a.seqs * a.splits, tiles = ceil_div((int64_t)a.max_new * a.group, kTile);
+    k_attn_few<DK, DV, E4M3><<<(unsigned)(ceil_div(units, 8) * 8 * tiles * (a.heads / a.group)), 256, 0, s>>>(a, (int)tiles, (int)units);
 }
 
 template <int DK, int DV, bool E4M3>

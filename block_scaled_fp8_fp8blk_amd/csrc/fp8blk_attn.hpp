@@ -115,10 +115,14 @@ typedef __attribute__((address_space(3))) char lds_char;
 
 constexpr int kTile = 32;
 
-// Rows in LDS are chunks of 16 bytes, and within every 8 chunks (128 bytes, all
-// banks once) row r holds chunk c at c ^ swizzle(r): 8 rows' reads of one chunk, and
-// 4 rows' of two, as the products need them, then meet in no bank.
+// Rows of COLS bf16 lie in LDS as blocks of 8 rows by 64 columns, 1 KB, what one load
+// of a wave brings; in a block, row r holds its 16-byte chunk c at c ^ swizzle(r): 8
+// rows' reads of one chunk, and 4 rows' of two, as the products need them, then meet
+// in no bank.
 __device__ __forceinline__ int swizzle(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
+template <int COLS>
+__device__ __forceinline__ int row_at(int row) { return (row >> 3) * (COLS / 64 * 1024) + (row & 7) * 128; }
+__device__ __forceinline__ int chunk_at(int chunk, int row) { return (chunk >> 3) * 1024 + (((chunk & 7) ^ swizzle(row)) << 4); }
 
 // Key (lane, register i) of a tile's scores.
 __device__ __forceinline__ int key_of(int lane, int i) { return (i & 3) + 8 * (i >> 2) + 4 * (lane >> 5); }
@@ -144,12 +148,12 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 // C += K Q^T of a tile: K's rows in LDS, Q's columns in registers.
 template <int DK>
 __device__ __forceinline__ v16f tile_scores(const char* k, const v8bf (&q)[DK / 16], int lane) {
-    const int row = lane & 31, h = lane >> 5, s = swizzle(row);
-    const char* at = k + row * DK * 2;
+    const int row = lane & 31, h = lane >> 5;
+    const char* at = k + row_at<DK>(row);
     v16f c = {};
 #pragma unroll
     for (int t = 0; t < DK / 16; ++t) {
-        const v8bf a = *(const v8bf*)(at + (t >> 2) * 128 + (((2 * (t & 3) + h) ^ s) << 4));
+        const v8bf a = *(const v8bf*)(at + (t >> 2) * 1024 + chunk_at(2 * (t & 3) + h, row));
         c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[t], c, 0, 0, 0);
     }
     return c;
@@ -160,12 +164,11 @@ __device__ __forceinline__ v16f tile_scores(const char* k, const v8bf (&q)[DK / 
 // + 15 read four rows of 16 columns, and are handed a column each.
 template <int COLS>
 __device__ __forceinline__ v8bf values_operand(const char* v, int t, int k, int lane) {
-    const int h = lane >> 5, row = 4 * h + ((lane & 15) >> 2), s = swizzle(row);
-    const int chunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-    const char* at = v + row * COLS * 2 + (lane & 1) * 8 + (t >> 1) * 128 + (((4 * (t & 1) + chunk) ^ s) << 4) + 16 * k * COLS * 2;
+    const int row = 4 * (lane >> 5) + ((lane & 15) >> 2), chunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    const char* at = v + row_at<COLS>(16 * k) + row * 128 + (lane & 1) * 8 + (t >> 1) * 1024 + chunk_at(4 * (t & 1) + chunk, row);
     typedef __attribute__((address_space(3))) v4s lds_v4s;
     const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)at);
-    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 8 * COLS * 2));
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + row_at<COLS>(8)));
     return __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
@@ -257,24 +260,23 @@ __device__ __forceinline__ const int32_t* entry(const AttnArgs& a, int s, int j)
     return a.table + s * a.max_pages + i;
 }
 
-// ROWS rows of COLS bf16 to LDS.
+// ROWS rows of COLS bf16 to LDS, a block a load: lanes 8 r .. 8 r + 7 a row's 128 bytes.
 template <int COLS, int ROWS = kTile>
 __device__ __forceinline__ void load_tile(const char* base, int64_t rows, uint32_t lds, int lane) {
-    constexpr int kChunks = COLS / 8;
 #pragma unroll
-    for (int n = 0; n < COLS * ROWS / 512; ++n) {
-        const int at = 64 * n + lane, row = at / kChunks, c = at % kChunks;
-        load_lds16(base + of_row(rows, row) + (((c & ~7) | ((c & 7) ^ swizzle(row))) << 4), lds + 1024 * n);
+    for (int r = 0; r < ROWS / 8; ++r) {
+        const char* p = base + of_row(rows, 8 * r + (lane >> 3)) + (((lane & 7) ^ swizzle(lane >> 3)) << 4);
+#pragma unroll
+        for (int c = 0; c < COLS / 64; ++c) load_lds16(p + 128 * c, lds + (r * (COLS / 64) + c) * 1024);
     }
 }
+
 // Rows of a tile in LDS that hold no key: zeros, for 0 * what lies there is 0.
 template <int COLS, int ROWS = kTile>
 __device__ __forceinline__ void clear_rows(char* lds, uint32_t held, int lane) {
 #pragma unroll 1
-    for (int n = 0; n < COLS * ROWS / 512; ++n) {
-        const int at = 64 * n + lane;
-        if (!(held >> (at / (COLS / 8)) & 1)) *(uint4*)(lds + at * 16) = make_uint4(0, 0, 0, 0);
-    }
+    for (int n = 0; n < COLS * ROWS / 512; ++n)
+        if (!(held >> (n / (COLS / 64) * 8 + (lane >> 3)) & 1)) *(uint4*)(lds + n * 1024 + lane * 16) = make_uint4(0, 0, 0, 0);
 }
 
 __device__ __forceinline__ float max_halves(float v) {
@@ -299,12 +301,23 @@ __device__ __forceinline__ void write_out(char* p, const float (&v)[8], float f)
                                                      pack_bf16(v[4] * f, v[5] * f), pack_bf16(v[6] * f, v[7] * f)};
 }
 
-// A row's 8 values of q at `p` as an operand.
-__device__ __forceinline__ v8bf q_operand(const AttnArgs& a, const char* p) {
-    uint4 d = load_global16(p);
-    d.x = (d.x & a.q_and) ^ a.q_xor, d.y = (d.y & a.q_and) ^ a.q_xor;
-    d.z = (d.z & a.q_and) ^ a.q_xor, d.w = (d.w & a.q_and) ^ a.q_xor;
-    return __builtin_bit_cast(v8bf, d);
+// A row's values of q, 8 at `p` and every `step` bytes on, as operands; as_operands,
+// once they have arrived, turns their sign or makes them 0 where scale asks for it.
+template <int N>
+__device__ __forceinline__ void load_q(const char* p, int step, v8bf (&q)[N]) {
+#pragma unroll
+    for (int t = 0; t < N; ++t) q[t] = __builtin_bit_cast(v8bf, load_global16(p + t * step));
+}
+template <int N>
+__device__ __forceinline__ void as_operands(const AttnArgs& a, v8bf (&q)[N]) {
+    if (!(a.q_xor | ~a.q_and)) return;
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+        uint4 d = __builtin_bit_cast(uint4, q[t]);
+        d.x = (d.x & a.q_and) ^ a.q_xor, d.y = (d.y & a.q_and) ^ a.q_xor;
+        d.z = (d.z & a.q_and) ^ a.q_xor, d.w = (d.w & a.q_and) ^ a.q_xor;
+        q[t] = __builtin_bit_cast(v8bf, d);
+    }
 }
 
 // Bits of the keys of the tile at `base` that lie in [lo, hi).
@@ -366,41 +379,57 @@ __device__ __forceinline__ void weights_operand(const v16f& z, v8bf (&p)[2]) {
     for (int i = 0; i < 16; ++i) p[i >> 3][i & 7] = (__bf16)z[i];
 }
 
-// The splits of a row and head, in order.
+// Joins the splits of a row and head: a workgroup for 128 columns of a row, kOnes
+// threads of 8 columns for every kWays-th chunk of keys, which they add in order; then
+// those sums, in order. Which chunks go together depends on the keys alone.
 template <int DV>
 static __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-    constexpr int kOnes = DV / 8;
-    const int id = blockIdx.x * (256 / kOnes) + threadIdx.x / kOnes, d = threadIdx.x % kOnes;
-    const int head = id % a.heads, i = id / a.heads % a.max_new, s = id / a.heads / a.max_new;
-    if (s >= a.seqs) return;
+    constexpr int kCols = DV < 128 ? DV : 128, kOnes = kCols / 8, kWays = 256 / kOnes;
+    __shared__ __attribute__((aligned(16))) float sums[kWays][kCols];
+    __shared__ float weights[kWays];
+    const int head = blockIdx.x % a.heads, i = blockIdx.x / a.heads % a.max_new, s = blockIdx.x / a.heads / a.max_new;
     const Seq seq = sequence(a, s);
     if (i >= seq.rows) return;
-    const int n = split_of(a, seq, 0).n;
-    if (n <= 1) return;
+    const Split split = split_of(a, seq, 0);
+    if (split.n <= 1) return;
+    const int col = blockIdx.y * kCols + threadIdx.x % kOnes * 8, way = threadIdx.x / kOnes;
     const int64_t at = partial(a, s, i, head, 0);
     const float2* ml = (const float2*)partial_ml(a, DV) + at;
+    const float* part = a.ws + at * DV + col;
     float top = -INFINITY;
-    for (int c = 0; c < n; ++c) top = fmaxf(top, ml[c].x);
+    for (int c = threadIdx.x & 63; c < split.n; c += 64) top = fmaxf(top, ml[c].x);
+    for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
     const float base = top == -INFINITY ? 0.0f : top;
     float sum = 0.0f, v[8] = {};
-    for (int c = 0; c < n; ++c) {
+#pragma unroll 4
+    for (int c = (way - split.lo / a.chunk) & (kWays - 1); c < split.n; c += kWays) {
         const float2 t = ml[c];
+        const float4 x = *(const float4*)(part + (int64_t)c * DV), y = *(const float4*)(part + (int64_t)c * DV + 4);
         const float f = exp2_fast(t.x - base);
         sum = __builtin_fmaf(f, t.y, sum);
-        const float4 x = *(const float4*)(a.ws + (at + c) * DV + 8 * d), y = *(const float4*)(a.ws + (at + c) * DV + 8 * d + 4);
         const float e[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = __builtin_fmaf(f, e[k], v[k]);
     }
-    write_out(a.out + (seq.first + i) * a.out_token + head * a.out_head + 16 * d, v, out_factor(a, head, top, sum));
+    float* const mine = &sums[way][threadIdx.x % kOnes * 8];
+    *(float4*)mine = make_float4(v[0], v[1], v[2], v[3]);
+    *(float4*)(mine + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    if (threadIdx.x % kOnes == 0) weights[way] = sum;
+    __syncthreads();
+    if (way > 0) return;
+#pragma unroll 4
+    for (int w = 1; w < kWays; ++w) {
+        sum += weights[w];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += mine[w * kCols + k];
+    }
+    write_out(a.out + (seq.first + i) * a.out_token + head * a.out_head + 2 * col, v, out_factor(a, head, top, sum));
 }
-
 
 template <int DV>
 void launch_join(const AttnArgs& a, hipStream_t s) {
     if (a.splits < 2) return;
-    const int64_t rows = (int64_t)a.seqs * a.max_new * a.heads;
-    k_attn_join<DV><<<(unsigned)ceil_div(rows * (DV / 8), 256), 256, 0, s>>>(a);
+    k_attn_join<DV><<<dim3((unsigned)((int64_t)a.seqs * a.max_new * a.heads), DV < 128 ? 1 : DV / 128), 256, 0, s>>>(a);
 }
 
 // A grid of units (splits of a key head's keys) and their row tiles: workgroup b runs

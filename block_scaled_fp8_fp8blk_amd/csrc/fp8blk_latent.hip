@@ -22,6 +22,7 @@ struct LatentLds {
     static constexpr int kRows = RT * kTile, kBuffer = kKeys * DK * 2;
     static constexpr int kP = 2 * kBuffer, kTop = kP + kRows * kKeys * 2, kKeep = kTop + 4 * kTile * 4, kSaid = kKeep + kRows * 4;
     static constexpr int kBytes = kSaid + 64;
+    static_assert(kRows * kLatent * 4 <= kP, "outputs take the place of the tiles");
 };
 
 __device__ __forceinline__ float max_groups(float v) {  // over the four lanes l % 16
@@ -37,14 +38,17 @@ __global__ __launch_bounds__(256, 1) void k_latent(AttnArgs a, int row_tiles, in
     const int unit = turn / per * (8 / spread) + xcd / spread, row_tile = row_tiles - 1 - (turn % per * spread + xcd % spread);
     if (unit >= units || row_tile < 0) return;
     const int c = unit % a.splits, s = unit / a.splits;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 4, mine = wave * kMine;
+    // Without a window the first tile is known before the sequence is: its pages are
+    // asked for at once.
+    int page = a.window > 0 ? 0 : *entry(a, s, c * a.chunk + mine + (lane & 31));
     const Seq seq = sequence(a, s);
     const int rows = seq.rows * a.group, r0 = row_tile * L::kRows;
     if (r0 >= rows) return;
     const Split split = split_of(a, seq, c);
     if (c > 0 && c >= split.n) return;
 
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int g = lane >> 4;
     const int at0 = seq.at + r0 / a.group, at1 = seq.at + (min(r0 + L::kRows, rows) - 1) / a.group;
     const int lo = max(split.lo, first_key(a, at0)), hi = min(split.hi, end_key(a, seq, at1));
     const int all_lo = first_key(a, at1), all_hi = end_key(a, seq, at0);  // keys that every row sees
@@ -52,23 +56,17 @@ __global__ __launch_bounds__(256, 1) void k_latent(AttnArgs a, int row_tiles, in
     // For scores: rows 32 rt + 16 ct + lane % 16, keys first .. of a tile, 16 kt + 4 g + i.
     constexpr int KT = RT;
     const int rt = RT == 2 ? wave & 1 : 0, part = RT == 2 ? wave >> 1 : wave, first = part * 16 * KT;
-    v8bf q[2][DK / 32];
     int own_lo[2], own_hi[2];
 #pragma unroll
     for (int ct = 0; ct < 2; ++ct) {
-        const int r = min(r0 + rt * kTile + 16 * ct + (lane & 15), rows - 1), token = r / a.group;
+        const int token = min(r0 + rt * kTile + 16 * ct + (lane & 15), rows - 1) / a.group;
         own_lo[ct] = first_key(a, seq.at + token), own_hi[ct] = end_key(a, seq, seq.at + token);
-        const char* p = a.q + (int64_t)(seq.first + token) * a.q_token + (r % a.group) * a.q_head + 16 * g;
-#pragma unroll
-        for (int t = 0; t < DK / 32; ++t) q[ct][t] = q_operand(a, p + 64 * t);
     }
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
     v16f o[kWaveCols / 32][RT] = {};
 
-    const int mine = wave * kMine;
     constexpr uint32_t kAllMine = (1u << kMine) - 1;
     int base = split.lo + (lo - split.lo) / kKeys * kKeys;
-    int page = 0;
     bool odd = false;
     TileRows next;
     const uint32_t lds_at = lds_offset(lds);
@@ -79,15 +77,35 @@ __global__ __launch_bounds__(256, 1) void k_latent(AttnArgs a, int row_tiles, in
     };
     auto load = [&](int buffer) { load_tile<DK, kMine>(a.k, next.k, lds_at + buffer * L::kBuffer + mine * DK * 2, lane); };
     if (base < hi) {
-        page = *entry(a, s, base + mine + (lane & 31));
+        if (a.window > 0) page = *entry(a, s, base + mine + (lane & 31));
         next = rows_of(base);
         page = *entry(a, s, base + kKeys + mine + (lane & 31));
         load(0);
+    }
+    // q's rows come through the other buffer, each once (a wave for itself would read
+    // rows that two or four of them need: 147 KB a workgroup).
+    v8bf q[2][DK / 32];
+    {
+        constexpr int kOwn = L::kRows / 4;
+        const int r = min(r0 + wave * kOwn + (lane & (kOwn - 1)), rows - 1), token = r / a.group;
+        load_tile<DK, kOwn>(a.q, (seq.first + token) * a.q_token + (r - token * a.group) * a.q_head,
+                            lds_at + L::kBuffer + wave * kOwn * DK * 2, lane);
+        wait_loads<0>();
+        __syncthreads();
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+            for (int t = 0; t < DK / 32; ++t) {
+                const int row = rt * kTile + 16 * ct + (lane & 15), chunk = 4 * (t & 1) + g;
+                q[ct][t] = *(const v8bf*)(lds + L::kBuffer + row_at<DK>(row) + (t >> 1) * 1024 + chunk_at(chunk, row));
+            }
     }
     char* const p_lds = lds + L::kP;
     float* const tops = (float*)(lds + L::kTop);
     float* const keeps = (float*)(lds + L::kKeep);
     uint32_t* const said = (uint32_t*)(lds + L::kSaid);  // by each wave: keys held, and whether some value is not finite
+    as_operands(a, q[0]);
+    as_operands(a, q[1]);
     for (int buffer = 0; base < hi; base += kKeys, buffer ^= 1) {
         char* const k_lds = lds + buffer * L::kBuffer;
         char* const own_rows = k_lds + mine * DK * 2;
@@ -110,7 +128,7 @@ __global__ __launch_bounds__(256, 1) void k_latent(AttnArgs a, int row_tiles, in
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
                 const int row = first + 16 * kt + (lane & 15), chunk = 4 * (t & 1) + g;
-                const v8bf k = *(const v8bf*)(k_lds + row * DK * 2 + (t >> 1) * 128 + ((chunk ^ swizzle(row)) << 4));
+                const v8bf k = *(const v8bf*)(k_lds + row_at<DK>(row) + (t >> 1) * 1024 + chunk_at(chunk, row));
 #pragma unroll
                 for (int ct = 0; ct < 2; ++ct) z[ct][kt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[ct][t], z[ct][kt], 0, 0, 0);
             }
@@ -192,18 +210,20 @@ __global__ __launch_bounds__(256, 1) void k_latent(AttnArgs a, int row_tiles, in
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 // keys 16 k + 8 (lane / 32) .., their natural order, for p's is the same
-                const int row = 8 * (lane >> 5) + ((lane & 15) >> 2), chunk = 4 * (t & 1) + 2 * (g & 1) + ((lane & 3) >> 1);
-                const char* at = k_lds + (16 * k + row) * DK * 2 + (2 * wave + (t >> 1)) * 128 + (lane & 1) * 8;
+                const int row = (lane & 15) >> 2, chunk = 4 * (t & 1) + 2 * (g & 1) + ((lane & 3) >> 1);
+                const char* at = k_lds + row_at<DK>(16 * k) + row_at<DK>(8 * (lane >> 5) + row) + (2 * wave + (t >> 1)) * 1024 + (lane & 1) * 8;
                 typedef __attribute__((address_space(3))) v4s lds_v4s;
-                const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + ((chunk ^ swizzle(row)) << 4)));
-                const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 4 * DK * 2 + ((chunk ^ swizzle(row + 4)) << 4)));
+                const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + chunk_at(chunk, row)));
+                const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 4 * 128 + chunk_at(chunk, row + 4)));
                 const v8bf v = __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
                 for (int r = 0; r < RT; ++r) o[t][r] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[r][k], o[t][r], 0, 0, 0);
             }
     }
 
-    // The waves' sums of weights, and the maxima, to every wave.
+    // Outputs through LDS, in place of the tiles, so that a row is written in one piece:
+    // rows of 512 floats, 16 bytes at chunk ^ (row % 8). The waves' sums of weights and
+    // the maxima go the same way.
     __syncthreads();
 #pragma unroll
     for (int ct = 0; ct < 2; ++ct) {
@@ -211,41 +231,55 @@ __global__ __launch_bounds__(256, 1) void k_latent(AttnArgs a, int row_tiles, in
         if (lane < 16) tops[wave * kTile + 16 * ct + lane] = sum;
         if (part == 0 && lane < 16) keeps[rt * kTile + 16 * ct + lane] = m[ct];
     }
-    __syncthreads();
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-        const int at = r * kTile + (lane & 31), row = r0 + at;
-        if (row >= rows) continue;
-        const float top = keeps[at];
-        float sum = tops[at] + tops[(RT == 2 ? 2 : 1) * kTile + at];
-        if constexpr (RT == 1) sum = sum + tops[2 * kTile + at] + tops[3 * kTile + at];
-        const int token = row / a.group, head = row % a.group;
-        const int64_t to = partial(a, s, token, head, c);
-        const float factor = out_factor(a, head, top, sum);
-        char* const out = a.out + (seq.first + token) * a.out_token + head * a.out_head;
+        const int at = r * kTile + (lane & 31);
 #pragma unroll
         for (int t = 0; t < kWaveCols / 32; ++t)
 #pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-                float v[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const auto x = __builtin_amdgcn_permlane32_swap(as_u32(o[t][r][4 * j + i]), as_u32(o[t][r][4 * j + 4 + i]), false, false);
-                    v[i] = as_f32(x[0]), v[4 + i] = as_f32(x[1]);
-                }
-                const int col = wave * kWaveCols + 32 * t + 8 * j + 8 * (lane >> 5);
-                if (odd)
-                    add_not_finite<kKeys>(a, s, a.v, false, col, split.lo, lo, hi, all_lo, all_hi, first_key(a, seq.at + token),
-                                          end_key(a, seq, seq.at + token), v);
-                if (split.n > 1) {
-                    float* p = a.ws + to * kLatent + col;
-                    *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
-                    *(float4*)(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-                } else {
-                    write_out(out + 2 * col, v, factor);
-                }
+            for (int j = 0; j < 4; ++j) {
+                const int chunk = (kWaveCols / 4 * wave + 8 * t + 2 * j + (lane >> 5)) ^ (at & 7);
+                *(float4*)(lds + at * kLatent * 4 + chunk * 16) =
+                    make_float4(o[t][r][4 * j], o[t][r][4 * j + 1], o[t][r][4 * j + 2], o[t][r][4 * j + 3]);
             }
-        if (split.n > 1 && wave == 0 && lane < 32) *(float2*)(partial_ml(a, kLatent) + 2 * to) = make_float2(top, sum);
+    }
+    __syncthreads();
+    // Wave w writes rows w, w + 4, ...; lane i knows where the ith of them goes.
+    constexpr int kOwn = L::kRows / 4;
+    const int own = wave + 4 * (lane & (kOwn - 1)), token = min(r0 + own, rows - 1) / a.group;
+    const int head = min(r0 + own, rows - 1) - token * a.group;
+    const float top = keeps[own];
+    float sum, factor = 1.0f;
+    if constexpr (RT == 2) sum = tops[own] + tops[2 * kTile + own];
+    else sum = tops[own] + tops[kTile + own] + tops[2 * kTile + own] + tops[3 * kTile + own];
+    char* to;
+    if (split.n > 1) {
+        const int64_t at = partial(a, s, token, head, c);
+        to = (char*)(a.ws + at * kLatent);
+        if (lane < kOwn && r0 + own < rows) *(float2*)(partial_ml(a, kLatent) + 2 * at) = make_float2(top, sum);
+    } else {
+        to = a.out + (seq.first + token) * a.out_token + head * a.out_head;
+        factor = out_factor(a, head, top, sum);
+    }
+#pragma unroll 4
+    for (int k = 0; k < kOwn; ++k) {
+        const int at = wave + 4 * k;
+        if (r0 + at >= rows) break;
+        const char* p = lds + at * kLatent * 4;
+        const float4 x = *(const float4*)(p + ((2 * lane) ^ (at & 7)) * 16), y = *(const float4*)(p + ((2 * lane + 1) ^ (at & 7)) * 16);
+        float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        if (odd) {
+            const int i = (r0 + at) / a.group;
+            add_not_finite<kKeys>(a, s, a.v, false, 8 * lane, split.lo, lo, hi, all_lo, all_hi, first_key(a, seq.at + i),
+                                  end_key(a, seq, seq.at + i), v);
+        }
+        char* const row = (char*)of_row((int64_t)to, k);
+        if (split.n > 1) {
+            *(float4*)(row + 32 * lane) = make_float4(v[0], v[1], v[2], v[3]);
+            *(float4*)(row + 32 * lane + 16) = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            write_out(row + 16 * lane, v, lane_value(factor, k));
+        }
     }
 }
 
