@@ -463,13 +463,17 @@ struct Plan {
 Plan plan(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, int64_t max_len, int64_t window) {
     const int64_t group = heads / c.heads;
     const bool panel = max_new <= FP8BLK_MAX_M, latent = !c.v;
-    Plan p;
-    p.few = latent ? panel && group <= kTile : panel;
     const int64_t seen = window > 0 ? std::min(max_len, window + (panel ? FP8BLK_MAX_M : max_new)) : max_len;
-    const int64_t units = seqs * c.heads * (p.few ? 1 : ceil_div(panel ? group : max_new * group, latent ? kLatentRows : kChunkRows));
-    const int64_t step = p.few ? 4 * kTile : 64, least = panel ? 128 : 512;
-    const int64_t want = std::max<int64_t>(1, (p.few && !latent ? 512 : 256) / units);
-    const int64_t n = std::min(want, ceil_div(seen, least));
+    Plan p;
+    p.few = panel && (!latent || group <= kTile || seqs * ceil_div(group, kLatentRows) * ceil_div(seen, 64) <= 256);
+    const int64_t tile = latent ? (p.few ? kTile : kLatentRows) : kChunkRows;
+    const int64_t units = seqs * c.heads * (p.few && !latent ? 1 : ceil_div(panel ? group : max_new * group, tile));
+    const int64_t step = p.few && !latent ? 4 * kTile : 64;
+    int64_t n;
+    if (latent) n = std::min((group <= 16 && panel ? 512 : 256) / units, ceil_div(seen, panel ? 128 : 512));
+    else if (p.few) n = seen <= 512 ? 1 : std::min(std::max(256 / units, units < 512 ? seen / 768 : 1), ceil_div(seen, step));
+    else n = std::min(256 / units, ceil_div(seen, 512));
+    n = std::max<int64_t>(n, 1);
     p.chunk = (int32_t)(ceil_div(ceil_div(seen, n), step) * step);
     p.splits = (int32_t)(ceil_div(seen, p.chunk) + (window > 0 ? 1 : 0));
     if (n == 1) p.splits = 1, p.chunk = 1 << 30;

@@ -145,16 +145,32 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
     return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_char*)p);
 }
 
+// Operands are read from LDS one group ahead of the products that take them: left to
+// itself the compiler reads each right before its product, and a wave waits for LDS
+// between any two. Vector and scalar instructions may move past this, reads of LDS and
+// products may not.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0x7); }
+
 // C += K Q^T of a tile: K's rows in LDS, Q's columns in registers.
 template <int DK>
 __device__ __forceinline__ v16f tile_scores(const char* k, const v8bf (&q)[DK / 16], int lane) {
+    constexpr int kAhead = 4;
     const int row = lane & 31, h = lane >> 5;
     const char* at = k + row_at<DK>(row);
+    v8bf x[2][kAhead];
     v16f c = {};
+    auto read = [&](int g) {
 #pragma unroll
-    for (int t = 0; t < DK / 16; ++t) {
-        const v8bf a = *(const v8bf*)(at + (t >> 2) * 1024 + chunk_at(2 * (t & 3) + h, row));
-        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[t], c, 0, 0, 0);
+        for (int t = 0; t < kAhead; ++t) x[g & 1][t] = *(const v8bf*)(at + g * 1024 + chunk_at(2 * t + h, row));
+    };
+    read(0);
+#pragma unroll
+    for (int g = 0; g < DK / 64; ++g) {
+        if (g + 1 < DK / 64) read(g + 1);
+        keep_order();
+#pragma unroll
+        for (int t = 0; t < kAhead; ++t) c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[g & 1][t], q[g * kAhead + t], c, 0, 0, 0);
+        keep_order();
     }
     return c;
 }
@@ -172,14 +188,23 @@ __device__ __forceinline__ v8bf values_operand(const char* v, int t, int k, int 
     return __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// out^T += V^T P^T of a tile: V, the first DV of rows of COLS in LDS, P as tile_scores leaves it.
-template <int DV, int COLS = DV>
+// out^T += V^T P^T of a tile: V's rows in LDS, P as tile_scores leaves it.
+template <int DV>
 __device__ __forceinline__ void tile_sums(const char* v, const v8bf (&p)[2], v16f (&o)[DV / 32], int lane) {
+    v8bf x[2][2];
+    auto read = [&](int t) {
 #pragma unroll
-    for (int t = 0; t < DV / 32; ++t)
+        for (int k = 0; k < 2; ++k) x[t & 1][k] = values_operand<DV>(v, t, k, lane);
+    };
+    read(0);
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values_operand<COLS>(v, t, k, lane), p[k], o[t], 0, 0, 0);
+    for (int t = 0; t < DV / 32; ++t) {
+        if (t + 1 < DV / 32) read(t + 1);
+        keep_order();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[t & 1][k], p[k], o[t], 0, 0, 0);
+        keep_order();
+    }
 }
 
 __device__ __forceinline__ bool not_finite(uint32_t d) {  // one of two bf16

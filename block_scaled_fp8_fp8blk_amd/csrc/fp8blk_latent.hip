@@ -17,12 +17,12 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 
 constexpr int kKeys = 64, kMine = kKeys / 4, kWaveCols = kLatent / 4;
 
-template <int DK, int RT>
+template <int DK, int ROWS, int BUFFERS>
 struct LatentLds {
-    static constexpr int kRows = RT * kTile, kBuffer = kKeys * DK * 2;
-    static constexpr int kP = 2 * kBuffer, kTop = kP + kRows * kKeys * 2, kKeep = kTop + 4 * kTile * 4, kSaid = kKeep + kRows * 4;
+    static constexpr int kPadded = ROWS < kTile ? kTile : ROWS, kBuffer = kKeys * DK * 2;
+    static constexpr int kP = BUFFERS * kBuffer, kTop = kP + kPadded * kKeys * 2, kKeep = kTop + 4 * kTile * 4, kSaid = kKeep + kPadded * 4;
     static constexpr int kBytes = kSaid + 64;
-    static_assert(kRows * kLatent * 4 <= kP, "outputs take the place of the tiles");
+    static_assert(kPadded * kLatent * 4 <= kP, "outputs take the place of the tiles");
 };
 
 __device__ __forceinline__ float max_groups(float v) {  // over the four lanes l % 16
@@ -30,9 +30,10 @@ __device__ __forceinline__ float max_groups(float v) {  // over the four lanes l
     return max_halves(fmaxf(as_f32(r[0]), as_f32(r[1])));
 }
 
-template <int DK, int RT>
-__global__ __launch_bounds__(256, 1) void k_latent(AttnArgs a, int row_tiles, int units, int spread) {
-    using L = LatentLds<DK, RT>;
+template <int DK, int ROWS, int BUFFERS>
+__global__ __launch_bounds__(256, (BUFFERS == 1 ? 2 : 1)) void k_latent(AttnArgs a, int row_tiles, int units, int spread) {
+    using L = LatentLds<DK, ROWS, BUFFERS>;
+    constexpr int kOther = (BUFFERS - 1) * L::kBuffer;  // where q passes through
     __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
     const int xcd = blockIdx.x & 7, turn = blockIdx.x >> 3, per = (row_tiles + spread - 1) / spread;
     const int unit = turn / per * (8 / spread) + xcd / spread, row_tile = row_tiles - 1 - (turn % per * spread + xcd % spread);
@@ -44,25 +45,27 @@ __global__ __launch_bounds__(256, 1) void k_latent(AttnArgs a, int row_tiles, in
     // asked for at once.
     int page = a.window > 0 ? 0 : *entry(a, s, c * a.chunk + mine + (lane & 31));
     const Seq seq = sequence(a, s);
-    const int rows = seq.rows * a.group, r0 = row_tile * L::kRows;
+    const int rows = seq.rows * a.group, r0 = row_tile * ROWS;
     if (r0 >= rows) return;
     const Split split = split_of(a, seq, c);
     if (c > 0 && c >= split.n) return;
 
-    const int at0 = seq.at + r0 / a.group, at1 = seq.at + (min(r0 + L::kRows, rows) - 1) / a.group;
+    const int at0 = seq.at + r0 / a.group, at1 = seq.at + (min(r0 + ROWS, rows) - 1) / a.group;
     const int lo = max(split.lo, first_key(a, at0)), hi = min(split.hi, end_key(a, seq, at1));
     const int all_lo = first_key(a, at1), all_hi = end_key(a, seq, at0);  // keys that every row sees
 
     // For scores: rows 32 rt + 16 ct + lane % 16, keys first .. of a tile, 16 kt + 4 g + i.
-    constexpr int KT = RT;
+    constexpr int RT = ROWS == 64 ? 2 : 1, KT = RT, CT = ROWS == 16 ? 1 : 2;
     const int rt = RT == 2 ? wave & 1 : 0, part = RT == 2 ? wave >> 1 : wave, first = part * 16 * KT;
-    int own_lo[2], own_hi[2];
+    int own_lo[CT], own_hi[CT];
 #pragma unroll
-    for (int ct = 0; ct < 2; ++ct) {
+    for (int ct = 0; ct < CT; ++ct) {
         const int token = min(r0 + rt * kTile + 16 * ct + (lane & 15), rows - 1) / a.group;
         own_lo[ct] = first_key(a, seq.at + token), own_hi[ct] = end_key(a, seq, seq.at + token);
     }
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    float m[CT], l[CT] = {};
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) m[ct] = -INFINITY;
     v16f o[kWaveCols / 32][RT] = {};
 
     constexpr uint32_t kAllMine = (1u << kMine) - 1;
@@ -80,33 +83,38 @@ __global__ __launch_bounds__(256, 1) void k_latent(AttnArgs a, int row_tiles, in
         if (a.window > 0) page = *entry(a, s, base + mine + (lane & 31));
         next = rows_of(base);
         page = *entry(a, s, base + kKeys + mine + (lane & 31));
-        load(0);
+        if constexpr (BUFFERS == 2) load(0);
     }
     // q's rows come through the other buffer, each once (a wave for itself would read
     // rows that two or four of them need: 147 KB a workgroup).
-    v8bf q[2][DK / 32];
+    v8bf q[CT][DK / 32];
     {
-        constexpr int kOwn = L::kRows / 4;
+        constexpr int kOwn = ROWS < 32 ? 8 : ROWS / 4;
         const int r = min(r0 + wave * kOwn + (lane & (kOwn - 1)), rows - 1), token = r / a.group;
-        load_tile<DK, kOwn>(a.q, (seq.first + token) * a.q_token + (r - token * a.group) * a.q_head,
-                            lds_at + L::kBuffer + wave * kOwn * DK * 2, lane);
+        if (wave * kOwn < ROWS)
+            load_tile<DK, kOwn>(a.q, (seq.first + token) * a.q_token + (r - token * a.group) * a.q_head,
+                                lds_at + kOther + wave * kOwn * DK * 2, lane);
         wait_loads<0>();
         __syncthreads();
 #pragma unroll
-        for (int ct = 0; ct < 2; ++ct)
+        for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
             for (int t = 0; t < DK / 32; ++t) {
                 const int row = rt * kTile + 16 * ct + (lane & 15), chunk = 4 * (t & 1) + g;
-                q[ct][t] = *(const v8bf*)(lds + L::kBuffer + row_at<DK>(row) + (t >> 1) * 1024 + chunk_at(chunk, row));
+                q[ct][t] = *(const v8bf*)(lds + kOther + row_at<DK>(row) + (t >> 1) * 1024 + chunk_at(chunk, row));
             }
     }
     char* const p_lds = lds + L::kP;
     float* const tops = (float*)(lds + L::kTop);
     float* const keeps = (float*)(lds + L::kKeep);
     uint32_t* const said = (uint32_t*)(lds + L::kSaid);  // by each wave: keys held, and whether some value is not finite
-    as_operands(a, q[0]);
-    as_operands(a, q[1]);
-    for (int buffer = 0; base < hi; base += kKeys, buffer ^= 1) {
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) as_operands(a, q[ct]);
+    if constexpr (BUFFERS == 1) {
+        __syncthreads();
+        if (base < hi) load(0);
+    }
+    for (int buffer = 0; base < hi; base += kKeys, buffer ^= BUFFERS - 1) {
         char* const k_lds = lds + buffer * L::kBuffer;
         char* const own_rows = k_lds + mine * DK * 2;
         wait_loads<0>();
@@ -118,20 +126,38 @@ __global__ __launch_bounds__(256, 1) void k_latent(AttnArgs a, int row_tiles, in
         if (base + kKeys < hi) {
             next = rows_of(base + kKeys);
             page = *entry(a, s, base + 2 * kKeys + mine + (lane & 31));
-            load(buffer ^ 1);
+            if constexpr (BUFFERS == 2) load(buffer ^ 1);
         }
         const bool edge = base < all_lo || base + kKeys > all_hi;
 
-        v4f z[2][KT] = {};
+        v4f z[CT][KT] = {};
+        {
+            constexpr int kSteps = DK / 32, kAhead = kSteps % 3 ? 4 : 6 / KT;
+            v8bf x[2][kAhead][KT];
+            auto read = [&](int b) {
 #pragma unroll
-        for (int t = 0; t < DK / 32; ++t)
+                for (int t = 0; t < kAhead; ++t)
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                const int row = first + 16 * kt + (lane & 15), chunk = 4 * (t & 1) + g;
-                const v8bf k = *(const v8bf*)(k_lds + row_at<DK>(row) + (t >> 1) * 1024 + chunk_at(chunk, row));
+                    for (int kt = 0; kt < KT; ++kt) {
+                        const int step = b * kAhead + t, row = first + 16 * kt + (lane & 15);
+                        x[b & 1][t][kt] = *(const v8bf*)(k_lds + row_at<DK>(row) + (step >> 1) * 1024 + chunk_at(4 * (step & 1) + g, row));
+                    }
+            };
+            read(0);
 #pragma unroll
-                for (int ct = 0; ct < 2; ++ct) z[ct][kt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[ct][t], z[ct][kt], 0, 0, 0);
+            for (int b = 0; b < kSteps / kAhead; ++b) {
+                if (b + 1 < kSteps / kAhead) read(b + 1);
+                keep_order();
+#pragma unroll
+                for (int t = 0; t < kAhead; ++t)
+#pragma unroll
+                    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct)
+                            z[ct][kt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[b & 1][t][kt], q[ct][b * kAhead + t], z[ct][kt], 0, 0, 0);
+                keep_order();
             }
+        }
         if (edge || held != ~(uint64_t)0) {
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
@@ -140,12 +166,12 @@ __global__ __launch_bounds__(256, 1) void k_latent(AttnArgs a, int row_tiles, in
                     const int j = first + 16 * kt + 4 * g + i;
                     const bool there = held >> j & 1;
 #pragma unroll
-                    for (int ct = 0; ct < 2; ++ct)
+                    for (int ct = 0; ct < CT; ++ct)
                         z[ct][kt][i] = there && base + j >= own_lo[ct] && base + j < own_hi[ct] ? z[ct][kt][i] : -INFINITY;
                 }
         }
 #pragma unroll
-        for (int ct = 0; ct < 2; ++ct) {
+        for (int ct = 0; ct < CT; ++ct) {
             float top = z[ct][0][0];
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
@@ -159,7 +185,7 @@ __global__ __launch_bounds__(256, 1) void k_latent(AttnArgs a, int row_tiles, in
         // Weights, against a maximum that all waves of these rows set alike (and lazily:
         // see tile_weights).
 #pragma unroll
-        for (int ct = 0; ct < 2; ++ct) {
+        for (int ct = 0; ct < CT; ++ct) {
             const int r = 16 * ct + (lane & 15);
             float top = fmaxf(tops[rt * kTile + r], tops[(RT == 2 ? rt + 2 : 1) * kTile + r]);
             if constexpr (RT == 1) top = fmaxf(top, fmaxf(tops[2 * kTile + r], tops[3 * kTile + r]));
@@ -196,7 +222,7 @@ __global__ __launch_bounds__(256, 1) void k_latent(AttnArgs a, int row_tiles, in
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             const int row = r * kTile + (lane & 31);
-            const float keep = keeps[row];
+            const float keep = ROWS < kTile && (lane & 16) ? 1.0f : keeps[row];
             if (__any(keep != 1.0f))
 #pragma unroll
                 for (int t = 0; t < kWaveCols / 32; ++t)
@@ -205,20 +231,34 @@ __global__ __launch_bounds__(256, 1) void k_latent(AttnArgs a, int row_tiles, in
 #pragma unroll
             for (int k = 0; k < 4; ++k) p[r][k] = *(const v8bf*)(p_lds + row * 128 + (((2 * k + (lane >> 5)) ^ (row & 7)) << 4));
         }
-#pragma unroll
-        for (int t = 0; t < kWaveCols / 32; ++t)
+        v8bf x[2][4];
+        auto read = [&](int t) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 // keys 16 k + 8 (lane / 32) .., their natural order, for p's is the same
                 const int row = (lane & 15) >> 2, chunk = 4 * (t & 1) + 2 * (g & 1) + ((lane & 3) >> 1);
                 const char* at = k_lds + row_at<DK>(16 * k) + row_at<DK>(8 * (lane >> 5) + row) + (2 * wave + (t >> 1)) * 1024 + (lane & 1) * 8;
                 typedef __attribute__((address_space(3))) v4s lds_v4s;
-                const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + chunk_at(chunk, row)));
-                const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 4 * 128 + chunk_at(chunk, row + 4)));
-                const v8bf v = __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-                for (int r = 0; r < RT; ++r) o[t][r] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[r][k], o[t][r], 0, 0, 0);
+                const v4s lo4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + chunk_at(chunk, row)));
+                const v4s hi4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 4 * 128 + chunk_at(chunk, row + 4)));
+                x[t & 1][k] = __builtin_bit_cast(v8bf, __builtin_shufflevector(lo4, hi4, 0, 1, 2, 3, 4, 5, 6, 7));
             }
+        };
+        read(0);
+#pragma unroll
+        for (int t = 0; t < kWaveCols / 32; ++t) {
+            if (t + 1 < kWaveCols / 32) read(t + 1);
+            keep_order();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int r = 0; r < RT; ++r) o[t][r] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[t & 1][k], p[r][k], o[t][r], 0, 0, 0);
+            keep_order();
+        }
+        if constexpr (BUFFERS == 1) {
+            __syncthreads();
+            if (base + kKeys < hi) load(0);
+        }
     }
 
     // Outputs through LDS, in place of the tiles, so that a row is written in one piece:
@@ -226,7 +266,7 @@ __global__ __launch_bounds__(256, 1) void k_latent(AttnArgs a, int row_tiles, in
     // the maxima go the same way.
     __syncthreads();
 #pragma unroll
-    for (int ct = 0; ct < 2; ++ct) {
+    for (int ct = 0; ct < CT; ++ct) {
         const float sum = bfly32(bfly16(l[ct]));
         if (lane < 16) tops[wave * kTile + 16 * ct + lane] = sum;
         if (part == 0 && lane < 16) keeps[rt * kTile + 16 * ct + lane] = m[ct];
@@ -245,7 +285,7 @@ __global__ __launch_bounds__(256, 1) void k_latent(AttnArgs a, int row_tiles, in
     }
     __syncthreads();
     // Wave w writes rows w, w + 4, ...; lane i knows where the ith of them goes.
-    constexpr int kOwn = L::kRows / 4;
+    constexpr int kOwn = ROWS / 4;
     const int own = wave + 4 * (lane & (kOwn - 1)), token = min(r0 + own, rows - 1) / a.group;
     const int head = min(r0 + own, rows - 1) - token * a.group;
     const float top = keeps[own];
@@ -283,19 +323,21 @@ __global__ __launch_bounds__(256, 1) void k_latent(AttnArgs a, int row_tiles, in
     }
 }
 
-template <int DK, int RT>
+template <int DK, int ROWS, int BUFFERS>
 void launch(const AttnArgs& a, hipStream_t s) {
-    const int64_t units = (int64_t)a.seqs * a.splits, tiles = ceil_div((int64_t)a.max_new * a.heads, RT * kTile);
+    const int64_t units = (int64_t)a.seqs * a.splits, tiles = ceil_div((int64_t)a.max_new * a.heads, ROWS);
     const Deal d = deal(units, tiles);
-    k_latent<DK, RT><<<d.grid, 256, 0, s>>>(a, (int)tiles, (int)units, d.spread);
+    k_latent<DK, ROWS, BUFFERS><<<d.grid, 256, 0, s>>>(a, (int)tiles, (int)units, d.spread);
     launch_join<kLatent>(a, s);
 }
 
 }  // namespace
 
 void launch_latent(const AttnArgs& a, int64_t k_cols, bool few, hipStream_t s) {
-    if (k_cols == kLatent) few ? launch<kLatent, 1>(a, s) : launch<kLatent, 2>(a, s);
-    else few ? launch<kLatent + 64, 1>(a, s) : launch<kLatent + 64, 2>(a, s);
+    const int64_t rows = (int64_t)a.max_new * a.heads;
+    const int kind = few ? rows <= 16 ? 16 : 32 : 64;
+    if (k_cols == kLatent) kind == 64 ? launch<kLatent, 64, 2>(a, s) : kind == 16 ? launch<kLatent, 16, 1>(a, s) : launch<kLatent, 32, 2>(a, s);
+    else kind == 64 ? launch<kLatent + 64, 64, 2>(a, s) : kind == 16 ? launch<kLatent + 64, 16, 1>(a, s) : launch<kLatent + 64, 32, 2>(a, s);
 }
 
 }  // namespace fp8blk
