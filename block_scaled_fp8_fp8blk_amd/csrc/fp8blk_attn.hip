@@ -28,13 +28,16 @@ struct Codes {
     static constexpr int kAll = COLS / 16 * ROWS, kN = (kAll + 63) / 64;  // 16-byte loads
     uint4 d[kN];
 };
-template <int COLS, int ROWS>
-__device__ __forceinline__ void load_codes(const char* base, int64_t rows, Codes<COLS, ROWS>& r, int lane) {
+template <bool ONE, int COLS, int ROWS>
+__device__ __forceinline__ void load_codes(const char* base, int64_t rows, int64_t slot, Codes<COLS, ROWS>& r, int lane) {
     constexpr int kChunks = COLS / 16;
 #pragma unroll
     for (int n = 0; n < Codes<COLS, ROWS>::kN; ++n) {
         const int at = min(64 * n + lane, Codes<COLS, ROWS>::kAll - 1);
-        r.d[n] = load_global16(base + of_row(rows, at / kChunks) + at % kChunks * 16);
+        if constexpr (ONE && 64 % kChunks == 0)
+            r.d[n] = load_global16(base + rows + n * (64 / kChunks) * slot + ((uint32_t)(lane / kChunks) * (uint32_t)slot + lane % kChunks * 16));
+        else if constexpr (ONE) r.d[n] = load_global16(base + rows + ((uint32_t)(at / kChunks) * (uint32_t)slot + at % kChunks * 16));
+        else r.d[n] = load_global16(base + of_row(rows, at / kChunks) + at % kChunks * 16);
     }
 }
 __device__ __forceinline__ uint2 widen4_e4m3(uint32_t d) {
@@ -55,7 +58,7 @@ __device__ __forceinline__ void store_codes(char* lds, const Codes<COLS, ROWS>& 
     }
 }
 
-template <int DK, int DV, bool E4M3>
+template <int DK, int DV, bool E4M3, bool ONE>
 __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1)) void k_attn_few(AttnArgs a, int row_tiles, int units) {
     using L = FewLds<DK, DV>;
     __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
@@ -71,7 +74,7 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
     // Without a window the wave's first tile is known before the sequence is: its pages
     // are asked for at once.
     const int early = c * a.chunk + wave * kTile;
-    int next_page = a.window > 0 ? 0 : *entry(a, s, early + (lane & 31));
+    int page = a.window > 0 ? 0 : page_at<ONE>(a, s, early, lane);
     const Seq seq = sequence(a, s);
     const int rows = seq.rows * a.group, r0 = row_tile * kTile;
     if (r0 >= rows) return;
@@ -102,23 +105,26 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
     int tile = (lo - split.lo) / kTile;
     tile += (wave - tile) & 3;
     int base = split.lo + tile * kTile;
-    TileRows next, here;
+    TileRows<ONE> next, here;
     Codes<E4M3 ? DK : 32> k_codes;
     Codes<E4M3 ? DV : 32> v_codes;
     bool odd = false;
+    const uint32_t k_off = load_offset(a.k_slot, lane), v_off = load_offset(a.v_slot, lane);
+    auto load_k = [&](int b) {  // of the tile at b, whose pages `page` has; and the pages of the wave's next
+        next = tile_rows<ONE>(a, page, b, lo, hi, lane);
+        if constexpr (E4M3 || ONE) page = page_at<ONE>(a, s, b + 4 * kTile, lane);
+        else load_lds4((const char*)entry(a, s, b + 4 * kTile + (lane & 31)), pages_at);
+        if constexpr (E4M3) load_codes<ONE>(k_base, next.k, a.k_slot, k_codes, lane);
+        else load_tile<DK, kTile, ONE>(k_base, next.k, a.k_slot, k_off, k_at, lane);
+    };
+    auto load_v = [&] {
+        if constexpr (E4M3) load_codes<ONE>(v_base, next.v, a.v_slot, v_codes, lane);
+        else load_tile<DV, kTile, ONE>(v_base, next.v, a.v_slot, v_off, v_at, lane);
+    };
     if (base < hi) {
-        if (a.window > 0) next_page = *entry(a, s, base + (lane & 31));
-        next = tile_rows(a, next_page, base, lo, hi, lane);
-        const int32_t* later = entry(a, s, base + 4 * kTile + (lane & 31));
-        if constexpr (E4M3) {
-            next_page = *later;
-            load_codes(k_base, next.k, k_codes, lane);
-            load_codes(v_base, next.v, v_codes, lane);
-        } else {
-            load_lds4((const char*)later, pages_at);
-            load_tile<DK>(k_base, next.k, k_at, lane);
-            load_tile<DV>(v_base, next.v, v_at, lane);
-        }
+        if (a.window > 0) page = page_at<ONE>(a, s, base, lane);
+        load_k(base);
+        load_v();
     }
     as_operands(a, q);
     for (; base < hi; base += 4 * kTile) {
@@ -128,23 +134,15 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
         else wait_loads<L::kV / 1024>();
         v16f z[1] = {tile_scores<DK>(k_lds, q, lane)};
         if (more) {
-            if constexpr (!E4M3) next_page = pages[lane & 31];
-            next = tile_rows(a, next_page, base + 4 * kTile, lo, hi, lane);
-            const int32_t* later = entry(a, s, base + 8 * kTile + (lane & 31));
-            if constexpr (E4M3) {
-                next_page = *later;
-                load_codes(k_base, next.k, k_codes, lane);
-            } else {
-                wait_reads();
-                load_lds4((const char*)later, pages_at);
-                load_tile<DK>(k_base, next.k, k_at, lane);
-            }
+            if constexpr (!E4M3 && !ONE) page = pages[lane & 31];
+            wait_reads();
+            load_k(base + 4 * kTile);
         }
         const bool edge = base < all_lo || base + kTile > all_hi;
         if (edge || here.held != ~0u) hide(z[0], here.held & keys_between(base, own_lo, own_hi), lane);
         rescale(o, tile_weights(z, a.z_scale, run));
         if constexpr (E4M3) store_codes(v_lds, v_codes, lane);
-        else if (more) wait_loads<DK / 16 + 1>();
+        else if (more) wait_loads<DK / 16 + (ONE ? 0 : 1)>();
         else wait_loads<0>();
         if (here.held != ~0u) clear_rows<DV>(v_lds, here.held, lane);
         if (edge) odd |= make_finite<DV, kTile>(v_lds, lane);
@@ -152,12 +150,8 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
         weights_operand(z[0], p);
         tile_sums<DV>(v_lds, p, o, lane);
         if (more) {
-            if constexpr (E4M3) {
-                load_codes(v_base, next.v, v_codes, lane);
-            } else {
-                wait_reads();
-                load_tile<DV>(v_base, next.v, v_at, lane);
-            }
+            wait_reads();
+            load_v();
         }
     }
 
@@ -233,7 +227,7 @@ struct ChunkLds {
 };
 constexpr int kChunkRows = 4 * kTile;
 
-template <int DK, int DV, bool E4M3>
+template <int DK, int DV, bool E4M3, bool ONE>
 __global__ __launch_bounds__(256, (DV <= 128 ? 2 : 1)) void k_attn_chunk(AttnArgs a, int row_tiles, int units, int spread) {
     using L = ChunkLds<DK, DV>;
     __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
@@ -272,32 +266,27 @@ __global__ __launch_bounds__(256, (DV <= 128 ? 2 : 1)) void k_attn_chunk(AttnArg
     const int mine = wave * L::kRows;
     constexpr uint32_t kMine = (uint32_t)(((uint64_t)1 << L::kRows) - 1);
     int base = split.lo + (lo - split.lo) / L::kKeys * L::kKeys;
-    TileRows next;
+    TileRows<ONE> next;
     int page = 0;
     bool odd = false;
     Codes<E4M3 ? DK : 64, E4M3 ? L::kRows : 16> k_codes;
     Codes<E4M3 ? DV : 64, E4M3 ? L::kRows : 16> v_codes;
-    const uint32_t lds_at = lds_offset(lds);
-    auto rows_of = [&](int b) {
-        TileRows t = tile_rows(a, page, b + mine, lo, hi, lane);
-        t.held &= kMine;
-        return t;
-    };
-    auto load = [&](int buffer) {
+    const uint32_t lds_at = lds_offset(lds), k_off = load_offset(a.k_slot, lane), v_off = load_offset(a.v_slot, lane);
+    auto load = [&](int b, int buffer) {  // the tile at b, whose pages `page` has; and the next one's pages
+        next = tile_rows<ONE, L::kRows>(a, page, b + mine, lo, hi, lane);
+        page = page_at<ONE>(a, s, b + L::kKeys + mine, lane);
         if constexpr (E4M3) {
-            load_codes(k_base, next.k, k_codes, lane);
-            load_codes(v_base, next.v, v_codes, lane);
+            load_codes<ONE>(k_base, next.k, a.k_slot, k_codes, lane);
+            load_codes<ONE>(v_base, next.v, a.v_slot, v_codes, lane);
         } else {
             const uint32_t to = lds_at + buffer * (L::kK + L::kV);
-            load_tile<DK, L::kRows>(k_base, next.k, to + mine * DK * 2, lane);
-            load_tile<DV, L::kRows>(v_base, next.v, to + L::kK + mine * DV * 2, lane);
+            load_tile<DK, L::kRows, ONE>(k_base, next.k, a.k_slot, k_off, to + mine * DK * 2, lane);
+            load_tile<DV, L::kRows, ONE>(v_base, next.v, a.v_slot, v_off, to + L::kK + mine * DV * 2, lane);
         }
     };
     if (base < hi) {
-        page = *entry(a, s, base + mine + (lane & 31));
-        next = rows_of(base);
-        page = *entry(a, s, base + L::kKeys + mine + (lane & 31));
-        load(0);
+        page = page_at<ONE>(a, s, base + mine, lane);
+        load(base, 0);
     }
     as_operands(a, q);
     for (int buffer = 0; base < hi; base += L::kKeys, buffer ^= 1) {
@@ -329,11 +318,7 @@ __global__ __launch_bounds__(256, (DV <= 128 ? 2 : 1)) void k_attn_chunk(AttnArg
             const uint4 w = *(const uint4*)(said + 4);
             odd |= (w.x | w.y | w.z | w.w) != 0;
         }
-        if (base + L::kKeys < hi) {
-            next = rows_of(base + L::kKeys);
-            page = *entry(a, s, base + 2 * L::kKeys + mine + (lane & 31));
-            load(buffer ^ 1);
-        }
+        if (base + L::kKeys < hi) load(base + L::kKeys, buffer ^ 1);
         const bool active = base < wave_hi && base + L::kKeys > wave_lo;
         if (!active) continue;
         v16f z[L::kTiles];
@@ -481,24 +466,24 @@ Plan plan(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, i
     return p;
 }
 
-template <int DK, int DV, bool E4M3>
+template <int DK, int DV, bool E4M3, bool ONE>
 void launch_few(const AttnArgs& a, hipStream_t s) {
     const int64_t units = (int64_t)a.seqs * a.splits, tiles = ceil_div((int64_t)a.max_new * a.group, kTile);
-    k_attn_few<DK, DV, E4M3><<<(unsigned)(ceil_div(units, 8) * 8 * tiles * (a.heads / a.group)), 256, 0, s>>>(a, (int)tiles, (int)units);
+    k_attn_few<DK, DV, E4M3, ONE><<<(unsigned)(ceil_div(units, 8) * 8 * tiles * (a.heads / a.group)), 256, 0, s>>>(a, (int)tiles, (int)units);
 }
 
-template <int DK, int DV, bool E4M3>
+template <int DK, int DV, bool E4M3, bool ONE>
 void launch_chunk(const AttnArgs& a, hipStream_t s) {
     const int64_t units = (int64_t)a.seqs * (a.heads / a.group) * a.splits;
     const int64_t tiles = ceil_div((int64_t)a.max_new * a.group, kChunkRows);
     const Deal d = deal(units, tiles);
-    k_attn_chunk<DK, DV, E4M3><<<d.grid, 256, 0, s>>>(a, (int)tiles, (int)units, d.spread);
+    k_attn_chunk<DK, DV, E4M3, ONE><<<d.grid, 256, 0, s>>>(a, (int)tiles, (int)units, d.spread);
 }
 
 template <int DK, int DV, bool E4M3>
 void launch(const AttnArgs& a, bool few, hipStream_t s) {
-    if (few) launch_few<DK, DV, E4M3>(a, s);
-    else launch_chunk<DK, DV, E4M3>(a, s);
+    if (few) one_page(a, kTile) ? launch_few<DK, DV, E4M3, true>(a, s) : launch_few<DK, DV, E4M3, false>(a, s);
+    else one_page(a, ChunkLds<DK, DV>::kRows) ? launch_chunk<DK, DV, E4M3, true>(a, s) : launch_chunk<DK, DV, E4M3, false>(a, s);
     launch_join<DV>(a, s);
 }
 

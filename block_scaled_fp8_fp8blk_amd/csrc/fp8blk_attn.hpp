@@ -132,6 +132,9 @@ __device__ __forceinline__ int key_of(int lane, int i) { return (i & 3) + 8 * (i
 __device__ __forceinline__ void load_lds16(const char* p, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory");
 }
+__device__ __forceinline__ void load_lds16(const char* p, uint32_t off, uint32_t lds) {  // p: the same for all lanes
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(p) : "memory");
+}
 __device__ __forceinline__ void load_lds4(const char* p, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(p) : "memory");
 }
@@ -260,19 +263,30 @@ __device__ __forceinline__ void add_not_finite(const AttnArgs& a, int s, const c
     }
 }
 
-// Byte offsets of a tile's rows: lane l has those of key l % 32.
+// Bits of the keys of the tile at `base` that lie in [lo, hi).
+__device__ __forceinline__ uint32_t keys_between(int base, int lo, int hi) {
+    const int b = min(max(lo - base, 0), kTile), e = min(max(hi - base, 0), kTile);
+    return (uint32_t)(((uint64_t)1 << e) - 1) & ~(uint32_t)(((uint64_t)1 << b) - 1);
+}
+
+// Where a wave's next ROWS rows lie. ONE: pages hold at least as many, so that they
+// are neighbours in one, all lanes agree and addresses are a scalar's business; else
+// lane l has the byte offsets of row l % 32.
+template <bool ONE>
 struct TileRows {
     int64_t k, v;
     uint32_t held;  // bit: a key that a page holds and the workgroup's rows may see
 };
-__device__ __forceinline__ TileRows tile_rows(const AttnArgs& a, int page, int base, int lo, int hi, int lane) {
-    const int j = base + (lane & 31);
-    const bool ok = (uint32_t)page < (uint32_t)a.pages && j >= lo && j < hi;
+template <bool ONE, int ROWS = kTile>
+__device__ __forceinline__ TileRows<ONE> tile_rows(const AttnArgs& a, int page, int base, int lo, int hi, int lane) {
+    constexpr uint32_t kAll = (uint32_t)(((uint64_t)1 << ROWS) - 1);
+    const int j = ONE ? base : base + (lane & 31);
+    const bool there = (uint32_t)page < (uint32_t)a.pages, ok = ONE ? there : there && j >= lo && j < hi;
     const int64_t p = ok ? page : 0, slot = ok ? j & ((1 << a.page_shift) - 1) : 0;
-    TileRows t;
+    TileRows<ONE> t;
     t.k = p * a.k_page + slot * a.k_slot;
     t.v = p * a.v_page + slot * a.v_slot;
-    t.held = (uint32_t)__ballot(ok);
+    t.held = (ONE ? ok ? keys_between(base, lo, hi) : 0u : (uint32_t)__ballot(ok)) & kAll;
     return t;
 }
 __device__ __forceinline__ int64_t of_row(int64_t v, int row) {
@@ -284,15 +298,29 @@ __device__ __forceinline__ const int32_t* entry(const AttnArgs& a, int s, int j)
     const int64_t i = min((int64_t)(j >> a.page_shift), a.max_pages - 1);
     return a.table + s * a.max_pages + i;
 }
+// The entries for the rows from key j on, as tile_rows takes them.
+template <bool ONE>
+__device__ __forceinline__ int page_at(const AttnArgs& a, int s, int j, int lane) {
+    if constexpr (ONE) return *(const __attribute__((address_space(4))) int32_t*)entry(a, s, j);
+    else return *entry(a, s, j + (lane & 31));
+}
 
 // ROWS rows of COLS bf16 to LDS, a block a load: lanes 8 r .. 8 r + 7 a row's 128 bytes.
-template <int COLS, int ROWS = kTile>
-__device__ __forceinline__ void load_tile(const char* base, int64_t rows, uint32_t lds, int lane) {
+// `lane_off` (ONE): load_offset of the rows' distance.
+__device__ __forceinline__ uint32_t load_offset(int64_t slot, int lane) {
+    return (uint32_t)((lane >> 3) * slot) + (((lane & 7) ^ swizzle(lane >> 3)) << 4);
+}
+template <int COLS, int ROWS, bool ONE>
+__device__ __forceinline__ void load_tile(const char* base, int64_t rows, int64_t slot, uint32_t lane_off, uint32_t lds, int lane) {
 #pragma unroll
     for (int r = 0; r < ROWS / 8; ++r) {
-        const char* p = base + of_row(rows, 8 * r + (lane >> 3)) + (((lane & 7) ^ swizzle(lane >> 3)) << 4);
+        const char* p = ONE ? base + rows + 8 * r * slot : base + of_row(rows, 8 * r + (lane >> 3)) + (((lane & 7) ^ swizzle(lane >> 3)) << 4);
 #pragma unroll
-        for (int c = 0; c < COLS / 64; ++c) load_lds16(p + 128 * c, lds + (r * (COLS / 64) + c) * 1024);
+        for (int c = 0; c < COLS / 64; ++c) {
+            const uint32_t to = lds + (r * (COLS / 64) + c) * 1024;
+            if constexpr (ONE) load_lds16(p + 128 * c, lane_off, to);
+            else load_lds16(p + 128 * c, to);
+        }
     }
 }
 
@@ -343,12 +371,6 @@ __device__ __forceinline__ void as_operands(const AttnArgs& a, v8bf (&q)[N]) {
         d.z = (d.z & a.q_and) ^ a.q_xor, d.w = (d.w & a.q_and) ^ a.q_xor;
         q[t] = __builtin_bit_cast(v8bf, d);
     }
-}
-
-// Bits of the keys of the tile at `base` that lie in [lo, hi).
-__device__ __forceinline__ uint32_t keys_between(int base, int lo, int hi) {
-    const int b = min(max(lo - base, 0), kTile), e = min(max(hi - base, 0), kTile);
-    return (uint32_t)(((uint64_t)1 << e) - 1) & ~(uint32_t)(((uint64_t)1 << b) - 1);
 }
 
 // Scores of keys that the lane's row does not see: -inf.
@@ -472,6 +494,11 @@ inline Deal deal(int64_t units, int64_t tiles) {
 // Latent attention (fp8blk_latent.hip): rows of a workgroup, value columns, and the launch.
 constexpr int kLatentRows = 64, kLatent = 512;
 void launch_latent(const AttnArgs& a, int64_t k_cols, bool few, hipStream_t s);
+
+// Whether `rows` neighbours in a page lie near enough for 32-bit offsets (see TileRows).
+inline bool one_page(const AttnArgs& a, int rows) {
+    return 1 << a.page_shift >= rows && a.k_slot < (INT64_C(1) << 26) && a.v_slot < (INT64_C(1) << 26);
+}
 
 // Checks the arguments of an attention call and writes its AttnArgs (the workspace
 // apart); FP8BLK_OK or what the call returns.

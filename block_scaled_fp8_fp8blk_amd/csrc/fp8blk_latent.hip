@@ -30,7 +30,7 @@ __device__ __forceinline__ float max_groups(float v) {  // over the four lanes l
     return max_halves(fmaxf(as_f32(r[0]), as_f32(r[1])));
 }
 
-template <int DK, int ROWS, int BUFFERS>
+template <int DK, int ROWS, int BUFFERS, bool ONE>
 __global__ __launch_bounds__(256, (BUFFERS == 1 ? 2 : 1)) void k_latent(AttnArgs a, int row_tiles, int units, int spread) {
     using L = LatentLds<DK, ROWS, BUFFERS>;
     constexpr int kOther = (BUFFERS - 1) * L::kBuffer;  // where q passes through
@@ -43,7 +43,7 @@ __global__ __launch_bounds__(256, (BUFFERS == 1 ? 2 : 1)) void k_latent(AttnArgs
     const int g = lane >> 4, mine = wave * kMine;
     // Without a window the first tile is known before the sequence is: its pages are
     // asked for at once.
-    int page = a.window > 0 ? 0 : *entry(a, s, c * a.chunk + mine + (lane & 31));
+    int page = a.window > 0 ? 0 : page_at<ONE>(a, s, c * a.chunk + mine, lane);
     const Seq seq = sequence(a, s);
     const int rows = seq.rows * a.group, r0 = row_tile * ROWS;
     if (r0 >= rows) return;
@@ -71,18 +71,18 @@ __global__ __launch_bounds__(256, (BUFFERS == 1 ? 2 : 1)) void k_latent(AttnArgs
     constexpr uint32_t kAllMine = (1u << kMine) - 1;
     int base = split.lo + (lo - split.lo) / kKeys * kKeys;
     bool odd = false;
-    TileRows next;
-    const uint32_t lds_at = lds_offset(lds);
-    auto rows_of = [&](int b) {
-        TileRows t = tile_rows(a, page, b + mine, lo, hi, lane);
-        t.held &= kAllMine;
-        return t;
+    TileRows<ONE> next;
+    const uint32_t lds_at = lds_offset(lds), off = load_offset(a.k_slot, lane);
+    auto find = [&](int b) {  // the tile at b, whose pages `page` has; and the next one's pages
+        next = tile_rows<ONE, kMine>(a, page, b + mine, lo, hi, lane);
+        page = page_at<ONE>(a, s, b + kKeys + mine, lane);
     };
-    auto load = [&](int buffer) { load_tile<DK, kMine>(a.k, next.k, lds_at + buffer * L::kBuffer + mine * DK * 2, lane); };
+    auto load = [&](int buffer) {
+        load_tile<DK, kMine, ONE>(a.k, next.k, a.k_slot, off, lds_at + buffer * L::kBuffer + mine * DK * 2, lane);
+    };
     if (base < hi) {
-        if (a.window > 0) page = *entry(a, s, base + mine + (lane & 31));
-        next = rows_of(base);
-        page = *entry(a, s, base + kKeys + mine + (lane & 31));
+        if (a.window > 0) page = page_at<ONE>(a, s, base + mine, lane);
+        find(base);
         if constexpr (BUFFERS == 2) load(0);
     }
     // q's rows come through the other buffer, each once (a wave for itself would read
@@ -92,8 +92,8 @@ __global__ __launch_bounds__(256, (BUFFERS == 1 ? 2 : 1)) void k_latent(AttnArgs
         constexpr int kOwn = ROWS < 32 ? 8 : ROWS / 4;
         const int r = min(r0 + wave * kOwn + (lane & (kOwn - 1)), rows - 1), token = r / a.group;
         if (wave * kOwn < ROWS)
-            load_tile<DK, kOwn>(a.q, (seq.first + token) * a.q_token + (r - token * a.group) * a.q_head,
-                                lds_at + kOther + wave * kOwn * DK * 2, lane);
+            load_tile<DK, kOwn, false>(a.q, (seq.first + token) * a.q_token + (r - token * a.group) * a.q_head, 0, 0,
+                                       lds_at + kOther + wave * kOwn * DK * 2, lane);
         wait_loads<0>();
         __syncthreads();
 #pragma unroll
@@ -124,8 +124,7 @@ __global__ __launch_bounds__(256, (BUFFERS == 1 ? 2 : 1)) void k_latent(AttnArgs
         const uint4 held4 = *(const uint4*)said;
         const uint64_t held = (uint64_t)(held4.z | held4.w << 16) << 32 | (held4.x | held4.y << 16);
         if (base + kKeys < hi) {
-            next = rows_of(base + kKeys);
-            page = *entry(a, s, base + 2 * kKeys + mine + (lane & 31));
+            find(base + kKeys);
             if constexpr (BUFFERS == 2) load(buffer ^ 1);
         }
         const bool edge = base < all_lo || base + kKeys > all_hi;
@@ -327,7 +326,8 @@ template <int DK, int ROWS, int BUFFERS>
 void launch(const AttnArgs& a, hipStream_t s) {
     const int64_t units = (int64_t)a.seqs * a.splits, tiles = ceil_div((int64_t)a.max_new * a.heads, ROWS);
     const Deal d = deal(units, tiles);
-    k_latent<DK, ROWS, BUFFERS><<<d.grid, 256, 0, s>>>(a, (int)tiles, (int)units, d.spread);
+    if (one_page(a, kMine)) k_latent<DK, ROWS, BUFFERS, true><<<d.grid, 256, 0, s>>>(a, (int)tiles, (int)units, d.spread);
+    else k_latent<DK, ROWS, BUFFERS, false><<<d.grid, 256, 0, s>>>(a, (int)tiles, (int)units, d.spread);
     launch_join<kLatent>(a, s);
 }
 
