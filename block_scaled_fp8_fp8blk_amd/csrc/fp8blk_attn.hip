@@ -220,16 +220,19 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
 // one while this one is worked on; one barrier a tile. Bound by the matrix cores,
 // their operands from LDS and the softmax between them, for which a compute unit
 // holds two waves a SIMD where registers and LDS allow.
-template <int DK, int DV>
+template <int DK, int DV, bool ONE>
 struct ChunkLds {
-    static constexpr int kKeys = DK + DV <= 256 ? 64 : 32, kTiles = kKeys / kTile, kRows = kKeys / 4;
-    static constexpr int kK = kKeys * DK * 2, kV = kKeys * DV * 2, kBytes = 2 * (kK + kV) + 64;
+    static constexpr int kKeys = 64, kTiles = kKeys / kTile, kRows = kKeys / 4;
+    static constexpr int kK = kKeys * DK * 2, kV = kKeys * DV * 2;
+    // ONE leaves nothing to say to other waves: with heads of 192 and 128 two workgroups
+    // take all 160 KB
+    static constexpr int kSaid = 2 * (kK + kV), kBytes = kSaid + (ONE ? 0 : 32);
 };
 constexpr int kChunkRows = 4 * kTile;
 
 template <int DK, int DV, bool E4M3, bool ONE>
-__global__ __launch_bounds__(256, (DV <= 128 ? 2 : 1)) void k_attn_chunk(AttnArgs a, int row_tiles, int units, int spread) {
-    using L = ChunkLds<DK, DV>;
+__global__ __launch_bounds__(256, (ChunkLds<DK, DV, ONE>::kBytes <= 80 * 1024 ? 2 : 1)) void k_attn_chunk(AttnArgs a, int row_tiles, int units, int spread) {
+    using L = ChunkLds<DK, DV, ONE>;
     __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
     // Workgroup b runs on XCD b % 8: a unit's row tiles, which read the same keys, on
     // `spread` XCDs, those with the most keys first.
@@ -267,14 +270,30 @@ __global__ __launch_bounds__(256, (DV <= 128 ? 2 : 1)) void k_attn_chunk(AttnArg
     constexpr uint32_t kMine = (uint32_t)(((uint64_t)1 << L::kRows) - 1);
     int base = split.lo + (lo - split.lo) / L::kKeys * L::kKeys;
     TileRows<ONE> next;
-    int page = 0;
+    uint32_t held[L::kTiles], held_next[L::kTiles] = {};  // the tile's keys that a page holds (else: what other waves say)
+    int page = 0, parts[4] = {};                          // the next tile's pages: the wave's (or its lanes'); ONE: of each wave
     bool odd = false;
     Codes<E4M3 ? DK : 64, E4M3 ? L::kRows : 16> k_codes;
     Codes<E4M3 ? DV : 64, E4M3 ? L::kRows : 16> v_codes;
     const uint32_t lds_at = lds_offset(lds), k_off = load_offset(a.k_slot, lane), v_off = load_offset(a.v_slot, lane);
-    auto load = [&](int b, int buffer) {  // the tile at b, whose pages `page` has; and the next one's pages
+    auto find = [&](int b) {
+        if constexpr (ONE)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) parts[w] = page_at<true>(a, s, b + w * L::kRows, lane);
+        else page = page_at<ONE>(a, s, b + mine, lane);
+    };
+    auto load = [&](int b, int buffer) {  // the tile at b
+        if constexpr (ONE) {
+            page = wave < 2 ? wave < 1 ? parts[0] : parts[1] : wave < 3 ? parts[2] : parts[3];
+#pragma unroll
+            for (int t = 0; t < L::kTiles; ++t) {
+                const uint32_t there = ((uint32_t)parts[2 * t] < (uint32_t)a.pages ? 0xffffu : 0u) |
+                                       ((uint32_t)parts[2 * t + 1] < (uint32_t)a.pages ? 0xffff0000u : 0u);
+                held_next[t] = there & keys_between(b + t * kTile, lo, hi);
+            }
+        }
         next = tile_rows<ONE, L::kRows>(a, page, b + mine, lo, hi, lane);
-        page = page_at<ONE>(a, s, b + L::kKeys + mine, lane);
+        find(b + L::kKeys);
         if constexpr (E4M3) {
             load_codes<ONE>(k_base, next.k, a.k_slot, k_codes, lane);
             load_codes<ONE>(v_base, next.v, a.v_slot, v_codes, lane);
@@ -285,7 +304,7 @@ __global__ __launch_bounds__(256, (DV <= 128 ? 2 : 1)) void k_attn_chunk(AttnArg
         }
     };
     if (base < hi) {
-        page = page_at<ONE>(a, s, base + mine, lane);
+        find(base);
         load(base, 0);
     }
     as_operands(a, q);
@@ -300,23 +319,16 @@ __global__ __launch_bounds__(256, (DV <= 128 ? 2 : 1)) void k_attn_chunk(AttnArg
         }
         char* const own_v = v_lds + mine * DV * 2;
         if (next.held != kMine) clear_rows<DV, L::kRows>(own_v, next.held, lane);
-        const bool edge = base < all_lo || base + L::kKeys > all_hi;
-        uint32_t* const said = (uint32_t*)(lds + 2 * (L::kK + L::kV)) + 8 * buffer;  // by each wave: the keys held, and whether some value is not finite
-        if (edge) {
-            const bool some = make_finite<DV, L::kRows>(own_v, lane);
-            if (lane == 0) said[4 + wave] = some;
-        }
-        if (lane == 0) said[wave] = next.held;
+        if (base < all_lo || base + L::kKeys > all_hi) odd |= make_finite<DV, L::kRows>(own_v, lane);
+        uint32_t* const said = (uint32_t*)(lds + L::kSaid) + 4 * buffer;
+        if (!ONE && lane == 0) said[wave] = next.held;
         __syncthreads();
-        uint32_t held[L::kTiles];
-        {
+        if constexpr (ONE) {
+#pragma unroll
+            for (int t = 0; t < L::kTiles; ++t) held[t] = held_next[t];
+        } else {
             const uint4 h = *(const uint4*)said;
-            if constexpr (L::kTiles == 2) held[0] = h.x | h.y << 16, held[1] = h.z | h.w << 16;
-            else held[0] = h.x | h.y << 8 | h.z << 16 | h.w << 24;
-        }
-        if (edge) {
-            const uint4 w = *(const uint4*)(said + 4);
-            odd |= (w.x | w.y | w.z | w.w) != 0;
+            held[0] = h.x | h.y << 16, held[1] = h.z | h.w << 16;
         }
         if (base + L::kKeys < hi) load(base + L::kKeys, buffer ^ 1);
         const bool active = base < wave_hi && base + L::kKeys > wave_lo;
@@ -342,6 +354,11 @@ __global__ __launch_bounds__(256, (DV <= 128 ? 2 : 1)) void k_attn_chunk(AttnArg
         }
     }
 
+    // Whether any wave has made a value finite.
+    __syncthreads();
+    if (lane == 0) ((int*)lds)[wave] = odd;
+    __syncthreads();
+    odd = ((const int*)lds)[0] | ((const int*)lds)[1] | ((const int*)lds)[2] | ((const int*)lds)[3];
     // Lanes of the two halves exchange columns, so that each has 8 in a row.
     run.l = bfly32(run.l);
     if (w0 + (lane & 31) >= rows) return;
@@ -483,7 +500,7 @@ void launch_chunk(const AttnArgs& a, hipStream_t s) {
 template <int DK, int DV, bool E4M3>
 void launch(const AttnArgs& a, bool few, hipStream_t s) {
     if (few) one_page(a, kTile) ? launch_few<DK, DV, E4M3, true>(a, s) : launch_few<DK, DV, E4M3, false>(a, s);
-    else one_page(a, ChunkLds<DK, DV>::kRows) ? launch_chunk<DK, DV, E4M3, true>(a, s) : launch_chunk<DK, DV, E4M3, false>(a, s);
+    else one_page(a, ChunkLds<DK, DV, true>::kRows) ? launch_chunk<DK, DV, E4M3, true>(a, s) : launch_chunk<DK, DV, E4M3, false>(a, s);
     launch_join<DV>(a, s);
 }
 
