@@ -1151,24 +1151,22 @@ class PagedCache:
         self.heads, self.k_cols, self.v_cols, self.latent = handle.heads, handle.k_cols, handle.v_cols, handle.v is None
 
 
-def _strided(t, device, dims, name):
-    """Pointer of a tensor on `device` whose last dimension is contiguous."""
-    if not isinstance(t, _torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+def _strided(t, device, dims, step, name):
+    """Pointer, shape and strides of a tensor on `device` whose last dimension is
+    contiguous; strides of dimensions of one, which say nothing, are a row's, rounded
+    up to `step`."""
     if t.get_device() != device:
-        raise ValueError(f"{name} must be on device {device}, it is on {t.device}")
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
-    if t.stride(dims - 1) != 1 and t.shape[dims - 1] != 1:
+        raise TypeError(f"{name} must be a CUDA tensor") if not t.is_cuda else \
+            ValueError(f"{name} must be on device {device}, it is on {t.device}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(shape)}")
+    if stride[-1] != 1 and shape[-1] != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t.data_ptr()
-
-
-def _outer(t, step):
-    """Strides of all dimensions but the last; those of dimensions of one, which
-    say nothing, as one row's, rounded up to `step`."""
-    row = -(-t.shape[-1] // step) * step
-    return [row if n == 1 else s for n, s in zip(t.shape[:-1], t.stride()[:-1])]
+    if 1 in shape:
+        row = -(-shape[-1] // step) * step
+        stride = tuple([row if n == 1 else d for n, d in zip(shape, stride)])
+    return t.data_ptr(), shape, stride
 
 
 def fp8blk_cache(k, v, k_scale=1.0, v_scale=1.0, v_cols=None):
@@ -1189,10 +1187,11 @@ def fp8blk_cache(k, v, k_scale=1.0, v_scale=1.0, v_cols=None):
             continue
         if isinstance(t, _torch.Tensor) and (t.dtype not in kinds or t.dtype != k.dtype):
             raise TypeError(f"{name}: dtype {t.dtype}, k and v must both be bfloat16 or float8_e4m3fn")
-        setattr(h, name, _strided(t, dev, 4, name))
-        if t.shape[:3] != k.shape[:3]:
-            raise ValueError(f"v must have k's pages, slots and heads {tuple(k.shape[:3])}, got shape {tuple(t.shape)}")
-        for part, stride in zip(("page", "slot", "head"), _outer(t, 16)):
+        p, shape, strides = _strided(t, dev, 4, 16, name)
+        setattr(h, name, p)
+        if shape[:3] != k.shape[:3]:
+            raise ValueError(f"v must have k's pages, slots and heads {tuple(k.shape[:3])}, got shape {tuple(shape)}")
+        for part, stride in zip(("page", "slot", "head"), strides):
             setattr(h, f"{name}_{part}", stride)
     if v is not None and v_cols is not None:
         raise ValueError("v_cols belongs to a cache without v")
@@ -1201,57 +1200,60 @@ def fp8blk_cache(k, v, k_scale=1.0, v_scale=1.0, v_cols=None):
     return PagedCache(h, dev, (k, v))
 
 
-def _heads(parts, device, N, rot, norm, rot_first, name):
-    """fp8blk_heads of (pass, rot), each [N, heads, cols] or None, and its heads
-    and columns."""
-    first, turned = parts
-    h = HeadsRecord()
-    kind = None
-    for part, field, t in (("pass", "pass_", first), ("rot", "rot", turned)):
-        if t is None:
-            continue
-        setattr(h, field, _strided(t, device, 3, name))
-        if t.dtype not in _f32 + _bf16 or kind not in (None, t.dtype):
-            raise TypeError(f"{name}: dtype {t.dtype}, both parts must be float32, or both bfloat16")
-        kind = t.dtype
-        if t.shape[0] != N or (h.heads and t.shape[1] != h.heads) or (part == "rot" and t.shape[2] != rot):
-            raise ValueError(f"{name} must be [N={N}, heads, cols] and [N, heads, rot={rot}], got shape {tuple(t.shape)}")
-        h.heads = t.shape[1]
-        token, head = _outer(t, 8)
-        setattr(h, part + "_token", token)
-        setattr(h, part + "_head", head)
-    if kind is None or (rot and turned is None):
-        raise ValueError(f"{name} is needed")
-    h.type = TYPE_F32 if kind in _f32 else TYPE_BF16
-    h.pass_cols = 0 if first is None else first.shape[2]
-    cols = h.pass_cols + rot
+def _heads(first, turned, device, N, rot, norm, name):
+    """fp8blk_heads of a part that stays and one that rotates, each [N, heads, cols] or
+    None, and its heads and columns."""
+    pass_p = rot_p = norm_p = None
+    pass_token = pass_head = rot_token = rot_head = pass_cols = norm_cols = 0
+    if first is not None:
+        kind = first.dtype
+        pass_p, shape, (pass_token, pass_head, _) = _strided(first, device, 3, 8, name)
+        _, heads, pass_cols = shape
+        if shape[0] != N:
+            raise ValueError(f"{name} must be [N={N}, heads, cols], got shape {tuple(shape)}")
+    if turned is not None:
+        if first is not None and turned.dtype != kind:
+            raise TypeError(f"{name}: dtypes {kind} and {turned.dtype}, both parts must be float32, or both bfloat16")
+        kind = turned.dtype
+        rot_p, shape, (rot_token, rot_head, _) = _strided(turned, device, 3, 8, name)
+        if shape[0] != N or shape[2] != rot or (first is not None and shape[1] != heads):
+            raise ValueError(f"{name}'s rotated part must be [N={N}, heads, rot={rot}], got shape {tuple(shape)}")
+        heads = shape[1]
+    elif rot or first is None:
+        raise ValueError(f"{name} is needed" if first is None else f"{name}'s rotated part is needed")
+    if kind not in _f32 and kind not in _bf16:
+        raise TypeError(f"{name}: dtype {kind}, it must be float32 or bfloat16")
+    cols = pass_cols + rot
     if norm is not None:
-        if norm.dim() != 1 or norm.shape[0] not in (cols, h.pass_cols):
-            raise ValueError(f"{name}'s norm must be [{cols}] or [{h.pass_cols}], got shape {tuple(norm.shape)}")
-        h.norm, h.norm_cols = _buf(norm, device, _bf16, norm.shape, name + "_norm"), norm.shape[0]
-    return h, h.heads, cols
+        shape = norm.shape
+        if shape != (cols,) and shape != (pass_cols,):
+            raise ValueError(f"{name}'s norm must be [{cols}] or [{pass_cols}], got shape {tuple(shape)}")
+        norm_p, norm_cols = _buf(norm, device, _bf16, shape, name + "_norm"), shape[0]
+    return HeadsRecord(pass_p, rot_p, pass_token, pass_head, rot_token, rot_head, heads, pass_cols, norm_cols, norm_p,
+                       TYPE_F32 if kind in _f32 else TYPE_BF16), heads, cols
 
 
 def _rope_append_args(rope, positions, q, q_out, k, v, cache, slots, q_norm=None, k_norm=None, eps=1e-6):
     if _torch is None:
         _load_torch()
     dev, rot = rope.device, rope.rot
-    if positions.dim() != 1:
-        raise ValueError(f"positions must be [N], got shape {tuple(positions.shape)}")
-    N = positions.shape[0]
-    positions_p = _buf(positions, dev, _i32, (N,), "positions")
-    hq = out_p = hk = hv = slots_p = None
-    out_strides = (0, 0)
+    shape = positions.shape
+    if len(shape) != 1:
+        raise ValueError(f"positions must be [N], got shape {tuple(shape)}")
+    N = shape[0]
+    positions_p = _buf(positions, dev, _i32, shape, "positions")
+    hq = out_p = hk = hv = cache_p = slots_p = None
+    token = head = 0
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out belong together")
     if q is not None:
-        hq, heads, cols = _heads(q, dev, N, rot, q_norm, rope.rot_first, "q")
-        out_p = _strided(q_out, dev, 3, "q_out")
+        hq, heads, cols = _heads(*q, dev, N, rot, q_norm, "q")
+        out_p, out_shape, (token, head, _) = _strided(q_out, dev, 3, 8, "q_out")
         if q_out.dtype not in _bf16:
             raise TypeError(f"q_out: dtype {q_out.dtype} not in {_bf16}")
-        if q_out.shape != (N, heads, cols):
-            raise ValueError(f"q_out must be {(N, heads, cols)}, got shape {tuple(q_out.shape)}")
-        out_strides = _outer(q_out, 8)
+        if out_shape != (N, heads, cols):
+            raise ValueError(f"q_out must be {(N, heads, cols)}, got shape {tuple(out_shape)}")
+        hq = ctypes.byref(hq)
     elif q_norm is not None:
         raise ValueError("q_norm without q")
     if k is None:
@@ -1262,19 +1264,19 @@ def _rope_append_args(rope, positions, q, q_out, k, v, cache, slots, q_norm=None
             raise ValueError("k needs a cache and slots")
         if cache.device != dev:
             raise ValueError(f"the cache is on device {cache.device}, the frequencies are on {dev}")
-        hk, heads, cols = _heads(k, dev, N, rot, k_norm, rope.rot_first, "k")
-        if (heads, cols) != (cache.heads, cache.k_cols):
+        hk, heads, cols = _heads(*k, dev, N, rot, k_norm, "k")
+        if heads != cache.heads or cols != cache.k_cols:
             raise ValueError(f"k must have the cache's {cache.heads} heads of {cache.k_cols}, got {heads} of {cols}")
-        slots_p = _buf(slots, dev, _i32, (N,), "slots")
+        slots_p = _buf(slots, dev, _i32, shape, "slots")
         if (v is None) != cache.latent:
             raise ValueError("v is needed, but for a latent cache, which has none")
         if v is not None:
-            hv, heads, cols = _heads((v, None), dev, N, 0, None, True, "v")
-            if (heads, cols) != (cache.heads, cache.v_cols):
+            hv, heads, cols = _heads(v, None, dev, N, 0, None, "v")
+            if heads != cache.heads or cols != cache.v_cols:
                 raise ValueError(f"v must have the cache's {cache.heads} heads of {cache.v_cols}, got {heads} of {cols}")
-    ref = lambda h: None if h is None else ctypes.byref(h)  # noqa: E731
-    return dev, (rope.pointer, positions_p, N, ref(hq), out_p, *out_strides, ref(hk), ref(hv),
-                 None if cache is None else cache.pointer, slots_p, eps)
+            hv = ctypes.byref(hv)
+        hk, cache_p = ctypes.byref(hk), cache.pointer
+    return dev, (rope.pointer, positions_p, N, hq, out_p, token, head, hk, hv, cache_p, slots_p, eps)
 
 
 def fp8blk_rope_append(rope, positions, q, q_out, k, v, cache, slots, q_norm=None, k_norm=None, eps=1e-6, stream=None,
@@ -1299,23 +1301,23 @@ def fp8blk_attn_bytes(cache, heads, seqs, max_new, max_len, window=0):
 
 def _attn_args(cache, q, table, lens, starts, max_new, max_len, scale, out, ws, causal=True, window=0, sinks=None):
     dev = cache.device
-    q_p, out_p = _strided(q, dev, 3, "q"), _strided(out, dev, 3, "out")
-    for name, t in (("q", q), ("out", out)):
-        if t.dtype not in _bf16:
-            raise TypeError(f"{name}: dtype {t.dtype} not in {_bf16}")
-    N, heads, cols = q.shape
+    q_p, shape, (q_token, q_head, _) = _strided(q, dev, 3, 8, "q")
+    out_p, out_shape, (out_token, out_head, _) = _strided(out, dev, 3, 8, "out")
+    if q.dtype not in _bf16 or out.dtype not in _bf16:
+        raise TypeError(f"q and out: dtypes {q.dtype} and {out.dtype} not in {_bf16}")
+    N, heads, cols = shape
     if cols != cache.k_cols:
-        raise ValueError(f"q must be [N, heads, {cache.k_cols}], got shape {tuple(q.shape)}")
-    if out.shape != (N, heads, cache.v_cols):
-        raise ValueError(f"out must be {(N, heads, cache.v_cols)}, got shape {tuple(out.shape)}")
-    if table.dim() != 2:
-        raise ValueError(f"table must be [seqs, pages], got shape {tuple(table.shape)}")
-    S = table.shape[0]
-    batch = BatchRecord(_buf(table, dev, _i32, table.shape, "table"), _buf(lens, dev, _i32, (S,), "lens"),
-                        _buf(starts, dev, _i32, (S + 1,), "starts"), S, table.shape[1], max_new, max_len)
+        raise ValueError(f"q must be [N, heads, {cache.k_cols}], got shape {tuple(shape)}")
+    if out_shape != (N, heads, cache.v_cols):
+        raise ValueError(f"out must be {(N, heads, cache.v_cols)}, got shape {tuple(out_shape)}")
+    on, table_p, S, width = _matrix(table, _i32, "table")
+    if on != dev:
+        raise ValueError(f"table must be on device {dev}, it is on {on}")
+    batch = BatchRecord(table_p, _buf(lens, dev, _i32, (S,), "lens"), _buf(starts, dev, _i32, (S + 1,), "starts"), S, width,
+                        max_new, max_len)
     wsp, wsb = _workspace(ws, dev)
-    return dev, (cache.pointer, q_p, *_outer(q, 8), N, heads, ctypes.byref(batch), scale, 1 if causal else 0, window,
-                 _buf(sinks, dev, _f32, (heads,), "sinks", False), out_p, *_outer(out, 8), wsp, wsb)
+    return dev, (cache.pointer, q_p, q_token, q_head, N, heads, ctypes.byref(batch), scale, 1 if causal else 0, window,
+                 None if sinks is None else _buf(sinks, dev, _f32, (heads,), "sinks"), out_p, out_token, out_head, wsp, wsb)
 
 
 def fp8blk_paged_attn(cache, q, table, lens, starts, max_new, max_len, scale, out, ws, causal=True, window=0, sinks=None,

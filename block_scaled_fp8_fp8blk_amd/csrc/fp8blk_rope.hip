@@ -24,6 +24,7 @@ struct RowsIn {  // q, k or v: [N, heads, pass | rot], and where its rows go
     char* out;
     int64_t out_page, out_slot, out_head;  // bytes; q: a token is a slot
     int32_t heads, pass_units, rot_units, norm_cols;
+    int32_t first;  // of the tasks that are its rows
     int32_t bf16, e4m3, rot_first;
     float scale;
 };
@@ -34,7 +35,7 @@ struct RopeArgs {
     const int32_t* positions;
     const int32_t* slots;
     int64_t n_slots;
-    int32_t rows, rot, page_shift, lanes_log2;
+    int32_t tasks, rot, page_shift, lanes_log2;
     float mscale, eps;
 };
 
@@ -89,88 +90,130 @@ __device__ __forceinline__ void store4(char* p, const RowsIn& t, int64_t i, cons
     }
 }
 
-// A workgroup takes rows (heads of q, k and v) of one token, a group of 2^lanes_log2
-// lanes a row and U units of 8 columns a lane. Cosines and sines are formed once
-// a workgroup, 4 threads' worth of pairs for every row that uses them.
+// The U units of a lane in a row of t: units at, at + lanes, ... of 8 columns, the
+// rotated ones 4 pairs.
+template <int U, bool INTERLEAVED>
+struct Units {
+    float v[U][kUnit];
+
+    // Columns of its first and last four values in the part that they come from and
+    // in the written row.
+    struct Place {
+        bool in, turned;
+        int from[2], to[2], pair;
+    };
+    static __device__ __forceinline__ Place place(const RowsIn& t, int u) {
+        const int first = t.rot_first ? 0 : t.pass_units, j = u - first;
+        Place p;
+        p.in = u < t.pass_units + t.rot_units;
+        p.turned = j >= 0 && j < t.rot_units;
+        const int half = t.rot_units * kUnit / 2, other = t.rot_first ? u - t.rot_units : u;
+        p.from[0] = !p.turned ? other * kUnit : INTERLEAVED ? kUnit * j : 4 * j;
+        p.from[1] = p.turned && !INTERLEAVED ? half + 4 * j : p.from[0] + 4;
+        const int start = p.turned ? first : t.rot_first ? t.rot_units : 0;
+        p.to[0] = start * kUnit + p.from[0], p.to[1] = start * kUnit + p.from[1];
+        p.pair = 4 * j;
+        return p;
+    }
+
+    __device__ __forceinline__ void load(const RowsIn& t, int64_t n, int head, int at, int lanes) {
+        if (head >= t.heads) return;
+        const char* pass = t.pass + n * t.pass_token + head * t.pass_head;
+        const char* rot = t.rot + n * t.rot_token + head * t.rot_head;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const Place p = place(t, at + k * lanes);
+            if (!p.in) continue;
+            load4(p.turned ? rot : pass, t.bf16, p.from[0], v[k]);
+            load4(p.turned ? rot : pass, t.bf16, p.from[1], v[k] + 4);
+        }
+    }
+
+    __device__ __forceinline__ void finish(const RowsIn& t, char* out, int head, int at, int lanes, float eps, const float (*turn)[FP8BLK_MAX_ROT / 2]) {
+        if (head >= t.heads) return;  // all lanes of a row
+        const bool whole = t.norm_cols > t.pass_units * kUnit;
+        float unit = 1.0f;
+        if (t.norm) {
+            float square = 0.0f;
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const Place p = place(t, at + k * lanes);
+                if (p.in && (whole || !p.turned))
+#pragma unroll
+                    for (int i = 0; i < kUnit; ++i) square = __builtin_fmaf(v[k][i], v[k][i], square);
+            }
+            for (int m = 1; m < lanes; m <<= 1) square += __shfl_xor(square, m);
+            unit = 1.0f / sqrtf(square / (float)t.norm_cols + eps);
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const Place p = place(t, at + k * lanes);
+            if (!p.in) continue;
+            if (t.norm && (whole || !p.turned)) {  // weights of the whole row by its columns, of the pass part alone by that part's
+                float w[kUnit];
+                load4((const char*)t.norm, true, whole ? p.to[0] : p.from[0], w);
+                load4((const char*)t.norm, true, whole ? p.to[1] : p.from[1], w + 4);
+#pragma unroll
+                for (int i = 0; i < kUnit; ++i) v[k][i] = v[k][i] * unit * w[i];
+            }
+            if (p.turned) {
+                const float4 c = *(const float4*)&turn[0][p.pair], s = *(const float4*)&turn[1][p.pair];
+                const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float& x = v[k][INTERLEAVED ? 2 * i : i];
+                    float& y = v[k][INTERLEAVED ? 2 * i + 1 : i + 4];
+                    const float x0 = x, y0 = y;
+                    x = x0 * cs[i] - y0 * sn[i];
+                    y = x0 * sn[i] + y0 * cs[i];
+                }
+            }
+            char* const row = out + head * t.out_head;
+            store4(row, t, p.to[0], v[k]);
+            store4(row, t, p.to[1], v[k] + 4);
+        }
+    }
+};
+
+// A workgroup takes the heads of q, k and v of one token, a wave 64 / lanes of one of
+// them at a time (so that all its lanes read the same description of it), a row
+// `lanes` lanes. The next rows are asked for before the present ones are worked on,
+// the first before the cosines and sines, which are formed once a workgroup.
 template <int U, bool INTERLEAVED>
 __global__ __launch_bounds__(kThreads) void k_rope_append(RopeArgs a) {
-    __shared__ float turn[2][FP8BLK_MAX_ROT / 2];
+    __shared__ __attribute__((aligned(16))) float turn[2][FP8BLK_MAX_ROT / 2];
     const int64_t n = blockIdx.x;
-    const int lanes = 1 << a.lanes_log2, at = threadIdx.x & (lanes - 1), step = (kThreads >> a.lanes_log2) * gridDim.y;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lanes = 1 << a.lanes_log2, at = lane & (lanes - 1), row = lane >> a.lanes_log2, rows = 64 >> a.lanes_log2;
+    const int step = 4 * gridDim.y;
+    int task = 4 * blockIdx.y + wave;
+    auto rows_in = [&](int t) -> const RowsIn& { return a.in[t >= a.in[2].first ? 2 : t >= a.in[1].first ? 1 : 0]; };
+    Units<U, INTERLEAVED> here, next;
+    if (task < a.tasks) {
+        const RowsIn& t = rows_in(task);
+        next.load(t, n, (task - t.first) * rows + row, at, lanes);
+    }
     if ((int)threadIdx.x < a.rot / 2) {
         double c, s;
         cos_sin((double)a.positions[n] * a.freqs[threadIdx.x], c, s);
         turn[0][threadIdx.x] = (float)((double)a.mscale * c);
         turn[1][threadIdx.x] = (float)((double)a.mscale * s);
     }
-    const int64_t slot = a.slots ? (int64_t)a.slots[n] : -1;
+    const int64_t slot = a.slots ? (int64_t)__builtin_amdgcn_readfirstlane(a.slots[n]) : -1;
+    const int64_t page = slot >> a.page_shift, in_page = slot & ((1 << a.page_shift) - 1);
+    const bool stored = slot >= 0 && slot < a.n_slots;
     __syncthreads();
-    for (int row = blockIdx.y * (kThreads >> a.lanes_log2) + (threadIdx.x >> a.lanes_log2); row < a.rows; row += step) {
-        const int which = row < a.in[0].heads ? 0 : row < a.in[0].heads + a.in[1].heads ? 1 : 2;
-        const RowsIn& t = a.in[which];
-        const int head = row - (which > 0 ? a.in[0].heads : 0) - (which > 1 ? a.in[1].heads : 0);
-        char* out = t.out + head * t.out_head;
-        if (which == 0) out += n * t.out_slot;
-        else if (slot < 0 || slot >= a.n_slots) continue;  // the whole group leaves: a group shares a row
-        else out += (slot >> a.page_shift) * t.out_page + (slot & ((1 << a.page_shift) - 1)) * t.out_slot;
-        const char* pass = t.pass + n * t.pass_token + head * t.pass_head;
-        const char* rot = t.rot + n * t.rot_token + head * t.rot_head;
-        const int units = t.pass_units + t.rot_units, rot_cols = t.rot_units * kUnit, first = t.rot_first ? 0 : t.pass_units;
-
-        float v[U][kUnit];
-        int col[U][2];  // in the written row, of the first and the last four columns
-        bool turned[U];
-        float square = 0.0f;
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int u = at + k * lanes;
-            const int j = u - first;  // among the rotated units
-            turned[k] = j >= 0 && j < t.rot_units;
-            const int p = t.rot_first ? u - t.rot_units : u;  // among the others
-            const bool apart = turned[k] && !INTERLEAVED;
-            const int lo = apart ? 4 * j : kUnit * j, hi = apart ? rot_cols / 2 + 4 * j : kUnit * j + 4;
-            col[k][0] = turned[k] ? first * kUnit + lo : u * kUnit;
-            col[k][1] = turned[k] ? first * kUnit + hi : u * kUnit + 4;
-            if (u < units) {
-                load4(turned[k] ? rot : pass, t.bf16, turned[k] ? lo : p * kUnit, v[k]);
-                load4(turned[k] ? rot : pass, t.bf16, turned[k] ? hi : p * kUnit + 4, v[k] + 4);
-            }
-            if (u < units && t.norm && (!turned[k] || t.norm_cols > t.pass_units * kUnit))
-#pragma unroll
-                for (int i = 0; i < kUnit; ++i) square = __builtin_fmaf(v[k][i], v[k][i], square);
+    for (; task < a.tasks; task += step) {
+        here = next;
+        if (task + step < a.tasks) {
+            const RowsIn& t = rows_in(task + step);
+            next.load(t, n, (task + step - t.first) * rows + row, at, lanes);
         }
-        float unit = 1.0f;
-        if (t.norm) {
-            for (int m = 1; m < lanes; m <<= 1) square += __shfl_xor(square, m);
-            unit = 1.0f / sqrtf(square / (float)t.norm_cols + a.eps);
-        }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (at + k * lanes >= units) continue;
-            if (t.norm && (!turned[k] || t.norm_cols > t.pass_units * kUnit)) {
-                // weights of the whole row by its columns, of the pass part alone by that part's
-                const int off = t.norm_cols > t.pass_units * kUnit || !t.rot_first ? 0 : rot_cols;
-                float w[kUnit];
-                load4((const char*)t.norm, true, col[k][0] - off, w);
-                load4((const char*)t.norm, true, col[k][1] - off, w + 4);
-#pragma unroll
-                for (int i = 0; i < kUnit; ++i) v[k][i] = v[k][i] * unit * w[i];
-            }
-            if (turned[k]) {
-                const int pair = (at + k * lanes - first) * 4;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float c = turn[0][pair + i], s = turn[1][pair + i];
-                    float& x = v[k][INTERLEAVED ? 2 * i : i];
-                    float& y = v[k][INTERLEAVED ? 2 * i + 1 : i + 4];
-                    const float x0 = x, y0 = y;
-                    x = x0 * c - y0 * s;
-                    y = x0 * s + y0 * c;
-                }
-            }
-            store4(out, t, col[k][0], v[k]);
-            store4(out, t, col[k][1], v[k] + 4);
-        }
+        const RowsIn& t = rows_in(task);
+        const bool is_q = task < a.in[1].first;
+        if (!is_q && !stored) continue;
+        char* const out = t.out + (is_q ? n * t.out_slot : page * t.out_page + in_page * t.out_slot);
+        here.finish(t, out, (task - t.first) * rows + row, at, lanes, a.eps, turn);
     }
 }
 
@@ -272,10 +315,9 @@ extern "C" int fp8blk_rope_append(const fp8blk_rope* rope, const int32_t* positi
         const int rot_units = i < 2 ? (int)(rope->rot / kUnit) : 0;
         a.in[i] = {(const char*)h.pass, (const char*)h.rot, h.pass_token * size, h.pass_head * size, h.rot_token * size,
                    h.rot_head * size, h.norm, nullptr, 0, 0, 0, (int32_t)h.heads, (int32_t)(h.pass_cols / kUnit), rot_units,
-                   (int32_t)h.norm_cols, h.type == FP8BLK_BF16, 0, rope->rot_first != 0, 1.0f};
+                   (int32_t)h.norm_cols, 0, h.type == FP8BLK_BF16, 0, rope->rot_first != 0, 1.0f};
         const int64_t units = h.pass_cols / kUnit + rot_units;
         most = units > most ? units : most;
-        a.rows += (int32_t)h.heads;
     }
     struct Span {
         const void* p;
@@ -334,9 +376,12 @@ extern "C" int fp8blk_rope_append(const fp8blk_rope* rope, const int32_t* positi
     a.mscale = rope->mscale;
     a.eps = eps;
     while (a.lanes_log2 < 6 && (1 << a.lanes_log2) < most) ++a.lanes_log2;
-    const int rows_at_once = kThreads >> a.lanes_log2;
-    const int64_t turns = ceil_div(a.rows, rows_at_once);
-    const dim3 grid((unsigned)N, (unsigned)(N >= 256 ? 1 : turns));
+    for (RowsIn& t : a.in) {
+        t.first = a.tasks;
+        a.tasks += (t.heads + (64 >> a.lanes_log2) - 1) >> (6 - a.lanes_log2);
+    }
+    // Few tokens: a workgroup for 4 tasks, many: one for all of a token's.
+    const dim3 grid((unsigned)N, (unsigned)(N >= 256 ? 1 : ceil_div(a.tasks, 4)));
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     (void)hipGetLastError();
     if (most <= 64) launch<1>(a, rope->interleaved != 0, grid, s);
