@@ -359,34 +359,48 @@ __global__ __launch_bounds__(256, (ChunkLds<DK, DV, ONE>::kBytes <= 80 * 1024 ? 
     if (lane == 0) ((int*)lds)[wave] = odd;
     __syncthreads();
     odd = ((const int*)lds)[0] | ((const int*)lds)[1] | ((const int*)lds)[2] | ((const int*)lds)[3];
-    // Lanes of the two halves exchange columns, so that each has 8 in a row.
-    run.l = bfly32(run.l);
-    if (w0 + (lane & 31) >= rows) return;
-    const float factor = out_factor(a, head, run.m, run.l);
-    char* const out = a.out + (seq.first + token) * a.out_token + head * a.out_head;
-    const int64_t part = partial(a, s, token, head, c);
+    __syncthreads();
+    // Outputs through LDS, so that a row is written in one piece: a wave's lie as rows of
+    // DV floats, 16 bytes at chunk ^ (row % 8). Lane r knows where row r % 32 goes.
+    static_assert(4 * kTile * DV * 4 <= 2 * (L::kK + L::kV), "outputs take the place of the tiles");
+    char* const o_lds = lds + wave * kTile * DV * 4;
 #pragma unroll
     for (int t = 0; t < DV / 32; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const auto r = __builtin_amdgcn_permlane32_swap(as_u32(o[t][4 * j + i]), as_u32(o[t][4 * j + 4 + i]), false, false);
-                v[i] = as_f32(r[0]), v[4 + i] = as_f32(r[1]);
-            }
-            const int col = 32 * t + 8 * j + 8 * (lane >> 5);
-            if (odd)
-                add_not_finite<L::kKeys>(a, s, v_base, E4M3, col, split.lo, lo, hi, all_lo, all_hi, own_lo, own_hi, v);
-            if (split.n > 1) {
-                float* p = a.ws + part * DV + col;
-                *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
-                *(float4*)(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-            } else {
-                write_out(out + 2 * col, v, factor);
-            }
+        for (int j = 0; j < 4; ++j)
+            *(float4*)(o_lds + (lane & 31) * DV * 4 + (((8 * t + 2 * j + (lane >> 5)) ^ (lane & 7)) << 4)) =
+                make_float4(o[t][4 * j], o[t][4 * j + 1], o[t][4 * j + 2], o[t][4 * j + 3]);
+    run.l = bfly32(run.l);
+    float factor = 1.0f;
+    char* to;
+    if (split.n > 1) {
+        const int64_t part = partial(a, s, token, head, c);
+        to = (char*)(a.ws + part * DV);
+        if (lane < 32 && w0 + lane < rows) *(float2*)(partial_ml(a, DV) + 2 * part) = make_float2(run.m, run.l);
+    } else {
+        to = a.out + (seq.first + token) * a.out_token + head * a.out_head;
+        factor = out_factor(a, head, run.m, run.l);
+    }
+    constexpr int kOnes = DV / 8;  // lanes a row
+#pragma unroll 4
+    for (int k = 0; k < kTile; k += 64 / kOnes) {
+        const int r = k + lane / kOnes, d = lane % kOnes;
+        char* const row = (char*)of_row((int64_t)to, r);
+        const float f = __shfl(factor, r);
+        const int row_lo = __shfl(own_lo, r), row_hi = __shfl(own_hi, r);
+        if (w0 + r >= rows) continue;
+        const char* const p = o_lds + r * DV * 4;
+        const float4 x = *(const float4*)(p + (((2 * d) ^ (r & 7)) << 4)), y = *(const float4*)(p + (((2 * d + 1) ^ (r & 7)) << 4));
+        float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        if (odd)
+            add_not_finite<L::kKeys>(a, s, v_base, E4M3, 8 * d, split.lo, lo, hi, all_lo, all_hi, row_lo, row_hi, v);
+        if (split.n > 1) {
+            *(float4*)(row + 32 * d) = make_float4(v[0], v[1], v[2], v[3]);
+            *(float4*)(row + 32 * d + 16) = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            write_out(row + 16 * d, v, f);
         }
-    if (split.n > 1 && lane < 32) *(float2*)(partial_ml(a, DV) + 2 * part) = make_float2(run.m, run.l);
+    }
 }
 
 bool attn_sizes_ok(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, int64_t max_len, int64_t window) {

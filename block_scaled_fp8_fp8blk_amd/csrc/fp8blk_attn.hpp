@@ -426,47 +426,50 @@ __device__ __forceinline__ void weights_operand(const v16f& z, v8bf (&p)[2]) {
     for (int i = 0; i < 16; ++i) p[i >> 3][i & 7] = (__bf16)z[i];
 }
 
-// Joins the splits of a row and head: a workgroup for 128 columns of a row, kOnes
-// threads of 8 columns for every kWays-th chunk of keys, which they add in order; then
-// those sums, in order. Which chunks go together depends on the keys alone.
-template <int DV>
+// Joins the splits of rows and heads: kOnes threads of 8 columns of a row for every
+// WAYS-th chunk of its keys, which they add in order; then those sums, in order. Which
+// chunks go together depends on the keys alone.
+template <int DV, int WAYS>
 static __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-    constexpr int kCols = DV < 128 ? DV : 128, kOnes = kCols / 8, kWays = 256 / kOnes;
-    __shared__ __attribute__((aligned(16))) float sums[kWays][kCols];
-    __shared__ float weights[kWays];
-    const int head = blockIdx.x % a.heads, i = blockIdx.x / a.heads % a.max_new, s = blockIdx.x / a.heads / a.max_new;
+    constexpr int kCols = DV < 128 ? DV : 128, kOnes = kCols / 8, kRows = 256 / kOnes / WAYS;
+    static_assert(kOnes * WAYS % 64 == 0, "a wave for a row, or for a part of one");
+    __shared__ __attribute__((aligned(16))) float sums[kRows][WAYS][kCols];
+    __shared__ float weights[kRows][WAYS];
+    const int one = threadIdx.x % kOnes, way = threadIdx.x / kOnes % WAYS, r = threadIdx.x / (kOnes * WAYS);
+    const int64_t id = (int64_t)blockIdx.x * kRows + r;
+    const int head = (int)(id % a.heads), i = (int)(id / a.heads % a.max_new), s = (int)min(id / a.heads / a.max_new, (int64_t)a.seqs - 1);
     const Seq seq = sequence(a, s);
-    if (i >= seq.rows) return;
     const Split split = split_of(a, seq, 0);
-    if (split.n <= 1) return;
-    const int col = blockIdx.y * kCols + threadIdx.x % kOnes * 8, way = threadIdx.x / kOnes;
+    const bool there = id < (int64_t)a.seqs * a.max_new * a.heads && i < seq.rows && split.n > 1;
+    const int col = blockIdx.y * kCols + one * 8;
     const int64_t at = partial(a, s, i, head, 0);
     const float2* ml = (const float2*)partial_ml(a, DV) + at;
     const float* part = a.ws + at * DV + col;
-    float top = -INFINITY;
-    for (int c = threadIdx.x & 63; c < split.n; c += 64) top = fmaxf(top, ml[c].x);
-    for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
-    const float base = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f, v[8] = {};
+    float top = -INFINITY, sum = 0.0f, v[8] = {};
+    if (there) {
+        for (int c = threadIdx.x & 63; c < split.n; c += 64) top = fmaxf(top, ml[c].x);  // a wave has one row's threads
+        for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
+        const float base = top == -INFINITY ? 0.0f : top;
 #pragma unroll 4
-    for (int c = (way - split.lo / a.chunk) & (kWays - 1); c < split.n; c += kWays) {
-        const float2 t = ml[c];
-        const float4 x = *(const float4*)(part + (int64_t)c * DV), y = *(const float4*)(part + (int64_t)c * DV + 4);
-        const float f = exp2_fast(t.x - base);
-        sum = __builtin_fmaf(f, t.y, sum);
-        const float e[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        for (int c = (way - split.lo / a.chunk) & (WAYS - 1); c < split.n; c += WAYS) {
+            const float2 t = ml[c];
+            const float4 x = *(const float4*)(part + (int64_t)c * DV), y = *(const float4*)(part + (int64_t)c * DV + 4);
+            const float f = exp2_fast(t.x - base);
+            sum = __builtin_fmaf(f, t.y, sum);
+            const float e[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = __builtin_fmaf(f, e[k], v[k]);
+            for (int k = 0; k < 8; ++k) v[k] = __builtin_fmaf(f, e[k], v[k]);
+        }
     }
-    float* const mine = &sums[way][threadIdx.x % kOnes * 8];
+    float* const mine = &sums[r][way][one * 8];
     *(float4*)mine = make_float4(v[0], v[1], v[2], v[3]);
     *(float4*)(mine + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    if (threadIdx.x % kOnes == 0) weights[way] = sum;
+    if (one == 0) weights[r][way] = sum;
     __syncthreads();
-    if (way > 0) return;
+    if (way > 0 || !there) return;
 #pragma unroll 4
-    for (int w = 1; w < kWays; ++w) {
-        sum += weights[w];
+    for (int w = 1; w < WAYS; ++w) {
+        sum += weights[r][w];
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] += mine[w * kCols + k];
     }
@@ -476,7 +479,10 @@ static __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 template <int DV>
 void launch_join(const AttnArgs& a, hipStream_t s) {
     if (a.splits < 2) return;
-    k_attn_join<DV><<<dim3((unsigned)((int64_t)a.seqs * a.max_new * a.heads), DV < 128 ? 1 : DV / 128), 256, 0, s>>>(a);
+    constexpr int kAll = DV < 128 ? 32 : 16, kBlocks = DV < 128 ? 1 : DV / 128;
+    const int64_t rows = (int64_t)a.seqs * a.max_new * a.heads;
+    if (a.splits <= kAll / 4) k_attn_join<DV, kAll / 4><<<dim3((unsigned)ceil_div(rows, 4), kBlocks), 256, 0, s>>>(a);
+    else k_attn_join<DV, kAll><<<dim3((unsigned)rows, kBlocks), 256, 0, s>>>(a);
 }
 
 // A grid of units (splits of a key head's keys) and their row tiles: workgroup b runs
