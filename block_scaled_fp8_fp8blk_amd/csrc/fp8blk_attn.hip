@@ -216,23 +216,26 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
 
 // --- many rows: a prompt's chunk ------------------------------------------------------
 //
-// Four waves of 32 rows share tiles of KEYS keys, which they load together, the next
-// one while this one is worked on; one barrier a tile. Bound by the matrix cores,
-// their operands from LDS and the softmax between them, for which a compute unit
-// holds two waves a SIMD where registers and LDS allow.
-template <int DK, int DV, bool ONE>
+// Four waves of 32 rows share tiles of 64 keys, which they load together, the next one
+// while this one is worked on; one barrier a tile. Bound by the matrix cores, their
+// operands from LDS and the softmax between them, which only another wave on the SIMD
+// hides: two workgroups a compute unit, or, with HALVES 2 (where registers or the number
+// of workgroups leave one), eight waves, of which two share 32 rows, each 32 keys of a
+// tile with maximum, sum and outputs of its own, joined at the end.
+template <int DK, int DV, bool ONE, int HALVES>
 struct ChunkLds {
-    static constexpr int kKeys = 64, kTiles = kKeys / kTile, kRows = kKeys / 4;
+    static constexpr int kKeys = 64, kTiles = kKeys / kTile / HALVES, kWaves = 4 * HALVES, kRows = kKeys / kWaves;
     static constexpr int kK = kKeys * DK * 2, kV = kKeys * DV * 2;
     // ONE leaves nothing to say to other waves: with heads of 192 and 128 two workgroups
     // take all 160 KB
-    static constexpr int kSaid = 2 * (kK + kV), kBytes = kSaid + (ONE ? 0 : 32);
+    static constexpr int kSaid = 2 * (kK + kV), kJoin = kSaid + (ONE ? 0 : 8 * kWaves);
+    static constexpr int kBytes = kJoin + (HALVES == 2 ? 4 * 64 * 8 : 0);
 };
 constexpr int kChunkRows = 4 * kTile;
 
-template <int DK, int DV, bool E4M3, bool ONE>
-__global__ __launch_bounds__(256, (ChunkLds<DK, DV, ONE>::kBytes <= 80 * 1024 ? 2 : 1)) void k_attn_chunk(AttnArgs a, int row_tiles, int units, int spread) {
-    using L = ChunkLds<DK, DV, ONE>;
+template <int DK, int DV, bool E4M3, bool ONE, int HALVES>
+__global__ __launch_bounds__(256 * HALVES, (HALVES == 2 || ChunkLds<DK, DV, ONE, HALVES>::kBytes <= 80 * 1024 ? 2 : 1)) void k_attn_chunk(AttnArgs a, int row_tiles, int units, int spread) {
+    using L = ChunkLds<DK, DV, ONE, HALVES>;
     __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
     // Workgroup b runs on XCD b % 8: a unit's row tiles, which read the same keys, on
     // `spread` XCDs, those with the most keys first.
@@ -248,7 +251,7 @@ __global__ __launch_bounds__(256, (ChunkLds<DK, DV, ONE>::kBytes <= 80 * 1024 ? 
     if (c > 0 && c >= split.n) return;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int w0 = r0 + wave * kTile, q_row = min(w0 + (lane & 31), rows - 1);
+    const int half = wave >> 2, w0 = r0 + (wave & 3) * kTile, q_row = min(w0 + (lane & 31), rows - 1);
     const int token = q_row / a.group, head = kv * a.group + q_row % a.group;
     // positions of the first and last row of the workgroup and of the wave
     const int at0 = seq.at + r0 / a.group, at1 = seq.at + (min(r0 + kChunkRows, rows) - 1) / a.group;
@@ -270,23 +273,24 @@ __global__ __launch_bounds__(256, (ChunkLds<DK, DV, ONE>::kBytes <= 80 * 1024 ? 
     constexpr uint32_t kMine = (uint32_t)(((uint64_t)1 << L::kRows) - 1);
     int base = split.lo + (lo - split.lo) / L::kKeys * L::kKeys;
     TileRows<ONE> next;
-    uint32_t held[L::kTiles], held_next[L::kTiles] = {};  // the tile's keys that a page holds (else: what other waves say)
-    int page = 0, parts[4] = {};                          // the next tile's pages: the wave's (or its lanes'); ONE: of each wave
+    uint32_t held[2], held_next[2] = {};  // the tile's keys that a page holds (else: what other waves say)
+    int page = 0, parts[4] = {};         // the next tile's pages: the wave's (or its lanes'); ONE: of each 16 keys
     bool odd = false;
     Codes<E4M3 ? DK : 64, E4M3 ? L::kRows : 16> k_codes;
     Codes<E4M3 ? DV : 64, E4M3 ? L::kRows : 16> v_codes;
+    const int own_part = wave / HALVES;
     const uint32_t lds_at = lds_offset(lds), k_off = load_offset(a.k_slot, lane), v_off = load_offset(a.v_slot, lane);
     auto find = [&](int b) {
         if constexpr (ONE)
 #pragma unroll
-            for (int w = 0; w < 4; ++w) parts[w] = page_at<true>(a, s, b + w * L::kRows, lane);
+            for (int w = 0; w < 4; ++w) parts[w] = page_at<true>(a, s, b + 16 * w, lane);
         else page = page_at<ONE>(a, s, b + mine, lane);
     };
     auto load = [&](int b, int buffer) {  // the tile at b
         if constexpr (ONE) {
-            page = wave < 2 ? wave < 1 ? parts[0] : parts[1] : wave < 3 ? parts[2] : parts[3];
+            page = own_part < 2 ? own_part < 1 ? parts[0] : parts[1] : own_part < 3 ? parts[2] : parts[3];
 #pragma unroll
-            for (int t = 0; t < L::kTiles; ++t) {
+            for (int t = 0; t < 2; ++t) {
                 const uint32_t there = ((uint32_t)parts[2 * t] < (uint32_t)a.pages ? 0xffffu : 0u) |
                                        ((uint32_t)parts[2 * t + 1] < (uint32_t)a.pages ? 0xffff0000u : 0u);
                 held_next[t] = there & keys_between(b + t * kTile, lo, hi);
@@ -320,15 +324,19 @@ __global__ __launch_bounds__(256, (ChunkLds<DK, DV, ONE>::kBytes <= 80 * 1024 ? 
         char* const own_v = v_lds + mine * DV * 2;
         if (next.held != kMine) clear_rows<DV, L::kRows>(own_v, next.held, lane);
         if (base < all_lo || base + L::kKeys > all_hi) odd |= make_finite<DV, L::kRows>(own_v, lane);
-        uint32_t* const said = (uint32_t*)(lds + L::kSaid) + 4 * buffer;
+        uint32_t* const said = (uint32_t*)(lds + L::kSaid) + L::kWaves * buffer;
         if (!ONE && lane == 0) said[wave] = next.held;
         __syncthreads();
         if constexpr (ONE) {
 #pragma unroll
-            for (int t = 0; t < L::kTiles; ++t) held[t] = held_next[t];
+            for (int t = 0; t < 2; ++t) held[t] = held_next[t];
         } else {
-            const uint4 h = *(const uint4*)said;
-            held[0] = h.x | h.y << 16, held[1] = h.z | h.w << 16;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                held[t] = 0;
+#pragma unroll
+                for (int w = 0; w < L::kWaves / 2; ++w) held[t] |= said[t * (L::kWaves / 2) + w] << (w * L::kRows);
+            }
         }
         if (base + L::kKeys < hi) load(base + L::kKeys, buffer ^ 1);
         const bool active = base < wave_hi && base + L::kKeys > wave_lo;
@@ -338,8 +346,9 @@ __global__ __launch_bounds__(256, (ChunkLds<DK, DV, ONE>::kBytes <= 80 * 1024 ? 
         bool all = true;
 #pragma unroll
         for (int t = 0; t < L::kTiles; ++t) {
-            z[t] = tile_scores<DK>(k_lds + t * kTile * DK * 2, q, lane);
-            seen[t] = held[t] & keys_between(base + t * kTile, own_lo, own_hi);
+            const int sub = HALVES == 2 ? half : t;
+            z[t] = tile_scores<DK>(k_lds + sub * kTile * DK * 2, q, lane);
+            seen[t] = (sub ? held[1] : held[0]) & keys_between(base + sub * kTile, own_lo, own_hi);
             all = all && seen[t] == ~0u;
         }
         if (!__all(all))
@@ -350,7 +359,7 @@ __global__ __launch_bounds__(256, (ChunkLds<DK, DV, ONE>::kBytes <= 80 * 1024 ? 
         for (int t = 0; t < L::kTiles; ++t) {
             v8bf p[2];
             weights_operand(z[t], p);
-            tile_sums<DV>(v_lds + t * kTile * DV * 2, p, o, lane);
+            tile_sums<DV>(v_lds + (HALVES == 2 ? half : t) * kTile * DV * 2, p, o, lane);
         }
     }
 
@@ -358,12 +367,42 @@ __global__ __launch_bounds__(256, (ChunkLds<DK, DV, ONE>::kBytes <= 80 * 1024 ? 
     __syncthreads();
     if (lane == 0) ((int*)lds)[wave] = odd;
     __syncthreads();
-    odd = ((const int*)lds)[0] | ((const int*)lds)[1] | ((const int*)lds)[2] | ((const int*)lds)[3];
+    odd = false;
+#pragma unroll
+    for (int w = 0; w < L::kWaves; ++w) odd |= ((const int*)lds)[w] != 0;
     __syncthreads();
     // Outputs through LDS, so that a row is written in one piece: a wave's lie as rows of
     // DV floats, 16 bytes at chunk ^ (row % 8). Lane r knows where row r % 32 goes.
     static_assert(4 * kTile * DV * 4 <= 2 * (L::kK + L::kV), "outputs take the place of the tiles");
-    char* const o_lds = lds + wave * kTile * DV * 4;
+    char* const o_lds = lds + (wave & 3) * kTile * DV * 4;
+    if constexpr (HALVES == 2) {
+        float2* const ml = (float2*)(lds + L::kJoin) + 64 * (wave & 3) + lane;
+        if (half) {
+            *ml = make_float2(run.m, run.l);
+#pragma unroll
+            for (int t = 0; t < DV / 32; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *(float4*)(o_lds + (4 * t + j) * 1024 + lane * 16) = make_float4(o[t][4 * j], o[t][4 * j + 1], o[t][4 * j + 2], o[t][4 * j + 3]);
+        }
+        __syncthreads();
+        if (half) return;
+        const float2 other = *ml;
+        const float top = fmaxf(run.m, other.x), at = top == -INFINITY ? 0.0f : top;
+        const float f = exp2_fast(run.m - at), g = exp2_fast(other.x - at);
+        run.m = top;
+        run.l = __builtin_fmaf(g, other.y, f * run.l);
+#pragma unroll
+        for (int t = 0; t < DV / 32; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 x = *(const float4*)(o_lds + (4 * t + j) * 1024 + lane * 16);
+                const float e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[t][4 * j + i] = __builtin_fmaf(g, e[i], f * o[t][4 * j + i]);
+            }
+        wait_reads();
+    }
 #pragma unroll
     for (int t = 0; t < DV / 32; ++t)
 #pragma unroll
@@ -508,13 +547,24 @@ void launch_chunk(const AttnArgs& a, hipStream_t s) {
     const int64_t units = (int64_t)a.seqs * (a.heads / a.group) * a.splits;
     const int64_t tiles = ceil_div((int64_t)a.max_new * a.group, kChunkRows);
     const Deal d = deal(units, tiles);
-    k_attn_chunk<DK, DV, E4M3, ONE><<<d.grid, 256, 0, s>>>(a, (int)tiles, (int)units, d.spread);
+    // Eight waves where one workgroup fits a compute unit anyway (3 sequences of 777
+    // tokens, heads of 256: 101 us, with four waves 127; 2000 tokens of 16 heads of 192
+    // and 128, 256 workgroups: 55, 60), two workgroups of four else (2048 of 8192 tokens,
+    // 512 of them: 266, 318). Heads of 64 gain nothing (512 tokens: 93, 91). Of heads of
+    // 256, e4m3 or in small pages, the registers do not allow for two waves a SIMD.
+    constexpr bool kFits = DV == 256 ? ONE && !E4M3 : DV == 128;
+    if constexpr (kFits)
+        if (DV == 256 || units * tiles <= 256) {
+            k_attn_chunk<DK, DV, E4M3, ONE, 2><<<d.grid, 512, 0, s>>>(a, (int)tiles, (int)units, d.spread);
+            return;
+        }
+    k_attn_chunk<DK, DV, E4M3, ONE, 1><<<d.grid, 256, 0, s>>>(a, (int)tiles, (int)units, d.spread);
 }
 
 template <int DK, int DV, bool E4M3>
 void launch(const AttnArgs& a, bool few, hipStream_t s) {
     if (few) one_page(a, kTile) ? launch_few<DK, DV, E4M3, true>(a, s) : launch_few<DK, DV, E4M3, false>(a, s);
-    else one_page(a, ChunkLds<DK, DV, true>::kRows) ? launch_chunk<DK, DV, E4M3, true>(a, s) : launch_chunk<DK, DV, E4M3, false>(a, s);
+    else one_page(a, 16) ? launch_chunk<DK, DV, E4M3, true>(a, s) : launch_chunk<DK, DV, E4M3, false>(a, s);
     launch_join<DV>(a, s);
 }
 

@@ -65,6 +65,21 @@ def test_long_caches(gpu, k, v, group, e4m3, new):
 
 
 @pytest.mark.parametrize("k,v", WIDTHS, ids=IDS)
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("page", [1, 8, 16, 64])
+def test_chunks_of_long_caches(gpu, k, v, e4m3, page):
+    """Few tiles of rows, their keys split over workgroups; many, which are not; windows that end inside a split; small and large pages."""
+    if e4m3 and v is None:
+        pytest.skip("latent caches are bf16")
+    for lens, new, group, window in (([5001, 700], [40, 17], 8, 0), ([3000], [300], 4, 700), ([1700, 64, 900], [200, 1, 200], 16, 0)):
+        what = f"{k} {v} e4m3 {e4m3} page {page} new {new}"
+        print(what, flush=True)
+        c = _setup(gpu, 16, lens, new, k, v, group, kv=2, page=page, e4m3=e4m3, sinks=window > 0, window=window, behind=1)
+        c.run()
+        c.check(what)
+
+
+@pytest.mark.parametrize("k,v", WIDTHS, ids=IDS)
 @pytest.mark.parametrize("max_new", [1, 5, 80])
 def test_rows_that_see_nothing(gpu, k, v, max_new):
     """No keys at all, more new tokens than keys, pages that are none; with sinks and without."""
@@ -213,11 +228,12 @@ def test_a_cache_past_32_bit_offsets(gpu, k, v, T):
     c.check(f"{k} {T}")
 
 
-@pytest.mark.parametrize("k,v", [(128, 128), (576, None)])
-def test_many_sequences(gpu, k, v):
+@pytest.mark.parametrize("k,v", [(128, 128), (256, 256), (576, None)])
+@pytest.mark.parametrize("T", [1, 30])
+def test_many_sequences(gpu, k, v, T):
     """More sequences than compute units, most without a new token."""
-    lens = [1 + (37 * i) % 150 for i in range(600)]
-    new = [int(i % 3 == 0) for i in range(600)]
+    lens = [max(T, 1 + (37 * i) % 150) for i in range(600)]
+    new = [T * int(i % 3 == 0) for i in range(600)]
     c = _setup(gpu, 13, lens, new, k, v, 4, behind=5)
     c.run()
     c.check("many")
