@@ -525,7 +525,7 @@ Plan plan(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, i
     const int64_t units = seqs * c.heads * (p.few && !latent ? 1 : ceil_div(panel ? group : max_new * group, tile));
     const int64_t step = p.few && !latent ? 4 * kTile : 64;
     int64_t n;
-    if (latent) n = std::min((group <= 16 && panel ? 512 : 256) / units, ceil_div(seen, panel ? 128 : 512));
+    if (latent) n = std::min((group <= 16 && panel ? 512 : 256) / units, ceil_div(seen, panel ? 128 : 256));
     else if (p.few) n = seen <= 512 ? 1 : std::min(std::max(256 / units, units < 512 ? seen / 768 : 1), ceil_div(seen, step));
     else n = std::min(256 / units, ceil_div(seen, 512));
     n = std::max<int64_t>(n, 1);

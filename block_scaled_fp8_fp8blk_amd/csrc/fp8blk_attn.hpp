@@ -5,7 +5,6 @@
 #include <stdint.h>
 
 #include <cmath>
-#include <numeric>
 
 #include "fp8blk.h"
 #include "fp8blk_device.hpp"
@@ -486,15 +485,20 @@ void launch_join(const AttnArgs& a, hipStream_t s) {
 }
 
 // A grid of units (splits of a key head's keys) and their row tiles: workgroup b runs
-// on XCD b % 8, and a unit's row tiles, which read the same keys, on as few XCDs as
-// give each the same number.
+// on XCD b % 8, and a unit's row tiles, which read the same keys, on `spread` XCDs, as
+// few as leave no more than a sixteenth of the places empty (or the fewest).
 struct Deal {
     unsigned grid;
     int spread;
 };
 inline Deal deal(int64_t units, int64_t tiles) {
-    const int64_t spread = 8 / std::gcd(units, (int64_t)8);
-    return {(unsigned)(units * spread * ceil_div(tiles, spread)), (int)spread};
+    Deal best = {};
+    for (int spread = 1; spread <= 8; spread *= 2) {
+        const int64_t grid = 8 * ceil_div(units, 8 / spread) * ceil_div(tiles, spread);
+        if (spread == 1 || grid < best.grid) best = {(unsigned)grid, spread};
+        if (grid * 16 <= units * tiles * 17) break;
+    }
+    return best;
 }
 
 // Latent attention (fp8blk_latent.hip): rows of a workgroup, value columns, and the launch.
