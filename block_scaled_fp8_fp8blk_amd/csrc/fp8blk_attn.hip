@@ -69,7 +69,7 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
     const int xcd = blockIdx.x & 7, turn = blockIdx.x >> 3;
     const int part = turn % parts, unit = turn / parts * 8 + xcd;
     if (unit >= units) return;
-    const int row_tile = part / kv_heads, kv = part % kv_heads, c = unit % a.splits, s = unit / a.splits;
+    const int row_tile = part / kv_heads, kv = part % kv_heads, s = unit / a.splits, c = split_at(a, unit, s);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // Without a window the wave's first tile is known before the sequence is: its pages
     // are asked for at once.
@@ -243,7 +243,7 @@ __global__ __launch_bounds__(256 * HALVES, (HALVES == 2 || ChunkLds<DK, DV, ONE,
     const int unit = turn / per * (8 / spread) + xcd / spread, row_tile = row_tiles - 1 - (turn % per * spread + xcd % spread);
     if (unit >= units || row_tile < 0) return;
     const int kv_heads = a.heads / a.group;
-    const int c = unit % a.splits, kv = unit / a.splits % kv_heads, s = unit / a.splits / kv_heads;
+    const int of = unit / a.splits, c = split_at(a, unit, of), kv = of % kv_heads, s = of / kv_heads;
     const Seq seq = sequence(a, s);
     const int rows = seq.rows * a.group, r0 = row_tile * kChunkRows;
     if (r0 >= rows) return;
@@ -525,9 +525,12 @@ Plan plan(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, i
     const int64_t units = seqs * c.heads * (p.few && !latent ? 1 : ceil_div(panel ? group : max_new * group, tile));
     const int64_t step = p.few && !latent ? 4 * kTile : 64;
     int64_t n;
-    if (latent) n = std::min((group <= 16 && panel ? 512 : 256) / units, ceil_div(seen, panel ? 128 : 256));
-    else if (p.few) n = seen <= 512 ? 1 : std::min(std::max(256 / units, units < 512 ? seen / 768 : 1), ceil_div(seen, step));
-    else n = std::min(256 / units, ceil_div(seen, 512));
+    if (latent) n = std::min((group <= 16 && panel ? 512 : 256) / units, ceil_div(seen, p.few ? 128 : 256));
+    else if (p.few) n = seen <= 512 ? 1 : std::min(std::max(256 / units, units < 512 ? ceil_div(seen, 768) : 1), ceil_div(seen, step));
+    else {
+        n = std::min(256 / units, ceil_div(seen, 512));
+        if (n < 4 && seen >= 5000 && units <= 384 && (seqs > 1 || units < 256)) n = 4;
+    }
     n = std::max<int64_t>(n, 1);
     p.chunk = (int32_t)(ceil_div(ceil_div(seen, n), step) * step);
     p.splits = (int32_t)(ceil_div(seen, p.chunk) + (window > 0 ? 1 : 0));

@@ -38,7 +38,7 @@ __global__ __launch_bounds__(256, (BUFFERS == 1 ? 2 : 1)) void k_latent(AttnArgs
     const int xcd = blockIdx.x & 7, turn = blockIdx.x >> 3, per = (row_tiles + spread - 1) / spread;
     const int unit = turn / per * (8 / spread) + xcd / spread, row_tile = row_tiles - 1 - (turn % per * spread + xcd % spread);
     if (unit >= units || row_tile < 0) return;
-    const int c = unit % a.splits, s = unit / a.splits;
+    const int s = unit / a.splits, c = split_at(a, unit, s);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, mine = wave * kMine;
     // Without a window the first tile is known before the sequence is: its pages are
