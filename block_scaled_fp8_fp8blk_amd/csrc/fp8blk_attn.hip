@@ -445,7 +445,8 @@ __global__ __launch_bounds__(256 * HALVES, (HALVES == 2 || ChunkLds<DK, DV, ONE,
 bool attn_sizes_ok(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, int64_t max_len, int64_t window) {
     constexpr int64_t kMost = INT64_C(1) << 30;
     return heads >= 1 && heads <= FP8BLK_MAX_HEADS && heads % c.heads == 0 && seqs >= 1 && seqs <= FP8BLK_MAX_PANEL &&
-           max_new >= 1 && max_new <= FP8BLK_MAX_PANEL && max_len >= 1 && max_len < kMost && window >= 0 && window < kMost;
+           max_new >= 1 && max_new <= FP8BLK_MAX_PANEL && max_len >= 1 && max_len < kMost && window >= 0 && window < kMost &&
+           seqs * heads * ceil_div(max_new, 128) <= INT64_C(1) << 22;  // a launch has less than 2^32 threads
 }
 
 }  // namespace
@@ -492,6 +493,7 @@ int attn_args(AttnArgs& a, const fp8blk_cache* cache, const uint16_t* q, int64_t
     a.pages = (int32_t)c.pages, a.page_shift = __builtin_ctzll((unsigned long long)c.page_size);
     a.max_new = (int32_t)b.max_new, a.window = (int32_t)window, a.causal = causal != 0;
     a.z_scale = std::fabs(scale) * c.k_scale * kLog2e;
+    if (std::isinf(a.z_scale)) return FP8BLK_ERR_ARG;
     a.q_and = a.z_scale > 0.0f ? ~0u : 0u;
     a.q_xor = a.z_scale > 0.0f && scale < 0.0f ? 0x80008000u : 0u;
     if (!(a.z_scale > 0.0f)) a.z_scale = 1.0f;
@@ -526,7 +528,7 @@ Plan plan(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, i
     const int64_t step = p.few && !latent ? 4 * kTile : 64;
     int64_t n;
     if (latent) n = std::min((group <= 16 && panel ? 512 : 256) / units, ceil_div(seen, p.few ? 128 : 256));
-    else if (p.few) n = seen <= 512 ? 1 : std::min(std::max(256 / units, units < 512 ? ceil_div(seen, 768) : 1), ceil_div(seen, step));
+    else if (p.few) n = seen <= 512 ? 1 : std::min(std::max(256 / units, units < 512 ? std::min(ceil_div(seen, 768), 16384 / units) : 1), ceil_div(seen, step));
     else {
         n = std::min(256 / units, ceil_div(seen, 512));
         if (n < 4 && seen >= 5000 && units <= 384 && (seqs > 1 || units < 256)) n = 4;

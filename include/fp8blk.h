@@ -943,21 +943,24 @@ int fp8blk_rope_append(const fp8blk_rope *rope, const int32_t *positions, int64_
  *     and a head stride in values (multiples of 8; out's at least v_cols);
  *     device, 16-byte aligned. out overlaps neither q nor the cache (else
  *     FP8BLK_ERR_ARG, for the span from first to last byte). heads: a multiple of
- *     the cache's, up to FP8BLK_MAX_HEADS; scale finite.
+ *     the cache's, up to FP8BLK_MAX_HEADS; scale, and scale * k_scale, finite and
+ *     below 2^127 (scores are f32).
  *   fp8blk_paged_attn: a cache with v of k_cols, v_cols = 64, 64; 128, 128; 192,
  *     128 or 256, 256, bf16 or e4m3 (with heads = cache heads and 192, 128 this is
  *     latent attention in its expanded form).
  *   fp8blk_latent_attn: a latent cache (v NULL), bf16, one head, v_cols 512 and
  *     k_cols 512 or 576 (latent attention in its absorbed form).
  *   1 <= N, seqs, max_new, max_pages <= FP8BLK_MAX_PANEL (max_pages: 2^30);
- *   1 <= max_len < 2^30; 0 <= window < 2^30.
+ *   1 <= max_len < 2^30 (lens past 2^30 count as 2^30); 0 <= window < 2^30;
+ *   seqs * heads * ceil(max_new / 128) <= 2^22.
  *   ws: device, 256-byte aligned, >= fp8blk_attn_bytes(...) bytes (0: none needed,
  *     or bad sizes; ws may then be NULL); its contents on entry do not matter.
- * Sums and the softmax's statistics are f32, the weights exp(z - max) are rounded
- * to bf16 for their product with v (the sum below them is of the unrounded ones).
- * With max_new <= FP8BLK_MAX_M a row's bits depend on its own sequence up to its
- * position, on seqs, max_len, window and the heads, and on nothing else: the rows of a
- * verify panel equal those of single-token calls, bit for bit.
+ * Sums and the softmax's statistics are f32, the weights (exp of z less a value
+ * near the row's maximum) are rounded to bf16 for their product with v; the sum below
+ * them is of the unrounded ones. With max_new <= FP8BLK_MAX_M a row's bits depend on
+ * what it sees, on seqs, max_len, window and the heads, and on nothing else: causal,
+ * the rows of a verify panel equal those of single-token calls, bit for bit. The same
+ * call gives the same bits each time, whatever max_new is.
  * Enqueued on `stream`; does not wait.
  */
 typedef struct fp8blk_batch {

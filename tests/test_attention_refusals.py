@@ -115,7 +115,8 @@ def attn(lib, latent=False, c=None, q=P + 2 * S, q_strides=(1024, 128), N=4, hea
     dict(sinks=P + 2), dict(batch=dict(table=None)), dict(batch=dict(lens=None)), dict(batch=dict(starts=None)), dict(batch=dict(table=P + 1)),
     dict(batch=dict(lens=P + 2)), dict(batch=dict(starts=P + 3)), dict(batch=dict(seqs=0)), dict(batch=dict(seqs=fb.MAX_PANEL + 1)),
     dict(batch=dict(max_pages=0)), dict(batch=dict(max_pages=(1 << 30) + 1)), dict(batch=dict(max_new=0)), dict(batch=dict(max_new=fb.MAX_PANEL + 1)),
-    dict(batch=dict(max_len=0)), dict(batch=dict(max_len=1 << 30)),
+    dict(batch=dict(max_len=0)), dict(batch=dict(max_len=1 << 30)), dict(scale=-3e38), dict(batch=dict(seqs=1 << 16, max_new=1025)),
+    dict(batch=dict(seqs=1 << 15, max_new=1 << 16), heads=64), dict(N=1 << 16, heads=1024, batch=dict(seqs=4097)),
     # out over q, the cache and the batch
     dict(out=P + 2 * S), dict(out=P + 2 * S + 48), dict(out=P), dict(out=P + 4 * S), dict(out=P + 5 * S), dict(out=P + 6 * S),
     dict(sinks=P + 3 * S + 16)] + [dict(c=b) for b in BAD_CACHES if "v" not in b and not any(k.startswith("v_") for k in b)])
@@ -126,7 +127,7 @@ def test_attention_refusals(lib, latent, kw):
 @pytest.mark.parametrize("kw", [
     dict(heads=7), dict(c=dict(v=None)), dict(c=dict(v=P + S + 8)), dict(out=P + S), dict(c=dict(k_cols=64, v_cols=128)), dict(c=dict(v_cols=64)),
     dict(c=dict(k_cols=96, v_cols=96)), dict(c=dict(k_cols=512, v_cols=512, k_head=512, k_slot=1024, v_head=512, v_slot=1024)),
-    dict(c=dict(k_cols=128, v_cols=128, v_slot=112))])
+    dict(c=dict(k_cols=128, v_cols=128, v_slot=112)), dict(c=dict(type=2, k_scale=2.0 ** 90), scale=2.0 ** 40)])
 def test_paged_attention_refusals(lib, kw):
     assert attn(lib, **kw) == fb.ERR_ARG
 
@@ -136,6 +137,25 @@ def test_paged_attention_refusals(lib, kw):
     dict(c=dict(k_cols=544)), dict(c=dict(v_cols=592)), dict(c=dict(k_cols=640, k_slot=640, k_head=640, k_page=10240))])
 def test_latent_attention_refusals(lib, kw):
     assert attn(lib, True, **kw) == fb.ERR_ARG
+
+
+def test_workspace(lib):
+    """attn_bytes is 0 for sizes that the call refuses, and one byte less than it
+    asks for, or none, is refused; the longest caches ask for no more splits than
+    a launch has room for."""
+    def need(latent=False, heads=8, seqs=2, max_new=2, max_len=100000, window=0):
+        base = dict(v=None, heads=1, k_cols=576, v_cols=512, k_page=16 * 576, k_slot=576, k_head=576) if latent else {}
+        return lib.fp8blk_attn_bytes(ctypes.byref(cache(**base)), heads, seqs, max_new, max_len, window)
+    for latent in (False, True):
+        n = need(latent)
+        assert n > 0
+        long = dict(batch=dict(max_len=100000))
+        assert attn(lib, latent, wsb=n - 1, **long) == attn(lib, latent, ws=None, **long) == attn(lib, latent, ws=P + 8 * S + 128, **long) == fb.ERR_WORKSPACE
+        assert need(latent, seqs=1 << 16, heads=128) == need(latent, seqs=0) == need(latent, max_len=1 << 30) == 0
+        cols = 514 if latent else 130
+        for seqs in (1, 100, 255):  # rows of the join's launch, and splits of f32 sums
+            n = need(latent, seqs=seqs, max_new=16, max_len=(1 << 30) - 1)
+            assert n % (seqs * 16 * 8 * cols * 4) == 0 and seqs * n // (seqs * 16 * 8 * cols * 4) <= 1 << 15
 
 
 U8, F32, BF, I32 = torch.uint8, torch.float32, torch.bfloat16, torch.int32
