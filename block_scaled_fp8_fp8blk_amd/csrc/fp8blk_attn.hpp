@@ -87,10 +87,12 @@ __device__ __forceinline__ Split split_of(const AttnArgs& a, const Seq& s, int c
 
 // The split that a unit works on, `of` being what it is a split of. Units go round the
 // XCDs, and a short sequence's last splits are empty: the splits of each next one begin
-// one further, and one more each time round, or an even number of splits left all the
-// work to some of the XCDs (3 sequences of 500 new tokens, 16 heads over 4, up to 6000
-// keys in 4 splits: 68 us, without 100).
-__device__ __forceinline__ int split_at(const AttnArgs& a, int unit, int of) { return (unit + of + of * a.splits / 8) % a.splits; }
+// one further (of less than 8 splits, one more each time round), or a number of them that
+// shares a factor with the 8 XCDs left all the work to some of those (3 sequences of 500
+// new tokens, 16 heads over 4, up to 6000 keys in 4 splits: 68 us, without 100).
+__device__ __forceinline__ int split_at(const AttnArgs& a, int unit, int of) {
+    return (unit + of + (a.splits < 8 ? of * a.splits / 8 : 0)) % a.splits;
+}
 
 // Split c's unnormalised sums, maximum and sum of weights of a row and head.
 __device__ __forceinline__ int64_t partial(const AttnArgs& a, int s, int i, int head, int c) {
