@@ -216,26 +216,31 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
 
 // --- many rows: a prompt's chunk ------------------------------------------------------
 //
-// Four waves of 32 rows share tiles of 64 keys, which they load together, the next one
-// while this one is worked on; one barrier a tile. Bound by the matrix cores, their
-// operands from LDS and the softmax between them, which only another wave on the SIMD
-// hides: two workgroups a compute unit, or, with HALVES 2 (where registers or the number
-// of workgroups leave one), eight waves, of which two share 32 rows, each 32 keys of a
-// tile with maximum, sum and outputs of its own, joined at the end.
-template <int DK, int DV, bool ONE, int HALVES>
+// GROUPS of 32 rows share tiles of 64 keys, which their waves load together, the next
+// one while this one is worked on; one barrier a tile. With HALVES 2 two waves share 32
+// rows, each 32 keys of a tile with maximum, sum and outputs of its own, joined at the
+// end. Bound by the matrix cores, their operands from LDS (a quarter of a tile's 4800
+// cycles each), the softmax between them and the barrier; only another wave on the SIMD
+// hides one behind the other. 2048 new tokens of 8192, 32 heads of 128 over 4: 256 us,
+// 940 TFLOP/s of the 1290 that a large matrix product reaches. Tiles of 64 keys, not
+// 32: half the barriers (heads of 192 and 128, 73 -> 59 us). A third buffer gave nothing.
+template <int DK, int DV, bool ONE, int GROUPS, int HALVES>
 struct ChunkLds {
-    static constexpr int kKeys = 64, kTiles = kKeys / kTile / HALVES, kWaves = 4 * HALVES, kRows = kKeys / kWaves;
+    static constexpr int kKeys = 64, kTiles = kKeys / kTile / HALVES, kWaves = GROUPS * HALVES, kRows = kKeys / kWaves;
     static constexpr int kK = kKeys * DK * 2, kV = kKeys * DV * 2;
     // ONE leaves nothing to say to other waves: with heads of 192 and 128 two workgroups
     // take all 160 KB
-    static constexpr int kSaid = 2 * (kK + kV), kJoin = kSaid + (ONE ? 0 : 8 * kWaves);
-    static constexpr int kBytes = kJoin + (HALVES == 2 ? 4 * 64 * 8 : 0);
+    static constexpr int kOut = GROUPS * kTile * DV * 4;  // outputs, where the tiles were
+    static constexpr int kSaid = 2 * (kK + kV), kEnd = kSaid + (ONE ? 0 : 8 * kWaves), kStates = HALVES == 2 ? GROUPS * 64 * 8 : 0;
+    static constexpr int kJoin = kOut + kStates <= kSaid ? kOut : kEnd;
+    static constexpr int kBytes = kJoin == kEnd ? kEnd + kStates : kEnd;
 };
 constexpr int kChunkRows = 4 * kTile;
 
-template <int DK, int DV, bool E4M3, bool ONE, int HALVES>
-__global__ __launch_bounds__(256 * HALVES, (HALVES == 2 || ChunkLds<DK, DV, ONE, HALVES>::kBytes <= 80 * 1024 ? 2 : 1)) void k_attn_chunk(AttnArgs a, int row_tiles, int units, int spread, bool pairs) {
-    using L = ChunkLds<DK, DV, ONE, HALVES>;
+template <int DK, int DV, bool E4M3, bool ONE, int GROUPS, int HALVES>
+__global__ __launch_bounds__(64 * GROUPS * HALVES, (GROUPS * HALVES == 8 || ChunkLds<DK, DV, ONE, GROUPS, HALVES>::kBytes <= 80 * 1024 ? 2 : 1)) void k_attn_chunk(AttnArgs a, int row_tiles, int units, int spread, bool pairs) {
+    using L = ChunkLds<DK, DV, ONE, GROUPS, HALVES>;
+    constexpr int kMost = GROUPS * kTile;
     __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
     // Workgroup b runs on XCD b % 8: a unit's row tiles, which read the same keys, on
     // `spread` XCDs, those with the most keys first. pairs: all units' longest tiles
@@ -252,16 +257,16 @@ __global__ __launch_bounds__(256 * HALVES, (HALVES == 2 || ChunkLds<DK, DV, ONE,
     const int kv_heads = a.heads / a.group;
     const int of = unit / a.splits, c = split_at(a, unit, of), kv = of % kv_heads, s = of / kv_heads;
     const Seq seq = sequence(a, s);
-    const int rows = seq.rows * a.group, r0 = row_tile * kChunkRows;
+    const int rows = seq.rows * a.group, r0 = row_tile * kMost;
     if (r0 >= rows) return;
     const Split split = split_of(a, seq, c);
     if (c > 0 && c >= split.n) return;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int half = wave >> 2, w0 = r0 + (wave & 3) * kTile, q_row = min(w0 + (lane & 31), rows - 1);
+    const int half = wave / GROUPS, w0 = r0 + wave % GROUPS * kTile, q_row = min(w0 + (lane & 31), rows - 1);
     const int token = q_row / a.group, head = kv * a.group + q_row % a.group;
     // positions of the first and last row of the workgroup and of the wave
-    const int at0 = seq.at + r0 / a.group, at1 = seq.at + (min(r0 + kChunkRows, rows) - 1) / a.group;
+    const int at0 = seq.at + r0 / a.group, at1 = seq.at + (min(r0 + kMost, rows) - 1) / a.group;
     const int wave0 = seq.at + min(w0, rows - 1) / a.group, wave1 = seq.at + min(w0 + kTile - 1, rows - 1) / a.group;
     const int lo = max(split.lo, first_key(a, at0)), hi = min(split.hi, end_key(a, seq, at1));
     const int all_lo = first_key(a, at1), all_hi = end_key(a, seq, at0);
@@ -285,7 +290,7 @@ __global__ __launch_bounds__(256 * HALVES, (HALVES == 2 || ChunkLds<DK, DV, ONE,
     bool odd = false;
     Codes<E4M3 ? DK : 64, E4M3 ? L::kRows : 16> k_codes;
     Codes<E4M3 ? DV : 64, E4M3 ? L::kRows : 16> v_codes;
-    const int own_part = wave / HALVES;
+    const int own_part = mine / 16;
     const uint32_t lds_at = lds_offset(lds), k_off = load_offset(a.k_slot, lane), v_off = load_offset(a.v_slot, lane);
     auto find = [&](int b) {
         if constexpr (ONE)
@@ -380,10 +385,10 @@ __global__ __launch_bounds__(256 * HALVES, (HALVES == 2 || ChunkLds<DK, DV, ONE,
     __syncthreads();
     // Outputs through LDS, so that a row is written in one piece: a wave's lie as rows of
     // DV floats, 16 bytes at chunk ^ (row % 8). Lane r knows where row r % 32 goes.
-    static_assert(4 * kTile * DV * 4 <= 2 * (L::kK + L::kV), "outputs take the place of the tiles");
-    char* const o_lds = lds + (wave & 3) * kTile * DV * 4;
+    static_assert(L::kOut <= 2 * (L::kK + L::kV), "outputs take the place of the tiles");
+    char* const o_lds = lds + wave % GROUPS * kTile * DV * 4;
     if constexpr (HALVES == 2) {
-        float2* const ml = (float2*)(lds + L::kJoin) + 64 * (wave & 3) + lane;
+        float2* const ml = (float2*)(lds + L::kJoin) + 64 * (wave % GROUPS) + lane;
         if (half) {
             *ml = make_float2(run.m, run.l);
 #pragma unroll
@@ -537,8 +542,21 @@ Plan plan(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, i
     if (latent) n = std::min((group <= 16 && panel ? 512 : 256) / units, ceil_div(seen, p.few ? 128 : 256));
     else if (p.few) n = seen <= 512 ? 1 : std::min(std::max(256 / units, units < 512 ? std::min(ceil_div(seen, 768), 16384 / units) : 1), ceil_div(seen, step));
     else {
-        n = std::min(256 / units, ceil_div(seen, 512));
-        if (n < 4 && seen >= 5000 && units <= 384 && (seqs > 1 || units < 256)) n = 4;
+        // A tile of 64 keys takes a workgroup 1.1 us, each split of a row writes and reads
+        // 8 bytes a column: n^2 splits are best where n^2 * rows * columns is some
+        // thousand times the keys (causal rows see max_new / 2 less; of sequences of
+        // different lengths fewer splits hold keys). Up to `fill` they only use idle
+        // compute units; more have to be twice as many, at least 4 and not past `most`.
+        // 500 new tokens of 3000, 32 heads over 4: 49 us in 4 splits, 53 in 2, 58 in one;
+        // 3 sequences of 500 of up to 6000, 16 heads: 68 in 4, 107 in one (alike long ones:
+        // 118, 128); 1000 of 1000, 16 heads: 25 in one, 33 in 2.
+        const int64_t fill = std::max<int64_t>(256 / units, 1), room = seqs > 1 ? 384 : 255;
+        const int64_t most = units <= room ? std::max<int64_t>((seqs > 1 ? 1024 : 512) / units, 4) : 1;
+        const double best = (seqs > 1 ? 18000.0 : 7500.0) * (double)std::max<int64_t>(seen - max_new / 2, 1) / ((double)seqs * max_new * heads * c.v_cols);
+        for (n = 1; 2 * n * n <= best; n *= 2) {
+        }
+        n = std::min(n, ceil_div(seen, 128));
+        while (n > fill && (n > most || n < 4 || n < 2 * fill)) n = std::max(n / 2, fill);
     }
     n = std::max<int64_t>(n, 1);
     p.chunk = (int32_t)(ceil_div(ceil_div(seen, n), step) * step);
@@ -559,22 +577,29 @@ void launch_chunk(const AttnArgs& a, hipStream_t s) {
     const int64_t units = (int64_t)a.seqs * (a.heads / a.group) * a.splits;
     const int64_t tiles = ceil_div((int64_t)a.max_new * a.group, kChunkRows);
     const Deal d = deal(units, tiles);
-    // Eight waves where one workgroup fits a compute unit anyway (3 sequences of 777
-    // tokens, heads of 256: 101 us, with four waves 127; 2000 tokens of 16 heads of 192
-    // and 128, 256 workgroups: 55, 60), two workgroups of four else (2048 of 8192 tokens,
-    // 512 of them: 266, 318). Heads of 64 gain nothing (512 tokens: 93, 91). Of heads of
-    // 256, e4m3 or in small pages, the registers do not allow for two waves a SIMD.
-    constexpr bool kFits = DV == 256 ? ONE && !E4M3 : DV == 128;
-    if constexpr (kFits)
-        if (DV == 256 || units * tiles <= 256) {
-            k_attn_chunk<DK, DV, E4M3, ONE, 2><<<d.grid, 512, 0, s>>>(a, (int)tiles, (int)units, d.spread, false);
+    // A wave waits for its own products and powers, so a SIMD wants two. Heads of 256,
+    // of which LDS holds one workgroup a compute unit: eight waves (3 sequences of 777
+    // tokens: 101 us, four waves 127; e4m3 or in small pages the registers do not allow
+    // for them). Up to 256 workgroups: 64 rows for four waves, twice as many workgroups
+    // (2000 tokens of 16 heads of 192 and 128: 48 us; 128 rows for four waves 60, for
+    // eight 55). More: 128 rows for four, which read a tile for twice as many rows (2048
+    // of 8192 tokens: 256 us, 64 rows 317).
+    if constexpr (DV == 256) {
+        if constexpr (ONE && !E4M3) {
+            k_attn_chunk<DK, DV, E4M3, ONE, 4, 2><<<d.grid, 512, 0, s>>>(a, (int)tiles, (int)units, d.spread, false);
             return;
         }
+    } else if (units * tiles <= 256) {
+        const int64_t fine = ceil_div((int64_t)a.max_new * a.group, 2 * kTile);
+        const Deal d = deal(units, fine);
+        k_attn_chunk<DK, DV, E4M3, ONE, 2, 2><<<d.grid, 256, 0, s>>>(a, (int)fine, (int)units, d.spread, d.grid <= 512);
+        return;
+    }
     // Of two workgroups a compute unit that all run at once, the long ones with short
     // ones (4 sequences of 1000 tokens, 16 heads: 34 us, else 41; 2048 of 8192 tokens, 256,
     // 262). Where there are more, the next one goes to whichever is free, and units one
     // after the other read their keys from L2 (6 of 1500 of 6000: 189 us, as above 243).
-    k_attn_chunk<DK, DV, E4M3, ONE, 1><<<d.grid, 256, 0, s>>>(a, (int)tiles, (int)units, d.spread, d.grid <= 512);
+    k_attn_chunk<DK, DV, E4M3, ONE, 4, 1><<<d.grid, 256, 0, s>>>(a, (int)tiles, (int)units, d.spread, d.grid <= 512);
 }
 
 template <int DK, int DV, bool E4M3>
