@@ -15,12 +15,14 @@ namespace {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 
-constexpr int kKeys = 64, kMine = kKeys / 4, kWaveCols = kLatent / 4;
+constexpr int kKeys = 64;
 
 template <int DK, int ROWS, int BUFFERS>
 struct LatentLds {
+    static constexpr int kWaves = ROWS == 16 ? 4 : 8, kMine = kKeys / kWaves, kWaveCols = kLatent / kWaves;
+    static constexpr int kGroups = ROWS / 16, kParts = kWaves / kGroups;  // of rows and of keys that waves take for the scores
     static constexpr int kPadded = ROWS < kTile ? kTile : ROWS, kBuffer = kKeys * DK * 2;
-    static constexpr int kP = BUFFERS * kBuffer, kTop = kP + kPadded * kKeys * 2, kKeep = kTop + 4 * kTile * 4, kSaid = kKeep + kPadded * 4;
+    static constexpr int kP = BUFFERS * kBuffer, kTop = kP + kPadded * kKeys * 2, kKeep = kTop + kParts * ROWS * 4, kSaid = kKeep + kPadded * 4;
     static constexpr int kBytes = kSaid + 64;
     static_assert(kPadded * kLatent * 4 <= kP, "outputs take the place of the tiles");
 };
@@ -31,9 +33,10 @@ __device__ __forceinline__ float max_groups(float v) {  // over the four lanes l
 }
 
 template <int DK, int ROWS, int BUFFERS, bool ONE>
-__global__ __launch_bounds__(256, (BUFFERS == 1 ? 2 : 1)) void k_latent(AttnArgs a, int row_tiles, int units, int spread) {
+__global__ __launch_bounds__((64 * LatentLds<DK, ROWS, BUFFERS>::kWaves), 2) void k_latent(AttnArgs a, int row_tiles, int units, int spread) {
     using L = LatentLds<DK, ROWS, BUFFERS>;
     constexpr int kOther = (BUFFERS - 1) * L::kBuffer;  // where q passes through
+    constexpr int kWaves = L::kWaves, kMine = L::kMine, kWaveCols = L::kWaveCols;
     __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
     const int xcd = blockIdx.x & 7, turn = blockIdx.x >> 3, per = (row_tiles + spread - 1) / spread;
     const int unit = turn / per * (8 / spread) + xcd / spread, row_tile = row_tiles - 1 - (turn % per * spread + xcd % spread);
@@ -54,18 +57,12 @@ __global__ __launch_bounds__(256, (BUFFERS == 1 ? 2 : 1)) void k_latent(AttnArgs
     const int lo = max(split.lo, first_key(a, at0)), hi = min(split.hi, end_key(a, seq, at1));
     const int all_lo = first_key(a, at1), all_hi = end_key(a, seq, at0);  // keys that every row sees
 
-    // For scores: rows 32 rt + 16 ct + lane % 16, keys first .. of a tile, 16 kt + 4 g + i.
-    constexpr int RT = ROWS == 64 ? 2 : 1, KT = RT, CT = ROWS == 16 ? 1 : 2;
-    const int rt = RT == 2 ? wave & 1 : 0, part = RT == 2 ? wave >> 1 : wave, first = part * 16 * KT;
-    int own_lo[CT], own_hi[CT];
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-        const int token = min(r0 + rt * kTile + 16 * ct + (lane & 15), rows - 1) / a.group;
-        own_lo[ct] = first_key(a, seq.at + token), own_hi[ct] = end_key(a, seq, seq.at + token);
-    }
-    float m[CT], l[CT] = {};
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) m[ct] = -INFINITY;
+    // For scores: rows first_row + lane % 16, keys first + 16 kt + 4 g + i of a tile.
+    constexpr int RT = L::kPadded / kTile, KT = kKeys / 16 / L::kParts;
+    const int first_row = wave % L::kGroups * 16, part = wave / L::kGroups, first = part * 16 * KT, own_row = first_row + (lane & 15);
+    const int own_token = min(r0 + own_row, rows - 1) / a.group;
+    const int own_lo = first_key(a, seq.at + own_token), own_hi = end_key(a, seq, seq.at + own_token);
+    float m = -INFINITY, l = 0.0f;
     v16f o[kWaveCols / 32][RT] = {};
 
     constexpr uint32_t kAllMine = (1u << kMine) - 1;
@@ -87,29 +84,23 @@ __global__ __launch_bounds__(256, (BUFFERS == 1 ? 2 : 1)) void k_latent(AttnArgs
     }
     // q's rows come through the other buffer, each once (a wave for itself would read
     // rows that two or four of them need: 147 KB a workgroup).
-    v8bf q[CT][DK / 32];
+    v8bf q[DK / 32];
     {
-        constexpr int kOwn = ROWS < 32 ? 8 : ROWS / 4;
-        const int r = min(r0 + wave * kOwn + (lane & (kOwn - 1)), rows - 1), token = r / a.group;
-        if (wave * kOwn < ROWS)
-            load_tile<DK, kOwn, false>(a.q, (seq.first + token) * a.q_token + (r - token * a.group) * a.q_head, 0, 0,
-                                       lds_at + kOther + wave * kOwn * DK * 2, lane);
+        const int r = min(r0 + wave * 8 + (lane & 7), rows - 1), token = r / a.group;
+        if (wave * 8 < ROWS)
+            load_tile<DK, 8, false>(a.q, (seq.first + token) * a.q_token + (r - token * a.group) * a.q_head, 0, 0,
+                                    lds_at + kOther + wave * 8 * DK * 2, lane);
         wait_loads<0>();
         __syncthreads();
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-            for (int t = 0; t < DK / 32; ++t) {
-                const int row = rt * kTile + 16 * ct + (lane & 15), chunk = 4 * (t & 1) + g;
-                q[ct][t] = *(const v8bf*)(lds + kOther + row_at<DK>(row) + (t >> 1) * 1024 + chunk_at(chunk, row));
-            }
+        for (int t = 0; t < DK / 32; ++t)
+            q[t] = *(const v8bf*)(lds + kOther + row_at<DK>(own_row) + (t >> 1) * 1024 + chunk_at(4 * (t & 1) + g, own_row));
     }
     char* const p_lds = lds + L::kP;
     float* const tops = (float*)(lds + L::kTop);
     float* const keeps = (float*)(lds + L::kKeep);
     uint32_t* const said = (uint32_t*)(lds + L::kSaid);  // by each wave: keys held, and whether some value is not finite
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) as_operands(a, q[ct]);
+    as_operands(a, q);
     if constexpr (BUFFERS == 1) {
         __syncthreads();
         if (base < hi) load(0);
@@ -121,15 +112,16 @@ __global__ __launch_bounds__(256, (BUFFERS == 1 ? 2 : 1)) void k_latent(AttnArgs
         if (next.held != kAllMine) clear_rows<DK, kMine>(own_rows, next.held, lane);
         if (lane == 0) said[wave] = next.held;
         __syncthreads();
-        const uint4 held4 = *(const uint4*)said;
-        const uint64_t held = (uint64_t)(held4.z | held4.w << 16) << 32 | (held4.x | held4.y << 16);
+        uint64_t held = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) held |= (uint64_t)said[w] << (kMine * w);
         if (base + kKeys < hi) {
             find(base + kKeys);
             if constexpr (BUFFERS == 2) load(buffer ^ 1);
         }
         const bool edge = base < all_lo || base + kKeys > all_hi;
 
-        v4f z[CT][KT] = {};
+        v4f z[KT] = {};
         {
             constexpr int kSteps = DK / 32, kAhead = kSteps % 3 ? 4 : 6 / KT;
             v8bf x[2][kAhead][KT];
@@ -151,9 +143,7 @@ __global__ __launch_bounds__(256, (BUFFERS == 1 ? 2 : 1)) void k_latent(AttnArgs
                 for (int t = 0; t < kAhead; ++t)
 #pragma unroll
                     for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct)
-                            z[ct][kt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[b & 1][t][kt], q[ct][b * kAhead + t], z[ct][kt], 0, 0, 0);
+                        z[kt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[b & 1][t][kt], q[b * kAhead + t], z[kt], 0, 0, 0);
                 keep_order();
             }
         }
@@ -163,57 +153,52 @@ __global__ __launch_bounds__(256, (BUFFERS == 1 ? 2 : 1)) void k_latent(AttnArgs
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int j = first + 16 * kt + 4 * g + i;
-                    const bool there = held >> j & 1;
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct)
-                        z[ct][kt][i] = there && base + j >= own_lo[ct] && base + j < own_hi[ct] ? z[ct][kt][i] : -INFINITY;
+                    z[kt][i] = (held >> j & 1) && base + j >= own_lo && base + j < own_hi ? z[kt][i] : -INFINITY;
                 }
         }
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-            float top = z[ct][0][0];
+        {
+            float top = z[0][0];
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) top = fmaxf(top, z[ct][kt][i]);
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, z[kt][i]);
             top = max_groups(top) * a.z_scale;
-            if (lane < 16) tops[wave * kTile + 16 * ct + lane] = top;
+            if (lane < 16) tops[part * ROWS + own_row] = top;
         }
         __syncthreads();
 
         // Weights, against a maximum that all waves of these rows set alike (and lazily:
         // see tile_weights).
+        {
+            float top = tops[own_row];
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-            const int r = 16 * ct + (lane & 15);
-            float top = fmaxf(tops[rt * kTile + r], tops[(RT == 2 ? rt + 2 : 1) * kTile + r]);
-            if constexpr (RT == 1) top = fmaxf(top, fmaxf(tops[2 * kTile + r], tops[3 * kTile + r]));
-            top = top > m[ct] + 8.0f ? top : m[ct];
-            const float at = top == -INFINITY ? 0.0f : top, keep = top == m[ct] ? 1.0f : exp2_fast(m[ct] - at);
+            for (int p = 1; p < L::kParts; ++p) top = fmaxf(top, tops[p * ROWS + own_row]);
+            top = top > m + 8.0f ? top : m;
+            const float at = top == -INFINITY ? 0.0f : top, keep = top == m ? 1.0f : exp2_fast(m - at);
             float sum = 0.0f;
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    z[ct][kt][i] = exp2_fast(__builtin_fmaf(z[ct][kt][i], a.z_scale, -at));
-                    sum += z[ct][kt][i];
+                    z[kt][i] = exp2_fast(__builtin_fmaf(z[kt][i], a.z_scale, -at));
+                    sum += z[kt][i];
                 }
-                const int row = rt * kTile + r, chunk = (first + 16 * kt) / 8 + (g >> 1);
-                *(uint2*)(p_lds + row * 128 + ((chunk ^ (row & 7)) << 4) + (g & 1) * 8) =
-                    make_uint2(pack_bf16(z[ct][kt][0], z[ct][kt][1]), pack_bf16(z[ct][kt][2], z[ct][kt][3]));
+                const int chunk = (first + 16 * kt) / 8 + (g >> 1);
+                *(uint2*)(p_lds + own_row * 128 + ((chunk ^ (own_row & 7)) << 4) + (g & 1) * 8) =
+                    make_uint2(pack_bf16(z[kt][0], z[kt][1]), pack_bf16(z[kt][2], z[kt][3]));
             }
-            l[ct] = __builtin_fmaf(l[ct], keep, sum);
-            m[ct] = top;
-            if (part == 0 && lane < 16) keeps[rt * kTile + r] = keep;
+            l = __builtin_fmaf(l, keep, sum);
+            m = top;
+            if (part == 0 && lane < 16) keeps[own_row] = keep;
         }
         if (edge) {
             const bool some = make_finite<DK, kMine>(own_rows, lane);
-            if (lane == 0) said[4 + wave] = some;
+            if (lane == 0) said[kWaves + wave] = some;
         }
         __syncthreads();
         if (edge) {
-            const uint4 w = *(const uint4*)(said + 4);
-            odd |= (w.x | w.y | w.z | w.w) != 0;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) odd |= said[kWaves + w] != 0;
         }
 
         // Sums: columns kWaveCols * wave .. of every row.
@@ -236,7 +221,7 @@ __global__ __launch_bounds__(256, (BUFFERS == 1 ? 2 : 1)) void k_latent(AttnArgs
             for (int k = 0; k < 4; ++k) {
                 // keys 16 k + 8 (lane / 32) .., their natural order, for p's is the same
                 const int row = (lane & 15) >> 2, chunk = 4 * (t & 1) + 2 * (g & 1) + ((lane & 3) >> 1);
-                const char* at = k_lds + row_at<DK>(16 * k) + row_at<DK>(8 * (lane >> 5) + row) + (2 * wave + (t >> 1)) * 1024 + (lane & 1) * 8;
+                const char* at = k_lds + row_at<DK>(16 * k) + row_at<DK>(8 * (lane >> 5) + row) + (kWaveCols / 64 * wave + (t >> 1)) * 1024 + (lane & 1) * 8;
                 typedef __attribute__((address_space(3))) v4s lds_v4s;
                 const v4s lo4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + chunk_at(chunk, row)));
                 const v4s hi4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 4 * 128 + chunk_at(chunk, row + 4)));
@@ -264,12 +249,9 @@ __global__ __launch_bounds__(256, (BUFFERS == 1 ? 2 : 1)) void k_latent(AttnArgs
     // rows of 512 floats, 16 bytes at chunk ^ (row % 8). The waves' sums of weights and
     // the maxima go the same way.
     __syncthreads();
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-        const float sum = bfly32(bfly16(l[ct]));
-        if (lane < 16) tops[wave * kTile + 16 * ct + lane] = sum;
-        if (part == 0 && lane < 16) keeps[rt * kTile + 16 * ct + lane] = m[ct];
-    }
+    const float mine_sum = bfly32(bfly16(l));
+    if (lane < 16) tops[part * ROWS + own_row] = mine_sum;
+    if (part == 0 && lane < 16) keeps[own_row] = m;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
         const int at = r * kTile + (lane & 31);
@@ -283,14 +265,14 @@ __global__ __launch_bounds__(256, (BUFFERS == 1 ? 2 : 1)) void k_latent(AttnArgs
             }
     }
     __syncthreads();
-    // Wave w writes rows w, w + 4, ...; lane i knows where the ith of them goes.
-    constexpr int kOwn = ROWS / 4;
-    const int own = wave + 4 * (lane & (kOwn - 1)), token = min(r0 + own, rows - 1) / a.group;
+    // Wave w writes rows w, w + kWaves, ...; lane i knows where the ith of them goes.
+    constexpr int kOwn = ROWS / kWaves;
+    const int own = wave + kWaves * (lane & (kOwn - 1)), token = min(r0 + own, rows - 1) / a.group;
     const int head = min(r0 + own, rows - 1) - token * a.group;
     const float top = keeps[own];
-    float sum, factor = 1.0f;
-    if constexpr (RT == 2) sum = tops[own] + tops[2 * kTile + own];
-    else sum = tops[own] + tops[kTile + own] + tops[2 * kTile + own] + tops[3 * kTile + own];
+    float sum = tops[own], factor = 1.0f;
+#pragma unroll
+    for (int p = 1; p < L::kParts; ++p) sum += tops[p * ROWS + own];
     char* to;
     if (split.n > 1) {
         const int64_t at = partial(a, s, token, head, c);
@@ -302,7 +284,7 @@ __global__ __launch_bounds__(256, (BUFFERS == 1 ? 2 : 1)) void k_latent(AttnArgs
     }
 #pragma unroll 4
     for (int k = 0; k < kOwn; ++k) {
-        const int at = wave + 4 * k;
+        const int at = wave + kWaves * k;
         if (r0 + at >= rows) break;
         const char* p = lds + at * kLatent * 4;
         const float4 x = *(const float4*)(p + ((2 * lane) ^ (at & 7)) * 16), y = *(const float4*)(p + ((2 * lane + 1) ^ (at & 7)) * 16);
@@ -326,8 +308,9 @@ template <int DK, int ROWS, int BUFFERS>
 void launch(const AttnArgs& a, hipStream_t s) {
     const int64_t units = (int64_t)a.seqs * a.splits, tiles = ceil_div((int64_t)a.max_new * a.heads, ROWS);
     const Deal d = deal(units, tiles);
-    if (one_page(a, kMine)) k_latent<DK, ROWS, BUFFERS, true><<<d.grid, 256, 0, s>>>(a, (int)tiles, (int)units, d.spread);
-    else k_latent<DK, ROWS, BUFFERS, false><<<d.grid, 256, 0, s>>>(a, (int)tiles, (int)units, d.spread);
+    using L = LatentLds<DK, ROWS, BUFFERS>;
+    if (one_page(a, L::kMine)) k_latent<DK, ROWS, BUFFERS, true><<<d.grid, 64 * L::kWaves, 0, s>>>(a, (int)tiles, (int)units, d.spread);
+    else k_latent<DK, ROWS, BUFFERS, false><<<d.grid, 64 * L::kWaves, 0, s>>>(a, (int)tiles, (int)units, d.spread);
     launch_join<kLatent>(a, s);
 }
 
