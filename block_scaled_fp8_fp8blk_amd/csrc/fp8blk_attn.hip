@@ -539,7 +539,7 @@ Plan plan(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, i
     const int64_t units = seqs * c.heads * (p.few && !latent ? 1 : ceil_div(panel ? group : max_new * group, tile));
     const int64_t step = p.few && !latent ? 4 * kTile : 64;
     int64_t n;
-    if (latent) n = std::min((group <= 16 && panel ? 512 : 256) / units, ceil_div(seen, p.few ? 128 : 256));
+    if (latent) n = std::min(256 / units, ceil_div(seen, p.few ? 128 : 256));
     else if (p.few) n = seen <= 512 ? 1 : std::min(std::max(256 / units, units < 512 ? std::min(ceil_div(seen, 768), 16384 / units) : 1), ceil_div(seen, step));
     else {
         // A tile of 64 keys takes a workgroup 1.1 us, each split of a row writes and reads

@@ -4,10 +4,16 @@
 // A row of 576 takes 2 * 576 * heads operations as keys and 2 * 512 * heads as values
 // and is 1152 bytes: 128 heads stand near the card's balance of matrix cores and
 // memory, 16 are bound by memory. What does not fit is registers: outputs of 512
-// columns and q of 576 for 32 rows are 400 of a lane's 512. So the four waves share
-// both products of a tile of 64 keys: scores by rows and keys (a wave 32 rows and 32
-// keys, or 16 keys where there are only 32 rows), sums by columns (a wave 128 columns
-// of every row), and the weights go from the one to the other through LDS.
+// columns and q of 576 for 32 rows are 400 of a lane's 512, and a SIMD wants two waves.
+// So eight waves share both products of a tile of 64 keys: scores by rows and keys (a
+// wave 16 rows, and 16 or 32 keys of the tile), sums by columns (a wave 64 columns of
+// every row), and the weights go from the one to the other through LDS; three barriers
+// a tile. Two tiles in LDS are all that fits: one workgroup a compute unit.
+//
+// 64 rows: a tile takes 2.8 us, of which the matrix cores work 0.9 (64 sequences of 8000
+// keys, 128 heads: 232 us, 560 TFLOP/s; with four waves, 32 rows and 128 columns each,
+// 254); LDS reads 420 KB of operands for it, 1.4 us. 32 rows: 16 sequences of 16384 keys,
+// 16 heads, 68 us, 4.4 TB/s; with 16 rows, one tile in LDS and two workgroups, 73.
 #include "fp8blk_attn.hpp"
 
 namespace fp8blk {
@@ -15,16 +21,15 @@ namespace {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 
-constexpr int kKeys = 64;
+constexpr int kKeys = 64, kWaves = 8, kMine = kKeys / kWaves, kWaveCols = kLatent / kWaves;
 
-template <int DK, int ROWS, int BUFFERS>
+template <int DK, int ROWS>
 struct LatentLds {
-    static constexpr int kWaves = ROWS == 16 ? 4 : 8, kMine = kKeys / kWaves, kWaveCols = kLatent / kWaves;
     static constexpr int kGroups = ROWS / 16, kParts = kWaves / kGroups;  // of rows and of keys that waves take for the scores
-    static constexpr int kPadded = ROWS < kTile ? kTile : ROWS, kBuffer = kKeys * DK * 2;
-    static constexpr int kP = BUFFERS * kBuffer, kTop = kP + kPadded * kKeys * 2, kKeep = kTop + kParts * ROWS * 4, kSaid = kKeep + kPadded * 4;
+    static constexpr int kBuffer = kKeys * DK * 2;
+    static constexpr int kP = 2 * kBuffer, kTop = kP + ROWS * kKeys * 2, kKeep = kTop + kParts * ROWS * 4, kSaid = kKeep + ROWS * 4;
     static constexpr int kBytes = kSaid + 64;
-    static_assert(kPadded * kLatent * 4 <= kP, "outputs take the place of the tiles");
+    static_assert(ROWS * kLatent * 4 <= kP, "outputs take the place of the tiles");
 };
 
 __device__ __forceinline__ float max_groups(float v) {  // over the four lanes l % 16
@@ -32,11 +37,9 @@ __device__ __forceinline__ float max_groups(float v) {  // over the four lanes l
     return max_halves(fmaxf(as_f32(r[0]), as_f32(r[1])));
 }
 
-template <int DK, int ROWS, int BUFFERS, bool ONE>
-__global__ __launch_bounds__((64 * LatentLds<DK, ROWS, BUFFERS>::kWaves), 2) void k_latent(AttnArgs a, int row_tiles, int units, int spread) {
-    using L = LatentLds<DK, ROWS, BUFFERS>;
-    constexpr int kOther = (BUFFERS - 1) * L::kBuffer;  // where q passes through
-    constexpr int kWaves = L::kWaves, kMine = L::kMine, kWaveCols = L::kWaveCols;
+template <int DK, int ROWS, bool ONE>
+__global__ __launch_bounds__(64 * kWaves, 2) void k_latent(AttnArgs a, int row_tiles, int units, int spread) {
+    using L = LatentLds<DK, ROWS>;
     __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
     const int xcd = blockIdx.x & 7, turn = blockIdx.x >> 3, per = (row_tiles + spread - 1) / spread;
     const int unit = turn / per * (8 / spread) + xcd / spread, row_tile = row_tiles - 1 - (turn % per * spread + xcd % spread);
@@ -58,7 +61,7 @@ __global__ __launch_bounds__((64 * LatentLds<DK, ROWS, BUFFERS>::kWaves), 2) voi
     const int all_lo = first_key(a, at1), all_hi = end_key(a, seq, at0);  // keys that every row sees
 
     // For scores: rows first_row + lane % 16, keys first + 16 kt + 4 g + i of a tile.
-    constexpr int RT = L::kPadded / kTile, KT = kKeys / 16 / L::kParts;
+    constexpr int RT = ROWS / kTile, KT = kKeys / 16 / L::kParts;
     const int first_row = wave % L::kGroups * 16, part = wave / L::kGroups, first = part * 16 * KT, own_row = first_row + (lane & 15);
     const int own_token = min(r0 + own_row, rows - 1) / a.group;
     const int own_lo = first_key(a, seq.at + own_token), own_hi = end_key(a, seq, seq.at + own_token);
@@ -80,7 +83,7 @@ __global__ __launch_bounds__((64 * LatentLds<DK, ROWS, BUFFERS>::kWaves), 2) voi
     if (base < hi) {
         if (a.window > 0) page = page_at<ONE>(a, s, base + mine, lane);
         find(base);
-        if constexpr (BUFFERS == 2) load(0);
+        load(0);
     }
     // q's rows come through the other buffer, each once (a wave for itself would read
     // rows that two or four of them need: 147 KB a workgroup).
@@ -89,23 +92,19 @@ __global__ __launch_bounds__((64 * LatentLds<DK, ROWS, BUFFERS>::kWaves), 2) voi
         const int r = min(r0 + wave * 8 + (lane & 7), rows - 1), token = r / a.group;
         if (wave * 8 < ROWS)
             load_tile<DK, 8, false>(a.q, (seq.first + token) * a.q_token + (r - token * a.group) * a.q_head, 0, 0,
-                                    lds_at + kOther + wave * 8 * DK * 2, lane);
+                                    lds_at + L::kBuffer + wave * 8 * DK * 2, lane);
         wait_loads<0>();
         __syncthreads();
 #pragma unroll
         for (int t = 0; t < DK / 32; ++t)
-            q[t] = *(const v8bf*)(lds + kOther + row_at<DK>(own_row) + (t >> 1) * 1024 + chunk_at(4 * (t & 1) + g, own_row));
+            q[t] = *(const v8bf*)(lds + L::kBuffer + row_at<DK>(own_row) + (t >> 1) * 1024 + chunk_at(4 * (t & 1) + g, own_row));
     }
     char* const p_lds = lds + L::kP;
     float* const tops = (float*)(lds + L::kTop);
     float* const keeps = (float*)(lds + L::kKeep);
     uint32_t* const said = (uint32_t*)(lds + L::kSaid);  // by each wave: keys held, and whether some value is not finite
     as_operands(a, q);
-    if constexpr (BUFFERS == 1) {
-        __syncthreads();
-        if (base < hi) load(0);
-    }
-    for (int buffer = 0; base < hi; base += kKeys, buffer ^= BUFFERS - 1) {
+    for (int buffer = 0; base < hi; base += kKeys, buffer ^= 1) {
         char* const k_lds = lds + buffer * L::kBuffer;
         char* const own_rows = k_lds + mine * DK * 2;
         wait_loads<0>();
@@ -117,7 +116,7 @@ __global__ __launch_bounds__((64 * LatentLds<DK, ROWS, BUFFERS>::kWaves), 2) voi
         for (int w = 0; w < kWaves; ++w) held |= (uint64_t)said[w] << (kMine * w);
         if (base + kKeys < hi) {
             find(base + kKeys);
-            if constexpr (BUFFERS == 2) load(buffer ^ 1);
+            load(buffer ^ 1);
         }
         const bool edge = base < all_lo || base + kKeys > all_hi;
 
@@ -206,7 +205,7 @@ __global__ __launch_bounds__((64 * LatentLds<DK, ROWS, BUFFERS>::kWaves), 2) voi
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             const int row = r * kTile + (lane & 31);
-            const float keep = ROWS < kTile && (lane & 16) ? 1.0f : keeps[row];
+            const float keep = keeps[row];
             if (__any(keep != 1.0f))
 #pragma unroll
                 for (int t = 0; t < kWaveCols / 32; ++t)
@@ -238,10 +237,6 @@ __global__ __launch_bounds__((64 * LatentLds<DK, ROWS, BUFFERS>::kWaves), 2) voi
 #pragma unroll
                 for (int r = 0; r < RT; ++r) o[t][r] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[t & 1][k], p[r][k], o[t][r], 0, 0, 0);
             keep_order();
-        }
-        if constexpr (BUFFERS == 1) {
-            __syncthreads();
-            if (base + kKeys < hi) load(0);
         }
     }
 
@@ -304,23 +299,20 @@ __global__ __launch_bounds__((64 * LatentLds<DK, ROWS, BUFFERS>::kWaves), 2) voi
     }
 }
 
-template <int DK, int ROWS, int BUFFERS>
+template <int DK, int ROWS>
 void launch(const AttnArgs& a, hipStream_t s) {
     const int64_t units = (int64_t)a.seqs * a.splits, tiles = ceil_div((int64_t)a.max_new * a.heads, ROWS);
     const Deal d = deal(units, tiles);
-    using L = LatentLds<DK, ROWS, BUFFERS>;
-    if (one_page(a, L::kMine)) k_latent<DK, ROWS, BUFFERS, true><<<d.grid, 64 * L::kWaves, 0, s>>>(a, (int)tiles, (int)units, d.spread);
-    else k_latent<DK, ROWS, BUFFERS, false><<<d.grid, 64 * L::kWaves, 0, s>>>(a, (int)tiles, (int)units, d.spread);
+    if (one_page(a, kMine)) k_latent<DK, ROWS, true><<<d.grid, 64 * kWaves, 0, s>>>(a, (int)tiles, (int)units, d.spread);
+    else k_latent<DK, ROWS, false><<<d.grid, 64 * kWaves, 0, s>>>(a, (int)tiles, (int)units, d.spread);
     launch_join<kLatent>(a, s);
 }
 
 }  // namespace
 
 void launch_latent(const AttnArgs& a, int64_t k_cols, bool few, hipStream_t s) {
-    const int64_t rows = (int64_t)a.max_new * a.heads;
-    const int kind = few ? rows <= 16 ? 16 : 32 : 64;
-    if (k_cols == kLatent) kind == 64 ? launch<kLatent, 64, 2>(a, s) : kind == 16 ? launch<kLatent, 16, 1>(a, s) : launch<kLatent, 32, 2>(a, s);
-    else kind == 64 ? launch<kLatent + 64, 64, 2>(a, s) : kind == 16 ? launch<kLatent + 64, 16, 1>(a, s) : launch<kLatent + 64, 32, 2>(a, s);
+    if (k_cols == kLatent) few ? launch<kLatent, 32>(a, s) : launch<kLatent, 64>(a, s);
+    else few ? launch<kLatent + 64, 32>(a, s) : launch<kLatent + 64, 64>(a, s);
 }
 
 }  // namespace fp8blk
