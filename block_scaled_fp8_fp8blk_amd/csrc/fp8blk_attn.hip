@@ -534,12 +534,21 @@ Plan plan(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, i
     const bool panel = max_new <= FP8BLK_MAX_M, latent = !c.v;
     const int64_t seen = window > 0 ? std::min(max_len, window + (panel ? FP8BLK_MAX_M : max_new)) : max_len;
     Plan p;
-    p.few = panel && (!latent || group <= kTile || seqs * ceil_div(group, kLatentRows) * ceil_div(seen, 64) <= 256);
+    // Latent: 32 rows a workgroup where it has few keys, 64 where that many read them more
+    // than once (128 heads: one sequence of 16000 keys 25 us and 30, 64 of 8000 266 and 226).
+    p.few = panel && (!latent || group <= kTile || seqs * ceil_div(group, kLatentRows) * ceil_div(seen, 64) <= 1024);
     const int64_t tile = latent ? (p.few ? kTile : kLatentRows) : kChunkRows;
     const int64_t units = seqs * c.heads * (p.few && !latent ? 1 : ceil_div(panel ? group : max_new * group, tile));
     const int64_t step = p.few && !latent ? 4 * kTile : 64;
     int64_t n;
+    // One workgroup a compute unit, with keys enough that the sums' way through memory
+    // does not take longer than they do (8192 keys, 128 heads: 64 splits 21 us, 32 22,
+    // 128 30).
     if (latent) n = std::min(256 / units, ceil_div(seen, p.few ? 128 : 256));
+    // A workgroup streams 768 keys a split or more, as many splits as fill the card at
+    // least: 4096 keys, 4 key heads: 32 splits 10.7 us, 8 13.8, one 41; 32 sequences of up
+    // to 16384: 22 splits 115, 4 136 (all of 16384: 212 and 205, one 233). From 512 units
+    // on none (128 sequences of 4096: 116, in 2 splits 140), nor below 512 keys.
     else if (p.few) n = seen <= 512 ? 1 : std::min(std::max(256 / units, units < 512 ? std::min(ceil_div(seen, 768), 16384 / units) : 1), ceil_div(seen, step));
     else {
         // A tile of 64 keys takes a workgroup 1.1 us, each split of a row writes and reads
