@@ -140,15 +140,14 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
         }
         const bool edge = base < all_lo || base + kTile > all_hi;
         if (edge || here.held != ~0u) hide(z[0], here.held & keys_between(base, own_lo, own_hi), lane);
-        rescale(o, tile_weights(z, a.z_scale, run));
+        v8bf p[1][2];
+        rescale(o, tile_weights(z, a.z_scale, run, p));
         if constexpr (E4M3) store_codes(v_lds, v_codes, lane);
         else if (more) wait_loads<DK / 16 + (ONE ? 0 : 1)>();
         else wait_loads<0>();
         if (here.held != ~0u) clear_rows<DV>(v_lds, here.held, lane);
         if (edge) odd |= make_finite<DV, kTile>(v_lds, lane);
-        v8bf p[2];
-        weights_operand(z[0], p);
-        tile_sums<DV>(v_lds, p, o, lane);
+        tile_sums<DV>(v_lds, p[0], o, lane);
         if (more) {
             wait_reads();
             load_v();
@@ -366,13 +365,10 @@ __global__ __launch_bounds__(64 * GROUPS * HALVES, (GROUPS * HALVES == 8 || Chun
         if (!__all(all))
 #pragma unroll
             for (int t = 0; t < L::kTiles; ++t) hide(z[t], seen[t], lane);
-        rescale(o, tile_weights(z, a.z_scale, run));
+        v8bf p[L::kTiles][2];
+        rescale(o, tile_weights(z, a.z_scale, run, p));
 #pragma unroll
-        for (int t = 0; t < L::kTiles; ++t) {
-            v8bf p[2];
-            weights_operand(z[t], p);
-            tile_sums<DV>(v_lds + (HALVES == 2 ? half : t) * kTile * DV * 2, p, o, lane);
-        }
+        for (int t = 0; t < L::kTiles; ++t) tile_sums<DV>(v_lds + (HALVES == 2 ? half : t) * kTile * DV * 2, p[t], o, lane);
     }
 
     // Whether any wave has made a value finite.
@@ -593,22 +589,22 @@ void launch_chunk(const AttnArgs& a, hipStream_t s) {
     // (2000 tokens of 16 heads of 192 and 128: 48 us; 128 rows for four waves 60, for
     // eight 55). More: 128 rows for four, which read a tile for twice as many rows (2048
     // of 8192 tokens: 256 us, 64 rows 317).
-    if constexpr (DV == 256) {
-        if constexpr (ONE && !E4M3) {
-            k_attn_chunk<DK, DV, E4M3, ONE, 4, 2><<<d.grid, 512, 0, s>>>(a, (int)tiles, (int)units, d.spread, false);
-            return;
-        }
-    } else if (units * tiles <= 256) {
-        const int64_t fine = ceil_div((int64_t)a.max_new * a.group, 2 * kTile);
-        const Deal d = deal(units, fine);
-        k_attn_chunk<DK, DV, E4M3, ONE, 2, 2><<<d.grid, 256, 0, s>>>(a, (int)fine, (int)units, d.spread, d.grid <= 512);
-        return;
+    if constexpr (DV == 256 && ONE && !E4M3) {
+        k_attn_chunk<DK, DV, E4M3, ONE, 4, 2><<<d.grid, 512, 0, s>>>(a, (int)tiles, (int)units, d.spread, false);
+    } else {
+        if constexpr (DV <= 128)
+            if (units * tiles <= 256) {
+                const int64_t fine = ceil_div((int64_t)a.max_new * a.group, 2 * kTile);
+                const Deal d = deal(units, fine);
+                k_attn_chunk<DK, DV, E4M3, ONE, 2, 2><<<d.grid, 256, 0, s>>>(a, (int)fine, (int)units, d.spread, d.grid <= 512);
+                return;
+            }
+        // Of two workgroups a compute unit that all run at once, the long ones with short
+        // ones (4 sequences of 1000 tokens, 16 heads: 34 us, else 41; 2048 of 8192 tokens, 256,
+        // 262). Where there are more, the next one goes to whichever is free, and units one
+        // after the other read their keys from L2 (6 of 1500 of 6000: 189 us, as above 243).
+        k_attn_chunk<DK, DV, E4M3, ONE, 4, 1><<<d.grid, 256, 0, s>>>(a, (int)tiles, (int)units, d.spread, d.grid <= 512);
     }
-    // Of two workgroups a compute unit that all run at once, the long ones with short
-    // ones (4 sequences of 1000 tokens, 16 heads: 34 us, else 41; 2048 of 8192 tokens, 256,
-    // 262). Where there are more, the next one goes to whichever is free, and units one
-    // after the other read their keys from L2 (6 of 1500 of 6000: 189 us, as above 243).
-    k_attn_chunk<DK, DV, E4M3, ONE, 4, 1><<<d.grid, 256, 0, s>>>(a, (int)tiles, (int)units, d.spread, d.grid <= 512);
 }
 
 template <int DK, int DV, bool E4M3>

@@ -165,19 +165,20 @@ __device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0x
 // C += K Q^T of a tile: K's rows in LDS, Q's columns in registers.
 template <int DK>
 __device__ __forceinline__ v16f tile_scores(const char* k, const v8bf (&q)[DK / 16], int lane) {
-    constexpr int kAhead = 4;
+    constexpr int kAhead = DK == 256 ? 2 : 4, kGroups = DK / 16 / kAhead;  // 256: what registers are left for
     const int row = lane & 31, h = lane >> 5;
     const char* at = k + row_at<DK>(row);
     v8bf x[2][kAhead];
     v16f c = {};
     auto read = [&](int g) {
 #pragma unroll
-        for (int t = 0; t < kAhead; ++t) x[g & 1][t] = *(const v8bf*)(at + g * 1024 + chunk_at(2 * t + h, row));
+        for (int t = g * kAhead; t < (g + 1) * kAhead; ++t)
+            x[g & 1][t % kAhead] = *(const v8bf*)(at + (t >> 2) * 1024 + chunk_at(2 * (t & 3) + h, row));
     };
     read(0);
 #pragma unroll
-    for (int g = 0; g < DK / 64; ++g) {
-        if (g + 1 < DK / 64) read(g + 1);
+    for (int g = 0; g < kGroups; ++g) {
+        if (g + 1 < kGroups) read(g + 1);
         keep_order();
 #pragma unroll
         for (int t = 0; t < kAhead; ++t) c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[g & 1][t], q[g * kAhead + t], c, 0, 0, 0);
@@ -388,16 +389,25 @@ __device__ __forceinline__ void hide(v16f& z, uint32_t seen, int lane) {
     for (int i = 0; i < 16; ++i) z[i] = seen >> ((i & 3) + 8 * (i >> 2)) & 1 ? z[i] : -INFINITY;
 }
 
-// The scores of N tiles become weights 2^(z - m): m is the row's maximum (in units of
-// log 2) when it was last set, l the lane's part of the running sum; returns the
-// factor of what was summed before. m follows the maximum only where that has grown
-// by more than 8: weights of up to 2^8 lose nothing, and the outputs are hardly
-// ever multiplied (not at all is what `rescale` checks for). scale > 0.
+// a + x[0] + x[1]
+__device__ __forceinline__ float add2(v2bf x, float a) {
+    return __builtin_amdgcn_fdot2_f32_bf16(x, v2bf{(__bf16)1.0f, (__bf16)1.0f}, a, false);
+}
+
+// The scores of N tiles become weights 2^(z - m), as bf16 for their product with the
+// values: m is the row's maximum (in units of log 2) when it was last set, l the
+// lane's part of the running sum; returns the factor of what was summed before. The sum
+// is of the rounded weights, so that they stay weights: their mean of equal values is
+// that value, and what rounding does to a row that few keys decide is less (the sum of
+// unrounded ones took 16 additions where this takes 8 instructions). m follows the
+// maximum only where that has grown by more than 8: weights of up to 2^8 lose nothing,
+// and the outputs are hardly ever multiplied (not at all is what `rescale` checks for).
+// scale > 0.
 struct Running {
     float m, l;
 };
 template <int N>
-__device__ __forceinline__ float tile_weights(v16f (&z)[N], float scale, Running& r) {
+__device__ __forceinline__ float tile_weights(const v16f (&z)[N], float scale, Running& r, v8bf (&p)[N][2]) {
     float top = z[0][0];
 #pragma unroll
     for (int n = 0; n < N; ++n)
@@ -411,9 +421,10 @@ __device__ __forceinline__ float tile_weights(v16f (&z)[N], float scale, Running
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            z[n][i] = exp2_fast(__builtin_fmaf(z[n][i], scale, -base));
-            sum += z[n][i];
+        for (int i = 0; i < 16; i += 2) {
+            const v2bf w = {(__bf16)exp2_fast(__builtin_fmaf(z[n][i], scale, -base)), (__bf16)exp2_fast(__builtin_fmaf(z[n][i + 1], scale, -base))};
+            p[n][i >> 3][i & 7] = w[0], p[n][i >> 3][(i & 7) + 1] = w[1];
+            sum = add2(w, sum);
         }
     r.l = __builtin_fmaf(r.l, keep, sum);
     r.m = top;
@@ -427,11 +438,6 @@ __device__ __forceinline__ void rescale(v16f (&o)[T], float keep) {
     for (int t = 0; t < T; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[t][i] *= keep;
-}
-
-__device__ __forceinline__ void weights_operand(const v16f& z, v8bf (&p)[2]) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) p[i >> 3][i & 7] = (__bf16)z[i];
 }
 
 // Joins the splits of rows and heads: kOnes threads of 8 columns of a row for every

@@ -178,13 +178,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_latent(AttnArgs a, int row_t
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    z[kt][i] = exp2_fast(__builtin_fmaf(z[kt][i], a.z_scale, -at));
-                    sum += z[kt][i];
-                }
+                for (int i = 0; i < 4; ++i) z[kt][i] = exp2_fast(__builtin_fmaf(z[kt][i], a.z_scale, -at));
+                const v2bf w[2] = {{(__bf16)z[kt][0], (__bf16)z[kt][1]}, {(__bf16)z[kt][2], (__bf16)z[kt][3]}};
+                sum = add2(w[1], add2(w[0], sum));
                 const int chunk = (first + 16 * kt) / 8 + (g >> 1);
                 *(uint2*)(p_lds + own_row * 128 + ((chunk ^ (own_row & 7)) << 4) + (g & 1) * 8) =
-                    make_uint2(pack_bf16(z[kt][0], z[kt][1]), pack_bf16(z[kt][2], z[kt][3]));
+                    make_uint2(__builtin_bit_cast(uint32_t, w[0]), __builtin_bit_cast(uint32_t, w[1]));
             }
             l = __builtin_fmaf(l, keep, sum);
             m = top;

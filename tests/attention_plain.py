@@ -142,9 +142,10 @@ def attend(k, v, q, at, scale, causal=True, window=0, sinks=None, absent=None):
 
     z is a sum of Dk products in f32, times a scale: (Dk + 8) U of the sum of their
     sizes; the difference to the maximum, in units of log 2, loses 2 U of both;
-    weights are within exp(2 dz) of theirs beside their sum, are rounded to bf16 (H),
-    and the sums over L keys, with every rescaling on the way, lose at most (L + 64)
-    steps."""
+    weights are within exp(2 dz) of theirs beside their sum; rounded to bf16 above and
+    below, w (1 + e) with e up to H, they move the quotient by sum w e (v - out) and H of
+    that: 1.01 H (size + |out|); and the sums over L keys, with every rescaling on the
+    way, lose at most (L + 64) steps."""
     L, h, Dk = k.shape
     rows, heads, _ = q.shape
     q = q.double()
@@ -180,7 +181,7 @@ def attend(k, v, q, at, scale, causal=True, window=0, sinks=None, absent=None):
             o = o + torch.where(seen[:, key, None] & odd[key], w[:, key, None] * vv[key], 0.0)
         size = w @ clean(vv).abs()
         out[:, head] = o
-        bound[:, head] = size * (H + 2.02 * dz + (L + 64) * 2 * U) + 2.0 ** -130
+        bound[:, head] = size * (2.02 * dz + (L + 64) * 2 * U) + 1.01 * H * (size + clean(o).abs()) + 2.0 ** -130
     return out, bound
 
 

@@ -58,6 +58,20 @@ def test_longer_than_max_len(gpu, k, v, T, window):
 
 
 @pytest.mark.parametrize("k,v", WIDTHS, ids=IDS)
+@pytest.mark.parametrize("T", [1, 7, 100])
+def test_values_that_are_all_alike(gpu, k, v, T):
+    """Their mean is that value, whatever the weights: these are rounded alike above and
+    below, and sums of 3000 f32 lose less than 2 * 3064 * 2^-24 < 2^-11, which does not move a
+    bf16 value by half a step (2^-9)."""
+    c = _call(gpu, 38, [3000, 70], [T, 1], k, v, group=3, spread=4.0)
+    cache = c.paged.cache_k if v is None else c.paged.cache_v
+    row = torch.linspace(-3, 3, c.v_cols).bfloat16().to(DEV)
+    cache[..., :c.v_cols] = row
+    c.run()
+    assert torch.equal(c.out, row.expand_as(c.out))
+
+
+@pytest.mark.parametrize("k,v", WIDTHS, ids=IDS)
 @pytest.mark.parametrize("T", [1, 30])
 def test_heads_that_share_a_row_of_q(gpu, k, v, T):
     """A head stride of 0, and q and out as slices of wider buffers."""
