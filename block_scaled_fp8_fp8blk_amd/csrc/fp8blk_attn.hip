@@ -14,7 +14,10 @@ namespace {
 // four waves tiles 0, 4, ...; 1, 5, ...; each with buffers, maximum, sum and outputs
 // of its own, so that nothing waits for another wave before the end, where the four
 // are joined in order. While a wave forms scores its values are on their way, and
-// while it sums values the next tile's keys are.
+// while it sums values the next tile's keys are. 32 sequences of up to 16384 keys, 32
+// heads of 128 over 4: 109 us and 6 for the join, 5.1 TB/s, what a copy reaches. e4m3 goes
+// through registers, where it is widened, to the same tiles: 70 and 6 us, 3.9 TB/s.
+// All key heads of a page on one XCD, one after the other: their rows are neighbours.
 template <int DK, int DV>
 struct FewLds {
     static constexpr int kK = kTile * DK * 2, kV = kTile * DV * 2, kPages = 256;

@@ -442,7 +442,9 @@ __device__ __forceinline__ void rescale(v16f (&o)[T], float keep) {
 
 // Joins the splits of rows and heads: kOnes threads of 8 columns of a row for every
 // WAYS-th chunk of its keys, which they add in order; then those sums, in order. Which
-// chunks go together depends on the keys alone.
+// chunks go together depends on the keys alone. A launch and two reads, the second of
+// which waits for the first: 5 us; few splits take a wave a row (64 new tokens of 8192,
+// 16 splits of 2048 rows: attention and join 30 us, with a workgroup a row 34).
 template <int DV, int WAYS>
 static __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     constexpr int kCols = DV < 128 ? DV : 128, kOnes = kCols / 8, kRows = 256 / kOnes / WAYS;

@@ -178,7 +178,9 @@ struct Units {
 // A workgroup takes the heads of q, k and v of one token, a wave 64 / lanes of one of
 // them at a time (so that all its lanes read the same description of it), a row
 // `lanes` lanes. The next rows are asked for before the present ones are worked on,
-// the first before the cosines and sines, which are formed once a workgroup.
+// the first before the cosines and sines, which are formed once a workgroup. Bound by
+// memory: 8191 tokens, 32 + 4 heads of 128, f32 to bf16 and e4m3, 50 us, 4.9 TB/s (rows
+// dealt to waves whatever their kind, and loads after the previous row's stores: 78).
 template <int U, bool INTERLEAVED>
 __global__ __launch_bounds__(kThreads) void k_rope_append(RopeArgs a) {
     __shared__ __attribute__((aligned(16))) float turn[2][FP8BLK_MAX_ROT / 2];
@@ -380,8 +382,10 @@ extern "C" int fp8blk_rope_append(const fp8blk_rope* rope, const int32_t* positi
         t.first = a.tasks;
         a.tasks += (t.heads + (64 >> a.lanes_log2) - 1) >> (6 - a.lanes_log2);
     }
-    // Few tokens: a workgroup for 4 tasks, many: one for all of a token's.
-    const dim3 grid((unsigned)N, (unsigned)(N >= 256 ? 1 : ceil_div(a.tasks, 4)));
+    // A workgroup for 4 tasks, so that a wave reads once; of many tokens one for all of a
+    // token's, which forms its angles once (256 tokens, 32 + 4 heads of 128: 4.8 us, 7.3 with
+    // one; 1024: 10.4, 10.8; 2048: 15.2, 14.9).
+    const dim3 grid((unsigned)N, (unsigned)(N > 1024 ? 1 : ceil_div(a.tasks, 4)));
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     (void)hipGetLastError();
     if (most <= 64) launch<1>(a, rope->interleaved != 0, grid, s);
