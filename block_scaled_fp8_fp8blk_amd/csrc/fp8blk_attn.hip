@@ -533,9 +533,11 @@ Plan plan(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, i
     const bool panel = max_new <= FP8BLK_MAX_M, latent = !c.v;
     const int64_t seen = window > 0 ? std::min(max_len, window + (panel ? FP8BLK_MAX_M : max_new)) : max_len;
     Plan p;
-    // Latent: 32 rows a workgroup where it has few keys, 64 where that many read them more
-    // than once (128 heads: one sequence of 16000 keys 25 us and 30, 64 of 8000 266 and 226).
-    p.few = panel && (!latent || group <= kTile || seqs * ceil_div(group, kLatentRows) * ceil_div(seen, 64) <= 1024);
+    // Latent: 32 rows a workgroup where there are few tiles, 64 where that many rows read
+    // the keys more than once, or write more splits (128 heads, one sequence of 4000 keys:
+    // 18 us, with 64 rows 25, two tokens 21 and 27; of 16000: 25, 30, two tokens 41 and 34;
+    // 64 of 8000: 266, 226).
+    p.few = panel && (!latent || group <= kTile || seqs * ceil_div(group, kLatentRows) * ceil_div(seen, 64) <= 256);
     const int64_t tile = latent ? (p.few ? kTile : kLatentRows) : kChunkRows;
     const int64_t units = seqs * c.heads * (p.few && !latent ? 1 : ceil_div(panel ? group : max_new * group, tile));
     const int64_t step = p.few && !latent ? 4 * kTile : 64;
