@@ -542,16 +542,22 @@ Plan plan(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, i
     const int64_t units = seqs * c.heads * (p.few && !latent ? 1 : ceil_div(panel ? group : max_new * group, tile));
     const int64_t step = p.few && !latent ? 4 * kTile : 64;
     int64_t n;
-    // One workgroup a compute unit, with keys enough that the sums' way through memory
-    // does not take longer than they do (8192 keys, 128 heads: 64 splits 21 us, 32 22,
-    // 128 30).
-    if (latent) n = std::min(256 / units, ceil_div(seen, p.few ? 128 : 256));
-    // A workgroup streams 768 keys a split or more, as many splits as fill the card at
-    // least: 4096 keys, 4 key heads: 32 splits 10.7 us, 8 13.8, one 41; 32 sequences of up
-    // to 16384: 22 splits 115, 4 136 (all of 16384: 212 and 205, one 233). From 512 units
-    // on none (128 sequences of 4096: 116, in 2 splits 140), nor below 512 keys.
-    else if (p.few) n = seen <= 512 ? 1 : std::min(std::max(256 / units, units < 512 ? std::min(ceil_div(seen, 768), 16384 / units) : 1), ceil_div(seen, step));
-    else {
+    if (latent) {
+        // One workgroup a compute unit, with keys enough that the sums' way through memory
+        // does not take longer than they do (8192 keys, 128 heads: 64 splits 21 us, 32 22,
+        // 128 30). A chunk's sequences are of unequal length: twice as many where they are
+        // long (8 of 100 tokens of up to 9000, 16 heads 382 -> 217, 4 of 877 of up to 14367,
+        // one head 172 -> 112, 3 of 64 of up to 16000 166 -> 170; where all are as long as
+        // that 5 to 16% more).
+        n = std::min(256 / units, ceil_div(seen, p.few ? 128 : 256));
+        if (!panel && seqs > 1 && n > 0 && seen >= 3000 * n) n *= 2;
+    } else if (p.few) {
+        // A workgroup streams 768 keys a split or more, as many splits as fill the card at
+        // least: 4096 keys, 4 key heads: 32 splits 10.7 us, 8 13.8, one 41; 32 sequences of
+        // up to 16384: 22 splits 115, 4 136 (all of 16384: 212 and 205, one 233). From 512
+        // units on none (128 sequences of 4096: 116, in 2 splits 140), nor below 512 keys.
+        n = seen <= 512 ? 1 : std::min(std::max(256 / units, units < 512 ? std::min(ceil_div(seen, 768), 16384 / units) : 1), ceil_div(seen, step));
+    } else {
         // A tile of 64 keys takes a workgroup 1.1 us, each split of a row writes and reads
         // 8 bytes a column: n^2 splits are best where n^2 * rows * columns is some
         // thousand times the keys (causal rows see max_new / 2 less; of sequences of
