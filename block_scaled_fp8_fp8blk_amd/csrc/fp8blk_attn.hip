@@ -457,7 +457,7 @@ bool attn_sizes_ok(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t m
     constexpr int64_t kMost = INT64_C(1) << 30;
     return heads >= 1 && heads <= FP8BLK_MAX_HEADS && heads % c.heads == 0 && seqs >= 1 && seqs <= FP8BLK_MAX_PANEL &&
            max_new >= 1 && max_new <= FP8BLK_MAX_PANEL && max_len >= 1 && max_len < kMost && window >= 0 && window < kMost &&
-           seqs * heads * ceil_div(max_new, 128) <= INT64_C(1) << 22;  // a launch has less than 2^32 threads
+           seqs * heads * ceil_div(max_new, 128) <= INT64_C(1) << 22;  // below 2^32 threads along x (latent rows: see kGridX)
 }
 
 }  // namespace

@@ -38,11 +38,16 @@ __device__ __forceinline__ float max_groups(float v) {  // over the four lanes l
     return max_halves(fmaxf(as_f32(r[0]), as_f32(r[1])));
 }
 
+// A launch has less than 2^32 threads along x: of more workgroups than this, every
+// kGridX are a row of the grid, and those past the last one have nothing to do.
+constexpr unsigned kGridX = 1u << 22;
+
 template <int DK, int ROWS, bool ONE>
 __global__ __launch_bounds__(64 * kWaves, 2) void k_latent(AttnArgs a, int row_tiles, int units, int spread) {
     using L = LatentLds<DK, ROWS>;
     __shared__ __attribute__((aligned(16))) char lds[L::kBytes];
-    const int xcd = blockIdx.x & 7, turn = blockIdx.x >> 3, per = (row_tiles + spread - 1) / spread;
+    const unsigned block = blockIdx.x + blockIdx.y * kGridX;
+    const int xcd = block & 7, turn = block >> 3, per = (row_tiles + spread - 1) / spread;
     const int unit = turn / per * (8 / spread) + xcd / spread, row_tile = row_tiles - 1 - (turn % per * spread + xcd % spread);
     if (unit >= units || row_tile < 0) return;
     const int s = unit / a.splits, c = split_at(a, unit, s);
@@ -303,8 +308,9 @@ template <int DK, int ROWS>
 void launch(const AttnArgs& a, hipStream_t s) {
     const int64_t units = (int64_t)a.seqs * a.splits, tiles = ceil_div((int64_t)a.max_new * a.heads, ROWS);
     const Deal d = deal(units, tiles);
-    if (one_page(a, kMine)) k_latent<DK, ROWS, true><<<d.grid, 64 * kWaves, 0, s>>>(a, (int)tiles, (int)units, d.spread);
-    else k_latent<DK, ROWS, false><<<d.grid, 64 * kWaves, 0, s>>>(a, (int)tiles, (int)units, d.spread);
+    const dim3 grid(d.grid < kGridX ? d.grid : kGridX, (unsigned)ceil_div(d.grid, kGridX));
+    if (one_page(a, kMine)) k_latent<DK, ROWS, true><<<grid, 64 * kWaves, 0, s>>>(a, (int)tiles, (int)units, d.spread);
+    else k_latent<DK, ROWS, false><<<grid, 64 * kWaves, 0, s>>>(a, (int)tiles, (int)units, d.spread);
     launch_join<kLatent>(a, s);
 }
 
