@@ -144,7 +144,7 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
         const bool edge = base < all_lo || base + kTile > all_hi;
         if (edge || here.held != ~0u) hide(z[0], here.held & keys_between(base, own_lo, own_hi), lane);
         v8bf p[1][2];
-        rescale(o, tile_weights(z, a.z_scale, run, p));
+        rescale(o, tile_weights(a, z, run, p));
         if constexpr (E4M3) store_codes(v_lds, v_codes, lane);
         else if (more) wait_loads<DK / 16 + (ONE ? 0 : 1)>();
         else wait_loads<0>();
@@ -369,7 +369,7 @@ __global__ __launch_bounds__(64 * GROUPS * HALVES, (GROUPS * HALVES == 8 || Chun
 #pragma unroll
             for (int t = 0; t < L::kTiles; ++t) hide(z[t], seen[t], lane);
         v8bf p[L::kTiles][2];
-        rescale(o, tile_weights(z, a.z_scale, run, p));
+        rescale(o, tile_weights(a, z, run, p));
 #pragma unroll
         for (int t = 0; t < L::kTiles; ++t) tile_sums<DV>(v_lds + (HALVES == 2 ? half : t) * kTile * DV * 2, p[t], o, lane);
     }
@@ -508,6 +508,7 @@ int attn_args(AttnArgs& a, const fp8blk_cache* cache, const uint16_t* q, int64_t
     a.q_and = a.z_scale > 0.0f ? ~0u : 0u;
     a.q_xor = a.z_scale > 0.0f && scale < 0.0f ? 0x80008000u : 0u;
     if (!(a.z_scale > 0.0f)) a.z_scale = 1.0f;
+    a.z_back = 1.0f / a.z_scale;
     a.splits = 1;
     a.chunk = 1 << 30;
     a.out_scale = latent ? c.k_scale : c.v_scale;

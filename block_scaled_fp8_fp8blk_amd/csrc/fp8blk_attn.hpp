@@ -29,6 +29,7 @@ struct AttnArgs {
     int32_t pages, page_shift;
     int32_t max_new, window, causal;
     float z_scale;    // |scale| * k_scale * log2(e): weights are powers of 2
+    float z_back;     // 1 / z_scale
     float out_scale;  // v_scale
     uint32_t q_and, q_xor;  // on two bf16 of q: its sign turned where scale < 0, 0 where it is 0 (then z_scale is 1)
     int32_t splits, chunk;  // workgroups along a sequence's keys, and their keys
@@ -394,6 +395,23 @@ __device__ __forceinline__ float add2(v2bf x, float a) {
     return __builtin_amdgcn_fdot2_f32_bf16(x, v2bf{(__bf16)1.0f, (__bf16)1.0f}, a, false);
 }
 
+// Of scores above 2^24 a step of f32 is 2 or more: z * scale, which weights 2^(z * scale -
+// m) take unrounded, is then as far from the rounded maximum m, and past 2^31 the highest
+// weight is 2^128 or 0 for it. In rows of such an m, z becomes (z * scale - m) / scale, the
+// product rounded like m's, and 0 is left to subtract (m else). A row's own m decides, so
+// that its bits do not depend on the others. One comparison a tile where there is none.
+template <int N, typename Z>
+__device__ __forceinline__ float less_coarse(const AttnArgs& a, Z (&z)[N], float m) {
+    const bool coarse = __builtin_fabsf(m) > 0x1p24f;
+    if (__any(coarse)) {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int i = 0; i < (int)(sizeof(Z) / sizeof(float)); ++i) z[n][i] = coarse ? (z[n][i] * a.z_scale - m) * a.z_back : z[n][i];
+    }
+    return coarse ? 0.0f : m;
+}
+
 // The scores of N tiles become weights 2^(z - m), as bf16 for their product with the
 // values: m is the row's maximum (in units of log 2) when it was last set, l the
 // lane's part of the running sum; returns the factor of what was summed before. The sum
@@ -402,27 +420,27 @@ __device__ __forceinline__ float add2(v2bf x, float a) {
 // unrounded ones took 16 additions where this takes 8 instructions). m follows the
 // maximum only where that has grown by more than 8: weights of up to 2^8 lose nothing,
 // and the outputs are hardly ever multiplied (not at all is what `rescale` checks for).
-// scale > 0.
 struct Running {
     float m, l;
 };
 template <int N>
-__device__ __forceinline__ float tile_weights(const v16f (&z)[N], float scale, Running& r, v8bf (&p)[N][2]) {
+__device__ __forceinline__ float tile_weights(const AttnArgs& a, v16f (&z)[N], Running& r, v8bf (&p)[N][2]) {
     float top = z[0][0];
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, z[n][i]);
-    top = max_halves(top) * scale;
+    top = max_halves(top) * a.z_scale;
     top = top > r.m + 8.0f ? top : r.m;
     const float base = top == -INFINITY ? 0.0f : top;
     const float keep = top == r.m ? 1.0f : exp2_fast(r.m - base);
+    const float less = less_coarse(a, z, base);
     float sum = 0.0f;
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-            const v2bf w = {(__bf16)exp2_fast(__builtin_fmaf(z[n][i], scale, -base)), (__bf16)exp2_fast(__builtin_fmaf(z[n][i + 1], scale, -base))};
+            const v2bf w = {(__bf16)exp2_fast(__builtin_fmaf(z[n][i], a.z_scale, -less)), (__bf16)exp2_fast(__builtin_fmaf(z[n][i + 1], a.z_scale, -less))};
             p[n][i >> 3][i & 7] = w[0], p[n][i >> 3][(i & 7) + 1] = w[1];
             sum = add2(w, sum);
         }

@@ -180,11 +180,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_latent(AttnArgs a, int row_t
             for (int p = 1; p < L::kParts; ++p) top = fmaxf(top, tops[p * ROWS + own_row]);
             top = top > m + 8.0f ? top : m;
             const float at = top == -INFINITY ? 0.0f : top, keep = top == m ? 1.0f : exp2_fast(m - at);
+            const float less = less_coarse(a, z, at);
             float sum = 0.0f;
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) z[kt][i] = exp2_fast(__builtin_fmaf(z[kt][i], a.z_scale, -at));
+                for (int i = 0; i < 4; ++i) z[kt][i] = exp2_fast(__builtin_fmaf(z[kt][i], a.z_scale, -less));
                 const v2bf w[2] = {{(__bf16)z[kt][0], (__bf16)z[kt][1]}, {(__bf16)z[kt][2], (__bf16)z[kt][3]}};
                 sum = add2(w[1], add2(w[0], sum));
                 const int chunk = (first + 16 * kt) / 8 + (g >> 1);
