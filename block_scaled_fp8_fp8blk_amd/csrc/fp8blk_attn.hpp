@@ -351,17 +351,19 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) { return __bui
 
 // What a row's sums of weights times values are multiplied by, from its maximum `top`
 // and the sum of its weights, both relative to that. A row that sees keys has a
-// weight of 1; one that sees none has sums of 0.
+// weight of 1; one that sees none, or only scores of -inf, gives 0 whatever its sums are
+// (0 * inf among the latter's): its factor is kNone, which no other is.
+constexpr float kNone = -1.0f;
 __device__ __forceinline__ float out_factor(const AttnArgs& a, int head, float top, float sum) {
-    if (sum == 0.0f) return 0.0f;
+    if (sum == 0.0f) return kNone;
     if (a.sinks) sum += exp2_fast(__builtin_fmaf(a.sinks[head], kLog2e, top == -INFINITY ? 0.0f : -top));
     return a.out_scale / sum;
 }
 
 // 8 columns of a row's output.
 __device__ __forceinline__ void write_out(char* p, const float (&v)[8], float f) {
-    *(__attribute__((address_space(1))) v4u*)p = v4u{pack_bf16(v[0] * f, v[1] * f), pack_bf16(v[2] * f, v[3] * f),
-                                                     pack_bf16(v[4] * f, v[5] * f), pack_bf16(v[6] * f, v[7] * f)};
+    const v4u d = {pack_bf16(v[0] * f, v[1] * f), pack_bf16(v[2] * f, v[3] * f), pack_bf16(v[4] * f, v[5] * f), pack_bf16(v[6] * f, v[7] * f)};
+    *(__attribute__((address_space(1))) v4u*)p = f == kNone ? v4u{} : d;
 }
 
 // A row's values of q, 8 at `p` and every `step` bytes on, as operands; as_operands,

@@ -930,8 +930,8 @@ int fp8blk_rope_append(const fp8blk_rope *rope, const int32_t *positions, int64_
  *   z[j] = scale * q . k[j];  out = sum_j exp(z[j]) v[j] / (sum_j exp(z[j]) + exp(sinks[h]))
  * It sees j <= p if causal, and j > p - window if window > 0. sinks: f32 [heads]
  * or NULL (no such term). A row that sees nothing, or only scores of -inf, gives
- * 0. What a row does not see does not touch it, infinities and NaN in it
- * included. Head h reads key head h / (heads / cache heads).
+ * 0, whatever the values are. What a row does not see does not touch it, infinities
+ * and NaN in it included. Head h reads key head h / (heads / cache heads).
  *   table: int32 [seqs, max_pages]; a page outside [0, pages) or past max_pages
  *     holds no keys. lens: int32 [seqs], starts: int32 [seqs + 1], not falling, in
  *     [0, N]; device, 4-byte aligned. A sequence may have no new tokens; rows

@@ -56,3 +56,27 @@ def test_scores_of_any_size(gpu, k, v, e4m3, T, power):
             got = c.out[:T, head].double()
             far = (got - want).abs() - H * want.abs() - 1.01 * (L + 64) * 2 * U * size - 2.0 ** -130
             assert not (~(far <= 0)).any(), f"{k} e4m3 {e4m3} T {T} 2^{power} scale {scale} head {head}: {int((~(far <= 0)).sum())} values off"
+
+
+@pytest.mark.parametrize("k,v", WIDTHS, ids=IDS)
+@pytest.mark.parametrize("T", [1, 8, 70])
+@pytest.mark.parametrize("L", [200, 3000])
+@pytest.mark.parametrize("sinks", [False, True])
+def test_rows_of_no_weight_over_values_that_are_not_finite(gpu, k, v, T, L, sinks):
+    """A row whose scores are all -inf gives 0, also where a value that it sees is an infinity
+    or NaN; the other rows have it. Latent values are keys too: there it is an infinity in
+    the column that makes the row's scores -inf."""
+    c = _call(gpu, 41, [L, 20], [T, 1], k, v, sinks=sinks)
+    p, i = c.paged.where(0, L)
+    c.paged.cache_k[p, i, :, 0] = 1.0
+    c.q[0, 1] = 0
+    c.q[0, 1, 0] = float("-inf")
+    for n, j in enumerate((3, L // 2, L - T)):  # seen by every row: inside whole tiles, and in the one where rows begin to differ
+        if v is None:
+            c.paged.cache_k[p[j], i[j], :, 0] = float("inf")
+        else:
+            c.paged.cache_v[p[j], i[j], :, 5 + n] = float("nan") if n == 1 else float("inf")
+    c.run()
+    assert (c.out[0, 1] == 0).all(), f"{k} {T} {L}: {int((c.out[0, 1] != 0).sum())} values are not 0"
+    if v is not None:
+        assert (~c.out[:T, [0, 2, 3], 5:8].isfinite()).all() and c.out[:T, [0, 2, 3], 8:].isfinite().all()
