@@ -129,21 +129,40 @@ struct Units {
         }
     }
 
+    __device__ __forceinline__ float mean_square(const RowsIn& t, int at, int lanes, bool whole) const {
+        float square = 0.0f;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const Place p = place(t, at + k * lanes);
+            if (p.in && (whole || !p.turned))
+#pragma unroll
+                for (int i = 0; i < kUnit; ++i) square = __builtin_fmaf(v[k][i], v[k][i], square);
+        }
+        for (int m = 1; m < lanes; m <<= 1) square += __shfl_xor(square, m);
+        return square / (float)t.norm_cols;
+    }
+
     __device__ __forceinline__ void finish(const RowsIn& t, char* out, int head, int at, int lanes, float eps, const float (*turn)[FP8BLK_MAX_ROT / 2]) {
         if (head >= t.heads) return;  // all lanes of a row
         const bool whole = t.norm_cols > t.pass_units * kUnit;
         float unit = 1.0f;
         if (t.norm) {
-            float square = 0.0f;
+            float mean = mean_square(t, at, lanes, whole) + eps;
+            const bool far = !(mean >= 0x1p-100f && mean <= 0x1p110f);
+            if (__any(far)) {
+                // Squares (and eps) that leave f32's range: once more, of such a row's
+                // values times a power of two that brings those of any size back into it.
+                const float by = !far ? 1.0f : mean < 1.0f ? 0x1p100f : 0x1p-70f;
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const Place p = place(t, at + k * lanes);
-                if (p.in && (whole || !p.turned))
+                for (int k = 0; k < U; ++k) {
+                    const Place p = place(t, at + k * lanes);
+                    if (p.in && (whole || !p.turned))
 #pragma unroll
-                    for (int i = 0; i < kUnit; ++i) square = __builtin_fmaf(v[k][i], v[k][i], square);
+                        for (int i = 0; i < kUnit; ++i) v[k][i] *= by;
+                }
+                mean = mean_square(t, at, lanes, whole) + eps * by * by;
             }
-            for (int m = 1; m < lanes; m <<= 1) square += __shfl_xor(square, m);
-            unit = 1.0f / sqrtf(square / (float)t.norm_cols + eps);
+            unit = 1.0f / sqrtf(mean);
         }
 #pragma unroll
         for (int k = 0; k < U; ++k) {

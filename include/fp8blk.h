@@ -881,7 +881,8 @@ int fp8blk_rope_freqs(int64_t rot, double base, double factor, double original, 
  * +-448 to +-448. A slot outside [0, pages * page_size) is not written (padding);
  * the others are distinct (of two tokens with one slot either may be left, in
  * parts). Angles are formed and reduced in 64 bits, cos and sin rounded to f32;
- * norms and rotation are f32, rounded once at the end.
+ * norms and rotation are f32, rounded once at the end. A norm takes rows of any
+ * size: their squares may leave f32's range.
  *   heads (HOST structs): pass [N, heads, pass_cols] and rot [N, heads, rot],
  *     both f32 or bf16 (type), each with a token and a head stride in values (0:
  *     the same for all); NULL: none, pass_cols 0 or no rotated columns (v has
