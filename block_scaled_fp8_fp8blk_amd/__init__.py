@@ -39,7 +39,8 @@ EXPORTS = ("fp8blk_abi_version", "fp8blk_strerror", "fp8blk_workspace_bytes", "f
            "fp4_load_check", "fp4_dequant_bf16", "fp4_expert_gemv", "fp4_expert_sequence_init",
            "fp4_expert_sequence", "fp8blk_chain_bytes", "fp8blk_chain_init", "fp8blk_gemv_chain",
            "fp8blk_chain_status", "fp8blk_block_norm", "fp8blk_moe_route", "fp4_moe_bytes", "fp4_moe", "int4_gemv",
-           "fp8blk_rope_freqs", "fp8blk_rope_append", "fp8blk_attn_bytes", "fp8blk_paged_attn", "fp8blk_latent_attn")
+           "fp8blk_rope_freqs", "fp8blk_rope_append", "fp8blk_attn_bytes", "fp8blk_attn_most_bytes", "fp8blk_paged_attn",
+           "fp8blk_latent_attn")
 MAX_GROUP = 8
 MAX_SEQ = 65536
 MAX_CHAIN = 65536
@@ -220,7 +221,8 @@ def load():
     L.fp8blk_rope_freqs.argtypes, L.fp8blk_rope_freqs.restype = [i64, f64, f64, f64, f64, f64, vp], i32
     L.fp8blk_rope_append.argtypes = [vp, vp, i64, vp, vp, i64, i64, vp, vp, vp, vp, f32, vp]
     L.fp8blk_rope_append.restype = i32
-    L.fp8blk_attn_bytes.argtypes, L.fp8blk_attn_bytes.restype = [vp, i64, i64, i64, i64, i64], sz
+    for need in (L.fp8blk_attn_bytes, L.fp8blk_attn_most_bytes):
+        need.argtypes, need.restype = [vp, i64, i64, i64, i64, i64], sz
     for attend in (L.fp8blk_paged_attn, L.fp8blk_latent_attn):
         attend.argtypes = [vp, vp, i64, i64, i64, i64, vp, f32, i32, i64, vp, vp, i64, i64, vp, sz, vp]
         attend.restype = i32
@@ -1295,8 +1297,14 @@ def fp8blk_rope_append(rope, positions, q, q_out, k, v, cache, slots, q_norm=Non
 
 
 def fp8blk_attn_bytes(cache, heads, seqs, max_new, max_len, window=0):
-    """Bytes of workspace of fp8blk_paged_attn and fp8blk_latent_attn (0: none)."""
+    """Bytes of workspace of fp8blk_paged_attn and fp8blk_latent_attn (0: none) of just
+    these sizes; smaller ones may need more."""
     return load().fp8blk_attn_bytes(cache.pointer, heads, seqs, max_new, max_len, window)
+
+
+def fp8blk_attn_most_bytes(cache, heads, seqs, max_new, max_len, window=0):
+    """Bytes of a workspace for every call of up to so many sequences, new tokens and keys."""
+    return load().fp8blk_attn_most_bytes(cache.pointer, heads, seqs, max_new, max_len, window)
 
 
 def _attn_args(cache, q, table, lens, starts, max_new, max_len, scale, out, ws, causal=True, window=0, sinks=None):

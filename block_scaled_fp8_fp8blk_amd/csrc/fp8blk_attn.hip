@@ -453,10 +453,13 @@ __global__ __launch_bounds__(64 * GROUPS * HALVES, (GROUPS * HALVES == 8 || Chun
     }
 }
 
-bool attn_sizes_ok(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, int64_t max_len, int64_t window) {
+bool attn_ranges_ok(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, int64_t max_len, int64_t window) {
     constexpr int64_t kMost = INT64_C(1) << 30;
     return heads >= 1 && heads <= FP8BLK_MAX_HEADS && heads % c.heads == 0 && seqs >= 1 && seqs <= FP8BLK_MAX_PANEL &&
-           max_new >= 1 && max_new <= FP8BLK_MAX_PANEL && max_len >= 1 && max_len < kMost && window >= 0 && window < kMost &&
+           max_new >= 1 && max_new <= FP8BLK_MAX_PANEL && max_len >= 1 && max_len < kMost && window >= 0 && window < kMost;
+}
+bool attn_sizes_ok(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, int64_t max_len, int64_t window) {
+    return attn_ranges_ok(c, heads, seqs, max_new, max_len, window) &&
            seqs * heads * ceil_div(max_new, 128) <= INT64_C(1) << 22;  // below 2^32 threads along x (latent rows: see kGridX)
 }
 
@@ -527,60 +530,132 @@ struct Plan {
     size_t bytes;
 };
 
+// Keys that a call's rows see at most of a sequence.
+int64_t seen_of(bool panel, int64_t max_new, int64_t max_len, int64_t window) {
+    return window > 0 ? std::min(max_len, window + (panel ? FP8BLK_MAX_M : max_new)) : max_len;
+}
+
+// Splits of a sequence's `seen` keys, from the workgroups that a call has without them.
+//
+// Latent: one workgroup a compute unit, with keys enough that the sums' way through memory
+// does not take longer than they do (8192 keys, 128 heads: 64 splits 21 us, 32 22,
+// 128 30). A chunk's sequences are of unequal length: twice as many where they are
+// long (8 of 100 tokens of up to 9000, 16 heads 382 -> 217, 4 of 877 of up to 14367,
+// one head 172 -> 112, 3 of 64 of up to 16000 166 -> 170; where all are as long as
+// that 5 to 16% more).
+int64_t latent_splits(int64_t units, int64_t seen, bool few, bool several_chunks) {
+    int64_t n = std::min(256 / units, ceil_div(seen, few ? 128 : 256));
+    if (several_chunks && n > 0 && seen >= 3000 * n) n *= 2;
+    return n;
+}
+
+// A workgroup streams 768 keys a split or more, as many splits as fill the card at
+// least: 4096 keys, 4 key heads: 32 splits 10.7 us, 8 13.8, one 41; 32 sequences of
+// up to 16384: 22 splits 115, 4 136 (all of 16384: 212 and 205, one 233). From 512
+// units on none (128 sequences of 4096: 116, in 2 splits 140), nor below 512 keys.
+constexpr int64_t kFewStep = 4 * kTile, kFewUnits = 512;
+int64_t few_splits(int64_t units, int64_t seen) {
+    return seen <= 512 ? 1 : std::min(std::max(256 / units, units < kFewUnits ? std::min(ceil_div(seen, 768), 16384 / units) : 1), ceil_div(seen, kFewStep));
+}
+
+// A tile of 64 keys takes a workgroup 1.1 us, each split of a row writes and reads
+// 8 bytes a column: n^2 splits are best where n^2 * rows * columns is some
+// thousand times the keys (causal rows see max_new / 2 less; of sequences of
+// different lengths fewer splits hold keys). Up to `fill` they only use idle
+// compute units; more have to be twice as many, at least 4 and not past `most`.
+// 500 new tokens of 3000, 32 heads over 4: 49 us in 4 splits, 53 in 2, 58 in one;
+// 3 sequences of 500 of up to 6000, 16 heads: 68 in 4, 107 in one (alike long ones:
+// 118, 128); 1000 of 1000, 16 heads: 25 in one, 33 in 2.
+struct ChunkSplits {
+    int64_t fill, most, best;
+};
+constexpr int64_t kChunkUnits = 384;
+ChunkSplits chunk_splits(int64_t units, int64_t seen, int64_t seqs, int64_t max_new, int64_t heads, int64_t cols) {
+    ChunkSplits c;
+    c.fill = std::max<int64_t>(256 / units, 1);
+    c.most = units <= (seqs > 1 ? kChunkUnits : 255) ? std::max<int64_t>((seqs > 1 ? 1024 : 512) / units, 4) : 1;
+    const double best = (seqs > 1 ? 18000.0 : 7500.0) * (double)std::max<int64_t>(seen - max_new / 2, 1) / ((double)seqs * max_new * heads * cols);
+    for (c.best = 1; 2 * c.best * c.best <= best; c.best *= 2) {
+    }
+    c.best = std::min(c.best, ceil_div(seen, 128));
+    return c;
+}
+
+// 32 rows of a latent panel a workgroup where there are few tiles, 64 where that many rows
+// read the keys more than once, or write more splits (128 heads, one sequence of 4000 keys:
+// 18 us, with 64 rows 25, two tokens 21 and 27; of 16000: 25, 30, two tokens 41 and 34;
+// 64 of 8000: 266, 226).
+constexpr int64_t kFewLatentTiles = 256;
+int64_t latent_tiles(int64_t seqs, int64_t heads, int64_t seen) { return seqs * ceil_div(heads, kLatentRows) * ceil_div(seen, 64); }
+
+size_t bytes_of(int64_t rows, int64_t splits, int64_t cols) { return splits > 1 ? (size_t)(rows * splits * (cols + 2)) * sizeof(float) : 0; }
+
 // Which kernel a call takes and how its keys are split. Up to FP8BLK_MAX_M new tokens
 // the number of them has no say, so that a row's bits do not depend on it.
 Plan plan(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, int64_t max_len, int64_t window) {
     const int64_t group = heads / c.heads;
     const bool panel = max_new <= FP8BLK_MAX_M, latent = !c.v;
-    const int64_t seen = window > 0 ? std::min(max_len, window + (panel ? FP8BLK_MAX_M : max_new)) : max_len;
+    const int64_t seen = seen_of(panel, max_new, max_len, window);
     Plan p;
-    // Latent: 32 rows a workgroup where there are few tiles, 64 where that many rows read
-    // the keys more than once, or write more splits (128 heads, one sequence of 4000 keys:
-    // 18 us, with 64 rows 25, two tokens 21 and 27; of 16000: 25, 30, two tokens 41 and 34;
-    // 64 of 8000: 266, 226).
-    p.few = panel && (!latent || group <= kTile || seqs * ceil_div(group, kLatentRows) * ceil_div(seen, 64) <= 256);
+    p.few = panel && (!latent || group <= kTile || latent_tiles(seqs, group, seen) <= kFewLatentTiles);
     const int64_t tile = latent ? (p.few ? kTile : kLatentRows) : kChunkRows;
     const int64_t units = seqs * c.heads * (p.few && !latent ? 1 : ceil_div(panel ? group : max_new * group, tile));
-    const int64_t step = p.few && !latent ? 4 * kTile : 64;
+    const int64_t step = p.few && !latent ? kFewStep : 64;
     int64_t n;
     if (latent) {
-        // One workgroup a compute unit, with keys enough that the sums' way through memory
-        // does not take longer than they do (8192 keys, 128 heads: 64 splits 21 us, 32 22,
-        // 128 30). A chunk's sequences are of unequal length: twice as many where they are
-        // long (8 of 100 tokens of up to 9000, 16 heads 382 -> 217, 4 of 877 of up to 14367,
-        // one head 172 -> 112, 3 of 64 of up to 16000 166 -> 170; where all are as long as
-        // that 5 to 16% more).
-        n = std::min(256 / units, ceil_div(seen, p.few ? 128 : 256));
-        if (!panel && seqs > 1 && n > 0 && seen >= 3000 * n) n *= 2;
+        n = latent_splits(units, seen, p.few, !panel && seqs > 1);
     } else if (p.few) {
-        // A workgroup streams 768 keys a split or more, as many splits as fill the card at
-        // least: 4096 keys, 4 key heads: 32 splits 10.7 us, 8 13.8, one 41; 32 sequences of
-        // up to 16384: 22 splits 115, 4 136 (all of 16384: 212 and 205, one 233). From 512
-        // units on none (128 sequences of 4096: 116, in 2 splits 140), nor below 512 keys.
-        n = seen <= 512 ? 1 : std::min(std::max(256 / units, units < 512 ? std::min(ceil_div(seen, 768), 16384 / units) : 1), ceil_div(seen, step));
+        n = few_splits(units, seen);
     } else {
-        // A tile of 64 keys takes a workgroup 1.1 us, each split of a row writes and reads
-        // 8 bytes a column: n^2 splits are best where n^2 * rows * columns is some
-        // thousand times the keys (causal rows see max_new / 2 less; of sequences of
-        // different lengths fewer splits hold keys). Up to `fill` they only use idle
-        // compute units; more have to be twice as many, at least 4 and not past `most`.
-        // 500 new tokens of 3000, 32 heads over 4: 49 us in 4 splits, 53 in 2, 58 in one;
-        // 3 sequences of 500 of up to 6000, 16 heads: 68 in 4, 107 in one (alike long ones:
-        // 118, 128); 1000 of 1000, 16 heads: 25 in one, 33 in 2.
-        const int64_t fill = std::max<int64_t>(256 / units, 1), room = seqs > 1 ? 384 : 255;
-        const int64_t most = units <= room ? std::max<int64_t>((seqs > 1 ? 1024 : 512) / units, 4) : 1;
-        const double best = (seqs > 1 ? 18000.0 : 7500.0) * (double)std::max<int64_t>(seen - max_new / 2, 1) / ((double)seqs * max_new * heads * c.v_cols);
-        for (n = 1; 2 * n * n <= best; n *= 2) {
-        }
-        n = std::min(n, ceil_div(seen, 128));
-        while (n > fill && (n > most || n < 4 || n < 2 * fill)) n = std::max(n / 2, fill);
+        const ChunkSplits r = chunk_splits(units, seen, seqs, max_new, heads, c.v_cols);
+        n = r.best;
+        while (n > r.fill && (n > r.most || n < 4 || n < 2 * r.fill)) n = std::max(n / 2, r.fill);
     }
     n = std::max<int64_t>(n, 1);
     p.chunk = (int32_t)(ceil_div(ceil_div(seen, n), step) * step);
     p.splits = (int32_t)(ceil_div(seen, p.chunk) + (window > 0 ? 1 : 0));
     if (n == 1) p.splits = 1, p.chunk = 1 << 30;
-    p.bytes = p.splits > 1 ? (size_t)(seqs * max_new * heads * p.splits * (c.v_cols + 2)) * sizeof(float) : 0;
+    p.bytes = bytes_of(seqs * max_new * heads, p.splits, c.v_cols);
     return p;
+}
+
+// The most bytes that plan asks for with up to so many sequences, new tokens and keys
+// (which is not what it asks for with just as many: more rows leave less room for splits).
+// All rules above give no fewer splits for more keys, a chunk's before it halves them; so the
+// largest max_len counts, for each number of sequences and of row tiles that leaves room
+// for splits; of the new tokens that make up such a number of tiles the fewest for
+// the splits, the most for the rows.
+size_t most_bytes(const fp8blk_cache& c, int64_t heads, int64_t seqs, int64_t max_new, int64_t max_len, int64_t window) {
+    const int64_t group = heads / c.heads, edge = window > 0 ? 1 : 0;
+    const bool latent = !c.v;
+    size_t most = 0;
+    auto take = [&](int64_t rows, int64_t n) { most = std::max(most, n > 1 ? bytes_of(rows, n + edge, c.v_cols) : 0); };
+    const int64_t panel = std::min<int64_t>(max_new, FP8BLK_MAX_M), seen = seen_of(true, panel, max_len, window);
+    for (int64_t s = 1; s <= seqs && s * c.heads < kFewUnits; ++s) {
+        const int64_t rows = s * panel * heads;
+        if (!latent) {
+            take(rows, few_splits(s * c.heads, seen));
+            continue;
+        }
+        const int64_t few_seen = group <= kTile ? seen : std::min(seen, 64 * (kFewLatentTiles / latent_tiles(s, group, 1)));
+        if (few_seen > 0) take(rows, latent_splits(s * ceil_div(group, kTile), few_seen, true, false));
+        if (few_seen < seen) take(rows, latent_splits(s * ceil_div(group, kLatentRows), seen, false, false));
+    }
+    const int64_t tile = latent ? kLatentRows : kChunkRows, units = latent ? 256 : kChunkUnits;
+    for (int64_t s = 1; s <= seqs && s * c.heads <= units; ++s)
+        for (int64_t tiles = 1; s * c.heads * tiles <= units; ++tiles) {
+            const int64_t from = std::max<int64_t>((tiles - 1) * tile / group + 1, FP8BLK_MAX_M + 1), to = std::min(tiles * tile / group, max_new);
+            if (from > max_new) break;
+            if (from > to) continue;
+            const int64_t u = s * c.heads * tiles, all = seen_of(false, to, max_len, window);
+            if (latent) {
+                take(s * to * heads, latent_splits(u, all, false, s > 1));
+            } else {
+                const ChunkSplits r = chunk_splits(u, all, s, from, heads, c.v_cols);
+                take(s * to * heads, r.best <= r.fill ? r.best : std::max(r.fill, std::min(r.best, r.most)));
+            }
+        }
+    return most;
 }
 
 template <int DK, int DV, bool E4M3, bool ONE>
@@ -632,6 +707,12 @@ extern "C" size_t fp8blk_attn_bytes(const fp8blk_cache* cache, int64_t heads, in
                                     int64_t max_len, int64_t window) {
     if (!cache || !cache_ok(*cache) || !attn_sizes_ok(*cache, heads, seqs, max_new, max_len, window)) return 0;
     return plan(*cache, heads, seqs, max_new, max_len, window).bytes;
+}
+
+extern "C" size_t fp8blk_attn_most_bytes(const fp8blk_cache* cache, int64_t heads, int64_t seqs, int64_t max_new,
+                                         int64_t max_len, int64_t window) {
+    if (!cache || !cache_ok(*cache) || !attn_ranges_ok(*cache, heads, seqs, max_new, max_len, window)) return 0;
+    return most_bytes(*cache, heads, seqs, max_new, max_len, window);
 }
 
 namespace {

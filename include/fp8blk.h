@@ -956,6 +956,10 @@ int fp8blk_rope_append(const fp8blk_rope *rope, const int32_t *positions, int64_
  *   seqs * heads * ceil(max_new / 128) <= 2^22.
  *   ws: device, 256-byte aligned, >= fp8blk_attn_bytes(...) bytes (0: none needed,
  *     or bad sizes; ws may then be NULL); its contents on entry do not matter.
+ *     Fewer sequences, tokens or keys may need more (one token of 32 sequences needs
+ *     a workspace, of 512 none): one for all calls of up to so many of each has
+ *     fp8blk_attn_most_bytes(...) bytes, of the same heads and window; there seqs,
+ *     max_new and max_len need not be the sizes of one call (no limit on their product).
  * Sums and the softmax's statistics are f32: scores of any size up to 2^126 count
  * (those far above 1 with f32's steps there), and values as long as their sum over the
  * keys, each times 2^9, is below 2^127. The weights (exp of z less a value near
@@ -973,6 +977,8 @@ typedef struct fp8blk_batch {
 
 size_t fp8blk_attn_bytes(const fp8blk_cache *cache, int64_t heads, int64_t seqs, int64_t max_new, int64_t max_len,
                          int64_t window);
+size_t fp8blk_attn_most_bytes(const fp8blk_cache *cache, int64_t heads, int64_t seqs, int64_t max_new, int64_t max_len,
+                              int64_t window);
 int fp8blk_paged_attn(const fp8blk_cache *cache, const uint16_t *q, int64_t q_token, int64_t q_head, int64_t N,
                       int64_t heads, const fp8blk_batch *batch, float scale, int causal, int64_t window,
                       const float *sinks, uint16_t *out, int64_t out_token, int64_t out_head, void *ws, size_t ws_bytes,
