@@ -353,7 +353,7 @@ extern "C" int fp8blk_rope_append(const fp8blk_rope* rope, const int32_t* positi
         outs[0] = {q_out, span(N, q_token, q->heads, q_head, cols, 2)};
     }
     if (k) {
-        if (!cache_ok(*cache) || !cache->v != !v) return FP8BLK_ERR_ARG;
+        if (!cache_ok(*cache) || !cache->v != !v || cache->k == cache->v) return FP8BLK_ERR_ARG;
         if (k->heads != cache->heads || k->pass_cols + rope->rot != cache->k_cols) return FP8BLK_ERR_ARG;
         if (v && (v->heads != cache->heads || v->pass_cols != cache->v_cols)) return FP8BLK_ERR_ARG;
         const int64_t size = cache->type == FP8BLK_E4M3 ? 1 : 2;
