@@ -1334,9 +1334,11 @@ def fp8blk_paged_attn(cache, q, table, lens, starts, max_new, max_len, scale, ou
     bfloat16, over a paged cache (fp8blk_cache): sequence s has lens[s] tokens in
     the pages table[s] (int32 [seqs, pages]), the last starts[s + 1] - starts[s]
     of them being rows starts[s] .. of q (int32 [seqs + 1]). max_new and max_len
-    are the most new tokens and tokens of a sequence, on the host. causal; window >
-    0: only the last `window` keys; sinks f32 [heads] or None: a logit in the sum
-    below. ws: fp8blk_attn_bytes(...) bytes. Key and value columns 64, 64; 128,
+    are the most new tokens and tokens of a sequence, on the host (bounds far above
+    them cost time, and so do single tokens beside a chunk: two calls take less).
+    causal; window > 0: only the last `window` keys; sinks f32 [heads] or None: a
+    logit in the sum below. ws: fp8blk_attn_bytes(...) bytes, or for calls of many
+    sizes fp8blk_attn_most_bytes(...). Key and value columns 64, 64; 128,
     128; 192, 128 or 256, 256."""
     dev, args = _attn_args(cache, q, table, lens, starts, max_new, max_len, scale, out, ws, causal, window, sinks)
     return _enqueue(load().fp8blk_paged_attn, dev, args, stream, "fp8blk_paged_attn", check)

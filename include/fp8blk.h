@@ -856,7 +856,9 @@ typedef struct fp8blk_cache {
  * (the YaRN paper's "NTK-by-parts"): with t = original * freqs[i] / (2 pi) turns
  * in the original context, freqs[i] stays where t > fast, is divided by factor
  * where t < slow, and changes in between as w + (1 - w) / factor, w = (t - slow)
- * / (fast - slow). fast == slow: at t >= fast it stays.
+ * / (fast - slow). fast == slow: at t >= fast it stays. (A model that is defined with
+ * a ramp over the pair's index i, between bounds rounded to whole i, fills its freqs
+ * itself.)
  *   rot: a multiple of 8, 8 .. FP8BLK_MAX_ROT; base > 0; factor >= 1; original
  *   >= 1 where factor > 1; 0 <= slow <= fast; all finite.
  * Pure host function.
@@ -894,7 +896,9 @@ int fp8blk_rope_freqs(int64_t rot, double base, double factor, double original, 
  *     FP8BLK_MAX_PANEL. eps >= 0 and finite.
  *   q and q_out may be NULL together; k, cache and slots too, and v is NULL with
  *     them or where the cache is a latent one. k has the cache's heads and k_cols
- *     columns, v the cache's heads and v_cols.
+ *     columns, v the cache's heads and v_cols. No row of the cache shares memory with
+ *     another, of keys or values (else parts of either are left; FP8BLK_ERR_ARG where
+ *     k and v are one address).
  *   q_out: [N, heads, cols] with strides q_token and q_head in values.
  *   All buffers: device; values 16-byte aligned, strides multiples of 8, an
  *   output's at least its columns. q_out and the cache overlap no input and not
@@ -932,14 +936,21 @@ int fp8blk_rope_append(const fp8blk_rope *rope, const int32_t *positions, int64_
  * It sees j <= p if causal, and j > p - window if window > 0. sinks: f32 [heads]
  * or NULL (no such term). A row that sees nothing, or only scores of -inf, gives
  * 0, whatever the values are. What a row does not see does not touch it, infinities
- * and NaN in it included. Head h reads key head h / (heads / cache heads).
+ * and NaN in it included; of those that it sees, each makes its column of the row an
+ * infinity or NaN (which of the two is not said where the weight is below f32's
+ * range). With a scale of 0 q counts as 0. Head h reads key head h / (heads / cache
+ * heads).
  *   table: int32 [seqs, max_pages]; a page outside [0, pages) or past max_pages
  *     holds no keys. lens: int32 [seqs], starts: int32 [seqs + 1], not falling, in
  *     [0, N]; device, 4-byte aligned. A sequence may have no new tokens; rows
  *     outside of all are left as they were.
  *   max_new, max_len (host): at least every sequence's new tokens and lens. A
  *     sequence's tokens past max_new get no output; lens past max_len only take
- *     longer.
+ *     longer (with a window a panel's rows may then have other bits than single
+ *     tokens'). How the keys are split follows from these, not from what is there:
+ *     bounds far above it cost time (fewer and longer splits), and with max_new >
+ *     FP8BLK_MAX_M every sequence is taken to have max_new rows, so that a chunk and
+ *     many single tokens are faster as two calls.
  *   q: bf16 [N, heads, k_cols], out: bf16 [N, heads, v_cols], each with a token
  *     and a head stride in values (multiples of 8; out's at least v_cols);
  *     device, 16-byte aligned. out overlaps neither q nor the cache (else
@@ -960,6 +971,7 @@ int fp8blk_rope_append(const fp8blk_rope *rope, const int32_t *positions, int64_
  *     a workspace, of 512 none): one for all calls of up to so many of each has
  *     fp8blk_attn_most_bytes(...) bytes, of the same heads and window; there seqs,
  *     max_new and max_len need not be the sizes of one call (no limit on their product).
+ *     ws overlaps nothing else.
  * Sums and the softmax's statistics are f32: scores of any size up to 2^126 count
  * (those far above 1 with f32's steps there), and values as long as their sum over the
  * keys, each times 2^9, is below 2^127. The weights (exp of z less a value near
