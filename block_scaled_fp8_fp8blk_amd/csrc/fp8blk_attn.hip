@@ -223,7 +223,7 @@ __global__ __launch_bounds__(256, (FewLds<DK, DV>::kBytes <= 80 * 1024 ? 2 : 1))
 // rows, each 32 keys of a tile with maximum, sum and outputs of its own, joined at the
 // end. Bound by the matrix cores, their operands from LDS (a quarter of a tile's 4800
 // cycles each), the softmax between them and the barrier; only another wave on the SIMD
-// hides one behind the other. 2048 new tokens of 8192, 32 heads of 128 over 4: 256 us,
+// hides one behind the other. 2048 new tokens of 8192, 32 heads of 128 over 4: 257 us,
 // 940 TFLOP/s of the 1290 that a large matrix product reaches. Tiles of 64 keys, not
 // 32: half the barriers (heads of 192 and 128, 73 -> 59 us). A third buffer gave nothing.
 template <int DK, int DV, bool ONE, int GROUPS, int HALVES>
@@ -550,9 +550,9 @@ int64_t latent_splits(int64_t units, int64_t seen, bool few, bool several_chunks
 }
 
 // A workgroup streams 768 keys a split or more, as many splits as fill the card at
-// least: 4096 keys, 4 key heads: 32 splits 10.7 us, 8 13.8, one 41; 32 sequences of
+// least: 4096 keys, 4 key heads: 32 splits 10.8 us, 8 13.8, one 41; 32 sequences of
 // up to 16384: 22 splits 115, 4 136 (all of 16384: 212 and 205, one 233). From 512
-// units on none (128 sequences of 4096: 116, in 2 splits 140), nor below 512 keys.
+// units on none (128 sequences of up to 4096: 116, in 2 splits 140), nor below 512 keys.
 constexpr int64_t kFewStep = 4 * kTile, kFewUnits = 512;
 int64_t few_splits(int64_t units, int64_t seen) {
     return seen <= 512 ? 1 : std::min(std::max(256 / units, units < kFewUnits ? std::min(ceil_div(seen, 768), 16384 / units) : 1), ceil_div(seen, kFewStep));
@@ -671,11 +671,11 @@ void launch_chunk(const AttnArgs& a, hipStream_t s) {
     const Deal d = deal(units, tiles);
     // A wave waits for its own products and powers, so a SIMD wants two. Heads of 256,
     // of which LDS holds one workgroup a compute unit: eight waves (3 sequences of 777
-    // tokens: 101 us, four waves 127; e4m3 or in small pages the registers do not allow
+    // tokens: 106 us, four waves some 25 more; e4m3 or in small pages the registers do not allow
     // for them). Up to 256 workgroups: 64 rows for four waves, twice as many workgroups
-    // (2000 tokens of 16 heads of 192 and 128: 48 us; 128 rows for four waves 60, for
+    // (2000 tokens of 16 heads of 192 and 128: 49 us; 128 rows for four waves 60, for
     // eight 55). More: 128 rows for four, which read a tile for twice as many rows (2048
-    // of 8192 tokens: 256 us, 64 rows 317).
+    // of 8192 tokens: 257 us, 64 rows 317).
     if constexpr (DV == 256 && ONE && !E4M3) {
         k_attn_chunk<DK, DV, E4M3, ONE, 4, 2><<<d.grid, 512, 0, s>>>(a, (int)tiles, (int)units, d.spread, false);
     } else {

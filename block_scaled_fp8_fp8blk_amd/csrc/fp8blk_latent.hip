@@ -12,7 +12,7 @@
 //
 // 64 rows: a tile takes 2.8 us (3.6 where all compute units read), of which the matrix
 // cores work 0.9; LDS reads 420 KB of operands for it, 1.4 us. 64 sequences of 8000
-// keys, 128 heads: 226 us, 630 TFLOP/s; with four waves, 32 rows and 128 columns each,
+// keys, 128 heads: 227 us, 630 TFLOP/s; with four waves, 32 rows and 128 columns each,
 // 252. 32 rows: 16 sequences of 16384 keys, 16 heads, 68 us, 4.4 TB/s; with 16 rows, one
 // tile in LDS and two workgroups a compute unit, 73.
 #include "fp8blk_attn.hpp"
