@@ -974,7 +974,8 @@ int fp8blk_rope_append(const fp8blk_rope *rope, const int32_t *positions, int64_
  *     ws overlaps nothing else.
  * Sums and the softmax's statistics are f32: scores of any size up to 2^126 count
  * (those far above 1 with f32's steps there), and values as long as their sum over the
- * keys, each times 2^9, is below 2^127. The weights (exp of z less a value near
+ * keys, each times 2^9, is below 2^127; what is less than 2^-126 of a row's sum below,
+ * its sink included, counts as 0. The weights (exp of z less a value near
  * the row's maximum) are rounded to bf16, for their product with v and in the sum below
  * alike. With max_new <= FP8BLK_MAX_M a row's bits depend on
  * what it sees, on seqs, max_len, window and the heads, and on nothing else: causal,
